@@ -1,7 +1,8 @@
 """Decode-time MSA lightning indexer for GB300 (sm_103a).
 
 The compute lives in ``libmsa_indexer.so`` (hand-written CUDA kernels behind
-a C ABI, declared in ``include/msa_indexer.h``); this package only builds and
+a C ABI, declared in ``include/msa_indexer.h`` and, for the operators that read
+the indexer's blocks, ``include/msa_attention.h``); this package only builds and
 binds it.  PyTorch supplies device memory and streams.
 """
 
@@ -46,4 +47,12 @@ from ._binding import (  # noqa: F401
     msa_indexer_workspace_bytes,
     msa_status_string,
     new_workspace,
+)
+
+from ._attention import (  # noqa: E402,F401
+    ATTENTION_EXPORTED,
+    MSA_FAULT_BLOCK_ID,
+    MSA_MAX_GROUP,
+    msa_attention_sparse,
+    msa_attention_sparse_fp8,
 )

@@ -1,0 +1,176 @@
+// Attention over the blocks the indexer selected: argument checks and launch of
+// block_attn_kernel (block_attn.cuh).
+#include "block_attn.cuh"
+
+namespace msa {
+
+// Tensor map of a paged cache as [page][head][token][dim]; strides in elements
+// (page, token, head).  The stride of an axis of length 1 is never used.
+bool make_cache_map(CUtensorMap *map, const void *base, const int64_t *strides, int64_t pages, int heads, bool fp8)
+{
+    EncodeTiledFn enc = encode_tiled();
+    if (!enc)
+        return false;
+    const cuuint64_t size = fp8 ? 1 : 2;
+    const cuuint64_t dims[4] = {static_cast<cuuint64_t>(kDim), static_cast<cuuint64_t>(kPage),
+                                static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(pages)};
+    const cuuint64_t bytes[3] = {static_cast<cuuint64_t>(strides[1]) * size,
+                                 static_cast<cuuint64_t>(heads > 1 ? strides[2] : kDim) * size,
+                                 static_cast<cuuint64_t>(pages > 1 ? strides[0] : kDim) * size};
+    const cuuint32_t box[4] = {fp8 ? 128u : 64u, 128u, 1u, 1u};
+    const cuuint32_t estr[4] = {1, 1, 1, 1};
+    return enc(map, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base),
+               dims, bytes, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// A cache's address and strides: 16-byte multiples, positive, within a tensor map's 2^40-byte strides.
+bool cache_ok(const void *base, const int64_t *strides, int64_t pages, int heads, bool fp8)
+{
+    if (!base || !strides || (reinterpret_cast<uintptr_t>(base) & 15))
+        return false;
+    const int64_t unit = fp8 ? 16 : 8;
+    for (int i = 0; i < 3; ++i) {
+        if ((i == 0 && pages == 1) || (i == 2 && heads == 1))
+            continue;
+        if (strides[i] < kDim || strides[i] % unit || strides[i] >= (int64_t{1} << 38))
+            return false;
+    }
+    return true;
+}
+
+bool unaligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) != 0; }
+
+// CTAs of the cluster that walks one list: enough to fill two CTAs an SM, at
+// most one per block of the list.
+int block_attn_split(int64_t units, int pages, int sms)
+{
+    int s = 1;
+    while (s < 8 && 2 * s <= pages && units * s * 2 <= 2 * static_cast<int64_t>(sms))
+        s *= 2;
+    return s;
+}
+
+template <class F, int MT, bool OWN>
+msa_status launch_block_attn(const BlockAttnParams &p, int64_t units, int split, cudaStream_t st)
+{
+    const size_t smem = block_attn_smem<F>(OWN || !p.mass ? 0 : (p.k + split - 1) / split);
+    auto *kernel = block_attn_kernel<F, MT, OWN>;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
+        return MSA_ERR_CUDA;
+    cudaLaunchConfig_t cfg;
+    std::memset(&cfg, 0, sizeof cfg);
+    cudaLaunchAttribute attr[1];
+    cfg.gridDim = dim3(static_cast<unsigned>(units * split));
+    cfg.blockDim = dim3(kAttnThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = split;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, p) == cudaSuccess ? MSA_OK : MSA_ERR_CUDA;
+}
+
+static msa_status sparse_entry(const void *q, int64_t q_stride, const void *k, const int64_t *k_strides,
+                               const float *k_scale, const void *v, const int64_t *v_strides, const float *v_scale,
+                               int64_t num_pages, const int32_t *block_table, int64_t bt_stride,
+                               const int32_t *seq_lens, int batch, int q_len, int kv_heads, int group,
+                               int max_model_len, const int32_t *ids, int sel_heads, int topk, float scale, void *out,
+                               float *out_lse, float *out_mass, void *workspace, size_t workspace_bytes, void *stream,
+                               bool fp8)
+{
+    if (batch < 0 || q_len < 1 || kv_heads < 1 || group < 1 || sel_heads < 1 || topk < 1 || num_pages < 1 ||
+        bt_stride < 1 || max_model_len < 1 || kv_heads % sel_heads || !(scale > 0.0f) || !(scale < INFINITY))
+        return MSA_ERR_INVALID_ARG;
+    if (batch > MSA_MAX_BATCH || num_pages > (int64_t{1} << 24) || topk > MSA_MAX_TOPK || group > MSA_MAX_GROUP ||
+        kv_heads > 1024 || q_len > 64 || static_cast<int64_t>(batch) * q_len * kv_heads > (int64_t{1} << 27))
+        return MSA_ERR_UNSUPPORTED;
+    if (!q || !block_table || !seq_lens || !ids || !out || !workspace || !cache_ok(k, k_strides, num_pages, kv_heads, fp8) ||
+        !cache_ok(v, v_strides, num_pages, kv_heads, fp8) || unaligned(q, 16) || q_stride % 8 ||
+        q_stride < static_cast<int64_t>(kv_heads) * group * kDim || unaligned(out, 16) || unaligned(workspace, 256))
+        return MSA_ERR_INVALID_ARG;
+    if (fp8 && (!k_scale || !v_scale || unaligned(k_scale, 16) || unaligned(v_scale, 16)))
+        return MSA_ERR_INVALID_ARG;
+    if (workspace_bytes < kHeaderBytes)
+        return MSA_ERR_WORKSPACE_TOO_SMALL;
+    if (batch == 0)
+        return MSA_OK;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess)
+        return MSA_ERR_CUDA;
+    const int sms = device_sms(dev);
+    if (sms <= 0)
+        return MSA_ERR_CUDA;
+    BlockAttnParams p;
+    std::memset(&p, 0, sizeof p);
+    if (!make_cache_map(&p.kmap, k, k_strides, num_pages, kv_heads, fp8) ||
+        !make_cache_map(&p.vmap, v, v_strides, num_pages, kv_heads, fp8))
+        return MSA_ERR_CUDA;
+    p.q = static_cast<const uint16_t *>(q);
+    p.kscale = k_scale;
+    p.vscale = v_scale;
+    p.block_table = block_table;
+    p.seq_lens = seq_lens;
+    p.ids = ids;
+    p.out = static_cast<uint16_t *>(out);
+    p.lse = out_lse;
+    p.mass = out_mass;
+    p.fault = &static_cast<WorkspaceHeader *>(workspace)->fault;
+    p.q_stride = q_stride;
+    p.bt_stride = bt_stride;
+    p.num_pages = num_pages;
+    p.batch = batch;
+    p.q_len = q_len;
+    p.kv_heads = kv_heads;
+    p.sel_heads = sel_heads;
+    p.group = group;
+    p.k = topk;
+    p.seq_limit = static_cast<int>(std::min<int64_t>(max_model_len, kPage * bt_stride));
+    p.unit_rows = group;
+    p.row_tiles = 1;
+    p.scale_log2 = scale * kLog2e;
+    const int64_t units = static_cast<int64_t>(batch) * q_len * kv_heads;
+    const int split = block_attn_split(units, topk, sms);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (fp8)
+        return group <= 16   ? launch_block_attn<AttnFp8, 1, false>(p, units, split, st)
+               : group <= 32 ? launch_block_attn<AttnFp8, 2, false>(p, units, split, st)
+                             : launch_block_attn<AttnFp8, 4, false>(p, units, split, st);
+    return group <= 16   ? launch_block_attn<AttnBf16, 1, false>(p, units, split, st)
+           : group <= 32 ? launch_block_attn<AttnBf16, 2, false>(p, units, split, st)
+                         : launch_block_attn<AttnBf16, 4, false>(p, units, split, st);
+}
+
+}  // namespace msa
+
+using namespace msa;
+
+extern "C" msa_status msa_attention_sparse(const void *q, int64_t q_stride, const void *k, const int64_t *k_strides,
+                                           const void *v, const int64_t *v_strides, int64_t num_pages,
+                                           const int32_t *block_table, int64_t bt_stride, const int32_t *seq_lens,
+                                           int batch, int q_len, int kv_heads, int group, int max_model_len,
+                                           const int32_t *ids, int sel_heads, int topk, float scale, void *out,
+                                           float *out_lse, float *out_mass, void *workspace, size_t workspace_bytes,
+                                           void *stream)
+{
+    return sparse_entry(q, q_stride, k, k_strides, nullptr, v, v_strides, nullptr, num_pages, block_table, bt_stride,
+                        seq_lens, batch, q_len, kv_heads, group, max_model_len, ids, sel_heads, topk, scale, out,
+                        out_lse, out_mass, workspace, workspace_bytes, stream, false);
+}
+
+extern "C" msa_status msa_attention_sparse_fp8(const void *q, int64_t q_stride, const void *k,
+                                               const int64_t *k_strides, const float *k_scale, const void *v,
+                                               const int64_t *v_strides, const float *v_scale, int64_t num_pages,
+                                               const int32_t *block_table, int64_t bt_stride, const int32_t *seq_lens,
+                                               int batch, int q_len, int kv_heads, int group, int max_model_len,
+                                               const int32_t *ids, int sel_heads, int topk, float scale, void *out,
+                                               float *out_lse, float *out_mass, void *workspace,
+                                               size_t workspace_bytes, void *stream)
+{
+    return sparse_entry(q, q_stride, k, k_strides, k_scale, v, v_strides, v_scale, num_pages, block_table, bt_stride,
+                        seq_lens, batch, q_len, kv_heads, group, max_model_len, ids, sel_heads, topk, scale, out,
+                        out_lse, out_mass, workspace, workspace_bytes, stream, true);
+}
