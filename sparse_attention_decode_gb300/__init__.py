@@ -52,7 +52,13 @@ from ._binding import (  # noqa: F401
 from ._attention import (  # noqa: E402,F401
     ATTENTION_EXPORTED,
     MSA_FAULT_BLOCK_ID,
+    MSA_FAULT_TOKEN,
+    MSA_MAX_CACHE_BLOCKS,
+    MSA_MAX_DRAFT,
     MSA_MAX_GROUP,
     msa_attention_sparse,
     msa_attention_sparse_fp8,
+    msa_cache_accumulate,
+    msa_cache_evict,
+    msa_verify_draft,
 )

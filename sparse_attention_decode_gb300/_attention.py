@@ -14,11 +14,17 @@ import torch
 from ._binding import MSA_HEAD_DIM, MSA_PAGE_TOKENS, _check, _ptr, _stream_ptr, load
 
 MSA_FAULT_BLOCK_ID = 0x10
+MSA_FAULT_TOKEN = 0x20
 MSA_MAX_GROUP = 64
+MSA_MAX_CACHE_BLOCKS = 32768
+MSA_MAX_DRAFT = 63
 
 ATTENTION_EXPORTED = (
     "msa_attention_sparse",
     "msa_attention_sparse_fp8",
+    "msa_cache_accumulate",
+    "msa_cache_evict",
+    "msa_verify_draft",
 )
 
 _Strides = ctypes.c_int64 * 3
@@ -41,6 +47,11 @@ _ARGTYPES = {
                               _P, _int, _int, _f32, _P, _P, _P, _P, _size, _P], _int),
     "msa_attention_sparse_fp8": ([_P, _i64, _P, _Strides, _P, _P, _Strides, _P, _i64, _P, _i64, _P, _int, _int, _int,
                                   _int, _int, _P, _int, _int, _f32, _P, _P, _P, _P, _size, _P], _int),
+    "msa_cache_accumulate": ([_P, _i64, _P, _P, _P, _int, _int, _int, _int, _int, _P, _size, _P], _int),
+    "msa_cache_evict": ([_P, _i64, _P, _P, _i64, _int, _int, _int, _int, _int, _int, _P, _i64, _P, _P, _P, _P, _P,
+                         _size, _P], _int),
+    "msa_verify_draft": ([_P, _int, _i64, _i64, _P, _P, _P, _P, _P, _P, _int, _int, _int, _P, _P, _P, _P, _size, _P],
+                         _int),
 }
 
 
@@ -128,3 +139,71 @@ def msa_attention_sparse_fp8(q, k, k_scale, v, v_scale, block_table, seq_lens, i
     """msa_attention_sparse on E4M3 codes with fp32 scales [pages, kv_heads, 128]."""
     _sparse("msa_attention_sparse_fp8", q, k, k_scale, v, v_scale, block_table, seq_lens, ids, out, workspace, scale,
             q_len, max_model_len, out_lse, out_mass, stream)
+
+
+def _is(t, dtype, shape, what: str):
+    assert t.dtype == dtype and tuple(t.shape) == shape and t.is_contiguous(), f"{what}: {dtype} {list(shape)}, contiguous"
+    return t.data_ptr()
+
+
+def msa_cache_accumulate(weights, ids, mass, workspace, *, q_len: int = 1, n_rows=None, stream=None) -> None:
+    """Adds the mass of each request's first n_rows positions to weights [batch, kv_heads, blocks], in place.
+
+    ``ids`` [batch * q_len, sel_heads, k] and ``mass`` [batch * q_len, kv_heads, k] as msa_attention_sparse takes and
+    gives them.  See include/msa_attention.h.
+    """
+    batch, kv_heads, cols = (int(x) for x in weights.shape)
+    rows, sel, topk = (int(x) for x in ids.shape)
+    assert rows == batch * q_len, "ids: batch * q_len rows"
+    st = _fn("msa_cache_accumulate")(
+        _is(weights, torch.float32, (batch, kv_heads, cols), "weights"), cols,
+        _is(ids, torch.int32, (rows, sel, topk), "ids"), _is(mass, torch.float32, (rows, kv_heads, topk), "mass"),
+        None if n_rows is None else _is(n_rows, torch.int32, (batch,), "n_rows"), batch, q_len, kv_heads, sel, topk,
+        *_ws(workspace), _stream_ptr(stream))
+    _check(st, "msa_cache_accumulate")
+
+
+def msa_cache_evict(block_table, seq_lens, weights, budget: int, n_sink: int, n_window: int, out_table, out_seq_lens,
+                    out_weights, out_freed, out_n_freed, workspace, *, max_model_len: Optional[int] = None,
+                    stream=None) -> None:
+    """Brings every request to at most ``budget`` blocks, keeping sink, window and the largest summed weights.
+
+    The new table, lengths and weights may be written over the old ones.  See include/msa_attention.h.
+    """
+    batch, cols, bt_stride = _requests(block_table, seq_lens)
+    o_batch, o_cols, o_stride = _requests(out_table, out_seq_lens)
+    assert o_batch == batch and o_cols == cols, "out_table, out_seq_lens: like the inputs"
+    kv_heads = int(weights.shape[1])
+    shape = (batch, kv_heads, cols)
+    st = _fn("msa_cache_evict")(
+        block_table.data_ptr(), bt_stride, seq_lens.data_ptr(), _is(weights, torch.float32, shape, "weights"), cols,
+        batch, kv_heads, MSA_PAGE_TOKENS * cols if max_model_len is None else max_model_len, budget, n_sink, n_window,
+        out_table.data_ptr(), o_stride, out_seq_lens.data_ptr(),
+        _is(out_weights, torch.float32, shape, "out_weights"), _is(out_freed, torch.int32, (batch, cols), "out_freed"),
+        _is(out_n_freed, torch.int32, (batch,), "out_n_freed"), *_ws(workspace), _stream_ptr(stream))
+    _check(st, "msa_cache_evict")
+
+
+def msa_verify_draft(logits, draft_probs, draft_tokens, uniforms, race, out_tokens, out_accepted, workspace, *,
+                     temperature=None, n_draft=None, out_logprobs=None, stream=None) -> None:
+    """Accepts drafted tokens against softmax(logits / temperature) and draws the next one, from given random numbers.
+
+    ``logits`` fp32 or bf16 [batch, drafts + 1, vocab] (rows of any stride), ``draft_probs`` fp32 [batch, drafts,
+    vocab], ``race`` fp32 [batch, vocab] of Exp(1) draws.  See include/msa_attention.h.
+    """
+    assert logits.dim() == 3 and logits.dtype in (torch.float32, torch.bfloat16) and logits.stride(2) == 1, \
+        "logits: fp32 or bf16 [batch, drafts + 1, vocab], rows contiguous"
+    batch, rows, vocab = (int(x) for x in logits.shape)
+    n = rows - 1
+    stride = logits.stride()
+    st = _fn("msa_verify_draft")(
+        logits.data_ptr(), 1 if logits.dtype == torch.bfloat16 else 0, stride[0] if batch > 1 else rows * vocab,
+        stride[1] if rows > 1 else vocab, _is(draft_probs, torch.float32, (batch, n, vocab), "draft_probs"),
+        _is(draft_tokens, torch.int32, (batch, n), "draft_tokens"),
+        _is(uniforms, torch.float32, (batch, n), "uniforms"), _is(race, torch.float32, (batch, vocab), "race"),
+        None if temperature is None else _is(temperature, torch.float32, (batch,), "temperature"),
+        None if n_draft is None else _is(n_draft, torch.int32, (batch,), "n_draft"), batch, n, vocab,
+        _is(out_tokens, torch.int32, (batch, rows), "out_tokens"),
+        _is(out_accepted, torch.int32, (batch,), "out_accepted"), _f32_out(out_logprobs, (batch, rows), "out_logprobs"),
+        *_ws(workspace), _stream_ptr(stream))
+    _check(st, "msa_verify_draft")

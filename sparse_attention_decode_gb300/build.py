@@ -14,7 +14,7 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB_DIR = os.path.join(HERE, "_lib")
 LIBRARY = os.path.join(LIB_DIR, "libmsa_indexer.so")
-UNITS = ("msa_indexer.cu", "prefill.cu", "attention.cu")  # translation units, compiled in parallel
+UNITS = ("msa_indexer.cu", "prefill.cu", "attention.cu", "evict.cu", "verify.cu")  # translation units, compiled in parallel
 
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
