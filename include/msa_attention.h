@@ -95,6 +95,27 @@ msa_status msa_attention_sparse_fp8(const void *q, int64_t q_stride, const void 
                                     float *out_mass, void *workspace, size_t workspace_bytes, void *stream);
 
 /*
+ * Decode attention of a batch whose requests share a prefix: position i of
+ * request b sees the prefix's tokens and the first seq_lens[b] - (q_len - 1 - i)
+ * tokens of its own (none where that is negative).  Same formula, same out and
+ * out_lse as msa_attention_sparse, over all of these tokens.
+ *
+ *   prefix_table   int32 [ceil(max_prefix_len / 128)]: the prefix's pages.
+ *   prefix_len     device int32 [1], in [0, max_prefix_len] (outside: 0).
+ *   block_table, seq_lens   each request's own pages and own tokens.
+ *   workspace      at least msa_attention_prefix_workspace_bytes(batch * q_len,
+ *                  kv_heads * group, kv_heads, max_prefix_len) bytes.
+ */
+size_t msa_attention_prefix_workspace_bytes(int max_rows, int heads, int kv_heads, int max_prefix_len);
+
+msa_status msa_attention_prefix(const void *q, int64_t q_stride, const void *k, const int64_t *k_strides,
+                                const void *v, const int64_t *v_strides, int64_t num_pages,
+                                const int32_t *prefix_table, const int32_t *prefix_len, int max_prefix_len,
+                                const int32_t *block_table, int64_t bt_stride, const int32_t *seq_lens,
+                                int batch, int q_len, int kv_heads, int group, int max_model_len, float scale,
+                                void *out, float *out_lse, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
  * Eviction from the cache by accumulated attention weight, in pages: the block
  * table is shared by the index-K cache and K/V, so a page leaves both at once.
  *

@@ -56,6 +56,8 @@ from ._attention import (  # noqa: E402,F401
     MSA_MAX_CACHE_BLOCKS,
     MSA_MAX_DRAFT,
     MSA_MAX_GROUP,
+    msa_attention_prefix,
+    msa_attention_prefix_workspace_bytes,
     msa_attention_sparse,
     msa_attention_sparse_fp8,
     msa_cache_accumulate,

@@ -20,6 +20,8 @@ MSA_MAX_CACHE_BLOCKS = 32768
 MSA_MAX_DRAFT = 63
 
 ATTENTION_EXPORTED = (
+    "msa_attention_prefix",
+    "msa_attention_prefix_workspace_bytes",
     "msa_attention_sparse",
     "msa_attention_sparse_fp8",
     "msa_cache_accumulate",
@@ -43,6 +45,9 @@ def _fn(name):
 
 
 _ARGTYPES = {
+    "msa_attention_prefix_workspace_bytes": ([_int, _int, _int, _int], _size),
+    "msa_attention_prefix": ([_P, _i64, _P, _Strides, _P, _Strides, _i64, _P, _P, _int, _P, _i64, _P, _int, _int, _int,
+                              _int, _int, _f32, _P, _P, _P, _size, _P], _int),
     "msa_attention_sparse": ([_P, _i64, _P, _Strides, _P, _Strides, _i64, _P, _i64, _P, _int, _int, _int, _int, _int,
                               _P, _int, _int, _f32, _P, _P, _P, _P, _size, _P], _int),
     "msa_attention_sparse_fp8": ([_P, _i64, _P, _Strides, _P, _P, _Strides, _P, _i64, _P, _i64, _P, _int, _int, _int,
@@ -207,3 +212,36 @@ def msa_verify_draft(logits, draft_probs, draft_tokens, uniforms, race, out_toke
         _is(out_accepted, torch.int32, (batch,), "out_accepted"), _f32_out(out_logprobs, (batch, rows), "out_logprobs"),
         *_ws(workspace), _stream_ptr(stream))
     _check(st, "msa_verify_draft")
+
+
+def msa_attention_prefix_workspace_bytes(max_rows: int, heads: int, kv_heads: int, max_prefix_len: int) -> int:
+    return int(_fn("msa_attention_prefix_workspace_bytes")(max_rows, heads, kv_heads, max_prefix_len))
+
+
+def msa_attention_prefix(q, k, v, prefix_table, prefix_len, block_table, seq_lens, out, workspace, *, scale: float,
+                         q_len: int = 1, max_prefix_len: Optional[int] = None, max_model_len: Optional[int] = None,
+                         out_lse=None, stream=None) -> None:
+    """Attention of q [batch * q_len, heads, 128] over a shared prefix and each request's own tokens (bf16 cache).
+
+    ``prefix_table`` int32 [pages], ``prefix_len`` an int32 tensor of one element on the GPU.  See
+    include/msa_attention.h.
+    """
+    ks, vs = _cache(k, False, "k"), _cache(v, False, "v")
+    assert k.shape == v.shape, "k and v: one shape"
+    pages, kv_heads = int(k.shape[0]), int(k.shape[2])
+    batch, cols, bt_stride = _requests(block_table, seq_lens)
+    rows = batch * q_len
+    heads, q_stride = _queries(q, out, rows)
+    assert heads % kv_heads == 0, "q heads: a multiple of kv_heads"
+    assert prefix_table.dtype == torch.int32 and prefix_table.dim() == 1 and prefix_table.is_contiguous(), \
+        "prefix_table: int32 [pages]"
+    assert prefix_len.dtype == torch.int32 and prefix_len.numel() == 1, "prefix_len: int32 [1]"
+    bound = MSA_PAGE_TOKENS * int(prefix_table.shape[0])
+    assert max_prefix_len is None or max_prefix_len <= bound, "max_prefix_len: within prefix_table"
+    st = _fn("msa_attention_prefix")(
+        q.data_ptr(), q_stride, k.data_ptr(), ks, v.data_ptr(), vs, pages, prefix_table.data_ptr(),
+        prefix_len.data_ptr(), bound if max_prefix_len is None else max_prefix_len, block_table.data_ptr(), bt_stride,
+        seq_lens.data_ptr(), batch, q_len, kv_heads, heads // kv_heads,
+        MSA_PAGE_TOKENS * cols if max_model_len is None else max_model_len, scale, out.data_ptr(),
+        _f32_out(out_lse, (rows, heads), "out_lse"), *_ws(workspace), _stream_ptr(stream))
+    _check(st, "msa_attention_prefix")

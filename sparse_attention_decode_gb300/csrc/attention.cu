@@ -144,9 +144,91 @@ static msa_status sparse_entry(const void *q, int64_t q_stride, const void *k, c
                          : launch_block_attn<AttnBf16, 4, false>(p, units, split, st);
 }
 
+static msa_status prefix_entry(const void *q, int64_t q_stride, const void *k, const int64_t *k_strides, const void *v,
+                               const int64_t *v_strides, int64_t num_pages, const int32_t *prefix_table,
+                               const int32_t *prefix_len, int max_prefix_len, const int32_t *block_table,
+                               int64_t bt_stride, const int32_t *seq_lens, int batch, int q_len, int kv_heads,
+                               int group, int max_model_len, float scale, void *out, float *out_lse, void *workspace,
+                               size_t workspace_bytes, void *stream)
+{
+    if (batch < 0 || q_len < 1 || kv_heads < 1 || group < 1 || num_pages < 1 || bt_stride < 1 || max_model_len < 1 ||
+        max_prefix_len < 0 || !(scale > 0.0f) || !(scale < INFINITY))
+        return MSA_ERR_INVALID_ARG;
+    if (batch > MSA_MAX_BATCH || num_pages > (int64_t{1} << 24) || group > MSA_MAX_GROUP || kv_heads > 1024 ||
+        q_len > 64 || static_cast<int64_t>(batch) * q_len * kv_heads * group > (int64_t{1} << 27))
+        return MSA_ERR_UNSUPPORTED;
+    if (!q || !block_table || !seq_lens || !prefix_table || !prefix_len || !out || !workspace ||
+        !cache_ok(k, k_strides, num_pages, kv_heads, false) || !cache_ok(v, v_strides, num_pages, kv_heads, false) ||
+        unaligned(q, 16) || q_stride % 8 || q_stride < static_cast<int64_t>(kv_heads) * group * kDim ||
+        unaligned(out, 16) || unaligned(workspace, 256))
+        return MSA_ERR_INVALID_ARG;
+    if (workspace_bytes < msa_attention_prefix_workspace_bytes(batch * q_len, kv_heads * group, kv_heads, max_prefix_len))
+        return MSA_ERR_WORKSPACE_TOO_SMALL;
+    if (batch == 0)
+        return MSA_OK;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess)
+        return MSA_ERR_CUDA;
+    const int sms = device_sms(dev);
+    if (sms <= 0)
+        return MSA_ERR_CUDA;
+    BlockAttnParams p;
+    std::memset(&p, 0, sizeof p);
+    if (!make_cache_map(&p.kmap, k, k_strides, num_pages, kv_heads, false) ||
+        !make_cache_map(&p.vmap, v, v_strides, num_pages, kv_heads, false))
+        return MSA_ERR_CUDA;
+    p.q = static_cast<const uint16_t *>(q);
+    p.block_table = block_table;
+    p.seq_lens = seq_lens;
+    p.out = static_cast<uint16_t *>(out);
+    p.lse = out_lse;
+    p.fault = &static_cast<WorkspaceHeader *>(workspace)->fault;
+    p.q_stride = q_stride;
+    p.bt_stride = bt_stride;
+    p.num_pages = num_pages;
+    p.batch = batch;
+    p.q_len = q_len;
+    p.kv_heads = kv_heads;
+    p.sel_heads = 1;
+    p.group = group;
+    p.seq_limit = static_cast<int>(std::min<int64_t>(max_model_len, kPage * bt_stride));
+    p.unit_rows = q_len * group;
+    p.row_tiles = (p.unit_rows + kAttnMaxRows - 1) / kAttnMaxRows;
+    p.prefix_table = prefix_table;
+    p.prefix_len = prefix_len;
+    p.prefix_limit = max_prefix_len;
+    p.scale_log2 = scale * kLog2e;
+    const int64_t units = static_cast<int64_t>(batch) * kv_heads * p.row_tiles;
+    const int split = block_attn_split(units, 8, sms);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    return p.unit_rows <= 16   ? launch_block_attn<AttnBf16, 1, true>(p, units, split, st)
+           : p.unit_rows <= 32 ? launch_block_attn<AttnBf16, 2, true>(p, units, split, st)
+                               : launch_block_attn<AttnBf16, 4, true>(p, units, split, st);
+}
+
 }  // namespace msa
 
 using namespace msa;
+
+extern "C" size_t msa_attention_prefix_workspace_bytes(int max_rows, int heads, int kv_heads, int max_prefix_len)
+{
+    if (max_rows < 0 || kv_heads < 1 || heads < kv_heads || heads % kv_heads || max_prefix_len < 0)
+        return 0;
+    return kHeaderBytes;
+}
+
+extern "C" msa_status msa_attention_prefix(const void *q, int64_t q_stride, const void *k, const int64_t *k_strides,
+                                           const void *v, const int64_t *v_strides, int64_t num_pages,
+                                           const int32_t *prefix_table, const int32_t *prefix_len, int max_prefix_len,
+                                           const int32_t *block_table, int64_t bt_stride, const int32_t *seq_lens,
+                                           int batch, int q_len, int kv_heads, int group, int max_model_len,
+                                           float scale, void *out, float *out_lse, void *workspace,
+                                           size_t workspace_bytes, void *stream)
+{
+    return prefix_entry(q, q_stride, k, k_strides, v, v_strides, num_pages, prefix_table, prefix_len, max_prefix_len,
+                        block_table, bt_stride, seq_lens, batch, q_len, kv_heads, group, max_model_len, scale, out,
+                        out_lse, workspace, workspace_bytes, stream);
+}
 
 extern "C" msa_status msa_attention_sparse(const void *q, int64_t q_stride, const void *k, const int64_t *k_strides,
                                            const void *v, const int64_t *v_strides, int64_t num_pages,

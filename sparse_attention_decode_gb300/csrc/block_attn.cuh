@@ -71,6 +71,9 @@ struct BlockAttnParams {
     int batch, q_len, kv_heads, sel_heads, group, k, seq_limit;
     int unit_rows;  // query rows of a unit: group, or q_len * group
     int row_tiles;  // tiles of kAttnMaxRows rows a unit's rows are cut into
+    const int32_t *prefix_table;  // own pages only: pages that every request reads before its own
+    const int32_t *prefix_len;    // their tokens (one int32)
+    int prefix_limit;             // the bound on them
     float scale_log2;
 };
 
@@ -78,6 +81,7 @@ template <class F>
 struct BlockAttnSmem {
     uint64_t full[F::kStages], empty[F::kStages];
     int meta[F::kStages];         // first token of the tile's page, or -1: a page that is skipped
+    int meta_all[F::kStages];     // a prefix page's tokens, which every row sees; -1: a page of the request
     int list_page[MSA_MAX_TOPK];  // with ids: this CTA's valid selected blocks in slot order
     int list_base[MSA_MAX_TOPK];
     int list_slot[MSA_MAX_TOPK];
@@ -197,7 +201,17 @@ __global__ void __launch_bounds__(kAttnThreads, 2) block_attn_kernel(const __gri
     if (tid == 0 && bad_len)
         atomicOr(p.fault, MSA_FAULT_SEQ_LEN);
     const int len = bad_len ? 0 : L;  // every position's tokens are below it
-    // tokens position i sees
+    int prefix = 0;
+    if (OWN && p.prefix_table) {
+        prefix = *p.prefix_len;
+        if (prefix < 0 || prefix > p.prefix_limit) {
+            if (tid == 0)
+                atomicOr(p.fault, MSA_FAULT_SEQ_LEN);
+            prefix = 0;
+        }
+    }
+    const int prefix_pages = (prefix + kPage - 1) / kPage;
+    // tokens position i sees, of its own
     auto visible = [&](int i) { return max(0, len - (p.q_len - 1 - i)); };
 
     if (tid == 0) {
@@ -210,7 +224,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2) block_attn_kernel(const __gri
     }
     if (warp == kAttnWarps) {
         if (OWN) {
-            const int nb = (len + kPage - 1) / kPage;
+            const int nb = prefix_pages + (len + kPage - 1) / kPage;
             if (lane == 0)
                 ctl->count = nb > crank ? (nb - crank + S - 1) / S : 0;
         } else {
@@ -256,20 +270,24 @@ __global__ void __launch_bounds__(kAttnThreads, 2) block_attn_kernel(const __gri
         bool alive = true;
         uint32_t it = 0;
         for (int i = 0; i < count && alive; ++i) {
-            int page, base;
+            int page, base, all = -1;
             if (OWN) {
                 if ((i & 31) == 0) {
                     const int j = crank + (i + lane) * S;
                     pages = -1;
                     if (i + lane < count)
-                        pages = p.block_table[static_cast<int64_t>(b) * p.bt_stride + j];
+                        pages = j < prefix_pages
+                                    ? p.prefix_table[j]
+                                    : p.block_table[static_cast<int64_t>(b) * p.bt_stride + j - prefix_pages];
                     if (i + lane < count && (pages < 0 || pages >= p.num_pages)) {
                         pages = -1;
                         atomicOr(p.fault, MSA_FAULT_PAGE_ID);
                     }
                 }
                 page = __shfl_sync(0xffffffffu, pages, i & 31);
-                base = page < 0 ? -1 : (crank + i * S) * kPage;
+                const int j = crank + i * S;
+                all = j < prefix_pages ? prefix - j * kPage : -1;
+                base = page < 0 ? -1 : all >= 0 ? 0 : (j - prefix_pages) * kPage;
             } else {
                 page = ctl->list_page[i];
                 base = ctl->list_base[i];
@@ -283,6 +301,8 @@ __global__ void __launch_bounds__(kAttnThreads, 2) block_attn_kernel(const __gri
                     break;
                 if (lane == 0) {
                     ctl->meta[s] = base;
+                    if (OWN)
+                        ctl->meta_all[s] = all;
                     if (base < 0) {
                         mbar_arrive(bar);
                     } else {
@@ -370,6 +390,9 @@ __global__ void __launch_bounds__(kAttnThreads, 2) block_attn_kernel(const __gri
             if (!alive)
                 break;
             const int base = ctl->meta[s_k];
+            const int all = OWN ? ctl->meta_all[s_k] : -1;
+            const int end0 = all >= 0 ? all : lim0 - base, end1 = all >= 0 ? all : lim1 - base;
+            const int vend = all >= 0 ? all : len - base;
             float ps0 = 0.0f, ps1 = 0.0f;  // this page's weight, at the running maximum
             const uint32_t kt = smem_addr(smem) + s_k * kStageBytes, vt = smem_addr(smem) + s_v * kStageBytes;
             bool v_waited = false;
@@ -421,7 +444,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2) block_attn_kernel(const __gri
                         s[f][3] *= sc.y * undo1;
                     }
                 }
-                const int left0 = lim0 - base - tok, left1 = lim1 - base - tok;  // visible tokens of the chunk
+                const int left0 = end0 - tok, left1 = end1 - tok;  // visible tokens of the chunk
                 if (min(left0, left1) < 32) {
 #pragma unroll
                     for (int f = 0; f < 4; ++f) {
@@ -472,7 +495,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2) block_attn_kernel(const __gri
                     if (!alive)
                         break;
                 }
-                const int vleft = len - base - tok;  // tokens of the chunk that are data
+                const int vleft = vend - tok;  // tokens of the chunk that are data
                 uint32_t pa[2][4];
                 if (!F::kFp8) {
 #pragma unroll
