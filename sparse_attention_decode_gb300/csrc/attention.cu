@@ -1,6 +1,7 @@
 // Attention over the blocks the indexer selected: argument checks and launch of
 // block_attn_kernel (block_attn.cuh).
 #include "block_attn.cuh"
+#include "prefix_attn.cuh"
 
 namespace msa {
 
@@ -60,7 +61,7 @@ msa_status launch_block_attn(const BlockAttnParams &p, int64_t units, int split,
         return MSA_ERR_CUDA;
     cudaLaunchConfig_t cfg;
     std::memset(&cfg, 0, sizeof cfg);
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     cfg.gridDim = dim3(static_cast<unsigned>(units * split));
     cfg.blockDim = dim3(kAttnThreads);
     cfg.dynamicSmemBytes = smem;
@@ -69,8 +70,11 @@ msa_status launch_block_attn(const BlockAttnParams &p, int64_t units, int split,
     attr[0].val.clusterDim.x = split;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
+    // behind prefix_attn_kernel: CTAs start as its CTAs end, and wait for all of it before they read its parts
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = p.parts.o ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kernel, p) == cudaSuccess ? MSA_OK : MSA_ERR_CUDA;
 }
 
@@ -144,6 +148,34 @@ static msa_status sparse_entry(const void *q, int64_t q_stride, const void *k, c
                          : launch_block_attn<AttnBf16, 4, false>(p, units, split, st);
 }
 
+// The units of a batch's rows; a tile of 128 rows where they do not fill more.
+static PrefixParts prefix_parts(int64_t rows, int group, int kv_heads, int max_prefix_len)
+{
+    PrefixParts a;
+    std::memset(&a, 0, sizeof a);
+    a.rows = static_cast<int>(rows);
+    a.group = group;
+    a.tile_rows = rows <= 128 ? 128 : 256;
+    a.head_tiles = static_cast<int>((rows + a.tile_rows - 1) / a.tile_rows);
+    a.units = a.head_tiles * kv_heads;
+    a.limit = max_prefix_len;
+    return a;
+}
+
+static size_t prefix_lse_offset(const PrefixParts &a)
+{
+    return kHeaderBytes + (static_cast<size_t>(kPrefixMaxGrid) + a.units) * a.tile_rows * kDim * sizeof(float);
+}
+
+static msa_status launch_prefix(const PrefixAttnParams &p, cudaStream_t st)
+{
+    if (cudaFuncSetAttribute(prefix_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(kPrefixSmemBytes)) != cudaSuccess)
+        return MSA_ERR_CUDA;
+    prefix_attn_kernel<<<p.parts.grid, kPrefixThreads, kPrefixSmemBytes, st>>>(p);
+    return cudaGetLastError() == cudaSuccess ? MSA_OK : MSA_ERR_CUDA;
+}
+
 static msa_status prefix_entry(const void *q, int64_t q_stride, const void *k, const int64_t *k_strides, const void *v,
                                const int64_t *v_strides, int64_t num_pages, const int32_t *prefix_table,
                                const int32_t *prefix_len, int max_prefix_len, const int32_t *block_table,
@@ -194,13 +226,32 @@ static msa_status prefix_entry(const void *q, int64_t q_stride, const void *k, c
     p.seq_limit = static_cast<int>(std::min<int64_t>(max_model_len, kPage * bt_stride));
     p.unit_rows = q_len * group;
     p.row_tiles = (p.unit_rows + kAttnMaxRows - 1) / kAttnMaxRows;
-    p.prefix_table = prefix_table;
     p.prefix_len = prefix_len;
-    p.prefix_limit = max_prefix_len;
     p.scale_log2 = scale * kLog2e;
+    p.parts = prefix_parts(static_cast<int64_t>(batch) * p.unit_rows, group, kv_heads, max_prefix_len);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
     const int64_t units = static_cast<int64_t>(batch) * kv_heads * p.row_tiles;
     const int split = block_attn_split(units, 8, sms);
-    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    {
+        p.parts.grid = std::min(sms, kPrefixMaxGrid);
+        p.parts.o = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + kHeaderBytes);
+        p.parts.lse = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + prefix_lse_offset(p.parts));
+        PrefixAttnParams a;
+        std::memset(&a, 0, sizeof a);
+        a.kmap = p.kmap;
+        a.vmap = p.vmap;
+        a.q = p.q;
+        a.prefix_table = prefix_table;
+        a.prefix_len = prefix_len;
+        a.parts = p.parts;
+        a.fault = p.fault;
+        a.q_stride = q_stride;
+        a.num_pages = num_pages;
+        a.scale_log2 = p.scale_log2;
+        const msa_status s = launch_prefix(a, st);
+        if (s != MSA_OK)
+            return s;
+    }
     return p.unit_rows <= 16   ? launch_block_attn<AttnBf16, 1, true>(p, units, split, st)
            : p.unit_rows <= 32 ? launch_block_attn<AttnBf16, 2, true>(p, units, split, st)
                                : launch_block_attn<AttnBf16, 4, true>(p, units, split, st);
@@ -214,7 +265,9 @@ extern "C" size_t msa_attention_prefix_workspace_bytes(int max_rows, int heads, 
 {
     if (max_rows < 0 || kv_heads < 1 || heads < kv_heads || heads % kv_heads || max_prefix_len < 0)
         return 0;
-    return kHeaderBytes;
+    const PrefixParts a = prefix_parts(static_cast<int64_t>(max_rows) * (heads / kv_heads), heads / kv_heads, kv_heads,
+                                       max_prefix_len);
+    return prefix_lse_offset(a) + (static_cast<size_t>(kPrefixMaxGrid) + a.units) * a.tile_rows * sizeof(float);
 }
 
 extern "C" msa_status msa_attention_prefix(const void *q, int64_t q_stride, const void *k, const int64_t *k_strides,

@@ -54,6 +54,43 @@ constexpr int kAttnThreads = 32 * (kAttnWarps + 1);
 constexpr int kAttnMaxRows = 64;  // rows of one unit: 1, 2 or 4 tiles of 16
 constexpr int kAttnOStride = kDim + 4;  // fp32 row stride of a partial O in shared memory (bank spread)
 
+// Parts of the attention over a shared prefix, made by prefix_attn_kernel.  A
+// unit is (KV head, tile of tile_rows rows); unit u = head * head_tiles + tile.
+// The units' pages stand one after the other, u * pages + j, and CTA g of the
+// `ctas` that take part covers [start(g), start(g + 1)); the part of CTA g in
+// unit u is in slot g + u (unique: both grow along the sequence).
+struct PrefixParts {
+    float *o;    // [slot][tile_rows][128], divided by the part's sum
+    float *lse;  // [slot][tile_rows], log2 units; -inf: nothing, +inf: not whole
+    int rows;    // rows of a KV head: batch * q_len * group
+    int group, tile_rows, head_tiles, units;
+    int limit;   // bound on the prefix's tokens
+    int grid;    // CTAs the kernel is launched with
+};
+
+constexpr int kPrefixMinPages = 2;  // pages a CTA's range should have at least
+
+struct PrefixSplit {
+    int pages, ctas;
+    int64_t total;
+    __device__ PrefixSplit(const PrefixParts &p, int tokens, int grid)
+    {
+        pages = (tokens + kPage - 1) / kPage;
+        total = static_cast<int64_t>(pages) * p.units;
+        ctas = static_cast<int>(min(static_cast<int64_t>(grid), (total + kPrefixMinPages - 1) / kPrefixMinPages));
+    }
+    __device__ int64_t start(int g) const { return g * total / ctas; }
+    // the CTA whose range holds page x of the sequence
+    __device__ int owner(int64_t x) const { return static_cast<int>(((x + 1) * ctas - 1) / total); }
+};
+
+// The prefix's tokens; 0 where the length is out of range.
+__device__ __forceinline__ int prefix_tokens(const PrefixParts &p, const int32_t *len)
+{
+    const int n = *len;
+    return n < 0 || n > p.limit ? 0 : n;
+}
+
 struct BlockAttnParams {
     CUtensorMap kmap, vmap;  // [page][head][token][dim], box 1 x 1 x 128 x (64 bf16 | 128 E4M3)
     const uint16_t *q;
@@ -73,7 +110,7 @@ struct BlockAttnParams {
     int row_tiles;  // tiles of kAttnMaxRows rows a unit's rows are cut into
     const int32_t *prefix_table;  // own pages only: pages that every request reads before its own
     const int32_t *prefix_len;    // their tokens (one int32)
-    int prefix_limit;             // the bound on them
+    PrefixParts parts;            // own pages only: or the parts that prefix_attn_kernel made (o != NULL)
     float scale_log2;
 };
 
@@ -203,12 +240,9 @@ __global__ void __launch_bounds__(kAttnThreads, 2) block_attn_kernel(const __gri
     const int len = bad_len ? 0 : L;  // every position's tokens are below it
     int prefix = 0;
     if (OWN && p.prefix_table) {
-        prefix = *p.prefix_len;
-        if (prefix < 0 || prefix > p.prefix_limit) {
-            if (tid == 0)
-                atomicOr(p.fault, MSA_FAULT_SEQ_LEN);
-            prefix = 0;
-        }
+        prefix = prefix_tokens(p.parts, p.prefix_len);
+        if (prefix == 0 && *p.prefix_len != 0 && tid == 0)
+            atomicOr(p.fault, MSA_FAULT_SEQ_LEN);
     }
     const int prefix_pages = (prefix + kPage - 1) / kPage;
     // tokens position i sees, of its own
@@ -655,14 +689,51 @@ __global__ void __launch_bounds__(kAttnThreads, 2) block_attn_kernel(const __gri
             }
         }
         consumer_barrier();
+        // the prefix's parts of this request's rows: the cluster's CTAs take them in turn
+        const bool parts = OWN && p.parts.o;
+        int part0 = 0, part1 = 0;
+        int64_t part_row0 = 0, unit0 = 0;
+        PrefixSplit ps(p.parts, 0, 1);
+        if (parts) {
+            griddep_wait();  // prefix_attn_kernel has ended
+            ps = PrefixSplit(p.parts, prefix_tokens(p.parts, p.prefix_len), p.parts.grid);
+            part_row0 = static_cast<int64_t>(owner) * p.q_len * p.group + row0;
+        }
         float *co = wo + kAttnWarps * 16 * kAttnOStride;  // [rows][kAttnOStride]: the CTA's part
         for (int n = tid >> 5; n < rows; n += kAttnWarps) {
             const int col = lane * 4, w0 = n / 16, r = n % 16;
             float M = -INFINITY, sum = 0.0f;
+            if (parts && ps.total > 0) {
+                const int tile = static_cast<int>((part_row0 + n) / p.parts.tile_rows);
+                unit0 = static_cast<int64_t>(h) * p.parts.head_tiles + tile;
+                part0 = ps.owner(unit0 * ps.pages);
+                part1 = ps.owner((unit0 + 1) * ps.pages - 1) + 1;
+                part0 += (crank - part0 % S + S) % S;
+            }
+            const int tr = static_cast<int>((part_row0 + n) % p.parts.tile_rows);
+            for (int g = part0; g < part1; g += S) {
+                const float e = p.parts.lse[(g + unit0) * p.parts.tile_rows + tr];
+                M = fmaxf(M, e);
+                if (e == INFINITY)
+                    ctl->abort_flag = 1;
+            }
 #pragma unroll
             for (int k = 0; k < KS; ++k)
                 M = fmaxf(M, ctl->wm[w0 + k * MT][r]);
             float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            for (int g = part0; g < part1; g += S) {
+                const int64_t at = (g + unit0) * p.parts.tile_rows + tr;
+                const float e = p.parts.lse[at];
+                if (e == -INFINITY)
+                    continue;
+                const float f = rescale(e, M);
+                const float4 v = *reinterpret_cast<const float4 *>(p.parts.o + at * kDim + col);
+                sum += f;
+                acc.x += f * v.x;
+                acc.y += f * v.y;
+                acc.z += f * v.z;
+                acc.w += f * v.w;
+            }
 #pragma unroll
             for (int k = 0; k < KS; ++k) {
                 const int w = w0 + k * MT;
