@@ -1,15 +1,20 @@
 // Verification of drafted tokens against the target's probabilities.
 //
-// With m the row's largest logit, c = log2 e / T and Z = sum 2^(c (l - m)):
-// p(v) = 2^(c (l_v - m)) / Z and ln p(v) = (l_v - m) / T - ln Z.  The draw is an
+// With c = log2 e / T, x = c max l as rounded and Z = sum 2^(c l - x):
+// p(v) = 2^(c l_v - x) / Z and ln p(v) = (c l_v - x - log2 Z) ln 2; x cancels, so
+// its rounding does no harm as long as every use takes the same one.  The draw is an
 // exponential race: the argmax of r(v) / e(v) over independent e ~ Exp(1) is v
 // with probability r(v) / sum r, so it needs no normalised cumulative sum, and
 // its argmax is the same however the vocabulary is split.
 //
-// What bounds it: every logit is used once for m and Z and those of one row
-// once more for the draw, so the stream of logits does.  One cluster a request:
-// its CTAs take slices of the vocabulary, exchange (m, Z) and the best key
-// through distributed shared memory, and decide alike; one launch.
+// What bounds it: the stream of logits (every one is read once for m and Z, those
+// of one row again, from L2, for the draw).  One cluster a request: its CTAs take
+// slices of the vocabulary in 16-byte loads, several in flight a thread, exchange
+// (m, Z) and the best key through distributed shared memory and decide alike; one
+// launch.  A row past the first refusal has no part in the result.  Where there
+// are requests enough to fill the GPU, rows are therefore taken one at a time, each
+// decided before the next is read; a few requests take all rows at once, since a
+// decision (two cluster barriers) would cost more than the rows it could save.
 #include "host_util.cuh"
 #include "keys.cuh"
 #include "layout.cuh"
@@ -34,24 +39,28 @@ struct VerifyParams {
     uint32_t *fault;
     int64_t stride_b, stride_i;
     int max_draft, vocab;
+    int rows_a_round;  // rows summed between two decisions
 };
 
-constexpr int kVerifyThreads = 512;
+constexpr int kVerifyThreads = 256;
 constexpr int kVerifyWarps = kVerifyThreads / 32;
 constexpr int kVerifyRows = MSA_MAX_DRAFT + 1;
 constexpr float kVLog2e = 1.4426950408889634f;
+constexpr float kVLn2 = 0.69314718055994531f;
 
 struct VerifySmem {
     float wm[kVerifyRows][kVerifyWarps], ws[kVerifyRows][kVerifyWarps];
-    uint64_t wk[kVerifyRows][kVerifyWarps];
+    int wi[kVerifyRows][kVerifyWarps];
     float m[kVerifyRows], s[kVerifyRows];  // the CTA's slice of each row, read by the cluster
-    uint64_t key[kVerifyRows];             // greedy: its largest logit and where
+    int i[kVerifyRows];                    // greedy: where its largest logit lies
     float gm[kVerifyRows], gs[kVerifyRows];
-    uint64_t gkey[kVerifyRows];
+    int gi[kVerifyRows];
+    int x[kVerifyRows];  // the drafts: token, its logit and draft probability, the uniform number
+    float lx[kVerifyRows], qx[kVerifyRows], u[kVerifyRows];
     int ok[kVerifyRows];
     float lp[kVerifyRows];
     uint64_t best[2];  // the CTA's draw: from the residual, from p
-    uint64_t wbest[2][kVerifyWarps];
+    uint64_t wbest[kVerifyWarps];
 };
 
 __device__ __forceinline__ uint64_t dsmem_ld_u64(uint32_t addr)
@@ -66,6 +75,12 @@ __device__ __forceinline__ float dsmem_ld_float(uint32_t addr)
     asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
     return v;
 }
+__device__ __forceinline__ int dsmem_ld_int(uint32_t addr)
+{
+    int v;
+    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+}
 __device__ __forceinline__ uint32_t verify_cluster_size()
 {
     uint32_t r;
@@ -73,13 +88,171 @@ __device__ __forceinline__ uint32_t verify_cluster_size()
     return r;
 }
 
-__device__ __forceinline__ float logit(const float *p, int v) { return p[v]; }
-__device__ __forceinline__ float logit(const uint16_t *p, int v) { return __uint_as_float(static_cast<uint32_t>(p[v]) << 16); }
+// Logits in 16-byte vectors; NaN counts as -inf.
+template <class T>
+struct Logits;
+template <>
+struct Logits<float> {
+    static constexpr int kVec = 4;
+    static __device__ __forceinline__ float one(const float *p) { return fmaxf(*p, -INFINITY); }
+    static __device__ __forceinline__ void unpack(const uint4 &v, float (&x)[4])
+    {
+        x[0] = fmaxf(__uint_as_float(v.x), -INFINITY);
+        x[1] = fmaxf(__uint_as_float(v.y), -INFINITY);
+        x[2] = fmaxf(__uint_as_float(v.z), -INFINITY);
+        x[3] = fmaxf(__uint_as_float(v.w), -INFINITY);
+    }
+};
+template <>
+struct Logits<uint16_t> {
+    static constexpr int kVec = 8;
+    static __device__ __forceinline__ float one(const uint16_t *p)
+    {
+        return fmaxf(__uint_as_float(static_cast<uint32_t>(*p) << 16), -INFINITY);
+    }
+    static __device__ __forceinline__ void unpack(const uint4 &v, float (&x)[8])
+    {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            x[2 * i] = fmaxf(__uint_as_float(w[i] << 16), -INFINITY);
+            x[2 * i + 1] = fmaxf(__uint_as_float(w[i] & 0xffff0000u), -INFINITY);
+        }
+    }
+};
 
-// (larger value, lower index) as one key; 0: none.
-__device__ __forceinline__ uint64_t value_key(float x, int v)
+// A part of a row in log2 units: x = c max l and s = sum 2^(c l - x).  Greedy: the
+// largest logit itself (c = 1) and where it first occurs.
+struct RowPart {
+    float x, s;
+    int i;
+    __device__ __forceinline__ void join(const RowPart &o)
+    {
+        const float n = fmaxf(x, o.x);
+        if (n == -INFINITY)
+            return;
+        i = x > o.x ? i : o.x > x ? o.i : min(i, o.i);
+        s = s * exp2_approx(x - n) + o.s * exp2_approx(o.x - n);
+        x = n;
+    }
+};
+
+// The join of all lanes' parts, in lane order pairwise: the same for the same parts.
+__device__ __forceinline__ void warp_join(RowPart &r)
 {
-    return (static_cast<uint64_t>(float_order_bits(x == 0.0f ? 0.0f : x)) << 32) | (0xffffffffu - static_cast<uint32_t>(v));
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const RowPart other{__shfl_xor_sync(0xffffffffu, r.x, o), __shfl_xor_sync(0xffffffffu, r.s, o),
+                            __shfl_xor_sync(0xffffffffu, r.i, o)};
+        r.join(other);
+    }
+}
+
+// Vector v of a row (elements [v * N, v * N + N)) wherever the row starts, so that a
+// row's sums are grouped by index alone, not by address: one 16-byte load where
+// every row is aligned to it, else word by word (five words that hold the eight
+// 2-byte elements, shifted into place when they are used; the outer two each hold a
+// byte of the vector).
+template <class T, bool ALIGNED>
+struct RawVec {
+    uint32_t w[ALIGNED || sizeof(T) == 4 ? 4 : 5];
+    __device__ __forceinline__ void load(const T *row, int v)
+    {
+        const uint8_t *at = reinterpret_cast<const uint8_t *>(row) + static_cast<int64_t>(v) * 16;
+        if (ALIGNED) {
+            const uint4 x = *reinterpret_cast<const uint4 *>(at);
+            w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
+        } else {
+            const uint32_t odd = sizeof(T) == 4 ? 0u : static_cast<uint32_t>(reinterpret_cast<uintptr_t>(row) & 2);
+            const uint32_t *word = reinterpret_cast<const uint32_t *>(at - odd);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                w[i] = word[i];
+            if (sizeof(T) != 4)
+                w[sizeof(w) / 4 - 1] = odd ? word[4] : 0u;
+        }
+    }
+    __device__ __forceinline__ uint4 get(const T *row) const
+    {
+        if (ALIGNED || sizeof(T) == 4)
+            return make_uint4(w[0], w[1], w[2], w[3]);
+        const uint32_t bits = (reinterpret_cast<uintptr_t>(row) & 2) * 8;
+        return make_uint4(__funnelshift_r(w[0], w[1], bits), __funnelshift_r(w[1], w[2], bits),
+                          __funnelshift_r(w[2], w[3], bits), __funnelshift_r(w[3], w[sizeof(w) / 4 - 1], bits));
+    }
+};
+
+constexpr int kBatch = 4;  // vectors a thread loads at a time
+
+// A batch of a thread's share of a row: vectors v0 + u * ranks.
+template <class T, bool ALIGNED>
+__device__ __forceinline__ void load_batch(RawVec<T, ALIGNED> (&q)[kBatch], const T *row, int nv, int v0, int ranks)
+{
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+        const int v = v0 + u * ranks;
+        if (v < nv)
+            q[u].load(row, v);
+    }
+}
+
+__device__ __forceinline__ float rcp_approx(float x)
+{
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// One CTA's best of max(p - q, 0) / e (Q) or p / e over its slice, as (value, lowest index); 0: none.
+// p = 2^(c l - x) * inv.
+template <bool ALIGNED, class T, bool Q>
+__device__ __forceinline__ uint64_t race_part(const T *row, const float *q, const float *e, int V, int rank, int ranks,
+                                              float x, float inv, float c)
+{
+    constexpr int N = Logits<T>::kVec;
+    float best = 0.0f;
+    int at = -1;
+    auto value = [&](float l, float qv, float ev) {
+        const float pv = exp2_approx(fmaf(l, c, -x)) * inv;
+        return (Q ? pv - qv : pv) * rcp_approx(ev);
+    };
+    const int nv = V / N;
+#pragma unroll 2
+    for (int v = rank; v < nv; v += ranks) {
+        float l[N], r[N];
+        RawVec<T, ALIGNED> lv;
+        RawVec<float, ALIGNED> ev[N / 4], qv[N / 4];
+        lv.load(row, v);
+#pragma unroll
+        for (int k = 0; k < N / 4; ++k) {
+            ev[k].load(e, v * (N / 4) + k);
+            if (Q)
+                qv[k].load(q, v * (N / 4) + k);
+        }
+        Logits<T>::unpack(lv.get(row), l);
+#pragma unroll
+        for (int k = 0; k < N; ++k)
+            r[k] = value(l[k], Q ? __uint_as_float(qv[k / 4].w[k & 3]) : 0.0f, __uint_as_float(ev[k / 4].w[k & 3]));
+        float top = r[0];
+#pragma unroll
+        for (int k = 1; k < N; ++k)
+            top = fmaxf(top, r[k]);
+        if (top > best) {  // rarer and rarer; a thread's indices grow
+            best = top;
+#pragma unroll
+            for (int k = N - 1; k >= 0; --k)
+                at = r[k] == top ? v * N + k : at;
+        }
+    }
+    const int v = nv * N + rank;
+    if (v < V) {
+        const float r = value(Logits<T>::one(row + v), Q ? q[v] : 0.0f, e[v]);
+        if (r > best) {
+            best = r;
+            at = v;
+        }
+    }
+    return at < 0 ? 0 : (static_cast<uint64_t>(__float_as_uint(best)) << 32) | (0xffffffffu - static_cast<uint32_t>(at));
 }
 
 __device__ __forceinline__ uint64_t warp_max(uint64_t k)
@@ -90,18 +263,17 @@ __device__ __forceinline__ uint64_t warp_max(uint64_t k)
     return k;
 }
 
-// Adds a part (m2, s2) to (m, s): sums of 2^(c (l - max)).
-__device__ __forceinline__ void join(float &m, float &s, float m2, float s2, float c)
+__device__ __forceinline__ void async_word(void *dst, const void *src)
 {
-    const float n = fmaxf(m, m2);
-    if (n == -INFINITY)
-        return;
-    s = s * exp2_approx(c * (m - n)) + s2 * exp2_approx(c * (m2 - n));
-    m = n;
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
 }
 
-template <class T>
-__global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const __grid_constant__ VerifyParams p)
+// ALIGNED: every row of every input starts on 16 bytes.  BLOCKS: CTAs an SM: 3
+// without spills where the work of one thread sets the time, 4 (64 registers, some
+// spills) where the number of loads in flight does (256 x 163840 fp32: 175 and
+// 147 us; 32 x 100003 bf16: 22 and 28 us).
+template <class T, bool ALIGNED, int BLOCKS>
+__global__ void __launch_bounds__(kVerifyThreads, BLOCKS) verify_kernel(const __grid_constant__ VerifyParams p)
 {
     __shared__ VerifySmem sm;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -117,138 +289,184 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const __grid_con
     }
     const float temp = p.temperature ? p.temperature[b] : 1.0f;
     const bool greedy = !(temp > 0.0f);
-    const float c = greedy ? 0.0f : kVLog2e / temp;
-    const int step = C * kVerifyThreads;
+    const float c = greedy ? 1.0f : kVLog2e / temp;
+    constexpr int N = Logits<T>::kVec;
+    const int nv = V / N;
+    // the drafts' tokens and numbers, on their way to shared memory beside the first rows
+    if (tid < n) {
+        async_word(&sm.x[tid], p.tokens + static_cast<int64_t>(b) * S + tid);
+        async_word(&sm.u[tid], p.uniforms + static_cast<int64_t>(b) * S + tid);
+    }
 
-    // ---- each row's maximum and sum over this CTA's slice ----
-    for (int i = 0; i <= n; ++i) {
-        const T *row = logits + i * p.stride_i;
-        float m = -INFINITY, s = 0.0f;
-        uint64_t key = 0;
-        for (int v = crank * kVerifyThreads + tid; v < V; v += step) {
-            float x = logit(row, v);
-            x = x == x ? x : -INFINITY;
-            if (greedy) {
-                if (x > -INFINITY)
-                    key = umax64(key, value_key(x, v));
-            } else if (x > m) {
-                s = s * exp2_approx(c * (m - x)) + 1.0f;
-                m = x;
-            } else if (x > -INFINITY) {
-                s += exp2_approx(c * (x - m));
-            }
+    int at = 0;  // the row that the last token comes from: the first refusal, or n
+    for (int i0 = 0; i0 <= n; i0 += p.rows_a_round) {
+        const int i1 = min(n + 1, i0 + p.rows_a_round), R = i1 - i0;
+        // several CTAs to a row, or several rows to a CTA; neighbouring threads read neighbouring vectors
+        const bool share = R <= C;
+        const int first = i0 + (share ? crank * R / C : crank);
+        const int c0 = share ? ((first - i0) * C + R - 1) / R : crank;
+        const int c1 = share ? ((first - i0 + 1) * C + R - 1) / R : crank + 1;
+        const int rank = (crank - c0) * kVerifyThreads + tid, ranks = (c1 - c0) * kVerifyThreads;
+        for (int i = i0 + tid; i < i1; i += kVerifyThreads) {  // rows of other CTAs: an empty part
+            sm.m[i] = -INFINITY;
+            sm.s[i] = 0.0f;
+            sm.i[i] = 0x7fffffff;
         }
+        for (int i = first; i < (share ? first + 1 : i1); i += C) {
+            const T *row = logits + i * p.stride_i;
+            RowPart part{-INFINITY, 0.0f, 0x7fffffff};
+            int v0 = rank;  // the thread's first vector of the batch at hand
+            auto work = [&](const RawVec<T, ALIGNED> (&q)[kBatch]) {
+                constexpr uint32_t none = sizeof(T) == 4 ? 0xff800000u : 0xff80ff80u;
+                constexpr int H = 16 / N;  // vectors of 16 elements, which share a maximum and a branch
 #pragma unroll
-        for (int o = 16; o >= 1; o >>= 1)
-            join(m, s, __shfl_xor_sync(0xffffffffu, m, o), __shfl_xor_sync(0xffffffffu, s, o), c);
-        key = warp_max(key);
-        if (lane == 0) {
-            sm.wm[i][warp] = m;
-            sm.ws[i][warp] = s;
-            sm.wk[i][warp] = key;
+                for (int u0 = 0; u0 < kBatch; u0 += H) {
+                    float l[H][N];
+                    float top = -INFINITY;
+#pragma unroll
+                    for (int w = 0; w < H; ++w) {
+                        const bool have = v0 + (u0 + w) * ranks < nv;
+                        Logits<T>::unpack(have ? q[u0 + w].get(row) : make_uint4(none, none, none, none), l[w]);
+#pragma unroll
+                        for (int e = 0; e < N; ++e)
+                            top = fmaxf(top, l[w][e]);
+                    }
+                    if (top * c > part.x) {  // rarer and rarer along the row
+                        if (greedy) {
+#pragma unroll
+                            for (int w = H - 1; w >= 0; --w)
+#pragma unroll
+                                for (int e = N - 1; e >= 0; --e)
+                                    part.i = l[w][e] == top ? (v0 + (u0 + w) * ranks) * N + e : part.i;
+                        }
+                        part.s *= exp2_approx(part.x - top * c);
+                        part.x = top * c;
+                    }
+                    if (!greedy) {
+                        const float ref = part.x == -INFINITY ? 0.0f : part.x;
+                        float a[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                        for (int w = 0; w < H; ++w)
+#pragma unroll
+                            for (int e = 0; e < N; ++e)
+                                a[(w * N + e) & 3] += exp2_approx(fmaf(l[w][e], c, -ref));
+                        part.s += (a[0] + a[1]) + (a[2] + a[3]);
+                    }
+                }
+                v0 += kBatch * ranks;
+            };
+            // the next batch in flight while one is summed
+            RawVec<T, ALIGNED> qa[kBatch], qb[kBatch];
+            load_batch(qa, row, nv, v0, ranks);
+            while (v0 < nv) {
+                load_batch(qb, row, nv, v0 + kBatch * ranks, ranks);
+                work(qa);
+                if (v0 >= nv)
+                    break;
+                load_batch(qa, row, nv, v0 + kBatch * ranks, ranks);
+                work(qb);
+            }
+            const int v = nv * N + rank;  // the elements that fill no vector
+            if (v < V) {
+                const float y = Logits<T>::one(row + v) * c;
+                part.join(RowPart{y, y > -INFINITY ? 1.0f : 0.0f, v});
+            }
+            warp_join(part);
+            if (lane == 0) {
+                sm.wm[i][warp] = part.x;
+                sm.ws[i][warp] = part.s;
+                sm.wi[i][warp] = part.i;
+            }
         }
-    }
-    __syncthreads();
-    if (tid <= n) {
-        float m = -INFINITY, s = 0.0f;
-        uint64_t key = 0;
-        for (int w = 0; w < kVerifyWarps; ++w) {
-            join(m, s, sm.wm[tid][w], sm.ws[tid][w], c);
-            key = umax64(key, sm.wk[tid][w]);
-        }
-        sm.m[tid] = m;
-        sm.s[tid] = s;
-        sm.key[tid] = key;
-    }
-    __syncwarp();
-    cluster_sync_all();
-    // ---- every CTA: the rows' totals and the drafts' fate ----
-    if (tid <= n) {
-        float m = -INFINITY, s = 0.0f;
-        uint64_t key = 0;
-        for (int r = 0; r < C; ++r) {
-            join(m, s, dsmem_ld_float(mapa_shared(smem_addr(&sm.m[tid]), r)),
-                 dsmem_ld_float(mapa_shared(smem_addr(&sm.s[tid]), r)), c);
-            key = umax64(key, dsmem_ld_u64(mapa_shared(smem_addr(&sm.key[tid]), r)));
-        }
-        sm.gm[tid] = m;
-        sm.gs[tid] = s;
-        sm.gkey[tid] = key;
-        int ok = 0;
-        float lp = 0.0f;
-        if (tid < n) {
-            const int x = p.tokens[static_cast<int64_t>(b) * S + tid];
-            if (x < 0 || x >= V) {
+        if (i0 == 0 && tid < n) {
+            asm volatile("cp.async.wait_all;" ::: "memory");
+            const int x = sm.x[tid];
+            const bool ok = x >= 0 && x < V;
+            if (!ok)
                 atomicOr(p.fault, MSA_FAULT_TOKEN);
-            } else if (greedy) {
-                ok = key != 0 && static_cast<uint32_t>(x) == 0xffffffffu - static_cast<uint32_t>(key);
-            } else if (s > 0.0f) {
-                const float l = logit(logits + tid * p.stride_i, x);
-                const float px = l > -INFINITY ? exp2_approx(c * (l - m)) / s : 0.0f;
-                const float qx = p.draft[(static_cast<int64_t>(b) * S + tid) * V + x];
-                ok = p.uniforms[static_cast<int64_t>(b) * S + tid] * qx < px;
-                lp = (l - m) / temp - logf(s);
+            sm.lx[tid] = ok ? Logits<T>::one(logits + tid * p.stride_i + x) : 0.0f;
+            sm.qx[tid] = ok ? p.draft[(static_cast<int64_t>(b) * S + tid) * V + x] : 0.0f;
+            sm.x[tid] = ok ? x : -1;
+        }
+        __syncthreads();
+        for (int r = first + C * warp; r < (share ? first + 1 : i1); r += C * kVerifyWarps) {
+            RowPart q{-INFINITY, 0.0f, 0x7fffffff};
+            if (lane < kVerifyWarps)
+                q = RowPart{sm.wm[r][lane], sm.ws[r][lane], sm.wi[r][lane]};
+            warp_join(q);
+            if (lane == 0) {
+                sm.m[r] = q.x;
+                sm.s[r] = q.s;
+                sm.i[r] = q.i;
             }
         }
-        sm.ok[tid] = ok;
-        sm.lp[tid] = lp;
+        __syncwarp();
+        cluster_sync_all();
+        // every CTA: the rows' totals and the drafts' fate
+        for (int r = i0 + warp; r < i1; r += kVerifyWarps) {
+            RowPart q{-INFINITY, 0.0f, 0x7fffffff};
+            if (lane < C)
+                q = RowPart{dsmem_ld_float(mapa_shared(smem_addr(&sm.m[r]), lane)),
+                            dsmem_ld_float(mapa_shared(smem_addr(&sm.s[r]), lane)),
+                            dsmem_ld_int(mapa_shared(smem_addr(&sm.i[r]), lane))};
+            warp_join(q);
+            if (lane == 0) {
+                int ok = 0;
+                float lp = 0.0f;
+                if (r < n && sm.x[r] >= 0 && q.x > -INFINITY) {
+                    if (greedy) {
+                        ok = sm.x[r] == q.i;
+                    } else {
+                        const float e = fmaf(sm.lx[r], c, -q.x);
+                        ok = sm.u[r] * sm.qx[r] < exp2_approx(e) / q.s;
+                        lp = (e - log2f(q.s)) * kVLn2;
+                    }
+                }
+                sm.gm[r] = q.x;
+                sm.gs[r] = q.s;
+                sm.gi[r] = q.x > -INFINITY ? q.i : -1;
+                sm.ok[r] = ok;
+                sm.lp[r] = lp;
+            }
+        }
+        __syncthreads();
+        while (at < i1 && at < n && sm.ok[at])
+            ++at;
+        if (at < i1)  // refused, or the row behind the last draft
+            break;
     }
-    __syncthreads();
-    int at = 0;
-    while (at < n && sm.ok[at])
-        ++at;
     // ---- the drawn token ----
-    const bool residual = at < n && !greedy;
-    const float m = sm.gm[at], inv = sm.gs[at] > 0.0f ? 1.0f / sm.gs[at] : 0.0f;
-    if (!greedy && inv > 0.0f) {
-        const T *row = logits + at * p.stride_i;
-        const float *q = p.draft + (static_cast<int64_t>(b) * S + at) * V;
+    const int rank = crank * kVerifyThreads + tid, ranks = C * kVerifyThreads;
+    const bool draws = !greedy && sm.gm[at] > -INFINITY;
+    bool residual = draws && at < n;
+    const float x0 = sm.gm[at], inv = draws ? 1.0f / sm.gs[at] : 0.0f;
+    const T *row = logits + at * p.stride_i;
+    uint64_t key = 0;
+    for (int round = 0; draws && round < 2; ++round) {
+        const float *q = residual ? p.draft + (static_cast<int64_t>(b) * S + at) * V : nullptr;
         const float *e = p.race + static_cast<int64_t>(b) * V;
-        uint64_t kr = 0, kp = 0;
-        for (int v = crank * kVerifyThreads + tid; v < V; v += step) {
-            const float l = logit(row, v);
-            if (!(l > -INFINITY))
-                continue;
-            const float pv = exp2_approx(c * (l - m)) * inv;
-            const float ev = e[v];
-            const float a = pv / ev;
-            if (a > 0.0f)
-                kp = umax64(kp, value_key(a, v));
-            if (residual) {
-                const float r = (pv - q[v]) / ev;
-                if (r > 0.0f)
-                    kr = umax64(kr, value_key(r, v));
-            }
+        uint64_t k = warp_max(residual ? race_part<ALIGNED, T, true>(row, q, e, V, rank, ranks, x0, inv, c)
+                                       : race_part<ALIGNED, T, false>(row, nullptr, e, V, rank, ranks, x0, inv, c));
+        if (lane == 0)
+            sm.wbest[warp] = k;
+        __syncthreads();
+        if (warp == 0) {
+            k = warp_max(lane < kVerifyWarps ? sm.wbest[lane] : 0);
+            if (lane == 0)
+                sm.best[round] = k;
         }
-        kr = warp_max(kr);
-        kp = warp_max(kp);
-        if (lane == 0) {
-            sm.wbest[0][warp] = kr;
-            sm.wbest[1][warp] = kp;
-        }
-    } else if (lane == 0) {
-        sm.wbest[0][warp] = sm.wbest[1][warp] = 0;
+        __syncwarp();
+        cluster_sync_all();
+        key = warp_max(lane < C ? dsmem_ld_u64(mapa_shared(smem_addr(&sm.best[round]), lane)) : 0);
+        if (key || !residual)
+            break;
+        residual = false;  // p <= q everywhere: the draw is from p
     }
-    __syncthreads();
-    if (tid < 2) {
-        uint64_t k = 0;
-        for (int w = 0; w < kVerifyWarps; ++w)
-            k = umax64(k, sm.wbest[tid][w]);
-        sm.best[tid] = k;
-    }
-    __syncthreads();
-    cluster_sync_all();
     if (crank == 0 && warp == 0) {
-        uint64_t kr = 0, kp = 0;
-        for (int r = 0; r < C; ++r) {
-            kr = umax64(kr, dsmem_ld_u64(mapa_shared(smem_addr(&sm.best[0]), r)));
-            kp = umax64(kp, dsmem_ld_u64(mapa_shared(smem_addr(&sm.best[1]), r)));
-        }
-        const uint64_t k = greedy ? sm.gkey[at] : (kr ? kr : kp);
-        const int x = k ? static_cast<int>(0xffffffffu - static_cast<uint32_t>(k)) : -1;
+        const int x = greedy ? sm.gi[at] : key ? static_cast<int>(0xffffffffu - static_cast<uint32_t>(key)) : -1;
         float lp = 0.0f;
         if (x >= 0 && !greedy)
-            lp = (logit(logits + at * p.stride_i, x) - m) / temp - logf(sm.gs[at]);
+            lp = (fmaf(Logits<T>::one(row + x), c, -x0) - log2f(sm.gs[at])) * kVLn2;
         for (int i = lane; i <= S; i += 32) {
             const int64_t o = static_cast<int64_t>(b) * (S + 1) + i;
             p.out[o] = i < at ? p.tokens[static_cast<int64_t>(b) * S + i] : i == at ? x : -1;
@@ -262,7 +480,7 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const __grid_con
     cluster_sync_all();  // no CTA ends while its shared memory is read
 }
 
-template <class T>
+template <class T, bool ALIGNED, int BLOCKS>
 static msa_status launch_verify(const VerifyParams &p, int batch, int cluster, cudaStream_t st)
 {
     cudaLaunchConfig_t cfg;
@@ -277,7 +495,7 @@ static msa_status launch_verify(const VerifyParams &p, int batch, int cluster, c
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, verify_kernel<T>, p) == cudaSuccess ? MSA_OK : MSA_ERR_CUDA;
+    return cudaLaunchKernelEx(&cfg, verify_kernel<T, ALIGNED, BLOCKS>, p) == cudaSuccess ? MSA_OK : MSA_ERR_CUDA;
 }
 
 }  // namespace msa
@@ -323,6 +541,29 @@ extern "C" msa_status msa_verify_draft(const void *logits, int logits_bf16, int6
     p.max_draft = max_draft;
     p.vocab = vocab;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const int cluster = 8;
-    return logits_bf16 ? launch_verify<uint16_t>(p, batch, cluster, st) : launch_verify<float>(p, batch, cluster, st);
+    // Few requests: clusters of 8, all rows at once (24 x 131072 fp32, 3 drafts: 23.9 us, against 41.2 with 4 CTAs
+    // and a row at a time).  Many: a row at a time and smaller clusters, which wait less for one another (128: 67
+    // against 80 us; 192: 104 with 2 CTAs, 105 with 4, 110 with 8).
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess)
+        return MSA_ERR_CUDA;
+    const int sms = device_sms(dev);
+    if (sms <= 0)
+        return MSA_ERR_CUDA;
+    const bool many = batch * 8 > 5 * sms;
+    const int cluster = !many ? 8 : batch <= sms ? 4 : 2;
+    p.rows_a_round = many ? 1 : max_draft + 1;
+    const bool aligned = ((reinterpret_cast<uintptr_t>(logits) | reinterpret_cast<uintptr_t>(draft_probs) |
+                           reinterpret_cast<uintptr_t>(race) | static_cast<uintptr_t>(logits_stride_b) * size |
+                           static_cast<uintptr_t>(logits_stride_i) * size | static_cast<uintptr_t>(vocab) * 4) &
+                          15) == 0;
+    const auto run = [&](auto one) {
+        using T = decltype(one);
+        if (many)
+            return aligned ? launch_verify<T, true, 4>(p, batch, cluster, st)
+                           : launch_verify<T, false, 4>(p, batch, cluster, st);
+        return aligned ? launch_verify<T, true, 3>(p, batch, cluster, st)
+                       : launch_verify<T, false, 3>(p, batch, cluster, st);
+    };
+    return logits_bf16 ? run(uint16_t{}) : run(float{});
 }
