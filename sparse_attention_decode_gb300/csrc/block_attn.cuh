@@ -691,69 +691,110 @@ __global__ void __launch_bounds__(kAttnThreads, 2) block_attn_kernel(const __gri
         consumer_barrier();
         // the prefix's parts of this request's rows: the cluster's CTAs take them in turn
         const bool parts = OWN && p.parts.o;
-        int part0 = 0, part1 = 0;
-        int64_t part_row0 = 0, unit0 = 0;
         PrefixSplit ps(p.parts, 0, 1);
         if (parts) {
             griddep_wait();  // prefix_attn_kernel has ended
             ps = PrefixSplit(p.parts, prefix_tokens(p.parts, p.prefix_len), p.parts.grid);
-            part_row0 = static_cast<int64_t>(owner) * p.q_len * p.group + row0;
         }
         float *co = wo + kAttnWarps * 16 * kAttnOStride;  // [rows][kAttnOStride]: the CTA's part
-        for (int n = tid >> 5; n < rows; n += kAttnWarps) {
-            const int col = lane * 4, w0 = n / 16, r = n % 16;
-            float M = -INFINITY, sum = 0.0f;
-            if (parts && ps.total > 0) {
-                const int tile = static_cast<int>((part_row0 + n) / p.parts.tile_rows);
-                unit0 = static_cast<int64_t>(h) * p.parts.head_tiles + tile;
-                part0 = ps.owner(unit0 * ps.pages);
-                part1 = ps.owner((unit0 + 1) * ps.pages - 1) + 1;
-                part0 += (crank - part0 % S + S) % S;
+        constexpr int kRowsAtOnce = 4;  // rows of a warp whose loads are in flight together
+        for (int n0 = warp; n0 < rows; n0 += kAttnWarps * kRowsAtOnce) {
+            const int col = lane * 4;
+            float M[kRowsAtOnce], sum[kRowsAtOnce], mine[kRowsAtOnce];
+            float4 acc[kRowsAtOnce];
+            int64_t slot[kRowsAtOnce];  // row of the first part that this CTA takes
+            int np[kRowsAtOnce], most = 0;
+#pragma unroll
+            for (int r = 0; r < kRowsAtOnce; ++r) {
+                const int n = min(n0 + kAttnWarps * r, rows - 1);
+                M[r] = -INFINITY;
+                sum[r] = 0.0f;
+                acc[r] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                np[r] = 0;
+                slot[r] = 0;
+                if (parts && ps.total > 0) {
+                    const int64_t row = static_cast<int64_t>(owner) * p.q_len * p.group + row0 + n;
+                    const int64_t u = static_cast<int64_t>(h) * p.parts.head_tiles + row / p.parts.tile_rows;
+                    const int g0 = ps.owner(u * ps.pages), g1 = ps.owner((u + 1) * ps.pages - 1) + 1;
+                    const int g = g0 + (crank - g0 % S + S) % S;
+                    np[r] = g < g1 ? (g1 - g + S - 1) / S : 0;
+                    slot[r] = (g + u) * p.parts.tile_rows + row % p.parts.tile_rows;
+                    most = max(most, np[r]);
+                }
+#pragma unroll
+                for (int k = 0; k < KS; ++k)
+                    M[r] = fmaxf(M[r], ctl->wm[n / 16 + k * MT][n % 16]);
             }
-            const int tr = static_cast<int>((part_row0 + n) % p.parts.tile_rows);
-            for (int g = part0; g < part1; g += S) {
-                const float e = p.parts.lse[(g + unit0) * p.parts.tile_rows + tr];
-                M = fmaxf(M, e);
-                if (e == INFINITY)
-                    ctl->abort_flag = 1;
+            const int64_t step = static_cast<int64_t>(S) * p.parts.tile_rows;  // rows to the CTA's next part
+            for (int i0 = 0; i0 < most; i0 += 32) {
+                // 32 parts at a time: a lane's part of each row, the maximum, the factors, then the vectors
+#pragma unroll
+                for (int r = 0; r < kRowsAtOnce; ++r)
+                    mine[r] = i0 + lane < np[r] ? __ldcg(p.parts.lse + slot[r] + (i0 + lane) * step) : -INFINITY;
+#pragma unroll
+                for (int r = 0; r < kRowsAtOnce; ++r) {
+                    if (mine[r] == INFINITY)
+                        ctl->abort_flag = 1;
+                    float top = mine[r];
+#pragma unroll
+                    for (int o = 16; o >= 1; o >>= 1)
+                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                    const float to = fmaxf(M[r], top), f = rescale(M[r], to);
+                    sum[r] *= f;
+                    acc[r].x *= f;
+                    acc[r].y *= f;
+                    acc[r].z *= f;
+                    acc[r].w *= f;
+                    M[r] = to;
+                    mine[r] = mine[r] == -INFINITY ? 0.0f : rescale(mine[r], to);
+                }
+                const int end = min(32, most - i0);
+#pragma unroll 2
+                for (int i = 0; i < end; ++i) {
+                    float4 v[kRowsAtOnce];
+#pragma unroll
+                    for (int r = 0; r < kRowsAtOnce; ++r) {
+                        v[r] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                        if (i0 + i < np[r])
+                            v[r] = __ldcg(reinterpret_cast<const float4 *>(p.parts.o + (slot[r] + (i0 + i) * step) * kDim + col));
+                    }
+#pragma unroll
+                    for (int r = 0; r < kRowsAtOnce; ++r) {
+                        const float f = __shfl_sync(0xffffffffu, mine[r], i);
+                        sum[r] += f;
+                        acc[r].x += f * v[r].x;
+                        acc[r].y += f * v[r].y;
+                        acc[r].z += f * v[r].z;
+                        acc[r].w += f * v[r].w;
+                    }
+                }
             }
 #pragma unroll
-            for (int k = 0; k < KS; ++k)
-                M = fmaxf(M, ctl->wm[w0 + k * MT][r]);
-            float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            for (int g = part0; g < part1; g += S) {
-                const int64_t at = (g + unit0) * p.parts.tile_rows + tr;
-                const float e = p.parts.lse[at];
-                if (e == -INFINITY)
-                    continue;
-                const float f = rescale(e, M);
-                const float4 v = *reinterpret_cast<const float4 *>(p.parts.o + at * kDim + col);
-                sum += f;
-                acc.x += f * v.x;
-                acc.y += f * v.y;
-                acc.z += f * v.z;
-                acc.w += f * v.w;
-            }
+            for (int r = 0; r < kRowsAtOnce; ++r) {
+                const int n = n0 + kAttnWarps * r;
+                if (n >= rows)
+                    break;
 #pragma unroll
-            for (int k = 0; k < KS; ++k) {
-                const int w = w0 + k * MT;
-                const float f = rescale(ctl->wm[w][r], M);
-                const float4 v = *reinterpret_cast<const float4 *>(wo + (w * 16 + r) * kAttnOStride + col);
-                sum += f * ctl->wl[w][r];
-                acc.x += f * v.x;
-                acc.y += f * v.y;
-                acc.z += f * v.z;
-                acc.w += f * v.w;
-            }
-            if (ctl->abort_flag) {  // a part that is not whole
-                acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                M = -INFINITY;
-                sum = 0.0f;
-            }
-            *reinterpret_cast<float4 *>(co + n * kAttnOStride + col) = acc;
-            if (lane == 0) {
-                ctl->cm[n] = M;
-                ctl->cl[n] = sum;
+                for (int k = 0; k < KS; ++k) {
+                    const int w = n / 16 + k * MT, i = n % 16;
+                    const float f = rescale(ctl->wm[w][i], M[r]);
+                    const float4 v = *reinterpret_cast<const float4 *>(wo + (w * 16 + i) * kAttnOStride + col);
+                    sum[r] += f * ctl->wl[w][i];
+                    acc[r].x += f * v.x;
+                    acc[r].y += f * v.y;
+                    acc[r].z += f * v.z;
+                    acc[r].w += f * v.w;
+                }
+                if (ctl->abort_flag) {  // a part that is not whole
+                    acc[r] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    M[r] = -INFINITY;
+                    sum[r] = 0.0f;
+                }
+                *reinterpret_cast<float4 *>(co + n * kAttnOStride + col) = acc[r];
+                if (lane == 0) {
+                    ctl->cm[n] = M[r];
+                    ctl->cl[n] = sum[r];
+                }
             }
         }
     }

@@ -380,21 +380,35 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_attn_kernel(const __
                 alive = attn_wait(&ctl->abort_flag, p.fault, smem_addr(&ctl->o_done[t]), (it - 1) & 1);
             tc_fence_after_sync();
             const int64_t slot = static_cast<int64_t>(cta) + u;
-            float *part = p.parts.o + (slot * p.parts.tile_rows + t * 128 + row) * kDim;
             const float inv = l == 0.0f ? 0.0f : 1.0f / l;
             if (alive) {
+                // through the tile's Q (every product with it is done), 64 dims at a time, each warp its 32 rows:
+                // a thread holds a row, a store of a warp should cover whole lines
+                float *part = p.parts.o + (slot * p.parts.tile_rows + t * 128 + (row & ~31)) * kDim;
+                uint8_t *turn = smem + t * kPageBytes + (row & ~31) * 256;
+                const int left = p.parts.rows - (nrow & ~31);  // rows of the warp that exist
 #pragma unroll 1
-                for (int q = 0; q < 4; ++q) {
-                    uint32_t o[32];
-                    tmem_ld32(to + q * 32, o);
-                    tmem_wait_ld(o);
-                    if (have)
+                for (int half = 0; half < 2; ++half) {
+                    __syncwarp();
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        uint32_t o[32];
+                        tmem_ld32(to + half * 64 + q * 32, o);
+                        tmem_wait_ld(o);
 #pragma unroll
                         for (int i = 0; i < 32; i += 4)
-                            *reinterpret_cast<float4 *>(part + q * 32 + i) =
+                            *reinterpret_cast<float4 *>(turn + lane * 256 + (((q * 8 + i / 4) ^ (lane & 7)) << 4)) =
                                 make_float4(__uint_as_float(o[i]) * inv, __uint_as_float(o[i + 1]) * inv,
                                             __uint_as_float(o[i + 2]) * inv, __uint_as_float(o[i + 3]) * inv);
+                    }
+                    __syncwarp();
+#pragma unroll 4
+                    for (int r = lane >> 4; r < 32; r += 2)
+                        if (r < left)
+                            *reinterpret_cast<float4 *>(part + r * kDim + half * 64 + (lane & 15) * 4) =
+                                *reinterpret_cast<const float4 *>(turn + r * 256 + (((lane & 15) ^ (r & 7)) << 4));
                 }
+                __syncwarp();
             }
             // +inf marks a part that is not whole
             p.parts.lse[slot * p.parts.tile_rows + t * 128 + row] =
