@@ -156,6 +156,7 @@ static PrefixParts prefix_parts(int64_t rows, int group, int kv_heads, int max_p
     a.rows = static_cast<int>(rows);
     a.group = group;
     a.tile_rows = rows <= 128 ? 128 : 256;
+    a.ways = 256 / a.tile_rows;
     a.head_tiles = static_cast<int>((rows + a.tile_rows - 1) / a.tile_rows);
     a.units = a.head_tiles * kv_heads;
     a.limit = max_prefix_len;
@@ -164,7 +165,7 @@ static PrefixParts prefix_parts(int64_t rows, int group, int kv_heads, int max_p
 
 static size_t prefix_lse_offset(const PrefixParts &a)
 {
-    return kHeaderBytes + (static_cast<size_t>(kPrefixMaxGrid) + a.units) * a.tile_rows * kDim * sizeof(float);
+    return kHeaderBytes + (static_cast<size_t>(kPrefixMaxGrid) + a.units) * 256 * kDim * sizeof(float);
 }
 
 static msa_status launch_prefix(const PrefixAttnParams &p, cudaStream_t st)
@@ -267,7 +268,7 @@ extern "C" size_t msa_attention_prefix_workspace_bytes(int max_rows, int heads, 
         return 0;
     const PrefixParts a = prefix_parts(static_cast<int64_t>(max_rows) * (heads / kv_heads), heads / kv_heads, kv_heads,
                                        max_prefix_len);
-    return prefix_lse_offset(a) + (static_cast<size_t>(kPrefixMaxGrid) + a.units) * a.tile_rows * sizeof(float);
+    return prefix_lse_offset(a) + (static_cast<size_t>(kPrefixMaxGrid) + a.units) * 256 * sizeof(float);
 }
 
 extern "C" msa_status msa_attention_prefix(const void *q, int64_t q_stride, const void *k, const int64_t *k_strides,

@@ -57,13 +57,15 @@ constexpr int kAttnOStride = kDim + 4;  // fp32 row stride of a partial O in sha
 // Parts of the attention over a shared prefix, made by prefix_attn_kernel.  A
 // unit is (KV head, tile of tile_rows rows); unit u = head * head_tiles + tile.
 // The units' pages stand one after the other, u * pages + j, and CTA g of the
-// `ctas` that take part covers [start(g), start(g + 1)); the part of CTA g in
-// unit u is in slot g + u (unique: both grow along the sequence).
+// `ctas` that take part covers [start(g), start(g + 1)); what CTA g has of unit u is
+// in slot g + u (unique: both grow along the sequence).  A slot holds two blocks of
+// 128 rows: the two halves of a tile of 256 rows (ways = 1), or two parts of the
+// same tile of 128 (ways = 2).
 struct PrefixParts {
-    float *o;    // [slot][tile_rows][128], divided by the part's sum
-    float *lse;  // [slot][tile_rows], log2 units; -inf: nothing, +inf: not whole
+    float *o;    // [slot][2][128][128], divided by the part's sum
+    float *lse;  // [slot][2][128], log2 units; -inf: nothing (o is not written), +inf: not whole
     int rows;    // rows of a KV head: batch * q_len * group
-    int group, tile_rows, head_tiles, units;
+    int group, tile_rows, ways, head_tiles, units;
     int limit;   // bound on the prefix's tokens
     int grid;    // CTAs the kernel is launched with
 };
@@ -716,16 +718,17 @@ __global__ void __launch_bounds__(kAttnThreads, 2) block_attn_kernel(const __gri
                     const int64_t row = static_cast<int64_t>(owner) * p.q_len * p.group + row0 + n;
                     const int64_t u = static_cast<int64_t>(h) * p.parts.head_tiles + row / p.parts.tile_rows;
                     const int g0 = ps.owner(u * ps.pages), g1 = ps.owner((u + 1) * ps.pages - 1) + 1;
-                    const int g = g0 + (crank - g0 % S + S) % S;
-                    np[r] = g < g1 ? (g1 - g + S - 1) / S : 0;
-                    slot[r] = (g + u) * p.parts.tile_rows + row % p.parts.tile_rows;
+                    // blocks of the unit's slots, in units of `ways` parts: part i of a row lies 256 / ways rows after i - 1
+                    const int total = (g1 - g0) * p.parts.ways;
+                    np[r] = total > crank ? (total - crank + S - 1) / S : 0;
+                    slot[r] = (g0 + u) * 256 + crank * (256 / p.parts.ways) + row % p.parts.tile_rows;
                     most = max(most, np[r]);
                 }
 #pragma unroll
                 for (int k = 0; k < KS; ++k)
                     M[r] = fmaxf(M[r], ctl->wm[n / 16 + k * MT][n % 16]);
             }
-            const int64_t step = static_cast<int64_t>(S) * p.parts.tile_rows;  // rows to the CTA's next part
+            const int64_t step = static_cast<int64_t>(S) * (256 / p.parts.ways);  // rows to the CTA's next part
             for (int i0 = 0; i0 < most; i0 += 32) {
                 // 32 parts at a time: a lane's part of each row, the maximum, the factors, then the vectors
 #pragma unroll
@@ -752,20 +755,21 @@ __global__ void __launch_bounds__(kAttnThreads, 2) block_attn_kernel(const __gri
 #pragma unroll 2
                 for (int i = 0; i < end; ++i) {
                     float4 v[kRowsAtOnce];
+                    float f[kRowsAtOnce];
 #pragma unroll
                     for (int r = 0; r < kRowsAtOnce; ++r) {
                         v[r] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                        if (i0 + i < np[r])
+                        f[r] = __shfl_sync(0xffffffffu, mine[r], i);
+                        if (f[r] != 0.0f)
                             v[r] = __ldcg(reinterpret_cast<const float4 *>(p.parts.o + (slot[r] + (i0 + i) * step) * kDim + col));
                     }
 #pragma unroll
                     for (int r = 0; r < kRowsAtOnce; ++r) {
-                        const float f = __shfl_sync(0xffffffffu, mine[r], i);
-                        sum[r] += f;
-                        acc[r].x += f * v[r].x;
-                        acc[r].y += f * v[r].y;
-                        acc[r].z += f * v[r].z;
-                        acc[r].w += f * v[r].w;
+                        sum[r] += f[r];
+                        acc[r].x += f[r] * v[r].x;
+                        acc[r].y += f[r] * v[r].y;
+                        acc[r].z += f[r] * v[r].z;
+                        acc[r].w += f[r] * v[r].w;
                     }
                 }
             }

@@ -17,6 +17,13 @@
 // only moved (and O, L rescaled) when the maximum outgrows it by more than 2^8:
 // weights then stay at most 2^8, which costs no precision in fp32 sums and bf16
 // operands, and the rescaling of O in tensor memory becomes rare.
+//
+// The time of a tile's page is its chain, scores (512 cycles) -> softmax (1360) ->
+// product (512), with a barrier between each; two chains run side by side, each
+// with an MMA thread of its own, so that one thread's waits pass while the other's
+// MMAs run (one thread for both tiles: 5000 cycles a page, the tensor pipe a third
+// busy).  Where a KV head has at most 128 rows, the two chains are the even and the
+// odd pages of one tile, and a range leaves two parts.
 #pragma once
 
 #include "block_attn.cuh"
@@ -24,7 +31,7 @@
 namespace msa {
 
 constexpr int kPrefixStages = 4;  // K and V tiles of two pages
-constexpr int kPrefixThreads = 320;  // two softmax warpgroups, a TMA warp, an MMA warp
+constexpr int kPrefixThreads = 352;  // two softmax warpgroups, a TMA warp, two MMA warps
 constexpr int kPrefixMaxGrid = 256;
 constexpr float kPrefixLag = 8.0f;
 
@@ -41,26 +48,103 @@ struct PrefixAttnParams {
 
 struct PrefixSmem {
     uint64_t kv_full[kPrefixStages], kv_empty[kPrefixStages];
-    uint64_t q_full[2], s_full[2], p_full[2], o_done[2];
-    uint64_t drained;
+    uint64_t q_full[2], s_full[2];
+    uint64_t p_half[2], p_full[2];  // the first 64 weights of each row and the turn to issue; all weights
+    uint64_t o_done[2];
+    uint64_t drained[2];
     uint32_t tmem;
     int abort_flag;
 };
 
 constexpr size_t kPrefixSmemBytes = 1024 + 2 * kPageBytes + kPrefixStages * kPageBytes + sizeof(PrefixSmem);
 
-// D[tmem] (+)= A[tmem] * B[smem] (kind::f16, cta_group::1): A's 128 rows lie in the lanes, two bf16 of K a column.
+// The MMA warps run their whole loop converged, with one elected lane behind a
+// predicate: descriptors and addresses are then the warp's, not a thread's, and an
+// instruction needs no moves from thread to uniform registers.  (Issued from inside
+// `if (lane == 0)`, an instruction of 64 cycles took about 110.)
+__device__ __forceinline__ uint32_t elect_one()
+{
+    uint32_t one;
+    asm volatile(
+        "{\n"
+        "  .reg .pred p;\n"
+        "  elect.sync _|p, 0xffffffff;\n"
+        "  selp.u32 %0, 1, 0, p;\n"
+        "}\n"
+        : "=r"(one));
+    return one;
+}
+
+// D[tmem] (+)= A[smem] * B[smem]^T, by the elected lane.
 template <bool ACC>
-__device__ __forceinline__ void umma_ts_f16(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t b_hi, uint32_t idesc)
+__device__ __forceinline__ void umma_ss_one(uint32_t one, uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t idesc)
 {
     asm volatile(
         "{\n"
-        "  .reg .b64 bd;\n"
+        "  .reg .pred p;\n"
+        "  .reg .b64 ad, bd;\n"
+        "  setp.ne.u32 p, %6, 0;\n"
+        "  mov.b64 ad, {%1, %5};\n"
         "  mov.b64 bd, {%2, %5};\n"
-        "  tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], bd, %3, %4;\n"
+        "  @p tcgen05.mma.cta_group::1.kind::f16 [%0], ad, bd, %3, %4;\n"
         "}\n" ::"r"(d_tmem),
-        "r"(a_tmem), "r"(b_lo), "r"(idesc), "n"(ACC ? 1 : 0), "r"(b_hi)
+        "r"(a_lo), "r"(b_lo), "r"(idesc), "n"(ACC ? 1 : 0), "r"(kUmmaDescHi), "r"(one)
         : "memory");
+}
+
+// D[tmem] (+)= A[tmem] * B[smem], by the elected lane: A's 128 rows lie in the lanes, two bf16 of K a column.
+template <bool ACC>
+__device__ __forceinline__ void umma_ts_one(uint32_t one, uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t idesc)
+{
+    asm volatile(
+        "{\n"
+        "  .reg .pred p;\n"
+        "  .reg .b64 bd;\n"
+        "  setp.ne.u32 p, %6, 0;\n"
+        "  mov.b64 bd, {%2, %5};\n"
+        "  @p tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], bd, %3, %4;\n"
+        "}\n" ::"r"(d_tmem),
+        "r"(a_tmem), "r"(b_lo), "r"(idesc), "n"(ACC ? 1 : 0), "r"(kUmmaDescHi), "r"(one)
+        : "memory");
+}
+
+__device__ __forceinline__ void umma_commit_one(uint32_t one, uint32_t bar)
+{
+    asm volatile(
+        "{\n"
+        "  .reg .pred p;\n"
+        "  setp.ne.u32 p, %1, 0;\n"
+        "  @p tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n"
+        "}\n" ::"r"(bar),
+        "r"(one)
+        : "memory");
+}
+
+// Two fp32 operations an instruction, and the maximum of three.
+__device__ __forceinline__ uint64_t pack2(float a, float b)
+{
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float &a, float &b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
 }
 
 // 32 consecutive 32-bit columns of one TMEM lane per thread (shape 32x32b).
@@ -85,16 +169,121 @@ __device__ __forceinline__ uint32_t umma_desc_v_lo(uint32_t saddr)
     return ((saddr >> 4) & 0x3FFFu) | (static_cast<uint32_t>(kHalfPageBytes >> 4) << 16);
 }
 
+// Chain t's MMAs, by one warp: for each of its pages the product of the weights
+// with V and the next page's scores.
+template <int t>
+__device__ __forceinline__ void issue_chain(const PrefixAttnParams &p, PrefixSmem *ctl, uint8_t *smem, uint8_t *kv,
+                                            uint32_t tmem, int64_t lo, int64_t hi, int P)
+{
+    constexpr uint32_t idesc_s = umma_idesc_bf16_f32(128, 128);
+    constexpr uint32_t idesc_o = umma_idesc_bf16_f32(128, 128) | (1u << 16);  // B with N contiguous
+    const uint32_t one = elect_one();
+    const int ways = p.parts.ways;
+    const uint32_t d_s = tmem + t * 128, d_o = tmem + 256 + t * 128;
+    const uint32_t q_desc = umma_desc_lo(smem_addr(smem) + t * kPageBytes), kv_addr = smem_addr(kv);
+    auto wait = [&](uint64_t *bar, uint32_t parity) {
+        if (__all_sync(0xffffffffu, mbar_try_wait(smem_addr(bar), parity)))
+            return true;
+        return attn_wait(&ctl->abort_flag, p.fault, smem_addr(bar), parity);
+    };
+    auto pass = [&](int chain) {
+        if (one)
+            mbar_arrive(smem_addr(&ctl->p_half[chain]));
+    };
+    // the scores of page number kp of the CTA, whose tile has landed; the turn goes to chain `next` (-1: it does not
+    // pass) while the last ones are still to be issued, so that its product reaches the pipe before it runs dry
+    auto scores = [&](uint32_t kp, int next) {
+        const uint32_t s = (2 * kp) % kPrefixStages;
+        const uint32_t b = umma_desc_lo(kv_addr + s * kPageBytes);
+#pragma unroll
+        for (int ks = 0; ks < 8; ++ks) {
+            const uint32_t off = ((ks >> 2) * kHalfPageBytes + (ks & 3) * 32) >> 4;
+            if (ks == 0)
+                umma_ss_one<false>(one, d_s, q_desc + off, b + off, idesc_s);
+            else
+                umma_ss_one<true>(one, d_s, q_desc + off, b + off, idesc_s);
+            if (ks == 5 && next >= 0)
+                pass(next);
+        }
+        umma_commit_one(one, smem_addr(&ctl->s_full[t]));
+        umma_commit_one(one, smem_addr(&ctl->kv_empty[s]));
+    };
+    auto landed = [&](uint32_t tile) { return wait(&ctl->kv_full[tile % kPrefixStages], (tile / kPrefixStages) & 1); };
+    // The chains take turns, product and next scores together: chain 0's softmax then runs beside chain 1's MMAs and
+    // the other way round (left alone they fall into step and share the pipe).  The turn is one of p_half's arrivals,
+    // so that one wait covers both; chain 0 begins.
+    if (t == 0)
+        pass(0);
+    bool alive = true;
+    uint32_t it = 0, kp0 = 0, seg = 0;
+    int left = static_cast<int>(hi - lo), in_unit = P - static_cast<int>(lo % P);
+    for (; left > 0 && alive; ++seg) {
+        const int n = min(left, in_unit);
+        left -= n;
+        in_unit = P;
+        alive = wait(&ctl->q_full[t], seg & 1);
+        const int j0 = ways == 2 ? t : 0;
+        if (alive && j0 < n) {
+            alive = landed(2 * (kp0 + j0));
+            if (!alive)
+                break;
+            tc_fence_after_sync();
+            scores(kp0 + j0, -1);
+        }
+        for (int j = j0; j < n; j += ways, ++it) {
+            const uint32_t kp = kp0 + j;
+            const bool more = j + ways < n;
+            // with one tile's pages in turn, the last page has no successor in the other chain: the turn stays
+            const int next = t == 0 && ways == 2 && j + 1 >= n ? 0 : 1 - t;
+            alive = landed(2 * kp + 1) && (!more || landed(2 * (kp + ways))) && wait(&ctl->p_half[t], it & 1);
+            if (!alive)
+                break;
+            tc_fence_after_sync();
+            // 16 tokens an instruction: 8 columns of weights, two atoms of V; the first half while the second half's
+            // weights are on their way
+            const uint32_t sv = (2 * kp + 1) % kPrefixStages;
+            const uint32_t b = umma_desc_v_lo(kv_addr + sv * kPageBytes);
+            if (j == j0)
+                umma_ts_one<false>(one, d_o, d_s, b, idesc_o);
+            else
+                umma_ts_one<true>(one, d_o, d_s, b, idesc_o);
+#pragma unroll
+            for (int ks = 1; ks < 4; ++ks)
+                umma_ts_one<true>(one, d_o, d_s + ks * 8, b + ((ks * 2048) >> 4), idesc_o);
+            alive = wait(&ctl->p_full[t], it & 1);
+            if (!alive)
+                break;
+            tc_fence_after_sync();
+#pragma unroll
+            for (int ks = 4; ks < 8; ++ks)
+                umma_ts_one<true>(one, d_o, d_s + ks * 8, b + ((ks * 2048) >> 4), idesc_o);
+            umma_commit_one(one, smem_addr(&ctl->o_done[t]));
+            umma_commit_one(one, smem_addr(&ctl->kv_empty[sv]));
+            // the next page's scores overwrite the weights that this product reads: MMAs of one thread run in the
+            // order of their issue
+            if (more)
+                scores(kp + ways, next);
+            else
+                pass(next);
+        }
+        kp0 += n;
+    }
+    umma_commit_one(one, smem_addr(&ctl->drained[t]));  // nothing in flight when the tensor memory is freed
+    mbar_wait(smem_addr(&ctl->drained[t]), 0);
+    __syncwarp();
+}
+
 __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_attn_kernel(const __grid_constant__ PrefixAttnParams p)
 {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t *kv = smem + 2 * kPageBytes;  // after the two Q tiles
     auto *ctl = reinterpret_cast<PrefixSmem *>(kv + kPrefixStages * kPageBytes);
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // the same in all lanes, and known to be
 
     griddep_launch_dependents();
-    const int prefix = prefix_tokens(p.parts, p.prefix_len);
+    const int prefix = __shfl_sync(0xffffffffu, prefix_tokens(p.parts, p.prefix_len), 0);
     const PrefixSplit split(p.parts, prefix, static_cast<int>(gridDim.x));
     if (prefix == 0 && *p.prefix_len != 0 && blockIdx.x == 0 && tid == 0)
         atomicOr(p.fault, MSA_FAULT_SEQ_LEN);
@@ -103,20 +292,21 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_attn_kernel(const __
         return;
     const int P = split.pages;
     const int64_t lo = split.start(cta), hi = split.start(cta + 1);
-    const int tiles = p.parts.tile_rows / 128;  // 128-row tiles of a unit: 1 or 2
+    const int ways = p.parts.ways;  // 1: two tiles, every page in both; 2: one tile, its pages in turn
 
     if (tid == 0) {
         for (int s = 0; s < kPrefixStages; ++s) {
             mbar_init(smem_addr(&ctl->kv_full[s]), 1);
-            mbar_init(smem_addr(&ctl->kv_empty[s]), 1);
+            mbar_init(smem_addr(&ctl->kv_empty[s]), 2 / ways);
         }
         for (int t = 0; t < 2; ++t) {
             mbar_init(smem_addr(&ctl->q_full[t]), 128);
             mbar_init(smem_addr(&ctl->s_full[t]), 1);
+            mbar_init(smem_addr(&ctl->p_half[t]), 129);  // the rows, and the other chain's passing of the turn
             mbar_init(smem_addr(&ctl->p_full[t]), 128);
             mbar_init(smem_addr(&ctl->o_done[t]), 1);
+            mbar_init(smem_addr(&ctl->drained[t]), 1);
         }
-        mbar_init(smem_addr(&ctl->drained), 1);
         ctl->abort_flag = 0;
         fence_barrier_init();
     }
@@ -127,7 +317,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_attn_kernel(const __
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
-    const uint32_t tmem = ctl->tmem;  // columns 0, 128: S (and the weights); 256, 384: O
+    const uint32_t tmem = __shfl_sync(0xffffffffu, ctl->tmem, 0);  // columns 0, 128: S (and the weights); 256, 384: O
 
     if (warp == 8) {
         // ---- K and V tiles, page after page ----
@@ -172,101 +362,23 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_attn_kernel(const __
         for (uint32_t j = it >= kPrefixStages ? it - kPrefixStages : 0; j < it; ++j)
             mbar_wait(smem_addr(&ctl->kv_full[j % kPrefixStages]), (j / kPrefixStages) & 1);
     } else if (warp == 9) {
-        // ---- one thread issues both products of both tiles ----
-        if (lane == 0) {
-            constexpr uint32_t idesc_s = umma_idesc_bf16_f32(128, 128);
-            constexpr uint32_t idesc_o = umma_idesc_bf16_f32(128, 128) | (1u << 16);  // B with N contiguous
-            volatile int *abort_flag = &ctl->abort_flag;
-            auto wait = [&](uint64_t *bar, uint32_t parity) {
-                if (*abort_flag || !mbar_wait(smem_addr(bar), parity)) {
-                    if (!*abort_flag)
-                        atomicOr(p.fault, MSA_FAULT_TIMEOUT);
-                    *abort_flag = 1;
-                    return false;
-                }
-                return true;
-            };
-            auto scores = [&](int t, int s) {
-                const uint32_t a = umma_desc_lo(smem_addr(smem) + t * kPageBytes);
-                const uint32_t b = umma_desc_lo(smem_addr(kv) + s * kPageBytes);
-#pragma unroll
-                for (int ks = 0; ks < 8; ++ks) {
-                    const uint32_t off = ((ks >> 2) * kHalfPageBytes + (ks & 3) * 32) >> 4;
-                    if (ks == 0)
-                        umma_f16<false>(tmem + t * 128, a + off, b + off, idesc_s);
-                    else
-                        umma_f16<true>(tmem + t * 128, a + off, b + off, idesc_s);
-                }
-                umma_commit(smem_addr(&ctl->s_full[t]));
-            };
-            bool alive = true;
-            uint32_t it = 0, seg = 0;
-            for (int64_t x = lo; x < hi && alive; ++seg) {
-                const int n = static_cast<int>(min(hi, (x / P + 1) * P) - x);
-                x += n;
-                for (int t = 0; t < tiles && alive; ++t)
-                    alive = wait(&ctl->q_full[t], seg & 1);
-                if (alive)
-                    alive = wait(&ctl->kv_full[(2 * it) % kPrefixStages], (2 * it / kPrefixStages) & 1);
-                if (!alive)
-                    break;
-                tc_fence_after_sync();
-                for (int t = 0; t < tiles; ++t)
-                    scores(t, (2 * it) % kPrefixStages);
-                umma_commit(smem_addr(&ctl->kv_empty[(2 * it) % kPrefixStages]));
-                for (int j = 0; j < n && alive; ++j, ++it) {
-                    const int sv = (2 * it + 1) % kPrefixStages, next = (2 * it + 2) % kPrefixStages;
-                    for (int t = 0; t < tiles && alive; ++t) {
-                        alive = wait(&ctl->p_full[t], it & 1);
-                        if (alive && t == 0)
-                            alive = wait(&ctl->kv_full[sv], ((2 * it + 1) / kPrefixStages) & 1);
-                        if (!alive)
-                            break;
-                        tc_fence_after_sync();
-                        const uint32_t b = umma_desc_v_lo(smem_addr(kv) + sv * kPageBytes);
-#pragma unroll
-                        for (int ks = 0; ks < 8; ++ks) {  // 16 tokens each: 8 columns of weights, two atoms of V
-                            const uint32_t bk = b + ((ks * 2048) >> 4);
-                            if (ks == 0 && j == 0)
-                                umma_ts_f16<false>(tmem + 256 + t * 128, tmem + t * 128, bk, kUmmaDescHi, idesc_o);
-                            else
-                                umma_ts_f16<true>(tmem + 256 + t * 128, tmem + t * 128 + ks * 8, bk, kUmmaDescHi, idesc_o);
-                        }
-                        umma_commit(smem_addr(&ctl->o_done[t]));
-                        if (t == tiles - 1)
-                            umma_commit(smem_addr(&ctl->kv_empty[sv]));
-                        // the next page's scores overwrite the weights that this product reads: MMAs of one
-                        // thread run in the order of their issue
-                        if (j + 1 < n) {
-                            if (t == 0)
-                                alive = wait(&ctl->kv_full[next], ((2 * it + 2) / kPrefixStages) & 1);
-                            if (!alive)
-                                break;
-                            scores(t, next);
-                            if (t == tiles - 1)
-                                umma_commit(smem_addr(&ctl->kv_empty[next]));
-                        }
-                    }
-                }
-            }
-            umma_commit(smem_addr(&ctl->drained));  // nothing in flight when the tensor memory is freed
-            mbar_wait(smem_addr(&ctl->drained), 0);
-        }
-        __syncwarp();
-    } else if (warp / 4 < tiles) {
+        issue_chain<0>(p, ctl, smem, kv, tmem, lo, hi, P);
+    } else if (warp == 10) {
+        issue_chain<1>(p, ctl, smem, kv, tmem, lo, hi, P);
+    } else {
         // ---- softmax: one thread a row ----
         const int t = warp >> 2, row = tid & 127;
         const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // (32 * (warp % 4)) << 16
         const uint32_t ts = tmem + t * 128 + lanes, to = tmem + 256 + t * 128 + lanes;
         const float c = p.scale_log2;
         bool alive = true;
-        uint32_t it = 0;
+        uint32_t it = 0, kp0 = 0;  // pages of this chain, pages of the CTA before the unit's
         for (int64_t x = lo; x < hi; ) {
             const int u = static_cast<int>(x / P), j0 = static_cast<int>(x % P);
             const int n = static_cast<int>(min(hi - x, static_cast<int64_t>(P - j0)));
             x += n;
             const int h = u / p.parts.head_tiles;
-            const int nrow = (u % p.parts.head_tiles) * p.parts.tile_rows + t * 128 + row;
+            const int nrow = (u % p.parts.head_tiles) * p.parts.tile_rows + (ways == 1 ? t * 128 : 0) + row;
             const bool have = nrow < p.parts.rows;
             {
                 const uint16_t *src = p.q + static_cast<int64_t>(nrow / p.parts.group) * p.q_stride +
@@ -284,12 +396,13 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_attn_kernel(const __
             tc_fence_before_sync();
             mbar_arrive(smem_addr(&ctl->q_full[t]));
             float m = -INFINITY, l = 0.0f;
-            int page = p.prefix_table[j0];
-            for (int j = 0; j < n && alive; ++j, ++it) {
+            const int first = ways == 2 ? t : 0;
+            int page = first < n ? p.prefix_table[j0 + first] : 0;
+            for (int j = first; j < n && alive; j += ways, ++it) {
                 // tokens of the page that count
                 const int valid = page < 0 || page >= p.num_pages ? 0 : min(kPage, prefix - (j0 + j) * kPage);
-                if (j + 1 < n)
-                    page = p.prefix_table[j0 + j + 1];
+                if (j + ways < n)
+                    page = p.prefix_table[j0 + j + ways];
                 alive = attn_wait(&ctl->abort_flag, p.fault, smem_addr(&ctl->s_full[t]), it & 1);
                 if (!alive)
                     break;
@@ -309,33 +422,32 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_attn_kernel(const __
                         for (int i = 0; i < 32; ++i)
                             if (q * 32 + i >= valid)
                                 s[q][i] = 0xff800000u;
-                    if (t == 0) {
-                        // what lies in V past the tokens is no data: zero it (0 x NaN is NaN)
-                        const int sv = (2 * it + 1) % kPrefixStages;
-                        alive = attn_wait(&ctl->abort_flag, p.fault, smem_addr(&ctl->kv_full[sv]),
-                                          ((2 * it + 1) / kPrefixStages) & 1);
-                        if (!alive)
-                            break;
-                        if (row >= valid) {
-                            uint8_t *at = kv + sv * kPageBytes + row * 128;
+                    // what lies in V past the tokens is no data: zero it (0 x NaN is NaN); both chains do, since
+                    // neither product waits for the other's softmax
+                    const uint32_t vt = 2 * (kp0 + j) + 1;
+                    alive = attn_wait(&ctl->abort_flag, p.fault, smem_addr(&ctl->kv_full[vt % kPrefixStages]),
+                                      (vt / kPrefixStages) & 1);
+                    if (!alive)
+                        break;
+                    if (row >= valid) {
+                        uint8_t *at = kv + (vt % kPrefixStages) * kPageBytes + row * 128;
 #pragma unroll
-                            for (int i = 0; i < 16; ++i)
-                                *reinterpret_cast<uint4 *>(at + (i >> 3) * kHalfPageBytes + (i & 7) * 16) =
-                                    make_uint4(0u, 0u, 0u, 0u);
-                        }
-                        fence_proxy_async_smem();
+                        for (int i = 0; i < 16; ++i)
+                            *reinterpret_cast<uint4 *>(at + (i >> 3) * kHalfPageBytes + (i & 7) * 16) =
+                                make_uint4(0u, 0u, 0u, 0u);
                     }
+                    fence_proxy_async_smem();
                 }
                 float mx[4];
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
-                    mx[q] = -INFINITY;
+                    mx[q] = fmaxf(__uint_as_float(s[q][0]), __uint_as_float(s[q][1]));
 #pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        mx[q] = fmaxf(mx[q], __uint_as_float(s[q][i]));
+                    for (int i = 2; i < 32; i += 2)
+                        mx[q] = max3(mx[q], __uint_as_float(s[q][i]), __uint_as_float(s[q][i + 1]));
                 }
                 const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
-                if (j == 0) {
+                if (j == first) {
                     m = top;
                 } else if (__any_sync(0xffffffffu, top > m + kPrefixLag)) {
                     const float to_m = fmaxf(m, top), f = rescale(m, to_m);
@@ -357,34 +469,44 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_attn_kernel(const __
                     }
                 }
                 const float ref = m == -INFINITY ? 0.0f : m;
-                float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                uint32_t w[2][32];
+                uint64_t sum[4] = {0, 0, 0, 0};  // two fp32 sums each
+                const uint64_t c2 = pack2(c, c), r2 = pack2(-ref, -ref);
 #pragma unroll
-                for (int q = 0; q < 4; ++q)
+                for (int half = 0; half < 2; ++half) {
+                    uint32_t w[32];
 #pragma unroll
-                    for (int i = 0; i < 32; i += 2) {
-                        const float a = exp2_approx(fmaf(__uint_as_float(s[q][i]), c, -ref));
-                        const float b = exp2_approx(fmaf(__uint_as_float(s[q][i + 1]), c, -ref));
-                        sum[q] += a + b;
-                        w[q >> 1][(q & 1) * 16 + i / 2] = f32x2_to_bf16x2(a, b);
-                    }
-                tmem_st32(ts, w[0]);
-                tmem_st32(ts + 32, w[1]);
-                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-                tmem_wait_st();
-                tc_fence_before_sync();
-                mbar_arrive(smem_addr(&ctl->p_full[t]));
+                    for (int q = 2 * half; q < 2 * half + 2; ++q)
+#pragma unroll
+                        for (int i = 0; i < 32; i += 2) {
+                            float a, b;
+                            unpack2(fma2(pack2(__uint_as_float(s[q][i]), __uint_as_float(s[q][i + 1])), c2, r2), a, b);
+                            a = exp2_approx(a);
+                            b = exp2_approx(b);
+                            sum[q] = add2(sum[q], pack2(a, b));
+                            w[(q & 1) * 16 + i / 2] = f32x2_to_bf16x2(a, b);
+                        }
+                    tmem_st32(ts + half * 32, w);
+                    tmem_wait_st();
+                    tc_fence_before_sync();
+                    mbar_arrive(smem_addr(half ? &ctl->p_full[t] : &ctl->p_half[t]));
+                }
+                float a, b;
+                unpack2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), a, b);
+                l += a + b;
             }
             // ---- the range's part of the unit ----
-            if (alive)
+            const bool some = first < n;
+            if (alive && some)
                 alive = attn_wait(&ctl->abort_flag, p.fault, smem_addr(&ctl->o_done[t]), (it - 1) & 1);
             tc_fence_after_sync();
-            const int64_t slot = static_cast<int64_t>(cta) + u;
+            kp0 += n;
+            // 128 rows in a row of slots: chain t of a unit with two tiles holds its rows t * 128 .., of one with one tile its part t
+            const int64_t block = (static_cast<int64_t>(cta) + u) * 2 + t;
             const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-            if (alive) {
+            if (alive && some) {
                 // through the tile's Q (every product with it is done), 64 dims at a time, each warp its 32 rows:
                 // a thread holds a row, a store of a warp should cover whole lines
-                float *part = p.parts.o + (slot * p.parts.tile_rows + t * 128 + (row & ~31)) * kDim;
+                float *part = p.parts.o + (block * 128 + (row & ~31)) * kDim;
                 uint8_t *turn = smem + t * kPageBytes + (row & ~31) * 256;
                 const int left = p.parts.rows - (nrow & ~31);  // rows of the warp that exist
 #pragma unroll 1
@@ -411,7 +533,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_attn_kernel(const __
                 __syncwarp();
             }
             // +inf marks a part that is not whole
-            p.parts.lse[slot * p.parts.tile_rows + t * 128 + row] =
+            p.parts.lse[block * 128 + row] =
                 !alive ? INFINITY : l == 0.0f ? -INFINITY : m + log2f(l);
         }
         tc_fence_before_sync();
