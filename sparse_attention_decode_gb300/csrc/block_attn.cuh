@@ -129,6 +129,8 @@ struct BlockAttnSmem {
     float wm[kAttnWarps][16], wl[kAttnWarps][16];  // each warp's rows: running maximum (log2 units) and sum
     float cm[kAttnMaxRows], cl[kAttnMaxRows];      // the CTA's rows, read by the whole cluster
     float rm[kAttnMaxRows], rinv[kAttnMaxRows];    // final maximum and 1 / sum
+    float fac[8][kAttnMaxRows];                    // what each rank's part of a row is multiplied by
+    int part_ctas[2][2];  // prefix parts: first CTA and one past the last, of the first row's tile and of the next
 };
 
 // Mass scratch: [page of this CTA][slice * rows] of (sum, maximum at that time); 64 entries a page.
@@ -408,6 +410,14 @@ __global__ void __launch_bounds__(kAttnThreads, 2) block_attn_kernel(const __gri
                         qa[ks][r] = f32x2_to_f16x2(bf16_lo(qa[ks][r]) * f, bf16_hi(qa[ks][r]) * f);
                     }
             }
+        }
+        if (OWN && p.parts.o && tid < 2) {  // while the first tile is on its way: which CTAs made the prefix's parts
+            const PrefixSplit ps(p.parts, prefix_tokens(p.parts, p.prefix_len), p.parts.grid);
+            const int tile = (owner * p.unit_rows + row0) / p.parts.tile_rows + tid;
+            const int64_t u = static_cast<int64_t>(h) * p.parts.head_tiles + tile;
+            const bool some = ps.total > 0 && tile < p.parts.head_tiles;
+            ctl->part_ctas[tid][0] = some ? ps.owner(u * ps.pages) : 0;
+            ctl->part_ctas[tid][1] = some ? ps.owner((u + 1) * ps.pages - 1) + 1 : 0;
         }
         float o[16][4];
 #pragma unroll
@@ -693,11 +703,8 @@ __global__ void __launch_bounds__(kAttnThreads, 2) block_attn_kernel(const __gri
         consumer_barrier();
         // the prefix's parts of this request's rows: the cluster's CTAs take them in turn
         const bool parts = OWN && p.parts.o;
-        PrefixSplit ps(p.parts, 0, 1);
-        if (parts) {
+        if (parts)
             griddep_wait();  // prefix_attn_kernel has ended
-            ps = PrefixSplit(p.parts, prefix_tokens(p.parts, p.prefix_len), p.parts.grid);
-        }
         float *co = wo + kAttnWarps * 16 * kAttnOStride;  // [rows][kAttnOStride]: the CTA's part
         constexpr int kRowsAtOnce = 4;  // rows of a warp whose loads are in flight together
         for (int n0 = warp; n0 < rows; n0 += kAttnWarps * kRowsAtOnce) {
@@ -714,14 +721,15 @@ __global__ void __launch_bounds__(kAttnThreads, 2) block_attn_kernel(const __gri
                 acc[r] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
                 np[r] = 0;
                 slot[r] = 0;
-                if (parts && ps.total > 0) {
-                    const int64_t row = static_cast<int64_t>(owner) * p.q_len * p.group + row0 + n;
-                    const int64_t u = static_cast<int64_t>(h) * p.parts.head_tiles + row / p.parts.tile_rows;
-                    const int g0 = ps.owner(u * ps.pages), g1 = ps.owner((u + 1) * ps.pages - 1) + 1;
-                    // blocks of the unit's slots, in units of `ways` parts: part i of a row lies 256 / ways rows after i - 1
+                if (parts) {
+                    const int first = owner * p.unit_rows + row0, row = first + n;
+                    const int tile = row / p.parts.tile_rows, which = tile - first / p.parts.tile_rows;
+                    const int g0 = ctl->part_ctas[which][0], g1 = ctl->part_ctas[which][1];
+                    // part i of a row lies 256 / ways rows after part i - 1
                     const int total = (g1 - g0) * p.parts.ways;
                     np[r] = total > crank ? (total - crank + S - 1) / S : 0;
-                    slot[r] = (g0 + u) * 256 + crank * (256 / p.parts.ways) + row % p.parts.tile_rows;
+                    slot[r] = (static_cast<int64_t>(g0) + h * p.parts.head_tiles + tile) * 256 +
+                              crank * (256 / p.parts.ways) + row % p.parts.tile_rows;
                     most = max(most, np[r]);
                 }
 #pragma unroll
@@ -752,24 +760,26 @@ __global__ void __launch_bounds__(kAttnThreads, 2) block_attn_kernel(const __gri
                     mine[r] = mine[r] == -INFINITY ? 0.0f : rescale(mine[r], to);
                 }
                 const int end = min(32, most - i0);
-#pragma unroll 2
+#pragma unroll 4
                 for (int i = 0; i < end; ++i) {
                     float4 v[kRowsAtOnce];
                     float f[kRowsAtOnce];
 #pragma unroll
                     for (int r = 0; r < kRowsAtOnce; ++r) {
-                        v[r] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
                         f[r] = __shfl_sync(0xffffffffu, mine[r], i);
-                        if (f[r] != 0.0f)
-                            v[r] = __ldcg(reinterpret_cast<const float4 *>(p.parts.o + (slot[r] + (i0 + i) * step) * kDim + col));
+                        // no branch, so that the loads of several parts go out together; what a part that holds nothing
+                        // has in its place may be anything
+                        v[r] = __ldcg(reinterpret_cast<const float4 *>(
+                            p.parts.o + (slot[r] + (f[r] != 0.0f ? (i0 + i) * step : 0)) * kDim + col));
                     }
 #pragma unroll
                     for (int r = 0; r < kRowsAtOnce; ++r) {
+                        const bool some = f[r] != 0.0f;
                         sum[r] += f[r];
-                        acc[r].x += f[r] * v[r].x;
-                        acc[r].y += f[r] * v[r].y;
-                        acc[r].z += f[r] * v[r].z;
-                        acc[r].w += f[r] * v[r].w;
+                        acc[r].x += some ? f[r] * v[r].x : 0.0f;
+                        acc[r].y += some ? f[r] * v[r].y : 0.0f;
+                        acc[r].z += some ? f[r] * v[r].z : 0.0f;
+                        acc[r].w += some ? f[r] * v[r].w : 0.0f;
                     }
                 }
             }
@@ -811,15 +821,30 @@ __global__ void __launch_bounds__(kAttnThreads, 2) block_attn_kernel(const __gri
     if (warp < kAttnWarps) {
         const float *co = reinterpret_cast<const float *>(smem) + kAttnWarps * 16 * kAttnOStride;
         const uint32_t a_co = smem_addr(co), a_cm = smem_addr(ctl->cm), a_cl = smem_addr(ctl->cl);
-        bool gave_up = false;
-        for (int c = 0; c < S; ++c)
-            gave_up |= dsmem_ld_s32(mapa_shared(smem_addr(&ctl->abort_flag), c)) != 0;
+        // a thread a row: maximum, sum and factors, every rank's numbers under way at once
         if (tid < rows) {
-            float M = -INFINITY, sum = 0.0f;
-            for (int c = 0; c < S; ++c)
-                M = fmaxf(M, dsmem_ld_f32(mapa_shared(a_cm + tid * 4, c)));
-            for (int c = 0; c < S; ++c)
-                sum += rescale(dsmem_ld_f32(mapa_shared(a_cm + tid * 4, c)), M) * dsmem_ld_f32(mapa_shared(a_cl + tid * 4, c));
+            float m[8], l[8];
+            int gave_up = 0;
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+                m[c] = -INFINITY;
+                l[c] = 0.0f;
+                if (c < S) {
+                    m[c] = dsmem_ld_f32(mapa_shared(a_cm + tid * 4, c));
+                    l[c] = dsmem_ld_f32(mapa_shared(a_cl + tid * 4, c));
+                    gave_up |= dsmem_ld_s32(mapa_shared(smem_addr(&ctl->abort_flag), c));
+                }
+            }
+            float M = m[0], sum = 0.0f;
+#pragma unroll
+            for (int c = 1; c < 8; ++c)
+                M = fmaxf(M, m[c]);
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+                const float f = rescale(m[c], M);
+                sum += f * l[c];
+                ctl->fac[c][tid] = f;
+            }
             if (gave_up)
                 sum = 0.0f;
             ctl->rm[tid] = M;
@@ -831,17 +856,24 @@ __global__ void __launch_bounds__(kAttnThreads, 2) block_attn_kernel(const __gri
             }
         }
         consumer_barrier();
+#pragma unroll 2
         for (int n = warp + kAttnWarps * crank; n < rows; n += kAttnWarps * S) {
-            const float M = ctl->rm[n], inv = ctl->rinv[n];
+            float4 v[8];
+#pragma unroll
+            for (int c = 0; c < 8; ++c)
+                if (c < S)
+                    v[c] = dsmem_ld_f32x4(mapa_shared(a_co + (n * kAttnOStride + lane * 4) * 4, c));
             float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            for (int c = 0; c < S; ++c) {
-                const float f = rescale(dsmem_ld_f32(mapa_shared(a_cm + n * 4, c)), M);
-                const float4 v = dsmem_ld_f32x4(mapa_shared(a_co + (n * kAttnOStride + lane * 4) * 4, c));
-                acc.x += f * v.x;
-                acc.y += f * v.y;
-                acc.z += f * v.z;
-                acc.w += f * v.w;
-            }
+#pragma unroll
+            for (int c = 0; c < 8; ++c)
+                if (c < S) {
+                    const float f = ctl->fac[c][n];
+                    acc.x += f * v[c].x;
+                    acc.y += f * v[c].y;
+                    acc.z += f * v[c].z;
+                    acc.w += f * v[c].w;
+                }
+            const float inv = ctl->rinv[n];
             const bool none = inv == 0.0f;  // nothing visible: zeros
             const int i = OWN ? (row0 + n) / p.group : 0, head = OWN ? (row0 + n) % p.group : row0 + n;
             const int64_t qr = OWN ? static_cast<int64_t>(owner) * p.q_len + i : owner;
