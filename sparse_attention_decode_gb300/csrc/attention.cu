@@ -46,7 +46,7 @@ bool unaligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>
 // most one per block of the list.
 int block_attn_split(int64_t units, int pages, int sms)
 {
-    if (const char *e = getenv("SPLIT")) return std::min(atoi(e), pages >= 8 ? 8 : pages >= 4 ? 4 : pages >= 2 ? 2 : 1);
+
     int s = 1;
     while (s < 8 && 2 * s <= pages && units * s * 2 <= 2 * static_cast<int64_t>(sms))
         s *= 2;
