@@ -78,135 +78,177 @@ struct EvictParams {
     int cols, kv_heads, seq_limit, budget, n_sink, n_window;
 };
 
-constexpr int kEvictThreads = 512;
-
 // A block's key, ordered as its weight: NaN lowest, then -inf .. inf, pinned blocks highest.
 __device__ __forceinline__ uint32_t evict_key(float w)
 {
     return w != w ? 0u : float_order_bits(w == 0.0f ? 0.0f : w);
 }
 
-// Exclusive prefix sum over the block's threads; *total gets the sum.
-__device__ __forceinline__ int block_exclusive_sum(int v, int *scratch, int *total)
+// Block sums W[j] = ((w_0 + w_1) + ..)[j] of N consecutive blocks, the loads of four heads at a time in flight.
+template <int N>
+__device__ __forceinline__ void block_sums(const float *w, int64_t cols, int heads, int j, float (&sum)[N])
 {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int x = v;
+    for (int h0 = 0; h0 < heads; h0 += 4) {
+        float v[4][N];
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o)
-            x += y;
-    }
-    if (lane == 31)
-        scratch[warp] = x;
-    __syncthreads();
-    if (warp == 0) {
-        int y = lane < kEvictThreads / 32 ? scratch[lane] : 0;
+        for (int h = 0; h < 4; ++h)
+            if (h0 + h < heads) {
+                const float *at = w + (h0 + h) * cols + j;
+                if (N == 4) {
+                    const float4 x = *reinterpret_cast<const float4 *>(at);
+                    v[h][0] = x.x, v[h][1 % N] = x.y, v[h][2 % N] = x.z, v[h][3 % N] = x.w;
+                } else {
+                    v[h][0] = *at;
+                }
+            }
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int z = __shfl_up_sync(0xffffffffu, y, o);
-            if (lane >= o)
-                y += z;
-        }
-        scratch[lane] = y;
+        for (int h = 0; h < 4; ++h)
+            if (h0 + h < heads)
+#pragma unroll
+                for (int k = 0; k < N; ++k)
+                    sum[k] = h0 + h == 0 ? v[h][k] : sum[k] + v[h][k];
     }
-    __syncthreads();
-    const int before = warp ? scratch[warp - 1] : 0;
-    *total = scratch[31];
-    __syncthreads();
-    return before + x - v;
 }
 
 // One CTA per request.  Keys in shared memory; the budget-th largest by four
-// 8-bit radix passes; equal keys at the threshold go by index through one prefix
-// sum, a second one numbers the kept and the freed blocks; then table and
-// weights are copied in increasing destination order (every read of a tile
-// before its writes, and a source never lies below its destination), so outputs
-// may be the inputs.
-__global__ void __launch_bounds__(kEvictThreads) evict_kernel(const __grid_constant__ EvictParams p)
+// 8-bit radix passes; in the first a warp adds up its counts per digit before it
+// touches shared memory (most weights share their exponent, and those never
+// selected are all zero).  A warp then takes a run of blocks, 32 at a time by ballot: how many
+// lie above the threshold and how many on it, one prefix sum over the warps, and
+// the blocks' places follow (blocks on the threshold stay in index order until it
+// is met).  Table and weights are copied in increasing destination order, kCopy
+// entries a thread at a time: every read of a piece before its writes, and a
+// source never lies below its destination, so outputs may be the inputs.  VEC:
+// rows start on 16 bytes.  T threads, two CTAs an SM: 1024 for long contexts,
+// whose rounds over the blocks are then few (256 x 8192 blocks, accumulation
+// included: 35 us, 38 with 512), 256 for short ones.
+//
+// Bound by latency: two rounds over the request's weights with the selection
+// between them.  What carries it are wide loads with several heads in flight and
+// few barriers (with a barrier every 512 entries and a load at a time: 62 us).
+constexpr int kCopy = 2;
+
+template <bool VEC, int T>
+__global__ void __launch_bounds__(T, 2) evict_kernel(const __grid_constant__ EvictParams p)
 {
+    constexpr int kWarps = T / 32;
     extern __shared__ uint32_t evict_smem[];
     uint32_t *keys = evict_smem;
-    uint16_t *list = reinterpret_cast<uint16_t *>(keys + p.cols);  // kept blocks, then the freed ones
-    __shared__ int scratch[32];
+    uint16_t *list = reinterpret_cast<uint16_t *>(keys + (p.cols + 3) / 4 * 4);  // kept blocks, then the freed ones
     __shared__ int hist[256];
+    __shared__ int above_of[kWarps], ties_of[kWarps];
     __shared__ uint32_t s_prefix;
     __shared__ int s_want;
-    const int b = blockIdx.x, tid = threadIdx.x;
+    const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int L = p.seq_lens[b];
     const bool bad = L < 0 || L > p.seq_limit;
     if (bad && tid == 0)
         atomicOr(p.fault, MSA_FAULT_SEQ_LEN);
     const int nb = bad ? p.cols : (L + kPage - 1) / kPage;
     const int keep = bad ? p.cols : min(nb, p.budget);
+    const bool all = keep == nb;
     const float *w = p.weights + static_cast<int64_t>(b) * p.kv_heads * p.cols;
     const int32_t *table = p.table + b * p.bt_stride;
-    const int per = (nb + kEvictThreads - 1) / kEvictThreads;
-    const int j0 = min(nb, tid * per), j1 = min(nb, j0 + per);
 
-    if (keep < nb) {
-        for (int j = tid; j < nb; j += kEvictThreads) {
-            float sum = w[j];
-            for (int h = 1; h < p.kv_heads; ++h)
-                sum += w[static_cast<int64_t>(h) * p.cols + j];
-            keys[j] = j < p.n_sink || j >= nb - p.n_window ? 0xffffffffu : evict_key(sum);
+    uint32_t bound = 0;  // the key of the last block that stays
+    int want = all ? 0 : keep;
+    if (!all) {
+        constexpr int N = VEC ? 4 : 1;
+#pragma unroll 2
+        for (int j = tid * N; j < nb; j += T * N) {  // VEC: a row is at least nb rounded up to 4 long
+            float sum[N];
+            block_sums<N>(w, p.cols, p.kv_heads, j, sum);
+#pragma unroll
+            for (int k = 0; k < N; ++k)
+                keys[j + k] = j + k < p.n_sink || j + k >= nb - p.n_window ? 0xffffffffu : evict_key(sum[k]);
         }
-        if (tid == 0) {
-            s_prefix = 0;
-            s_want = keep;
-        }
+        uint32_t mask = 0;
         for (int shift = 24; shift >= 0; shift -= 8) {
-            for (int i = tid; i < 256; i += kEvictThreads)
+            for (int i = tid; i < 256; i += T)
                 hist[i] = 0;
             __syncthreads();
-            const uint32_t prefix = s_prefix;
-            const uint32_t mask = shift == 24 ? 0u : 0xffffffffu << (shift + 8);
-            for (int j = tid; j < nb; j += kEvictThreads)
-                if ((keys[j] & mask) == prefix)
-                    atomicAdd(&hist[(keys[j] >> shift) & 255], 1);
-            __syncthreads();
-            // the bin, from the top, in which the want-th largest lies
-            if (tid < 256) {
-                int above = 0;
-                for (int i = tid + 1; i < 256; ++i)
-                    above += hist[i];
-                const int want = s_want;
-                if (above < want && above + hist[tid] >= want)
-                    scratch[0] = tid, scratch[1] = want - above;
+#pragma unroll 4
+            for (int i0 = 0; i0 < nb; i0 += T) {
+                const uint32_t key = i0 + tid < nb ? keys[i0 + tid] : 0u;
+                const bool in = i0 + tid < nb && (key & mask) == bound;
+                if (!__any_sync(0xffffffffu, in))
+                    continue;
+                const uint32_t digit = in ? (key >> shift) & 255 : 256;
+                if (shift == 24) {
+                    const uint32_t same = __match_any_sync(0xffffffffu, digit);
+                    if (in && (same & ((1u << lane) - 1u)) == 0)
+                        atomicAdd(&hist[digit], __popc(same));
+                } else if (in) {
+                    atomicAdd(&hist[digit], 1);
+                }
             }
             __syncthreads();
-            if (tid == 0) {
-                s_prefix = prefix | static_cast<uint32_t>(scratch[0]) << shift;
-                s_want = scratch[1];
+            if (warp == 0) {
+                // the digit, from the top, in which the want-th largest lies: lane 0 has the 8 highest digits
+                int mine[8], sum = 0;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    mine[k] = hist[255 - lane * 8 - k];
+                    sum += mine[k];
+                }
+                int above = sum;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int y = __shfl_up_sync(0xffffffffu, above, o);
+                    if (lane >= o)
+                        above += y;
+                }
+                above -= sum;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    if (above < want && above + mine[k] >= want) {
+                        s_prefix = bound | static_cast<uint32_t>(255 - lane * 8 - k) << shift;
+                        s_want = want - above;
+                    }
+                    above += mine[k];
+                }
             }
             __syncthreads();
+            bound = s_prefix;
+            want = s_want;  // how many of the blocks that share the digits so far stay
+            mask |= 255u << shift;
         }
     }
-    const bool all = keep == nb;
-    const uint32_t bound = all ? 0u : s_prefix;
-    const int want = all ? 0 : s_want;  // blocks at the bound that stay
-    int total;
-    int ties = 0;
-    if (!all)
-        for (int j = j0; j < j1; ++j)
-            ties += keys[j] == bound;
-    const int tie0 = block_exclusive_sum(ties, scratch, &total);
-    // stays(j, rank): rank counts the thread's blocks at the bound in block order
-    auto stays = [&](int j, int &rank) {
-        return all || keys[j] > bound || (keys[j] == bound && rank++ < want);
-    };
-    int mine = 0, rank = tie0;
-    for (int j = j0; j < j1; ++j)
-        mine += stays(j, rank);
-    int at = block_exclusive_sum(mine, scratch, &total);
-    int gone = keep + (j0 - at);  // freed blocks are listed after the kept ones
-    rank = tie0;
-    for (int j = j0; j < j1; ++j)
-        list[stays(j, rank) ? at++ : gone++] = static_cast<uint16_t>(j);
+    // a warp's run: rows of 32 blocks
+    const int rows = (nb + 31) / 32, per = (rows + kWarps - 1) / kWarps;
+    const int r0 = min(rows, warp * per), r1 = min(rows, r0 + per);
+    int above = 0, ties = 0;
+    for (int r = r0; r < r1; ++r) {
+        const int j = r * 32 + lane;
+        const uint32_t key = j < nb && !all ? keys[j] : 0u;
+        above += __popc(__ballot_sync(0xffffffffu, j < nb && (all || key > bound)));
+        ties += __popc(__ballot_sync(0xffffffffu, j < nb && !all && key == bound));
+    }
+    if (lane == 0) {
+        above_of[warp] = above;
+        ties_of[warp] = ties;
+    }
+    __syncthreads();
+    above = __reduce_add_sync(0xffffffffu, lane < warp ? above_of[lane] : 0);  // before the warp's run
+    ties = __reduce_add_sync(0xffffffffu, lane < warp ? ties_of[lane] : 0);
+    for (int r = r0; r < r1; ++r) {
+        const int j = r * 32 + lane;
+        const uint32_t lower = (1u << lane) - 1u;
+        const uint32_t key = j < nb && !all ? keys[j] : 0u;
+        const uint32_t on = __ballot_sync(0xffffffffu, j < nb && !all && key == bound);
+        const bool stays = j < nb && (all || key > bound || (key == bound && ties + __popc(on & lower) < want));
+        const uint32_t kept = __ballot_sync(0xffffffffu, stays);
+        const int at = above + min(want, ties) + __popc(kept & lower);  // kept blocks before j
+        if (j < nb)
+            list[stays ? at : keep + j - at] = static_cast<uint16_t>(j);
+        ties += __popc(on);
+        above += __popc(__ballot_sync(0xffffffffu, j < nb && (all || key > bound)));
+    }
     __syncthreads();
 
     int32_t *freed = p.freed + static_cast<int64_t>(b) * p.cols;
-    for (int i = tid; i < p.cols; i += kEvictThreads)
+#pragma unroll 4
+    for (int i = tid; i < p.cols; i += T)
         freed[i] = i < nb - keep ? table[list[keep + i]] : -1;
     if (tid == 0) {
         p.n_freed[b] = nb - keep;
@@ -214,24 +256,50 @@ __global__ void __launch_bounds__(kEvictThreads) evict_kernel(const __grid_const
     }
     __syncthreads();  // the freed pages are read before any entry is overwritten
     int32_t *out_table = p.out_table + b * p.out_stride;
-    for (int i0 = 0; i0 < p.cols; i0 += kEvictThreads) {
-        const int i = i0 + tid;
-        const int32_t v = i < keep ? table[list[i]] : -1;
-        __syncthreads();
-        if (i < p.cols)
-            out_table[i] = v;
-    }
     float *out_w = p.out_weights + static_cast<int64_t>(b) * p.kv_heads * p.cols;
-    for (int h = 0; h < p.kv_heads; ++h) {
-        const float *from = w + static_cast<int64_t>(h) * p.cols;
-        float *to = out_w + static_cast<int64_t>(h) * p.cols;
-        for (int i0 = 0; i0 < p.cols; i0 += kEvictThreads) {
-            const int i = i0 + tid;
-            const float v = i < keep ? from[list[i]] : 0.0f;
-            __syncthreads();
-            if (i < p.cols)
-                to[i] = v;
+    for (int i0 = 0; i0 < keep; i0 += T * kCopy) {
+        int from[kCopy];
+        int32_t page[kCopy];
+#pragma unroll
+        for (int k = 0; k < kCopy; ++k) {
+            const int i = i0 + k * T + tid;
+            from[k] = i < keep ? list[i] : -1;
+            page[k] = from[k] >= 0 ? table[from[k]] : -1;
         }
+        for (int h0 = 0; h0 < p.kv_heads; h0 += 4) {
+            float v[4][kCopy];
+#pragma unroll
+            for (int h = 0; h < 4; ++h)
+#pragma unroll
+                for (int k = 0; k < kCopy; ++k)
+                    if (h0 + h < p.kv_heads && from[k] >= 0)
+                        v[h][k] = w[static_cast<int64_t>(h0 + h) * p.cols + from[k]];
+            __syncthreads();
+#pragma unroll
+            for (int h = 0; h < 4; ++h)
+#pragma unroll
+                for (int k = 0; k < kCopy; ++k)
+                    if (h0 + h < p.kv_heads && from[k] >= 0)
+                        out_w[static_cast<int64_t>(h0 + h) * p.cols + i0 + k * T + tid] = v[h][k];
+        }
+#pragma unroll
+        for (int k = 0; k < kCopy; ++k)
+            if (from[k] >= 0)
+                out_table[i0 + k * T + tid] = page[k];
+    }
+    __syncthreads();  // the last piece's sources are read before the rest is cleared
+#pragma unroll 4
+    for (int i = keep + tid; i < p.cols; i += T)
+        out_table[i] = -1;
+    for (int h = 0; h < p.kv_heads; ++h) {
+        float *row = out_w + static_cast<int64_t>(h) * p.cols;
+        const int first = VEC ? min(p.cols, (keep + 3) / 4 * 4) : p.cols;
+#pragma unroll 4
+        for (int i = keep + tid; i < first; i += T)
+            row[i] = 0.0f;
+#pragma unroll 4
+        for (int i = first + tid * 4; i < p.cols; i += T * 4)
+            *reinterpret_cast<float4 *>(row + i) = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     }
 }
 
@@ -295,10 +363,13 @@ extern "C" msa_status msa_cache_evict(const int32_t *block_table, int64_t bt_str
     p.budget = budget;
     p.n_sink = n_sink;
     p.n_window = n_window;
-    const size_t smem = static_cast<size_t>(cols) * 6 + 8;
-    if (cudaFuncSetAttribute(evict_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) !=
-        cudaSuccess)
+    const size_t smem = (static_cast<size_t>(cols) + 3) / 4 * 16 + static_cast<size_t>(cols) * 2;
+    const bool vec = cols % 4 == 0 && ((reinterpret_cast<uintptr_t>(weights) | reinterpret_cast<uintptr_t>(out_weights)) & 15) == 0;
+    const bool wide = cols > 1024;
+    auto *kernel = wide ? (vec ? evict_kernel<true, 1024> : evict_kernel<false, 1024>)
+                        : (vec ? evict_kernel<true, 256> : evict_kernel<false, 256>);
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
         return MSA_ERR_CUDA;
-    evict_kernel<<<batch, kEvictThreads, smem, static_cast<cudaStream_t>(stream)>>>(p);
+    kernel<<<batch, wide ? 1024 : 256, smem, static_cast<cudaStream_t>(stream)>>>(p);
     return cudaGetLastError() == cudaSuccess ? MSA_OK : MSA_ERR_CUDA;
 }
