@@ -1,5 +1,5 @@
-// Attention over the blocks the indexer selected: argument checks and launch of
-// block_attn_kernel (block_attn.cuh).
+// Attention over the blocks the indexer selected (block_attn.cuh) and of a batch
+// that shares a prefix (prefix_attn.cuh): argument checks and launches.
 #include "block_attn.cuh"
 #include "prefix_attn.cuh"
 
@@ -56,7 +56,7 @@ int block_attn_split(int64_t units, int pages, int sms)
 template <class F, int MT, bool OWN>
 msa_status launch_block_attn(const BlockAttnParams &p, int64_t units, int split, cudaStream_t st)
 {
-    const size_t smem = block_attn_smem<F>(OWN || !p.mass ? 0 : (p.k + split - 1) / split);
+    const size_t smem = block_attn_smem<F>(p.mass ? (p.k + split - 1) / split : 0);
     auto *kernel = block_attn_kernel<F, MT, OWN>;
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
         return MSA_ERR_CUDA;
@@ -71,11 +71,11 @@ msa_status launch_block_attn(const BlockAttnParams &p, int64_t units, int split,
     attr[0].val.clusterDim.x = split;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
-    // behind prefix_attn_kernel: CTAs start as its CTAs end, and wait for all of it before they read its parts
+    // beside prefix_attn_kernel: CTAs start where it leaves room
     attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = p.parts.o ? 2 : 1;
+    cfg.numAttrs = OWN ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kernel, p) == cudaSuccess ? MSA_OK : MSA_ERR_CUDA;
 }
 
@@ -134,8 +134,6 @@ static msa_status sparse_entry(const void *q, int64_t q_stride, const void *k, c
     p.group = group;
     p.k = topk;
     p.seq_limit = static_cast<int>(std::min<int64_t>(max_model_len, kPage * bt_stride));
-    p.unit_rows = group;
-    p.row_tiles = 1;
     p.scale_log2 = scale * kLog2e;
     const int64_t units = static_cast<int64_t>(batch) * q_len * kv_heads;
     const int split = block_attn_split(units, topk, sms);
@@ -149,33 +147,59 @@ static msa_status sparse_entry(const void *q, int64_t q_stride, const void *k, c
                          : launch_block_attn<AttnBf16, 4, false>(p, units, split, st);
 }
 
-// The units of a batch's rows; a tile of 128 rows where they do not fill more.
-static PrefixParts prefix_parts(int64_t rows, int group, int kv_heads, int max_prefix_len)
+// The units of a batch's rows (a tile of 128 rows of a KV head where they do not fill more).
+static void prefix_units(PrefixParts &a, int64_t rows, int kv_heads)
 {
-    PrefixParts a;
-    std::memset(&a, 0, sizeof a);
-    a.rows = static_cast<int>(rows);
-    a.group = group;
     a.tile_rows = rows <= 128 ? 128 : 256;
     a.ways = 256 / a.tile_rows;
     a.head_tiles = static_cast<int>((rows + a.tile_rows - 1) / a.tile_rows);
     a.units = a.head_tiles * kv_heads;
+}
+
+// Bytes: rows of the prefix's slots and one own part a row and head, 516 each.
+static size_t prefix_workspace(int max_rows, int group, int kv_heads)
+{
+    PrefixParts a;
+    const int64_t rows = static_cast<int64_t>(max_rows) * group;
+    prefix_units(a, rows, kv_heads);
+    const size_t prefix = (static_cast<size_t>(kPrefixMaxGrid) + a.units) * 256;
+    return kHeaderBytes + (prefix + static_cast<size_t>(rows) * kv_heads) * (kDim + 1) * sizeof(float) + 4 * 256;
+}
+
+static void prefix_parts(PrefixParts &a, int batch, int q_len, int group, int kv_heads, int max_prefix_len,
+                         uint8_t *workspace)
+{
+    std::memset(&a, 0, sizeof a);
+    a.batch = batch;
+    a.q_len = q_len;
+    a.group = group;
+    a.kv_heads = kv_heads;
+    a.rows = batch * q_len * group;
+    prefix_units(a, a.rows, kv_heads);
+    a.own_tiles = (q_len * group + kAttnMaxRows - 1) / kAttnMaxRows;
     a.limit = max_prefix_len;
-    return a;
+    uint8_t *at = workspace + kHeaderBytes;
+    auto take = [&](size_t bytes) {
+        uint8_t *here = at;
+        at += round_up(bytes, 256);
+        return here;
+    };
+    const size_t rows = (static_cast<size_t>(kPrefixMaxGrid) + a.units) * 256;
+    const size_t own_rows = static_cast<size_t>(a.rows) * kv_heads;
+    a.lse = reinterpret_cast<float *>(take(rows * sizeof(float)));
+    a.own_lse = reinterpret_cast<float *>(take(own_rows * sizeof(float)));
+    a.o = reinterpret_cast<float *>(take(rows * kDim * sizeof(float)));
+    a.own_o = reinterpret_cast<float *>(take(own_rows * kDim * sizeof(float)));
 }
 
-static size_t prefix_lse_offset(const PrefixParts &a)
+template <int WPR>
+static msa_status launch_join(const JoinParams &p, int64_t rows, cudaStream_t st)
 {
-    return kHeaderBytes + (static_cast<size_t>(kPrefixMaxGrid) + a.units) * 256 * kDim * sizeof(float);
-}
-
-static msa_status launch_prefix(const PrefixAttnParams &p, cudaStream_t st)
-{
-    if (cudaFuncSetAttribute(prefix_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             static_cast<int>(kPrefixSmemBytes)) != cudaSuccess)
-        return MSA_ERR_CUDA;
-    prefix_attn_kernel<<<p.parts.grid, kPrefixThreads, kPrefixSmemBytes, st>>>(p);
-    return cudaGetLastError() == cudaSuccess ? MSA_OK : MSA_ERR_CUDA;
+    constexpr int kRows = kJoinWarps / WPR;
+    cudaLaunchAttribute attr[1];
+    const cudaLaunchConfig_t cfg =
+        pdl_config(dim3(static_cast<unsigned>((rows + kRows - 1) / kRows)), dim3(32 * kJoinWarps), 0, st, attr);
+    return cudaLaunchKernelEx(&cfg, join_kernel<WPR>, p) == cudaSuccess ? MSA_OK : MSA_ERR_CUDA;
 }
 
 static msa_status prefix_entry(const void *q, int64_t q_stride, const void *k, const int64_t *k_strides, const void *v,
@@ -196,8 +220,11 @@ static msa_status prefix_entry(const void *q, int64_t q_stride, const void *k, c
         unaligned(q, 16) || q_stride % 8 || q_stride < static_cast<int64_t>(kv_heads) * group * kDim ||
         unaligned(out, 16) || unaligned(workspace, 256))
         return MSA_ERR_INVALID_ARG;
-    if (workspace_bytes < msa_attention_prefix_workspace_bytes(batch * q_len, kv_heads * group, kv_heads, max_prefix_len))
+    PrefixAttnParams p;
+    std::memset(&p, 0, sizeof p);
+    if (workspace_bytes < prefix_workspace(batch * q_len, group, kv_heads))
         return MSA_ERR_WORKSPACE_TOO_SMALL;
+    prefix_parts(p.parts, batch, q_len, group, kv_heads, max_prefix_len, static_cast<uint8_t *>(workspace));
     if (batch == 0)
         return MSA_OK;
     int dev = 0;
@@ -206,57 +233,67 @@ static msa_status prefix_entry(const void *q, int64_t q_stride, const void *k, c
     const int sms = device_sms(dev);
     if (sms <= 0)
         return MSA_ERR_CUDA;
-    BlockAttnParams p;
-    std::memset(&p, 0, sizeof p);
     if (!make_cache_map(&p.kmap, k, k_strides, num_pages, kv_heads, false) ||
         !make_cache_map(&p.vmap, v, v_strides, num_pages, kv_heads, false))
         return MSA_ERR_CUDA;
     p.q = static_cast<const uint16_t *>(q);
-    p.block_table = block_table;
+    p.prefix_table = prefix_table;
+    p.prefix_len = prefix_len;
     p.seq_lens = seq_lens;
-    p.out = static_cast<uint16_t *>(out);
-    p.lse = out_lse;
     p.fault = &static_cast<WorkspaceHeader *>(workspace)->fault;
     p.q_stride = q_stride;
-    p.bt_stride = bt_stride;
     p.num_pages = num_pages;
-    p.batch = batch;
-    p.q_len = q_len;
-    p.kv_heads = kv_heads;
-    p.sel_heads = 1;
-    p.group = group;
-    p.seq_limit = static_cast<int>(std::min<int64_t>(max_model_len, kPage * bt_stride));
-    p.unit_rows = q_len * group;
-    p.row_tiles = (p.unit_rows + kAttnMaxRows - 1) / kAttnMaxRows;
-    p.prefix_len = prefix_len;
     p.scale_log2 = scale * kLog2e;
-    p.parts = prefix_parts(static_cast<int64_t>(batch) * p.unit_rows, group, kv_heads, max_prefix_len);
+    p.parts.seq_limit = static_cast<int>(std::min<int64_t>(max_model_len, kPage * bt_stride));
+    p.parts.grid = std::min(sms, kPrefixMaxGrid);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const int64_t units = static_cast<int64_t>(batch) * kv_heads * p.row_tiles;
-    const int split = block_attn_split(units, 8, sms);
-    {
-        p.parts.grid = std::min(sms, kPrefixMaxGrid);
-        p.parts.o = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + kHeaderBytes);
-        p.parts.lse = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + prefix_lse_offset(p.parts));
-        PrefixAttnParams a;
-        std::memset(&a, 0, sizeof a);
-        a.kmap = p.kmap;
-        a.vmap = p.vmap;
-        a.q = p.q;
-        a.prefix_table = prefix_table;
-        a.prefix_len = prefix_len;
-        a.parts = p.parts;
-        a.fault = p.fault;
-        a.q_stride = q_stride;
-        a.num_pages = num_pages;
-        a.scale_log2 = p.scale_log2;
-        const msa_status s = launch_prefix(a, st);
-        if (s != MSA_OK)
-            return s;
-    }
-    return p.unit_rows <= 16   ? launch_block_attn<AttnBf16, 1, true>(p, units, split, st)
-           : p.unit_rows <= 32 ? launch_block_attn<AttnBf16, 2, true>(p, units, split, st)
-                               : launch_block_attn<AttnBf16, 4, true>(p, units, split, st);
+    if (cudaFuncSetAttribute(prefix_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(kPrefixSmemBytes)) != cudaSuccess)
+        return MSA_ERR_CUDA;
+    prefix_attn_kernel<<<p.parts.grid, kPrefixThreads, kPrefixSmemBytes, st>>>(p);
+    if (cudaGetLastError() != cudaSuccess)
+        return MSA_ERR_CUDA;
+    BlockAttnParams o;
+    std::memset(&o, 0, sizeof o);
+    o.kmap = p.kmap;
+    o.vmap = p.vmap;
+    o.q = p.q;
+    o.block_table = block_table;
+    o.seq_lens = seq_lens;
+    o.part = p.parts.own_o;
+    o.lse = p.parts.own_lse;
+    o.fault = p.fault;
+    o.q_stride = q_stride;
+    o.bt_stride = bt_stride;
+    o.num_pages = num_pages;
+    o.batch = batch;
+    o.q_len = q_len;
+    o.kv_heads = kv_heads;
+    o.sel_heads = 1;
+    o.group = group;
+    o.seq_limit = p.parts.seq_limit;
+    o.row_tiles = p.parts.own_tiles;
+    o.scale_log2 = p.scale_log2;
+    // beside the prefix, own pages have a part of the SMs: few CTAs that walk longer lists (8 x 4 positions over 16384 +
+    // 8000 tokens: 33.6 us with 64 CTAs, 38 with 256, 49 with 32)
+    const int64_t units = static_cast<int64_t>(batch) * kv_heads * o.row_tiles;
+    const int split = block_attn_split(units, 8, sms / 4), unit_rows = std::min(q_len * group, kAttnMaxRows);
+    const msa_status own = unit_rows <= 16   ? launch_block_attn<AttnBf16, 1, true>(o, units, split, st)
+                           : unit_rows <= 32 ? launch_block_attn<AttnBf16, 2, true>(o, units, split, st)
+                                             : launch_block_attn<AttnBf16, 4, true>(o, units, split, st);
+    if (own != MSA_OK)
+        return own;
+    JoinParams j;
+    std::memset(&j, 0, sizeof j);
+    j.parts = p.parts;
+    j.prefix_len = prefix_len;
+    j.seq_lens = seq_lens;
+    j.out = static_cast<uint16_t *>(out);
+    j.lse = out_lse;
+    const int64_t rows = static_cast<int64_t>(p.parts.rows) * kv_heads;
+    // few rows have many parts each: more warps to a row
+    return rows <= 4 * sms ? launch_join<8>(j, rows, st) : rows <= 16 * sms ? launch_join<4>(j, rows, st)
+                                                                              : launch_join<1>(j, rows, st);
 }
 
 }  // namespace msa
@@ -267,9 +304,7 @@ extern "C" size_t msa_attention_prefix_workspace_bytes(int max_rows, int heads, 
 {
     if (max_rows < 0 || kv_heads < 1 || heads < kv_heads || heads % kv_heads || max_prefix_len < 0)
         return 0;
-    const PrefixParts a = prefix_parts(static_cast<int64_t>(max_rows) * (heads / kv_heads), heads / kv_heads, kv_heads,
-                                       max_prefix_len);
-    return prefix_lse_offset(a) + (static_cast<size_t>(kPrefixMaxGrid) + a.units) * 256 * sizeof(float);
+    return prefix_workspace(max_rows, heads / kv_heads, kv_heads);
 }
 
 extern "C" msa_status msa_attention_prefix(const void *q, int64_t q_stride, const void *k, const int64_t *k_strides,

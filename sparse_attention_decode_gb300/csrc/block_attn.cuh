@@ -1,6 +1,6 @@
-// Attention of a few query rows over a list of 128-token cache pages: the
-// kernel behind the attention over selected blocks and behind a request's own
-// pages in the attention with a shared prefix.
+// Attention of a few query rows over a list of 128-token cache pages: the blocks
+// selected for them, or (OWN) all pages of their request, whose result is then one
+// part of the attention with a shared prefix.
 //
 // Mathematics.  For a row n with query q_n and the valid tokens T_n,
 //     s = scale * q_n . K[t],   out_n = sum_T 2^(c s - M) V[t] / L,
@@ -14,11 +14,12 @@
 // What bounds it: every K and V byte is used by the 1..64 rows of one KV head
 // only, so the cache stream does (64 KiB a page in bf16).  Hence TMA into a ring
 // of tiles with two CTAs an SM (192 KiB in flight an SM), mma.sync on 16-row
-// tiles read by ldmatrix (the tensor work of 16 rows is a sixth of the stream
+// tiles read by ldmatrix (the tensor work of 16 rows is a third of the stream
 // time; the 128-row tiles of tcgen05 would be filled to an eighth), and a
 // cluster of up to 8 CTAs that splits one list when there are few: the parts
 // join through distributed shared memory, in cluster-rank order, so there is one
-// launch, no scratch, and the same result each time.
+// launch, no scratch, and the same result each time.  256 requests x 4 heads x 16
+// blocks (1.05 GB): 175-178 us, 0.87-0.88 of the copy rate.
 #pragma once
 
 #include "host_util.cuh"
@@ -51,47 +52,8 @@ struct AttnFp8 {
 
 constexpr int kAttnWarps = 4;  // consumer warps; one producer warp after them
 constexpr int kAttnThreads = 32 * (kAttnWarps + 1);
-constexpr int kAttnMaxRows = 64;  // rows of one unit: 1, 2 or 4 tiles of 16
+constexpr int kAttnMaxRows = 64;  // rows of one unit (query heads of a KV head): 1, 2 or 4 tiles of 16
 constexpr int kAttnOStride = kDim + 4;  // fp32 row stride of a partial O in shared memory (bank spread)
-
-// Parts of the attention over a shared prefix, made by prefix_attn_kernel.  A
-// unit is (KV head, tile of tile_rows rows); unit u = head * head_tiles + tile.
-// The units' pages stand one after the other, u * pages + j, and CTA g of the
-// `ctas` that take part covers [start(g), start(g + 1)); what CTA g has of unit u is
-// in slot g + u (unique: both grow along the sequence).  A slot holds two blocks of
-// 128 rows: the two halves of a tile of 256 rows (ways = 1), or two parts of the
-// same tile of 128 (ways = 2).
-struct PrefixParts {
-    float *o;    // [slot][2][128][128], divided by the part's sum
-    float *lse;  // [slot][2][128], log2 units; -inf: nothing (o is not written), +inf: not whole
-    int rows;    // rows of a KV head: batch * q_len * group
-    int group, tile_rows, ways, head_tiles, units;
-    int limit;   // bound on the prefix's tokens
-    int grid;    // CTAs the kernel is launched with
-};
-
-constexpr int kPrefixMinPages = 2;  // pages a CTA's range should have at least
-
-struct PrefixSplit {
-    int pages, ctas;
-    int64_t total;
-    __device__ PrefixSplit(const PrefixParts &p, int tokens, int grid)
-    {
-        pages = (tokens + kPage - 1) / kPage;
-        total = static_cast<int64_t>(pages) * p.units;
-        ctas = static_cast<int>(min(static_cast<int64_t>(grid), (total + kPrefixMinPages - 1) / kPrefixMinPages));
-    }
-    __device__ int64_t start(int g) const { return g * total / ctas; }
-    // the CTA whose range holds page x of the sequence
-    __device__ int owner(int64_t x) const { return static_cast<int>(((x + 1) * ctas - 1) / total); }
-};
-
-// The prefix's tokens; 0 where the length is out of range.
-__device__ __forceinline__ int prefix_tokens(const PrefixParts &p, const int32_t *len)
-{
-    const int n = *len;
-    return n < 0 || n > p.limit ? 0 : n;
-}
 
 struct BlockAttnParams {
     CUtensorMap kmap, vmap;  // [page][head][token][dim], box 1 x 1 x 128 x (64 bf16 | 128 E4M3)
@@ -99,29 +61,25 @@ struct BlockAttnParams {
     const float *kscale, *vscale;  // E4M3: [page, head, 128]
     const int32_t *block_table;
     const int32_t *seq_lens;
-    const int32_t *ids;  // selected blocks [rows, sel_heads, k]; NULL: the request's own pages in order
+    const int32_t *ids;  // selected blocks [rows, sel_heads, k]
     uint16_t *out;
-    float *lse;   // optional
-    float *mass;  // optional, with ids only: [rows, kv heads, k]
+    float *part;  // OWN: in place of out, fp32 [rows, heads, 128]
+    float *lse;   // optional; OWN: required, in log2 units
+    float *mass;  // optional: [rows, kv heads, k]
     uint32_t *fault;
     int64_t q_stride;  // elements between query rows
     int64_t bt_stride;
     int64_t num_pages;
     int batch, q_len, kv_heads, sel_heads, group, k, seq_limit;
-    int unit_rows;  // query rows of a unit: group, or q_len * group
-    int row_tiles;  // tiles of kAttnMaxRows rows a unit's rows are cut into
-    const int32_t *prefix_table;  // own pages only: pages that every request reads before its own
-    const int32_t *prefix_len;    // their tokens (one int32)
-    PrefixParts parts;            // own pages only: or the parts that prefix_attn_kernel made (o != NULL)
+    int row_tiles;  // OWN: tiles of kAttnMaxRows rows that a request's q_len * group are cut into
     float scale_log2;
 };
 
 template <class F>
 struct BlockAttnSmem {
     uint64_t full[F::kStages], empty[F::kStages];
-    int meta[F::kStages];         // first token of the tile's page, or -1: a page that is skipped
-    int meta_all[F::kStages];     // a prefix page's tokens, which every row sees; -1: a page of the request
-    int list_page[MSA_MAX_TOPK];  // with ids: this CTA's valid selected blocks in slot order
+    int own_base[F::kStages];     // OWN: first token of the tile's page, or -1: a page that is skipped
+    int list_page[MSA_MAX_TOPK];  // this CTA's valid selected blocks in slot order
     int list_base[MSA_MAX_TOPK];
     int list_slot[MSA_MAX_TOPK];
     int count;                    // pages this CTA walks
@@ -130,7 +88,6 @@ struct BlockAttnSmem {
     float cm[kAttnMaxRows], cl[kAttnMaxRows];      // the CTA's rows, read by the whole cluster
     float rm[kAttnMaxRows], rinv[kAttnMaxRows];    // final maximum and 1 / sum
     float fac[8][kAttnMaxRows];                    // what each rank's part of a row is multiplied by
-    int part_ctas[2][2];  // prefix parts: first CTA and one past the last, of the first row's tile and of the next
 };
 
 // Mass scratch: [page of this CTA][slice * rows] of (sum, maximum at that time); 64 entries a page.
@@ -212,7 +169,8 @@ __device__ __forceinline__ float bf16_lo(uint32_t v) { return __uint_as_float(v 
 __device__ __forceinline__ float bf16_hi(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
 
 // MT: 16-row tiles of a unit (the four warps are MT tiles x 4 / MT slices of a
-// page's tokens).  OWN: the list is the request's own pages.
+// page's tokens).  A unit is (query row, KV head) with its group's rows, or, OWN,
+// (request, row tile, KV head) with the rows of all positions.
 template <class F, int MT, bool OWN>
 __global__ void __launch_bounds__(kAttnThreads, 2) block_attn_kernel(const __grid_constant__ BlockAttnParams p)
 {
@@ -227,30 +185,31 @@ __global__ void __launch_bounds__(kAttnThreads, 2) block_attn_kernel(const __gri
     float2 *mass_part = reinterpret_cast<float2 *>(ctl + 1);
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (OWN)
+        griddep_launch_dependents();  // the join may take its place; it waits for this grid's end
     const int S = static_cast<int>(cluster_nctarank()), crank = static_cast<int>(cluster_ctarank());
-    int unit = static_cast<int>(blockIdx.x) / S;
-    const int h = unit % p.kv_heads;
-    unit /= p.kv_heads;
-    const int rt = unit % p.row_tiles;
-    const int owner = unit / p.row_tiles;  // with ids: the query row; own pages: the request
-    const int b = OWN ? owner : owner / p.q_len;
-    const int row0 = rt * kAttnMaxRows;
-    const int rows = min(p.unit_rows - row0, kAttnMaxRows);
+    const int unit = static_cast<int>(blockIdx.x) / S;
+    const int h = unit % p.kv_heads, owner = unit / p.kv_heads;  // KV head; query row, or request and row tile
+    const int b = owner / (OWN ? p.row_tiles : p.q_len);
+    const int row0 = OWN ? owner % p.row_tiles * kAttnMaxRows : 0;
+    const int rows = OWN ? min(p.q_len * p.group - row0, kAttnMaxRows) : p.group;
+    // row n of the unit: its position in the request, and its place among [query rows, query heads]
+    auto position = [&](int n) { return OWN ? (row0 + n) / p.group : owner % p.q_len; };
+    auto place = [&](int n) {
+        const int64_t q = OWN ? static_cast<int64_t>(b) * p.q_len + (row0 + n) / p.group : owner;
+        return (q * p.kv_heads + h) * p.group + (OWN ? (row0 + n) % p.group : n);
+    };
 
     const int L = p.seq_lens[b];
+    // a lane's selected block, asked for together with the length
+    const int sel_id = !OWN && warp == kAttnWarps && lane < p.k
+                           ? p.ids[(static_cast<int64_t>(owner) * p.sel_heads + h / (p.kv_heads / p.sel_heads)) * p.k + lane]
+                           : -1;
     const bool bad_len = L < 0 || L > p.seq_limit;
     if (tid == 0 && bad_len)
         atomicOr(p.fault, MSA_FAULT_SEQ_LEN);
-    const int len = bad_len ? 0 : L;  // every position's tokens are below it
-    int prefix = 0;
-    if (OWN && p.prefix_table) {
-        prefix = prefix_tokens(p.parts, p.prefix_len);
-        if (prefix == 0 && *p.prefix_len != 0 && tid == 0)
-            atomicOr(p.fault, MSA_FAULT_SEQ_LEN);
-    }
-    const int prefix_pages = (prefix + kPage - 1) / kPage;
-    // tokens position i sees, of its own
-    auto visible = [&](int i) { return max(0, len - (p.q_len - 1 - i)); };
+    const int len = bad_len ? 0 : L;  // the request's tokens: what lies past them is no data
+    auto visible = [&](int i) { return max(0, len - (p.q_len - 1 - i)); };  // tokens position i sees
 
     if (tid == 0) {
         for (int s = 0; s < F::kStages; ++s) {
@@ -262,16 +221,13 @@ __global__ void __launch_bounds__(kAttnThreads, 2) block_attn_kernel(const __gri
     }
     if (warp == kAttnWarps) {
         if (OWN) {
-            const int nb = prefix_pages + (len + kPage - 1) / kPage;
+            const int nb = (len + kPage - 1) / kPage;
             if (lane == 0)
                 ctl->count = nb > crank ? (nb - crank + S - 1) / S : 0;
         } else {
-            const int mine = visible(owner % p.q_len);
-            const int nb = (mine + kPage - 1) / kPage;
-            const int sel = h / (p.kv_heads / p.sel_heads);
-            int id = -1, page = -1;
-            if (lane < p.k)
-                id = p.ids[(static_cast<int64_t>(owner) * p.sel_heads + sel) * p.k + lane];
+            const int nb = (visible(position(0)) + kPage - 1) / kPage;
+            const int id = sel_id;
+            int page = -1;
             bool ok = id >= 0;
             if (ok && id >= nb) {
                 ok = false;
@@ -304,33 +260,26 @@ __global__ void __launch_bounds__(kAttnThreads, 2) block_attn_kernel(const __gri
 
     if (warp == kAttnWarps) {
         // ---- producer: K and V tile of each page, one stage each ----
-        int pages = 0;  // own pages: a lane's share of the next 32 block-table entries
         bool alive = true;
         uint32_t it = 0;
+        int pages = -1;
         for (int i = 0; i < count && alive; ++i) {
-            int page, base, all = -1;
+            int page;
             if (OWN) {
-                if ((i & 31) == 0) {
-                    const int j = crank + (i + lane) * S;
+                if ((i & 31) == 0) {  // a lane's share of the next 32 pages
                     pages = -1;
                     if (i + lane < count)
-                        pages = j < prefix_pages
-                                    ? p.prefix_table[j]
-                                    : p.block_table[static_cast<int64_t>(b) * p.bt_stride + j - prefix_pages];
+                        pages = p.block_table[static_cast<int64_t>(b) * p.bt_stride + crank + (i + lane) * S];
                     if (i + lane < count && (pages < 0 || pages >= p.num_pages)) {
                         pages = -1;
                         atomicOr(p.fault, MSA_FAULT_PAGE_ID);
                     }
                 }
                 page = __shfl_sync(0xffffffffu, pages, i & 31);
-                const int j = crank + i * S;
-                all = j < prefix_pages ? prefix - j * kPage : -1;
-                base = page < 0 ? -1 : all >= 0 ? 0 : (j - prefix_pages) * kPage;
             } else {
                 page = ctl->list_page[i];
-                base = ctl->list_base[i];
             }
-            for (int kv = 0; kv < 2 && alive; ++kv, ++it) {
+            for (int kv = 0; kv < 2; ++kv, ++it) {
                 const int s = static_cast<int>(it % F::kStages);
                 const uint32_t bar = smem_addr(&ctl->full[s]);
                 if (it >= F::kStages)
@@ -338,25 +287,23 @@ __global__ void __launch_bounds__(kAttnThreads, 2) block_attn_kernel(const __gri
                 if (!alive)
                     break;
                 if (lane == 0) {
-                    ctl->meta[s] = base;
-                    if (OWN)
-                        ctl->meta_all[s] = all;
-                    if (base < 0) {
-                        mbar_arrive(bar);
-                    } else {
-                        const CUtensorMap *map = kv ? &p.vmap : &p.kmap;
-                        const uint32_t dst = smem_addr(smem) + s * kStageBytes;
-                        mbar_arrive_expect_tx(bar, F::kTileBytes + F::kScaleBytes);
-                        if (F::kFp8) {
-                            tma_load_4d(dst, map, 0, 0, h, page, bar);
-                            bulk_load(smem_addr(scales + s * kPage),
-                                      (kv ? p.vscale : p.kscale) + (static_cast<int64_t>(page) * p.kv_heads + h) * kPage,
-                                      F::kScaleBytes, bar);
-                        } else {
-                            tma_load_4d(dst, map, 0, 0, h, page, bar);
-                            tma_load_4d(dst + kHalfPageBytes, map, 64, 0, h, page, bar);
+                    if (OWN) {
+                        ctl->own_base[s] = page < 0 ? -1 : (crank + i * S) * kPage;
+                        if (page < 0) {
+                            mbar_arrive(bar);
+                            continue;
                         }
                     }
+                    const CUtensorMap *map = kv ? &p.vmap : &p.kmap;
+                    const uint32_t dst = smem_addr(smem) + s * kStageBytes;
+                    mbar_arrive_expect_tx(bar, F::kTileBytes + F::kScaleBytes);
+                    tma_load_4d(dst, map, 0, 0, h, page, bar);
+                    if (F::kFp8)
+                        bulk_load(smem_addr(scales + s * kPage),
+                                  (kv ? p.vscale : p.kscale) + (static_cast<int64_t>(page) * p.kv_heads + h) * kPage,
+                                  F::kScaleBytes, bar);
+                    else
+                        tma_load_4d(dst + kHalfPageBytes, map, 64, 0, h, page, bar);
                 }
             }
         }
@@ -370,18 +317,16 @@ __global__ void __launch_bounds__(kAttnThreads, 2) block_attn_kernel(const __gri
         // query fragments of rows g and g + 8, zero past the unit's rows
         uint32_t qa[8][4];
         float undo0 = 1.0f, undo1 = 1.0f;
-        int lim0, lim1;  // tokens the two rows see
+        int sees0, sees1;  // tokens the two rows see
         {
             float am0 = 0.0f, am1 = 0.0f;
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
                 const int n = mt * 16 + g + 8 * r;
                 const bool have = n < rows;
-                const int i = OWN ? (row0 + n) / p.group : owner % p.q_len;
-                const int head = OWN ? (row0 + n) % p.group : row0 + n;
-                const int64_t qr = OWN ? static_cast<int64_t>(owner) * p.q_len + i : owner;
-                (r ? lim1 : lim0) = have ? visible(i) : 0;
-                const uint16_t *src = p.q + qr * p.q_stride + (h * p.group + head) * kDim;
+                (r ? sees1 : sees0) = have ? visible(position(n)) : 0;
+                const int64_t qr = OWN ? static_cast<int64_t>(b) * p.q_len + position(n) : owner;
+                const uint16_t *src = p.q + qr * p.q_stride + (h * p.group + (OWN ? (row0 + n) % p.group : n)) * kDim;
 #pragma unroll
                 for (int ks = 0; ks < 8; ++ks) {
                     // bf16: columns 2t, 2t+1 and 2t+8, 2t+9 of each 16; E4M3: 4t .. 4t+3, as the codes' bytes lie
@@ -411,14 +356,6 @@ __global__ void __launch_bounds__(kAttnThreads, 2) block_attn_kernel(const __gri
                     }
             }
         }
-        if (OWN && p.parts.o && tid < 2) {  // while the first tile is on its way: which CTAs made the prefix's parts
-            const PrefixSplit ps(p.parts, prefix_tokens(p.parts, p.prefix_len), p.parts.grid);
-            const int tile = (owner * p.unit_rows + row0) / p.parts.tile_rows + tid;
-            const int64_t u = static_cast<int64_t>(h) * p.parts.head_tiles + tile;
-            const bool some = ps.total > 0 && tile < p.parts.head_tiles;
-            ctl->part_ctas[tid][0] = some ? ps.owner(u * ps.pages) : 0;
-            ctl->part_ctas[tid][1] = some ? ps.owner((u + 1) * ps.pages - 1) + 1 : 0;
-        }
         float o[16][4];
 #pragma unroll
         for (int d = 0; d < 16; ++d)
@@ -435,17 +372,14 @@ __global__ void __launch_bounds__(kAttnThreads, 2) block_attn_kernel(const __gri
             alive = attn_wait(&ctl->abort_flag, p.fault, smem_addr(&ctl->full[s_k]), (it / F::kStages) & 1);
             if (!alive)
                 break;
-            const int base = ctl->meta[s_k];
-            const int all = OWN ? ctl->meta_all[s_k] : -1;
-            const int end0 = all >= 0 ? all : lim0 - base, end1 = all >= 0 ? all : lim1 - base;
-            const int vend = all >= 0 ? all : len - base;
+            const int base = OWN ? ctl->own_base[s_k] : ctl->list_base[i];
             float ps0 = 0.0f, ps1 = 0.0f;  // this page's weight, at the running maximum
             const uint32_t kt = smem_addr(smem) + s_k * kStageBytes, vt = smem_addr(smem) + s_v * kStageBytes;
             bool v_waited = false;
 #pragma unroll 1
             for (int ch = 0; ch < kChunks; ++ch) {
                 const int tok = slice * kSlice + ch * 32;  // first token of the chunk in the page
-                if (base < 0)
+                if (OWN && base < 0)
                     break;
                 // S = Q K^T: 16 rows x 32 tokens
                 float s[4][4];
@@ -490,7 +424,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2) block_attn_kernel(const __gri
                         s[f][3] *= sc.y * undo1;
                     }
                 }
-                const int left0 = end0 - tok, left1 = end1 - tok;  // visible tokens of the chunk
+                const int left0 = sees0 - base - tok, left1 = sees1 - base - tok;  // visible tokens of the chunk
                 if (min(left0, left1) < 32) {
 #pragma unroll
                     for (int f = 0; f < 4; ++f) {
@@ -541,7 +475,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2) block_attn_kernel(const __gri
                     if (!alive)
                         break;
                 }
-                const int vleft = vend - tok;  // tokens of the chunk that are data
+                const int vleft = len - base - tok;  // tokens of the chunk that are data
                 uint32_t pa[2][4];
                 if (!F::kFp8) {
 #pragma unroll
@@ -701,114 +635,34 @@ __global__ void __launch_bounds__(kAttnThreads, 2) block_attn_kernel(const __gri
             }
         }
         consumer_barrier();
-        // the prefix's parts of this request's rows: the cluster's CTAs take them in turn
-        const bool parts = OWN && p.parts.o;
-        if (parts)
-            griddep_wait();  // prefix_attn_kernel has ended
         float *co = wo + kAttnWarps * 16 * kAttnOStride;  // [rows][kAttnOStride]: the CTA's part
-        constexpr int kRowsAtOnce = 4;  // rows of a warp whose loads are in flight together
-        for (int n0 = warp; n0 < rows; n0 += kAttnWarps * kRowsAtOnce) {
-            const int col = lane * 4;
-            float M[kRowsAtOnce], sum[kRowsAtOnce], mine[kRowsAtOnce];
-            float4 acc[kRowsAtOnce];
-            int64_t slot[kRowsAtOnce];  // row of the first part that this CTA takes
-            int np[kRowsAtOnce], most = 0;
+        for (int n = warp; n < rows; n += kAttnWarps) {
+            const int col = lane * 4, w0 = n / 16, r = n % 16;
+            float M = -INFINITY, sum = 0.0f;
 #pragma unroll
-            for (int r = 0; r < kRowsAtOnce; ++r) {
-                const int n = min(n0 + kAttnWarps * r, rows - 1);
-                M[r] = -INFINITY;
-                sum[r] = 0.0f;
-                acc[r] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                np[r] = 0;
-                slot[r] = 0;
-                if (parts) {
-                    const int first = owner * p.unit_rows + row0, row = first + n;
-                    const int tile = row / p.parts.tile_rows, which = tile - first / p.parts.tile_rows;
-                    const int g0 = ctl->part_ctas[which][0], g1 = ctl->part_ctas[which][1];
-                    // part i of a row lies 256 / ways rows after part i - 1
-                    const int total = (g1 - g0) * p.parts.ways;
-                    np[r] = total > crank ? (total - crank + S - 1) / S : 0;
-                    slot[r] = (static_cast<int64_t>(g0) + h * p.parts.head_tiles + tile) * 256 +
-                              crank * (256 / p.parts.ways) + row % p.parts.tile_rows;
-                    most = max(most, np[r]);
-                }
+            for (int k = 0; k < KS; ++k)
+                M = fmaxf(M, ctl->wm[w0 + k * MT][r]);
+            float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-                for (int k = 0; k < KS; ++k)
-                    M[r] = fmaxf(M[r], ctl->wm[n / 16 + k * MT][n % 16]);
+            for (int k = 0; k < KS; ++k) {
+                const int w = w0 + k * MT;
+                const float f = rescale(ctl->wm[w][r], M);
+                const float4 v = *reinterpret_cast<const float4 *>(wo + (w * 16 + r) * kAttnOStride + col);
+                sum += f * ctl->wl[w][r];
+                acc.x += f * v.x;
+                acc.y += f * v.y;
+                acc.z += f * v.z;
+                acc.w += f * v.w;
             }
-            const int64_t step = static_cast<int64_t>(S) * (256 / p.parts.ways);  // rows to the CTA's next part
-            for (int i0 = 0; i0 < most; i0 += 32) {
-                // 32 parts at a time: a lane's part of each row, the maximum, the factors, then the vectors
-#pragma unroll
-                for (int r = 0; r < kRowsAtOnce; ++r)
-                    mine[r] = i0 + lane < np[r] ? __ldcg(p.parts.lse + slot[r] + (i0 + lane) * step) : -INFINITY;
-#pragma unroll
-                for (int r = 0; r < kRowsAtOnce; ++r) {
-                    if (mine[r] == INFINITY)
-                        ctl->abort_flag = 1;
-                    float top = mine[r];
-#pragma unroll
-                    for (int o = 16; o >= 1; o >>= 1)
-                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-                    const float to = fmaxf(M[r], top), f = rescale(M[r], to);
-                    sum[r] *= f;
-                    acc[r].x *= f;
-                    acc[r].y *= f;
-                    acc[r].z *= f;
-                    acc[r].w *= f;
-                    M[r] = to;
-                    mine[r] = mine[r] == -INFINITY ? 0.0f : rescale(mine[r], to);
-                }
-                const int end = min(32, most - i0);
-#pragma unroll 4
-                for (int i = 0; i < end; ++i) {
-                    float4 v[kRowsAtOnce];
-                    float f[kRowsAtOnce];
-#pragma unroll
-                    for (int r = 0; r < kRowsAtOnce; ++r) {
-                        f[r] = __shfl_sync(0xffffffffu, mine[r], i);
-                        // no branch, so that the loads of several parts go out together; what a part that holds nothing
-                        // has in its place may be anything
-                        v[r] = __ldcg(reinterpret_cast<const float4 *>(
-                            p.parts.o + (slot[r] + (f[r] != 0.0f ? (i0 + i) * step : 0)) * kDim + col));
-                    }
-#pragma unroll
-                    for (int r = 0; r < kRowsAtOnce; ++r) {
-                        const bool some = f[r] != 0.0f;
-                        sum[r] += f[r];
-                        acc[r].x += some ? f[r] * v[r].x : 0.0f;
-                        acc[r].y += some ? f[r] * v[r].y : 0.0f;
-                        acc[r].z += some ? f[r] * v[r].z : 0.0f;
-                        acc[r].w += some ? f[r] * v[r].w : 0.0f;
-                    }
-                }
+            if (ctl->abort_flag) {  // a part that is not whole
+                acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                M = -INFINITY;
+                sum = 0.0f;
             }
-#pragma unroll
-            for (int r = 0; r < kRowsAtOnce; ++r) {
-                const int n = n0 + kAttnWarps * r;
-                if (n >= rows)
-                    break;
-#pragma unroll
-                for (int k = 0; k < KS; ++k) {
-                    const int w = n / 16 + k * MT, i = n % 16;
-                    const float f = rescale(ctl->wm[w][i], M[r]);
-                    const float4 v = *reinterpret_cast<const float4 *>(wo + (w * 16 + i) * kAttnOStride + col);
-                    sum[r] += f * ctl->wl[w][i];
-                    acc[r].x += f * v.x;
-                    acc[r].y += f * v.y;
-                    acc[r].z += f * v.z;
-                    acc[r].w += f * v.w;
-                }
-                if (ctl->abort_flag) {  // a part that is not whole
-                    acc[r] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                    M[r] = -INFINITY;
-                    sum[r] = 0.0f;
-                }
-                *reinterpret_cast<float4 *>(co + n * kAttnOStride + col) = acc[r];
-                if (lane == 0) {
-                    ctl->cm[n] = M[r];
-                    ctl->cl[n] = sum[r];
-                }
+            *reinterpret_cast<float4 *>(co + n * kAttnOStride + col) = acc;
+            if (lane == 0) {
+                ctl->cm[n] = M;
+                ctl->cl[n] = sum;
             }
         }
     }
@@ -849,10 +703,10 @@ __global__ void __launch_bounds__(kAttnThreads, 2) block_attn_kernel(const __gri
                 sum = 0.0f;
             ctl->rm[tid] = M;
             ctl->rinv[tid] = sum == 0.0f ? 0.0f : 1.0f / sum;
-            if (p.lse && crank == 0) {
-                const int i = OWN ? (row0 + tid) / p.group : 0, head = OWN ? (row0 + tid) % p.group : row0 + tid;
-                const int64_t qr = OWN ? static_cast<int64_t>(owner) * p.q_len + i : owner;
-                p.lse[(qr * p.kv_heads + h) * p.group + head] = sum == 0.0f ? -INFINITY : (M + log2f(sum)) * kLn2;
+            if ((OWN || p.lse) && crank == 0) {
+                // OWN: +inf marks a part that is not whole
+                const float e = sum == 0.0f ? -INFINITY : M + log2f(sum);
+                p.lse[place(tid)] = OWN ? (gave_up ? INFINITY : e) : e * kLn2;
             }
         }
         consumer_barrier();
@@ -875,12 +729,16 @@ __global__ void __launch_bounds__(kAttnThreads, 2) block_attn_kernel(const __gri
                 }
             const float inv = ctl->rinv[n];
             const bool none = inv == 0.0f;  // nothing visible: zeros
-            const int i = OWN ? (row0 + n) / p.group : 0, head = OWN ? (row0 + n) % p.group : row0 + n;
-            const int64_t qr = OWN ? static_cast<int64_t>(owner) * p.q_len + i : owner;
+            if (OWN) {
+                *reinterpret_cast<float4 *>(p.part + place(n) * kDim + lane * 4) =
+                    make_float4(none ? 0.0f : acc.x * inv, none ? 0.0f : acc.y * inv, none ? 0.0f : acc.z * inv,
+                                none ? 0.0f : acc.w * inv);
+                continue;
+            }
             uint2 w;
             w.x = none ? 0u : f32x2_to_bf16x2(acc.x * inv, acc.y * inv);
             w.y = none ? 0u : f32x2_to_bf16x2(acc.z * inv, acc.w * inv);
-            *reinterpret_cast<uint2 *>(p.out + ((qr * p.kv_heads + h) * p.group + head) * kDim + lane * 4) = w;
+            *reinterpret_cast<uint2 *>(p.out + place(n) * kDim + lane * 4) = w;
         }
         if (!OWN && p.mass) {
             // a block's mass: its 64 (slice, row) sums, moved to their rows' final maximum and sum
@@ -901,6 +759,10 @@ __global__ void __launch_bounds__(kAttnThreads, 2) block_attn_kernel(const __gri
             }
         }
     }
+    // This grid runs beside prefix_attn_kernel and needs nothing of it, but must not complete before it: who waits for
+    // this grid reads the parts of both.
+    if (OWN && blockIdx.x == 0)
+        griddep_wait();
     __syncwarp();
     if (S > 1)
         cluster_sync_all();  // no CTA ends while another reads its shared memory

@@ -3,27 +3,35 @@
 //
 // The rows of one KV head (batch * q_len * group of them) read the same keys, so
 // they stand side by side as the M rows of S = Q K^T and O = P V.  A unit is
-// (KV head, tile of 256 rows); the prefix's pages of all units, one after the
-// other, are cut into one equal range a CTA, and a range's part of a unit goes
-// to the workspace as (O / L, M + log2 L) in fp32; the kernel that walks each
-// request's own pages joins the parts (block_attn.cuh), always in page order.
+// (KV head, tile of 256 rows), or of 128 where there are not more; the prefix's
+// pages of all units, one after the other, are cut into one equal range a CTA, and
+// a range's part of a unit goes to the workspace as (O / L, M + log2 L) in fp32.
+// block_attn_kernel makes one more part of each request's own pages, and
+// join_kernel adds a row's parts up, always in page order.
+//
+// The prefix is bound by the tensor cores and the softmax, own pages by the cache
+// stream.  So the two run side by side: this kernel takes as many SMs as its share
+// of the work by the live lengths (its other CTAs end at once), and the own pages'
+// CTAs, launched as its dependents, start on the rest and follow as its CTAs end.
+// (One after the other: 125 us for 64 requests over 32768 + 147000 tokens; own
+// pages as further units of this kernel: 193 us, a few microseconds of latency for
+// each of their short runs.)
 //
 // Per page and 128-row tile: S (128 x 128, fp32) in tensor memory; a warpgroup
 // with one thread a row takes the row's maximum, 2^(c s - m) and the sum, and
 // writes the weights as bf16 over S; the second product reads them from there
 // (A in tensor memory, V's page from shared memory with the dims contiguous:
-// the B operand's transposed form).  Two tiles alternate, so that one is in the
-// tensor cores while the other is in its softmax.  The reference m of a row is
-// only moved (and O, L rescaled) when the maximum outgrows it by more than 2^8:
-// weights then stay at most 2^8, which costs no precision in fp32 sums and bf16
-// operands, and the rescaling of O in tensor memory becomes rare.
+// the B operand's transposed form).  The reference m of a row is only moved (and
+// O, L rescaled) when the maximum outgrows it by more than 2^8: weights then stay
+// at most 2^8, which costs no precision in fp32 sums and bf16 operands, and the
+// rescaling of O in tensor memory becomes rare.
 //
-// The time of a tile's page is its chain, scores (512 cycles) -> softmax (1360) ->
-// product (512), with a barrier between each; two chains run side by side, each
-// with an MMA thread of its own, so that one thread's waits pass while the other's
-// MMAs run (one thread for both tiles: 5000 cycles a page, the tensor pipe a third
-// busy).  Where a KV head has at most 128 rows, the two chains are the even and the
-// odd pages of one tile, and a range leaves two parts.
+// The time of a tile's page is its chain, scores (512 cycles) -> softmax (1000 to
+// 1400) -> product (512), with a barrier between each.  Two chains run side by
+// side, each with an MMA warp of its own, and take turns at the tensor cores: the
+// two tiles of 256 rows, or the even and the odd pages of one tile, whose range
+// then leaves two parts.  2700 cycles a page of 256 rows, 3/4 of the MMA rate; one
+// issuing thread for both took 5000, two without turns 5000 as well.
 #pragma once
 
 #include "block_attn.cuh"
@@ -35,16 +43,83 @@ constexpr int kPrefixThreads = 352;  // two softmax warpgroups, a TMA warp, two 
 constexpr int kPrefixMaxGrid = 256;
 constexpr float kPrefixLag = 8.0f;
 
+// Where the parts lie.  Unit u = head * head_tiles + tile; the units' pages stand
+// one after the other, u * pages + j, and CTA g of the `ctas` that take part covers
+// [start(g), start(g + 1)); what it has of unit u is in slot g + u (unique: both
+// grow along the sequence).  A slot holds two blocks of 128 rows: the halves of a
+// tile of 256 rows (ways = 1), or two parts of a tile of 128 (ways = 2).
+struct PrefixParts {
+    float *o, *lse;          // [slot][2][128] rows, lse in log2 units; -inf: nothing (o is not written), +inf: not whole
+    float *own_o, *own_lse;  // [query rows, heads]: the part of a row's own pages
+    int batch, q_len, group, kv_heads;
+    int rows;  // rows of a KV head: batch * q_len * group
+    int tile_rows, ways, head_tiles, units;
+    int own_tiles;         // times that own pages are read
+    int limit, seq_limit;  // bounds on the prefix's and a request's tokens
+    int grid;              // CTAs prefix_attn_kernel is launched with
+};
+
+__device__ __forceinline__ int tokens_in(int n, int limit) { return n < 0 || n > limit ? 0 : n; }
+__device__ __forceinline__ int pages_of(int tokens) { return (tokens + kPage - 1) / kPage; }
+
+constexpr int kPrefixMinPages = 2;  // pages a CTA's range should have at least
+
+struct PrefixSplit {
+    int pages, ctas;
+    int64_t total;
+    // own: the batch's own pages.  A page of a 256-row tile takes an SM 2700 cycles, of a 128-row tile half of that;
+    // an own page of one head (64 KiB) about 1300 where the rest of the GPU leaves the SM its bandwidth.  (64 requests
+    // over 32768 + 147000 tokens: 98 us; with own pages at half that weight 119, at twice 127.)
+    __device__ PrefixSplit(const PrefixParts &p, int prefix, int64_t own)
+    {
+        pages = pages_of(prefix);
+        total = static_cast<int64_t>(pages) * p.units;
+        const int64_t mine = total * 2 / p.ways, theirs = own * p.own_tiles * p.kv_heads;
+        int most = p.grid;
+        if (mine > 0)
+            most = max(1, static_cast<int>((static_cast<int64_t>(p.grid) * mine + (mine + theirs) / 2) / (mine + theirs)));
+        ctas = static_cast<int>(min(static_cast<int64_t>(most), (total + kPrefixMinPages - 1) / kPrefixMinPages));
+        // the same number of CTAs for every unit where that leaves few out: no range then ends in a second unit, and
+        // the tiles of a head walk the same pages at the same time, from L2 but for the first
+        const int even = ctas / p.units * p.units;
+        if (even * 8 >= ctas * 7)
+            ctas = even;
+    }
+    __device__ int64_t start(int g) const { return g * total / ctas; }
+    // the CTA whose range holds page x of the sequence
+    __device__ int owner(int64_t x) const { return static_cast<int>(((x + 1) * ctas - 1) / total); }
+};
+
 struct PrefixAttnParams {
     CUtensorMap kmap, vmap;
     const uint16_t *q;
     const int32_t *prefix_table;
     const int32_t *prefix_len;
+    const int32_t *seq_lens;
     PrefixParts parts;
     uint32_t *fault;
     int64_t q_stride, num_pages;
     float scale_log2;
 };
+
+// The batch's own pages, added up by a whole block (every thread gets the sum).
+// `sums`: shared, one entry a warp.
+template <int THREADS>
+__device__ __forceinline__ int64_t own_pages(const int32_t *seq_lens, int batch, int limit, int *sums)
+{
+    const int tid = threadIdx.x;
+    int n = 0;
+    for (int b = tid; b < batch; b += THREADS)
+        n += pages_of(tokens_in(seq_lens[b], limit));
+    n = __reduce_add_sync(0xffffffffu, n);
+    if ((tid & 31) == 0)
+        sums[tid >> 5] = n;
+    __syncthreads();
+    int64_t all = 0;
+    for (int w = 0; w < THREADS / 32; ++w)
+        all += sums[w];
+    return all;
+}
 
 struct PrefixSmem {
     uint64_t kv_full[kPrefixStages], kv_empty[kPrefixStages];
@@ -52,11 +127,12 @@ struct PrefixSmem {
     uint64_t p_half[2], p_full[2];  // the first 64 weights of each row and the turn to issue; all weights
     uint64_t o_done[2];
     uint64_t drained[2];
+    int warp_sums[12];
     uint32_t tmem;
     int abort_flag;
 };
 
-constexpr size_t kPrefixSmemBytes = 1024 + 2 * kPageBytes + kPrefixStages * kPageBytes + sizeof(PrefixSmem);
+constexpr size_t kPrefixSmemBytes = 1024 + (2 + kPrefixStages) * kPageBytes + sizeof(PrefixSmem);
 
 // The MMA warps run their whole loop converged, with one elected lane behind a
 // predicate: descriptors and addresses are then the warp's, not a thread's, and an
@@ -283,16 +359,16 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_attn_kernel(const __
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // the same in all lanes, and known to be
 
     griddep_launch_dependents();
-    const int prefix = __shfl_sync(0xffffffffu, prefix_tokens(p.parts, p.prefix_len), 0);
-    const PrefixSplit split(p.parts, prefix, static_cast<int>(gridDim.x));
-    if (prefix == 0 && *p.prefix_len != 0 && blockIdx.x == 0 && tid == 0)
-        atomicOr(p.fault, MSA_FAULT_SEQ_LEN);
     const int cta = blockIdx.x;
+    const int prefix = __shfl_sync(0xffffffffu, tokens_in(*p.prefix_len, p.parts.limit), 0);
+    if (cta == 0 && tid == 0 && prefix == 0 && *p.prefix_len != 0)
+        atomicOr(p.fault, MSA_FAULT_SEQ_LEN);
+    const PrefixSplit split(p.parts, prefix,
+                            own_pages<kPrefixThreads>(p.seq_lens, p.parts.batch, p.parts.seq_limit, ctl->warp_sums));
     if (cta >= split.ctas)
         return;
-    const int P = split.pages;
+    const int P = split.pages, ways = p.parts.ways;
     const int64_t lo = split.start(cta), hi = split.start(cta + 1);
-    const int ways = p.parts.ways;  // 1: two tiles, every page in both; 2: one tile, its pages in turn
 
     if (tid == 0) {
         for (int s = 0; s < kPrefixStages; ++s) {
@@ -374,12 +450,13 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_attn_kernel(const __
         bool alive = true;
         uint32_t it = 0, kp0 = 0;  // pages of this chain, pages of the CTA before the unit's
         for (int64_t x = lo; x < hi; ) {
-            const int u = static_cast<int>(x / P), j0 = static_cast<int>(x % P);
-            const int n = static_cast<int>(min(hi - x, static_cast<int64_t>(P - j0)));
+            const int u = static_cast<int>(x / P), page0 = static_cast<int>(x % P);
+            const int n = static_cast<int>(min(hi - x, static_cast<int64_t>(P - page0)));
             x += n;
             const int h = u / p.parts.head_tiles;
             const int nrow = (u % p.parts.head_tiles) * p.parts.tile_rows + (ways == 1 ? t * 128 : 0) + row;
             const bool have = nrow < p.parts.rows;
+            const bool some_row = __any_sync(0xffffffffu, have);  // a warp without rows only keeps the barriers going
             {
                 const uint16_t *src = p.q + static_cast<int64_t>(nrow / p.parts.group) * p.q_stride +
                                       (h * p.parts.group + nrow % p.parts.group) * kDim;
@@ -397,16 +474,22 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_attn_kernel(const __
             mbar_arrive(smem_addr(&ctl->q_full[t]));
             float m = -INFINITY, l = 0.0f;
             const int first = ways == 2 ? t : 0;
-            int page = first < n ? p.prefix_table[j0 + first] : 0;
+            int page = first < n ? p.prefix_table[page0 + first] : 0;
             for (int j = first; j < n && alive; j += ways, ++it) {
                 // tokens of the page that count
-                const int valid = page < 0 || page >= p.num_pages ? 0 : min(kPage, prefix - (j0 + j) * kPage);
+                const int valid = page < 0 || page >= p.num_pages ? 0 : min(kPage, prefix - (page0 + j) * kPage);
                 if (j + ways < n)
-                    page = p.prefix_table[j0 + j + ways];
+                    page = p.prefix_table[page0 + j + ways];
                 alive = attn_wait(&ctl->abort_flag, p.fault, smem_addr(&ctl->s_full[t]), it & 1);
                 if (!alive)
                     break;
                 tc_fence_after_sync();
+                if (!some_row && valid == kPage) {
+                    tc_fence_before_sync();
+                    mbar_arrive(smem_addr(&ctl->p_half[t]));
+                    mbar_arrive(smem_addr(&ctl->p_full[t]));
+                    continue;
+                }
                 uint32_t s[4][32];
 #pragma unroll
                 for (int q = 0; q < 4; ++q)
@@ -500,15 +583,19 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_attn_kernel(const __
                 alive = attn_wait(&ctl->abort_flag, p.fault, smem_addr(&ctl->o_done[t]), (it - 1) & 1);
             tc_fence_after_sync();
             kp0 += n;
-            // 128 rows in a row of slots: chain t of a unit with two tiles holds its rows t * 128 .., of one with one tile its part t
-            const int64_t block = (static_cast<int64_t>(cta) + u) * 2 + t;
+            // chain t's block of the slot: its rows of a tile of 256, or its part of the one tile
+            const int64_t block = ((static_cast<int64_t>(cta) + u) * 2 + t) * 128;
             const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-            if (alive && some) {
-                // through the tile's Q (every product with it is done), 64 dims at a time, each warp its 32 rows:
-                // a thread holds a row, a store of a warp should cover whole lines
-                float *part = p.parts.o + (block * 128 + (row & ~31)) * kDim;
-                uint8_t *turn = smem + t * kPageBytes + (row & ~31) * 256;
-                const int left = p.parts.rows - (nrow & ~31);  // rows of the warp that exist
+            if (alive && some && some_row) {
+                // through the warp's own rows of the tile's Q (every product with it is done; the other warps may be
+                // loading theirs for the next run), 64 dims at a time: a thread holds a row, a store of a warp should
+                // cover whole lines
+                float *part = p.parts.o + (block + (row & ~31)) * kDim;
+                uint8_t *turn = smem + t * kPageBytes + (row & ~31) * 128;
+                auto chunk = [&](int r, int c) {  // 16 bytes c of 16 of row r of the warp
+                    return reinterpret_cast<float4 *>(turn + (c >> 3) * kHalfPageBytes + r * 128 + (((c ^ r) & 7) << 4));
+                };
+                const int left = p.parts.rows - (nrow - lane);  // rows of the warp that exist
 #pragma unroll 1
                 for (int half = 0; half < 2; ++half) {
                     __syncwarp();
@@ -519,7 +606,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_attn_kernel(const __
                         tmem_wait_ld(o);
 #pragma unroll
                         for (int i = 0; i < 32; i += 4)
-                            *reinterpret_cast<float4 *>(turn + lane * 256 + (((q * 8 + i / 4) ^ (lane & 7)) << 4)) =
+                            *chunk(lane, q * 8 + i / 4) =
                                 make_float4(__uint_as_float(o[i]) * inv, __uint_as_float(o[i + 1]) * inv,
                                             __uint_as_float(o[i + 2]) * inv, __uint_as_float(o[i + 3]) * inv);
                     }
@@ -528,19 +615,136 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_attn_kernel(const __
                     for (int r = lane >> 4; r < 32; r += 2)
                         if (r < left)
                             *reinterpret_cast<float4 *>(part + r * kDim + half * 64 + (lane & 15) * 4) =
-                                *reinterpret_cast<const float4 *>(turn + r * 256 + (((lane & 15) ^ (r & 7)) << 4));
+                                *chunk(r, lane & 15);
                 }
                 __syncwarp();
             }
             // +inf marks a part that is not whole
-            p.parts.lse[block * 128 + row] =
-                !alive ? INFINITY : l == 0.0f ? -INFINITY : m + log2f(l);
+            if (have)
+                p.parts.lse[block + row] =
+                    !alive ? INFINITY : l == 0.0f ? -INFINITY : m + log2f(l);
         }
         tc_fence_before_sync();
     }
     __syncthreads();
     if (warp == 9)
         tmem_dealloc(tmem, 512);
+}
+
+// ---------------------------------------------------------------------------
+// out = sum 2^(e - M) o / sum 2^(e - M) over a row's parts (o, e), prefix first,
+// then own.  WPR warps a row take the parts in turn; each has the numbers of 32
+// parts in its lanes and asks for several vectors at once.  Bound by those reads
+// (L2): 4096 rows with 8 parts, 17 MB.
+struct JoinParams {
+    PrefixParts parts;
+    const int32_t *prefix_len;
+    const int32_t *seq_lens;
+    uint16_t *out;
+    float *lse;
+};
+
+constexpr int kJoinWarps = 8;
+
+template <int WPR>
+__global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_constant__ JoinParams p)
+{
+    constexpr int kRows = kJoinWarps / WPR;  // rows of a block
+    __shared__ float4 s_acc[kJoinWarps][32];
+    __shared__ float s_m[kJoinWarps], s_sum[kJoinWarps];
+    __shared__ int s_bad[kJoinWarps];
+    const PrefixParts &a = p.parts;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, sub = warp % WPR;
+    const int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + warp / WPR;  // (query row, KV head, head of the group)
+    const bool exists = row < static_cast<int64_t>(a.rows) * a.kv_heads;
+    const int g = static_cast<int>(row % a.group), h = static_cast<int>(row / a.group % a.kv_heads);
+    const int query = static_cast<int>(row / a.group / a.kv_heads);
+    const int n = query * a.group + g;
+    const PrefixSplit split(a, tokens_in(*p.prefix_len, a.limit),
+                            own_pages<32 * kJoinWarps>(p.seq_lens, a.batch, a.seq_limit, s_bad));
+    __syncthreads();
+    const float *o[2] = {a.o, a.own_o}, *e[2] = {a.lse, a.own_lse};
+    int64_t first[2] = {0, 0};  // row of the first part
+    const int step[2] = {256 / a.ways, 0};
+    int count[2] = {0, exists ? 1 : 0};
+    if (exists && split.pages > 0) {
+        const int64_t u = static_cast<int64_t>(h) * a.head_tiles + n / a.tile_rows;
+        const int g0 = split.owner(u * split.pages), g1 = split.owner((u + 1) * split.pages - 1) + 1;
+        count[0] = (g1 - g0) * a.ways;
+        first[0] = (g0 + u) * 256 + n % a.tile_rows;
+    }
+    first[1] = exists ? (static_cast<int64_t>(query) * a.kv_heads + h) * a.group + g : 0;
+    griddep_wait();  // both kernels have ended
+    float M = -INFINITY, sum = 0.0f;
+    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    bool bad = false;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const int mine = count[k] > sub ? (count[k] - sub + WPR - 1) / WPR : 0;
+        for (int i0 = 0; i0 < mine; i0 += 32) {
+            const int end = min(32, mine - i0);
+            const int64_t at = first[k] + static_cast<int64_t>(sub + i0 * WPR) * step[k];
+            const float x = lane < end ? __ldcg(e[k] + at + static_cast<int64_t>(lane * WPR) * step[k]) : -INFINITY;
+            bad |= __any_sync(0xffffffffu, x == INFINITY);
+            float to = fmaxf(M, x);
+#pragma unroll
+            for (int q = 16; q >= 1; q >>= 1)
+                to = fmaxf(to, __shfl_xor_sync(0xffffffffu, to, q));
+            const float old = rescale(M, to), f = x == -INFINITY ? 0.0f : rescale(x, to);
+            M = to;
+            sum *= old;
+            acc.x *= old;
+            acc.y *= old;
+            acc.z *= old;
+            acc.w *= old;
+#pragma unroll 8
+            for (int i = 0; i < end; ++i) {
+                const float fi = __shfl_sync(0xffffffffu, f, i);
+                // no branch, so that several loads go out together; what a part that holds nothing has there may be anything
+                const float4 v = __ldcg(reinterpret_cast<const float4 *>(o[k] + (at + static_cast<int64_t>(i * WPR) * step[k]) * kDim) + lane);
+                const bool some = fi != 0.0f;
+                sum += fi;
+                acc.x += some ? fi * v.x : 0.0f;
+                acc.y += some ? fi * v.y : 0.0f;
+                acc.z += some ? fi * v.z : 0.0f;
+                acc.w += some ? fi * v.w : 0.0f;
+            }
+        }
+    }
+    if (WPR > 1) {
+        s_acc[warp][lane] = acc;
+        if (lane == 0) {
+            s_m[warp] = M;
+            s_sum[warp] = sum;
+            s_bad[warp] = bad;
+        }
+        __syncthreads();
+        if (sub != 0)
+            return;
+#pragma unroll
+        for (int w = 1; w < WPR; ++w) {
+            const float m = s_m[warp + w], to = fmaxf(M, m), fa = rescale(M, to), fb = rescale(m, to);
+            const float4 v = s_acc[warp + w][lane];
+            sum = sum * fa + s_sum[warp + w] * fb;
+            acc.x = acc.x * fa + v.x * fb;
+            acc.y = acc.y * fa + v.y * fb;
+            acc.z = acc.z * fa + v.z * fb;
+            acc.w = acc.w * fa + v.w * fb;
+            M = to;
+            bad |= s_bad[warp + w] != 0;
+        }
+    }
+    if (!exists)
+        return;
+    const bool none = bad || sum == 0.0f;  // nothing visible, or a part that is not whole
+    const float inv = none ? 0.0f : 1.0f / sum;
+    const int64_t to = (static_cast<int64_t>(query) * a.kv_heads + h) * a.group + g;
+    uint2 w;
+    w.x = none ? 0u : f32x2_to_bf16x2(acc.x * inv, acc.y * inv);
+    w.y = none ? 0u : f32x2_to_bf16x2(acc.z * inv, acc.w * inv);
+    *reinterpret_cast<uint2 *>(p.out + to * kDim + lane * 4) = w;
+    if (p.lse && lane == 0)
+        p.lse[to] = none ? -INFINITY : (M + log2f(sum)) * kLn2;
 }
 
 }  // namespace msa
