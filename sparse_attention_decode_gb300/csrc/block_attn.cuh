@@ -375,7 +375,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2) block_attn_kernel(const __gri
             const int base = OWN ? ctl->own_base[s_k] : ctl->list_base[i];
             float ps0 = 0.0f, ps1 = 0.0f;  // this page's weight, at the running maximum
             const uint32_t kt = smem_addr(smem) + s_k * kStageBytes, vt = smem_addr(smem) + s_v * kStageBytes;
-            bool v_waited = false;
+            bool v_waited = false, k_held = true;
 #pragma unroll 1
             for (int ch = 0; ch < kChunks; ++ch) {
                 const int tok = slice * kSlice + ch * 32;  // first token of the chunk in the page
@@ -423,6 +423,12 @@ __global__ void __launch_bounds__(kAttnThreads, 2) block_attn_kernel(const __gri
                         s[f][2] *= sc.x * undo1;
                         s[f][3] *= sc.y * undo1;
                     }
+                }
+                if (ch == kChunks - 1) {  // K's tile is free for the next page while this one's weights are worked on
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(smem_addr(&ctl->empty[s_k]));
+                    k_held = false;
                 }
                 const int left0 = sees0 - base - tok, left1 = sees1 - base - tok;  // visible tokens of the chunk
                 if (min(left0, left1) < 32) {
@@ -582,7 +588,8 @@ __global__ void __launch_bounds__(kAttnThreads, 2) block_attn_kernel(const __gri
                 alive = attn_wait(&ctl->abort_flag, p.fault, smem_addr(&ctl->full[s_v]), ((it + 1) / F::kStages) & 1);
             __syncwarp();
             if (lane == 0) {
-                mbar_arrive(smem_addr(&ctl->empty[s_k]));
+                if (k_held)
+                    mbar_arrive(smem_addr(&ctl->empty[s_k]));
                 mbar_arrive(smem_addr(&ctl->empty[s_v]));
             }
             if (!OWN && p.mass) {

@@ -19,6 +19,7 @@ __global__ void __launch_bounds__(128) accumulate_kernel(float *weights, int64_t
                                                          int q_len, int kv_heads, int sel_heads, int topk,
                                                          uint32_t *fault)
 {
+    griddep_launch_dependents();  // an eviction that follows may take its place
     const int64_t w = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
     const int lane = threadIdx.x & 31;
     if (w >= static_cast<int64_t>(batch) * kv_heads)
@@ -140,6 +141,7 @@ __global__ void __launch_bounds__(T, 2) evict_kernel(const __grid_constant__ Evi
     __shared__ uint32_t s_prefix;
     __shared__ int s_want;
     const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    griddep_wait();  // the weights of a call to accumulate just before
     const int L = p.seq_lens[b];
     const bool bad = L < 0 || L > p.seq_limit;
     if (bad && tid == 0)
@@ -370,6 +372,8 @@ extern "C" msa_status msa_cache_evict(const int32_t *block_table, int64_t bt_str
                         : (vec ? evict_kernel<true, 256> : evict_kernel<false, 256>);
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
         return MSA_ERR_CUDA;
-    kernel<<<batch, wide ? 1024 : 256, smem, static_cast<cudaStream_t>(stream)>>>(p);
-    return cudaGetLastError() == cudaSuccess ? MSA_OK : MSA_ERR_CUDA;
+    cudaLaunchAttribute attr[1];
+    const cudaLaunchConfig_t cfg =
+        pdl_config(dim3(batch), dim3(wide ? 1024 : 256), smem, static_cast<cudaStream_t>(stream), attr);
+    return cudaLaunchKernelEx(&cfg, kernel, p) == cudaSuccess ? MSA_OK : MSA_ERR_CUDA;
 }
