@@ -132,10 +132,29 @@ __device__ __forceinline__ void consumer_barrier()
     asm volatile("bar.sync 1, %0;" ::"n"(32 * kAttnWarps) : "memory");
 }
 
+__device__ __forceinline__ bool mbar_test_wait(uint32_t bar, uint32_t parity)
+{
+    uint32_t done;
+    asm volatile(
+        "{\n"
+        "  .reg .pred p;\n"
+        "  mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+        "  selp.u32 %0, 1, 0, p;\n"
+        "}\n"
+        : "=r"(done)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return done != 0;
+}
+
 // Bounded wait of a whole warp; false, with the CTA's abort flag and the fault
-// bit set, when it ran out or another warp gave up before.
+// bit set, when it ran out or another warp gave up before.  A phase that is
+// complete already, the common case in a page loop that the cache stream does not
+// hold up, costs one test.
 __device__ __forceinline__ bool attn_wait(int *abort_flag, uint32_t *fault, uint32_t bar, uint32_t parity)
 {
+    if (__all_sync(0xffffffffu, mbar_test_wait(bar, parity)))
+        return true;
     bool ok = false;
     if (!*reinterpret_cast<volatile int *>(abort_flag)) {
         ok = mbar_wait(bar, parity);
@@ -363,7 +382,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2) block_attn_kernel(const __gri
             for (int e = 0; e < 4; ++e)
                 o[d][e] = 0.0f;
         float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.0f, l1 = 0.0f;
-        float vref = 0.0f;  // E4M3: o is held in units of vref, the largest V scale met so far
+        float vref = 0.0f, vinv = 0.0f;  // E4M3: o is held in units of vref, the largest V scale met so far; its inverse
 
         bool alive = true;
         uint32_t it = 0;
@@ -511,12 +530,12 @@ __global__ void __launch_bounds__(kAttnThreads, 2) block_attn_kernel(const __gri
                         a0 *= down;
                         a1 *= down;
                         vref = top;
+                        vinv = 1.0f / top;
                     }
-                    const float inv = vref > 0.0f ? 1.0f / vref : 0.0f;
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
-                        const float2 sa = make_float2(sc[2 * j].x * inv, sc[2 * j].y * inv);
-                        const float2 sb = make_float2(sc[2 * j + 1].x * inv, sc[2 * j + 1].y * inv);
+                        const float2 sa = make_float2(sc[2 * j].x * vinv, sc[2 * j].y * vinv);
+                        const float2 sb = make_float2(sc[2 * j + 1].x * vinv, sc[2 * j + 1].y * vinv);
                         pa[j][0] = f32x2_to_f16x2(s[2 * j][0] * sa.x, s[2 * j][1] * sa.y);
                         pa[j][1] = f32x2_to_f16x2(s[2 * j][2] * sa.x, s[2 * j][3] * sa.y);
                         pa[j][2] = f32x2_to_f16x2(s[2 * j + 1][0] * sb.x, s[2 * j + 1][1] * sb.y);

@@ -258,8 +258,6 @@ __device__ __forceinline__ void issue_chain(const PrefixAttnParams &p, PrefixSme
     const uint32_t d_s = tmem + t * 128, d_o = tmem + 256 + t * 128;
     const uint32_t q_desc = umma_desc_lo(smem_addr(smem) + t * kPageBytes), kv_addr = smem_addr(kv);
     auto wait = [&](uint64_t *bar, uint32_t parity) {
-        if (__all_sync(0xffffffffu, mbar_try_wait(smem_addr(bar), parity)))
-            return true;
         return attn_wait(&ctl->abort_flag, p.fault, smem_addr(bar), parity);
     };
     auto pass = [&](int chain) {
