@@ -5,6 +5,8 @@
 
 namespace msa {
 
+bool test_withhold_pages();  // msa_indexer_test_withhold_pages
+
 // Tensor map of a paged cache as [page][head][token][dim]; strides in elements
 // (page, token, head).  The stride of an axis of length 1 is never used.
 bool make_cache_map(CUtensorMap *map, const void *base, const int64_t *strides, int64_t pages, int heads, bool fp8)
@@ -135,6 +137,7 @@ static msa_status sparse_entry(const void *q, int64_t q_stride, const void *k, c
     p.k = topk;
     p.seq_limit = static_cast<int>(std::min<int64_t>(max_model_len, kPage * bt_stride));
     p.scale_log2 = scale * kLog2e;
+    p.withhold = test_withhold_pages();
     const int64_t units = static_cast<int64_t>(batch) * q_len * kv_heads;
     const int split = block_attn_split(units, topk, sms);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -244,6 +247,7 @@ static msa_status prefix_entry(const void *q, int64_t q_stride, const void *k, c
     p.q_stride = q_stride;
     p.num_pages = num_pages;
     p.scale_log2 = scale * kLog2e;
+    p.withhold = test_withhold_pages();
     p.parts.seq_limit = static_cast<int>(std::min<int64_t>(max_model_len, kPage * bt_stride));
     p.parts.grid = std::min(sms, kPrefixMaxGrid);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -274,6 +278,7 @@ static msa_status prefix_entry(const void *q, int64_t q_stride, const void *k, c
     o.seq_limit = p.parts.seq_limit;
     o.row_tiles = p.parts.own_tiles;
     o.scale_log2 = p.scale_log2;
+    o.withhold = p.withhold;
     // beside the prefix, own pages have a part of the SMs: few CTAs that walk longer lists (8 x 4 positions over 16384 +
     // 8000 tokens: 33.6 us with 64 CTAs, 38 with 256, 49 with 32)
     const int64_t units = static_cast<int64_t>(batch) * kv_heads * o.row_tiles;

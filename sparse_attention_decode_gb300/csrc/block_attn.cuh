@@ -73,6 +73,7 @@ struct BlockAttnParams {
     int batch, q_len, kv_heads, sel_heads, group, k, seq_limit;
     int row_tiles;  // OWN: tiles of kAttnMaxRows rows that a request's q_len * group are cut into
     float scale_log2;
+    int withhold;  // test of the bounded waits: the producer loads and signals no page
 };
 
 template <class F>
@@ -150,14 +151,19 @@ __device__ __forceinline__ bool mbar_test_wait(uint32_t bar, uint32_t parity)
 // Bounded wait of a whole warp; false, with the CTA's abort flag and the fault
 // bit set, when it ran out or another warp gave up before.  A phase that is
 // complete already, the common case in a page loop that the cache stream does not
-// hold up, costs one test.
-__device__ __forceinline__ bool attn_wait(int *abort_flag, uint32_t *fault, uint32_t bar, uint32_t parity)
+// hold up, costs one test.  `withhold`: the test of the bounded waits, with far
+// fewer polls.
+constexpr uint32_t kWithheldPolls = 1u << 14;
+
+__device__ __forceinline__ bool attn_wait(int *abort_flag, uint32_t *fault, uint32_t bar, uint32_t parity, int withhold)
 {
     if (__all_sync(0xffffffffu, mbar_test_wait(bar, parity)))
         return true;
     bool ok = false;
     if (!*reinterpret_cast<volatile int *>(abort_flag)) {
-        ok = mbar_wait(bar, parity);
+        const uint32_t polls = withhold ? kWithheldPolls : kSpinLimit;
+        for (uint32_t i = 0; i < polls && !ok; ++i)
+            ok = mbar_try_wait(bar, parity);
         if (!ok) {
             atomicOr(fault, MSA_FAULT_TIMEOUT);
             *reinterpret_cast<volatile int *>(abort_flag) = 1;
@@ -302,10 +308,10 @@ __global__ void __launch_bounds__(kAttnThreads, 2) block_attn_kernel(const __gri
                 const int s = static_cast<int>(it % F::kStages);
                 const uint32_t bar = smem_addr(&ctl->full[s]);
                 if (it >= F::kStages)
-                    alive = attn_wait(&ctl->abort_flag, p.fault, smem_addr(&ctl->empty[s]), (it / F::kStages + 1) & 1);
+                    alive = attn_wait(&ctl->abort_flag, p.fault, smem_addr(&ctl->empty[s]), (it / F::kStages + 1) & 1, p.withhold);
                 if (!alive)
                     break;
-                if (lane == 0) {
+                if (lane == 0 && !p.withhold) {
                     if (OWN) {
                         ctl->own_base[s] = page < 0 ? -1 : (crank + i * S) * kPage;
                         if (page < 0) {
@@ -327,7 +333,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2) block_attn_kernel(const __gri
             }
         }
         // the copies in flight land before the CTA may end, also where a consumer gave up
-        for (uint32_t j = it >= F::kStages ? it - F::kStages : 0; j < it; ++j)
+        for (uint32_t j = it >= F::kStages ? it - F::kStages : 0; j < it && !p.withhold; ++j)
             mbar_wait(smem_addr(&ctl->full[j % F::kStages]), (j / F::kStages) & 1);
     } else {
         // ---- consumers ----
@@ -388,7 +394,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2) block_attn_kernel(const __gri
         uint32_t it = 0;
         for (int i = 0; i < count && alive; ++i, it += 2) {
             const int s_k = static_cast<int>(it % F::kStages), s_v = static_cast<int>((it + 1) % F::kStages);
-            alive = attn_wait(&ctl->abort_flag, p.fault, smem_addr(&ctl->full[s_k]), (it / F::kStages) & 1);
+            alive = attn_wait(&ctl->abort_flag, p.fault, smem_addr(&ctl->full[s_k]), (it / F::kStages) & 1, p.withhold);
             if (!alive)
                 break;
             const int base = OWN ? ctl->own_base[s_k] : ctl->list_base[i];
@@ -495,7 +501,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2) block_attn_kernel(const __gri
                 l0 += r0;
                 l1 += r1;
                 if (!v_waited) {
-                    alive = attn_wait(&ctl->abort_flag, p.fault, smem_addr(&ctl->full[s_v]), ((it + 1) / F::kStages) & 1);
+                    alive = attn_wait(&ctl->abort_flag, p.fault, smem_addr(&ctl->full[s_v]), ((it + 1) / F::kStages) & 1, p.withhold);
                     v_waited = true;
                     if (!alive)
                         break;
@@ -604,7 +610,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2) block_attn_kernel(const __gri
                 }
             }
             if (alive && !v_waited)
-                alive = attn_wait(&ctl->abort_flag, p.fault, smem_addr(&ctl->full[s_v]), ((it + 1) / F::kStages) & 1);
+                alive = attn_wait(&ctl->abort_flag, p.fault, smem_addr(&ctl->full[s_v]), ((it + 1) / F::kStages) & 1, p.withhold);
             __syncwarp();
             if (lane == 0) {
                 if (k_held)

@@ -100,6 +100,7 @@ struct PrefixAttnParams {
     uint32_t *fault;
     int64_t q_stride, num_pages;
     float scale_log2;
+    int withhold;  // test of the bounded waits: the producer loads and signals no page
 };
 
 // The batch's own pages, added up by a whole block (every thread gets the sum).
@@ -258,7 +259,7 @@ __device__ __forceinline__ void issue_chain(const PrefixAttnParams &p, PrefixSme
     const uint32_t d_s = tmem + t * 128, d_o = tmem + 256 + t * 128;
     const uint32_t q_desc = umma_desc_lo(smem_addr(smem) + t * kPageBytes), kv_addr = smem_addr(kv);
     auto wait = [&](uint64_t *bar, uint32_t parity) {
-        return attn_wait(&ctl->abort_flag, p.fault, smem_addr(bar), parity);
+        return attn_wait(&ctl->abort_flag, p.fault, smem_addr(bar), parity, p.withhold);
     };
     auto pass = [&](int chain) {
         if (one)
@@ -291,14 +292,13 @@ __device__ __forceinline__ void issue_chain(const PrefixAttnParams &p, PrefixSme
     bool alive = true;
     uint32_t it = 0, kp0 = 0, seg = 0;
     int left = static_cast<int>(hi - lo), in_unit = P - static_cast<int>(lo % P);
-    for (; left > 0 && alive; ++seg) {
+    while (left > 0 && alive) {
         const int n = min(left, in_unit);
         left -= n;
         in_unit = P;
-        alive = wait(&ctl->q_full[t], seg & 1);
         const int j0 = ways == 2 ? t : 0;
-        if (alive && j0 < n) {
-            alive = landed(2 * (kp0 + j0));
+        if (j0 < n) {  // a chain without a page of the unit takes no part: its query tile is not loaded either
+            alive = wait(&ctl->q_full[t], seg++ & 1) && landed(2 * (kp0 + j0));
             if (!alive)
                 break;
             tc_fence_after_sync();
@@ -416,10 +416,10 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_attn_kernel(const __
                 const int s = static_cast<int>(it % kPrefixStages);
                 if (it >= kPrefixStages)
                     alive = attn_wait(&ctl->abort_flag, p.fault, smem_addr(&ctl->kv_empty[s]),
-                                      (it / kPrefixStages + 1) & 1);
+                                      (it / kPrefixStages + 1) & 1, p.withhold);
                 if (!alive)
                     break;
-                if (lane == 0) {
+                if (lane == 0 && !p.withhold) {
                     const uint32_t bar = smem_addr(&ctl->kv_full[s]), dst = smem_addr(kv) + s * kPageBytes;
                     if (page < 0) {
                         mbar_arrive(bar);
@@ -433,7 +433,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_attn_kernel(const __
             }
         }
         // the copies in flight land before the CTA may end, also where another role gave up
-        for (uint32_t j = it >= kPrefixStages ? it - kPrefixStages : 0; j < it; ++j)
+        for (uint32_t j = it >= kPrefixStages ? it - kPrefixStages : 0; j < it && !p.withhold; ++j)
             mbar_wait(smem_addr(&ctl->kv_full[j % kPrefixStages]), (j / kPrefixStages) & 1);
     } else if (warp == 9) {
         issue_chain<0>(p, ctl, smem, kv, tmem, lo, hi, P);
@@ -455,7 +455,13 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_attn_kernel(const __
             const int nrow = (u % p.parts.head_tiles) * p.parts.tile_rows + (ways == 1 ? t * 128 : 0) + row;
             const bool have = nrow < p.parts.rows;
             const bool some_row = __any_sync(0xffffffffu, have);  // a warp without rows only keeps the barriers going
-            {
+            const int first = ways == 2 ? t : 0;
+            const bool some = first < n;  // pages of the unit for this chain
+            // Both chains are through with the units before (named barrier 2, the two softmax warpgroups): a wait tells a
+            // phase by its parity, so a chain that begins with a stage must know that the stage's phase before, which may
+            // have been the other chain's, is over, and a chain without a page of a unit must not run ahead.
+            asm volatile("bar.sync 2, 256;" ::: "memory");
+            if (some) {
                 const uint16_t *src = p.q + static_cast<int64_t>(nrow / p.parts.group) * p.q_stride +
                                       (h * p.parts.group + nrow % p.parts.group) * kDim;
                 uint4 v[16];
@@ -466,19 +472,18 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_attn_kernel(const __
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
                     *reinterpret_cast<uint4 *>(dst + (i >> 3) * kHalfPageBytes + (((i & 7) ^ (row & 7)) << 4)) = v[i];
+                fence_proxy_async_smem();
+                tc_fence_before_sync();
+                mbar_arrive(smem_addr(&ctl->q_full[t]));
             }
-            fence_proxy_async_smem();
-            tc_fence_before_sync();
-            mbar_arrive(smem_addr(&ctl->q_full[t]));
             float m = -INFINITY, l = 0.0f;
-            const int first = ways == 2 ? t : 0;
-            int page = first < n ? p.prefix_table[page0 + first] : 0;
+            int page = some ? p.prefix_table[page0 + first] : 0;
             for (int j = first; j < n && alive; j += ways, ++it) {
                 // tokens of the page that count
                 const int valid = page < 0 || page >= p.num_pages ? 0 : min(kPage, prefix - (page0 + j) * kPage);
                 if (j + ways < n)
                     page = p.prefix_table[page0 + j + ways];
-                alive = attn_wait(&ctl->abort_flag, p.fault, smem_addr(&ctl->s_full[t]), it & 1);
+                alive = attn_wait(&ctl->abort_flag, p.fault, smem_addr(&ctl->s_full[t]), it & 1, p.withhold);
                 if (!alive)
                     break;
                 tc_fence_after_sync();
@@ -507,7 +512,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_attn_kernel(const __
                     // neither product waits for the other's softmax
                     const uint32_t vt = 2 * (kp0 + j) + 1;
                     alive = attn_wait(&ctl->abort_flag, p.fault, smem_addr(&ctl->kv_full[vt % kPrefixStages]),
-                                      (vt / kPrefixStages) & 1);
+                                      (vt / kPrefixStages) & 1, p.withhold);
                     if (!alive)
                         break;
                     if (row >= valid) {
@@ -534,7 +539,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_attn_kernel(const __
                     const float to_m = fmaxf(m, top), f = rescale(m, to_m);
                     m = to_m;
                     l *= f;
-                    alive = attn_wait(&ctl->abort_flag, p.fault, smem_addr(&ctl->o_done[t]), (it - 1) & 1);
+                    alive = attn_wait(&ctl->abort_flag, p.fault, smem_addr(&ctl->o_done[t]), (it - 1) & 1, p.withhold);
                     if (!alive)
                         break;
                     tc_fence_after_sync();
@@ -576,9 +581,8 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_attn_kernel(const __
                 l += a + b;
             }
             // ---- the range's part of the unit ----
-            const bool some = first < n;
             if (alive && some)
-                alive = attn_wait(&ctl->abort_flag, p.fault, smem_addr(&ctl->o_done[t]), (it - 1) & 1);
+                alive = attn_wait(&ctl->abort_flag, p.fault, smem_addr(&ctl->o_done[t]), (it - 1) & 1, p.withhold);
             tc_fence_after_sync();
             kp0 += n;
             // chain t's block of the slot: its rows of a tile of 256, or its part of the one tile

@@ -190,3 +190,28 @@ def test_refusals():
     for kw in (dict(q=w["q"].half()), dict(kp=w["kp"][:, :64]), dict(shared=w["shared"].long())):
         with pytest.raises(AssertionError):
             call(msa, dict(w, **kw))
+
+
+@pytest.mark.parametrize("rows", [2, 40], ids=["one_tile", "two_tiles"])
+def test_waits_that_run_out_empty_the_rows(rows):
+    """The producers withhold every page: bounded waits give up, the rows are empty, the next call is exact."""
+    import sparse_attention_decode_gb300 as msa
+    w = make(19, 3000, [100 + i for i in range(rows)], 1, 2, 16, "hnd")
+    whole = call(msa, w)
+    msa.msa_indexer_test_withhold_pages(1)
+    try:
+        out, lse, fault = call(msa, w)
+    finally:
+        msa.msa_indexer_test_withhold_pages(0)
+    assert fault == msa.MSA_FAULT_TIMEOUT
+    assert not bool(out.any()) and bool((lse == -float("inf")).all())
+    again = call(msa, w)
+    assert again[2] == 0 and torch.equal(again[0], whole[0]) and torch.equal(again[1], whole[1])
+
+
+def test_many_units_of_a_single_page():
+    """A CTA's range holds several units of one page each: one of the two chains has nothing to do in any of them."""
+    import sparse_attention_decode_gb300 as msa
+    for prefix, heads in ((100, 8), (128, 7), (300, 5)):
+        w = make(20, prefix, [3, 200, 0], 1, heads, 4, "hnd")
+        assert verify(msa, w) == 0

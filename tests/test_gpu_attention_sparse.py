@@ -196,3 +196,20 @@ def test_refusals():
     for kw in (dict(q=q.half()), dict(k=kp[..., :64]), dict(k=kp.float()), dict(ids=ids.long()), dict(out=out[:, :4]),
                dict(seq=seq.long()), dict(k=kp[:2]), dict(ids=ids[:, :, ::2])):
         assert status(**kw) == "refused", kw
+
+
+@pytest.mark.parametrize("e4m3", [False, True], ids=["bf16", "e4m3"])
+def test_waits_that_run_out_empty_the_rows(e4m3):
+    """The producer withholds every page: bounded waits give up, the rows are empty, the next call is exact."""
+    import sparse_attention_decode_gb300 as msa
+    w = make(19, [1000, 300], 2, 4, 16, 4, 16, "hnd", e4m3)
+    whole = call(msa, w)
+    msa.msa_indexer_test_withhold_pages(1)
+    try:
+        out, lse, mass, fault = call(msa, w)
+    finally:
+        msa.msa_indexer_test_withhold_pages(0)
+    assert fault == msa.MSA_FAULT_TIMEOUT
+    assert not bool(out.any()) and bool((lse == -float("inf")).all()) and not bool(mass.any())
+    again = call(msa, w)
+    assert again[3] == 0 and all(torch.equal(a, b) for a, b in zip(again[:3], whole[:3]))
