@@ -179,7 +179,7 @@ static void prefix_parts(PrefixParts &a, int batch, int q_len, int group, int kv
     a.kv_heads = kv_heads;
     a.rows = batch * q_len * group;
     prefix_units(a, a.rows, kv_heads);
-    a.own_tiles = (q_len * group + kAttnMaxRows - 1) / kAttnMaxRows;
+    a.own_cost = (q_len * group + 15) / 16;
     a.limit = max_prefix_len;
     uint8_t *at = workspace + kHeaderBytes;
     auto take = [&](size_t bytes) {
@@ -276,13 +276,13 @@ static msa_status prefix_entry(const void *q, int64_t q_stride, const void *k, c
     o.sel_heads = 1;
     o.group = group;
     o.seq_limit = p.parts.seq_limit;
-    o.row_tiles = p.parts.own_tiles;
+    o.row_tiles = (p.parts.q_len * group + kAttnMaxRows - 1) / kAttnMaxRows;
     o.scale_log2 = p.scale_log2;
     o.withhold = p.withhold;
-    // beside the prefix, own pages have a part of the SMs: few CTAs that walk longer lists (8 x 4 positions over 16384 +
-    // 8000 tokens: 33.6 us with 64 CTAs, 38 with 256, 49 with 32)
+    // Clusters of up to 4 (16 requests x 4 positions x 16 heads over 8192 + 37000 tokens: 155 us unsplit, 88 with 2, 65
+    // with 4, 68 with 8; 8 x 4 x 8 over 16384 + 8000: 46, 32, 30.5, 36).
     const int64_t units = static_cast<int64_t>(batch) * kv_heads * o.row_tiles;
-    const int split = block_attn_split(units, 8, sms / 4), unit_rows = std::min(q_len * group, kAttnMaxRows);
+    const int split = block_attn_split(units, 4, sms), unit_rows = std::min(q_len * group, kAttnMaxRows);
     const msa_status own = unit_rows <= 16   ? launch_block_attn<AttnBf16, 1, true>(o, units, split, st)
                            : unit_rows <= 32 ? launch_block_attn<AttnBf16, 2, true>(o, units, split, st)
                                              : launch_block_attn<AttnBf16, 4, true>(o, units, split, st);

@@ -54,7 +54,7 @@ struct PrefixParts {
     int batch, q_len, group, kv_heads;
     int rows;  // rows of a KV head: batch * q_len * group
     int tile_rows, ways, head_tiles, units;
-    int own_tiles;         // times that own pages are read
+    int own_cost;          // of an own page and KV head: 16-row tiles it is multiplied with
     int limit, seq_limit;  // bounds on the prefix's and a request's tokens
     int grid;              // CTAs prefix_attn_kernel is launched with
 };
@@ -74,7 +74,7 @@ struct PrefixSplit {
     {
         pages = pages_of(prefix);
         total = static_cast<int64_t>(pages) * p.units;
-        const int64_t mine = total * 2 / p.ways, theirs = own * p.own_tiles * p.kv_heads;
+        const int64_t mine = total * 2 / p.ways, theirs = own * p.own_cost * p.kv_heads;
         int most = p.grid;
         if (mine > 0)
             most = max(1, static_cast<int>((static_cast<int64_t>(p.grid) * mine + (mine + theirs) / 2) / (mine + theirs)));
