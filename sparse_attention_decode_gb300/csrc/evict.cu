@@ -77,6 +77,7 @@ struct EvictParams {
     uint32_t *fault;
     int64_t bt_stride, out_stride;
     int cols, kv_heads, seq_limit, budget, n_sink, n_window;
+    int apart;  // the outputs are not the inputs
 };
 
 // A block's key, ordered as its weight: NaN lowest, then -inf .. inf, pinned blocks highest.
@@ -112,9 +113,8 @@ __device__ __forceinline__ void block_sums(const float *w, int64_t cols, int hea
 }
 
 // One CTA per request.  Keys in shared memory; the budget-th largest by four
-// 8-bit radix passes; in the first a warp adds up its counts per digit before it
-// touches shared memory (most weights share their exponent, and those never
-// selected are all zero).  A warp then takes a run of blocks, 32 at a time by ballot: how many
+// 8-bit radix passes, the first one's counts taken as the keys are made (adding
+// up a warp's equal digits by match before they are counted was slower).  A warp then takes a run of blocks, 32 at a time by ballot: how many
 // lie above the threshold and how many on it, one prefix sum over the warps, and
 // the blocks' places follow (blocks on the threshold stay in index order until it
 // is met).  Table and weights are copied in increasing destination order, kCopy
@@ -152,37 +152,56 @@ __global__ void __launch_bounds__(T, 2) evict_kernel(const __grid_constant__ Evi
     const float *w = p.weights + static_cast<int64_t>(b) * p.kv_heads * p.cols;
     const int32_t *table = p.table + b * p.bt_stride;
 
+    int32_t *out_table = p.out_table + b * p.out_stride;
+    float *out_w = p.out_weights + static_cast<int64_t>(b) * p.kv_heads * p.cols;
+    // what lies past the kept blocks
+    auto clear = [&] {
+#pragma unroll 4
+        for (int i = keep + tid; i < p.cols; i += T)
+            out_table[i] = -1;
+        for (int h = 0; h < p.kv_heads; ++h) {
+            float *row = out_w + static_cast<int64_t>(h) * p.cols;
+            const int first = VEC ? min(p.cols, (keep + 3) / 4 * 4) : p.cols;
+#pragma unroll 4
+            for (int i = keep + tid; i < first; i += T)
+                row[i] = 0.0f;
+#pragma unroll 4
+            for (int i = first + tid * 4; i < p.cols; i += T * 4)
+                *reinterpret_cast<float4 *>(row + i) = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        }
+    };
+    if (p.apart)  // beside the loads; in place, it would clear what is still to be read
+        clear();
+
     uint32_t bound = 0;  // the key of the last block that stays
     int want = all ? 0 : keep;
     if (!all) {
         constexpr int N = VEC ? 4 : 1;
+        for (int i = tid; i < 256; i += T)
+            hist[i] = 0;
+        __syncthreads();
 #pragma unroll 2
         for (int j = tid * N; j < nb; j += T * N) {  // VEC: a row is at least nb rounded up to 4 long
             float sum[N];
             block_sums<N>(w, p.cols, p.kv_heads, j, sum);
 #pragma unroll
-            for (int k = 0; k < N; ++k)
-                keys[j + k] = j + k < p.n_sink || j + k >= nb - p.n_window ? 0xffffffffu : evict_key(sum[k]);
+            for (int k = 0; k < N; ++k) {
+                const uint32_t key = j + k < p.n_sink || j + k >= nb - p.n_window ? 0xffffffffu : evict_key(sum[k]);
+                keys[j + k] = key;
+                if (j + k < nb)
+                    atomicAdd(&hist[key >> 24], 1);  // the first digit's count
+            }
         }
         uint32_t mask = 0;
         for (int shift = 24; shift >= 0; shift -= 8) {
-            for (int i = tid; i < 256; i += T)
-                hist[i] = 0;
-            __syncthreads();
+            if (shift < 24) {
+                for (int i = tid; i < 256; i += T)
+                    hist[i] = 0;
+                __syncthreads();
 #pragma unroll 4
-            for (int i0 = 0; i0 < nb; i0 += T) {
-                const uint32_t key = i0 + tid < nb ? keys[i0 + tid] : 0u;
-                const bool in = i0 + tid < nb && (key & mask) == bound;
-                if (!__any_sync(0xffffffffu, in))
-                    continue;
-                const uint32_t digit = in ? (key >> shift) & 255 : 256;
-                if (shift == 24) {
-                    const uint32_t same = __match_any_sync(0xffffffffu, digit);
-                    if (in && (same & ((1u << lane) - 1u)) == 0)
-                        atomicAdd(&hist[digit], __popc(same));
-                } else if (in) {
-                    atomicAdd(&hist[digit], 1);
-                }
+                for (int j = tid; j < nb; j += T)
+                    if ((keys[j] & mask) == bound)
+                        atomicAdd(&hist[(keys[j] >> shift) & 255], 1);
             }
             __syncthreads();
             if (warp == 0) {
@@ -257,8 +276,6 @@ __global__ void __launch_bounds__(T, 2) evict_kernel(const __grid_constant__ Evi
         p.out_seq[b] = L - (nb - keep) * kPage;
     }
     __syncthreads();  // the freed pages are read before any entry is overwritten
-    int32_t *out_table = p.out_table + b * p.out_stride;
-    float *out_w = p.out_weights + static_cast<int64_t>(b) * p.kv_heads * p.cols;
     for (int i0 = 0; i0 < keep; i0 += T * kCopy) {
         int from[kCopy];
         int32_t page[kCopy];
@@ -289,19 +306,9 @@ __global__ void __launch_bounds__(T, 2) evict_kernel(const __grid_constant__ Evi
             if (from[k] >= 0)
                 out_table[i0 + k * T + tid] = page[k];
     }
-    __syncthreads();  // the last piece's sources are read before the rest is cleared
-#pragma unroll 4
-    for (int i = keep + tid; i < p.cols; i += T)
-        out_table[i] = -1;
-    for (int h = 0; h < p.kv_heads; ++h) {
-        float *row = out_w + static_cast<int64_t>(h) * p.cols;
-        const int first = VEC ? min(p.cols, (keep + 3) / 4 * 4) : p.cols;
-#pragma unroll 4
-        for (int i = keep + tid; i < first; i += T)
-            row[i] = 0.0f;
-#pragma unroll 4
-        for (int i = first + tid * 4; i < p.cols; i += T * 4)
-            *reinterpret_cast<float4 *>(row + i) = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (!p.apart) {
+        __syncthreads();  // the last piece's sources are read before the rest is cleared
+        clear();
     }
 }
 
@@ -365,6 +372,7 @@ extern "C" msa_status msa_cache_evict(const int32_t *block_table, int64_t bt_str
     p.budget = budget;
     p.n_sink = n_sink;
     p.n_window = n_window;
+    p.apart = out_table != block_table && out_weights != weights;
     const size_t smem = (static_cast<size_t>(cols) + 3) / 4 * 16 + static_cast<size_t>(cols) * 2;
     const bool vec = cols % 4 == 0 && ((reinterpret_cast<uintptr_t>(weights) | reinterpret_cast<uintptr_t>(out_weights)) & 15) == 0;
     const bool wide = cols > 1024;
