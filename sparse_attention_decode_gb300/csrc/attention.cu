@@ -179,7 +179,12 @@ static void prefix_parts(PrefixParts &a, int batch, int q_len, int group, int kv
     a.kv_heads = kv_heads;
     a.rows = batch * q_len * group;
     prefix_units(a, a.rows, kv_heads);
-    a.own_cost = (q_len * group + 15) / 16;
+    // An own page takes an SM about as long as a 128-row tile's page of the prefix (1350 cycles) where the stream
+    // bounds it (16 rows), and its share of the mma.sync rate where that does.  Measured on 11 batches: for 16 rows
+    // 6/8 to 7/8 are the fastest (64 requests over 32768 + 147000 tokens: 96 us, 101 at 8/8, 114 at 5/8), for 32 and
+    // 64 rows 12/8 a tile of 16 (8 x 4 x 8 over 16384 + 8000: 27 us, 31 at 8/8).
+    const int tiles = (q_len * group + 15) / 16;
+    a.own_cost = tiles == 1 ? 7 : 12 * tiles;
     a.limit = max_prefix_len;
     uint8_t *at = workspace + kHeaderBytes;
     auto take = [&](size_t bytes) {

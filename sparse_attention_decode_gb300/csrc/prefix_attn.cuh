@@ -54,7 +54,7 @@ struct PrefixParts {
     int batch, q_len, group, kv_heads;
     int rows;  // rows of a KV head: batch * q_len * group
     int tile_rows, ways, head_tiles, units;
-    int own_cost;          // of an own page and KV head: 16-row tiles it is multiplied with
+    int own_cost;          // of an own page and KV head, in eighths of a 128-row tile's page of the prefix
     int limit, seq_limit;  // bounds on the prefix's and a request's tokens
     int grid;              // CTAs prefix_attn_kernel is launched with
 };
@@ -67,14 +67,12 @@ constexpr int kPrefixMinPages = 2;  // pages a CTA's range should have at least
 struct PrefixSplit {
     int pages, ctas;
     int64_t total;
-    // own: the batch's own pages.  A page of a 256-row tile takes an SM 2700 cycles, of a 128-row tile half of that;
-    // an own page of one head (64 KiB) about 1300 where the rest of the GPU leaves the SM its bandwidth.  (64 requests
-    // over 32768 + 147000 tokens: 98 us; with own pages at half that weight 119, at twice 127.)
+    // own: the batch's own pages, which run beside the prefix on the SMs that are left
     __device__ PrefixSplit(const PrefixParts &p, int prefix, int64_t own)
     {
         pages = pages_of(prefix);
         total = static_cast<int64_t>(pages) * p.units;
-        const int64_t mine = total * 2 / p.ways, theirs = own * p.own_cost * p.kv_heads;
+        const int64_t mine = total * 2 / p.ways, theirs = own * p.own_cost * p.kv_heads / 8;
         int most = p.grid;
         if (mine > 0)
             most = max(1, static_cast<int>((static_cast<int64_t>(p.grid) * mine + (mine + theirs) / 2) / (mine + theirs)));
@@ -533,9 +531,37 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_attn_kernel(const __
                         mx[q] = max3(mx[q], __uint_as_float(s[q][i]), __uint_as_float(s[q][i + 1]));
                 }
                 const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
-                if (j == first) {
+                if (j == first)
                     m = top;
-                } else if (__any_sync(0xffffffffu, top > m + kPrefixLag)) {
+                // two quarters of the scores to weights (bf16 pairs) and their sums, at the reference m
+                const uint64_t c2 = pack2(c, c);
+                auto weigh = [&](const uint32_t (&x)[32], const uint32_t (&y)[32], uint32_t (&w)[32]) {
+                    const float ref = m == -INFINITY ? 0.0f : m;
+                    const uint64_t r2 = pack2(-ref, -ref);
+                    uint64_t sx = 0, sy = 0;  // two fp32 sums each
+#pragma unroll
+                    for (int i = 0; i < 32; i += 2) {
+                        float a, b, d, e;
+                        unpack2(fma2(pack2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), c2, r2), a, b);
+                        unpack2(fma2(pack2(__uint_as_float(y[i]), __uint_as_float(y[i + 1])), c2, r2), d, e);
+                        a = exp2_approx(a);
+                        b = exp2_approx(b);
+                        d = exp2_approx(d);
+                        e = exp2_approx(e);
+                        sx = add2(sx, pack2(a, b));
+                        sy = add2(sy, pack2(d, e));
+                        w[i / 2] = f32x2_to_bf16x2(a, b);
+                        w[16 + i / 2] = f32x2_to_bf16x2(d, e);
+                    }
+                    float a, b;
+                    unpack2(add2(sx, sy), a, b);
+                    return a + b;
+                };
+                uint32_t w[32];
+                // The first half is weighed beside the search for the maximum, at the reference so far; where a row of
+                // the warp has outgrown it, the reference moves and the half, still in tensor memory, is weighed again.
+                float sum = weigh(s[0], s[1], w);
+                if (j != first && __any_sync(0xffffffffu, top > m + kPrefixLag)) {
                     const float to_m = fmaxf(m, top), f = rescale(m, to_m);
                     m = to_m;
                     l *= f;
@@ -553,32 +579,30 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_attn_kernel(const __
                             o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
                         tmem_st32(to + q * 32, o);
                     }
+                    tmem_ld32(ts, s[0]);
+                    tmem_ld32(ts + 32, s[1]);
+                    tmem_wait_ld(s[0]);
+                    tmem_regs_ready(s[1]);
+                    if (valid < kPage) {
+#pragma unroll
+                        for (int q = 0; q < 2; ++q)
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                if (q * 32 + i >= valid)
+                                    s[q][i] = 0xff800000u;
+                    }
+                    sum = weigh(s[0], s[1], w);
                 }
-                const float ref = m == -INFINITY ? 0.0f : m;
-                uint64_t sum[4] = {0, 0, 0, 0};  // two fp32 sums each
-                const uint64_t c2 = pack2(c, c), r2 = pack2(-ref, -ref);
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    uint32_t w[32];
-#pragma unroll
-                    for (int q = 2 * half; q < 2 * half + 2; ++q)
-#pragma unroll
-                        for (int i = 0; i < 32; i += 2) {
-                            float a, b;
-                            unpack2(fma2(pack2(__uint_as_float(s[q][i]), __uint_as_float(s[q][i + 1])), c2, r2), a, b);
-                            a = exp2_approx(a);
-                            b = exp2_approx(b);
-                            sum[q] = add2(sum[q], pack2(a, b));
-                            w[(q & 1) * 16 + i / 2] = f32x2_to_bf16x2(a, b);
-                        }
-                    tmem_st32(ts + half * 32, w);
-                    tmem_wait_st();
-                    tc_fence_before_sync();
-                    mbar_arrive(smem_addr(half ? &ctl->p_full[t] : &ctl->p_half[t]));
-                }
-                float a, b;
-                unpack2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), a, b);
-                l += a + b;
+                tmem_st32(ts, w);
+                tmem_wait_st();
+                tc_fence_before_sync();
+                mbar_arrive(smem_addr(&ctl->p_half[t]));
+                l += sum;
+                l += weigh(s[2], s[3], w);
+                tmem_st32(ts + 32, w);
+                tmem_wait_st();
+                tc_fence_before_sync();
+                mbar_arrive(smem_addr(&ctl->p_full[t]));
             }
             // ---- the range's part of the unit ----
             if (alive && some)

@@ -16,14 +16,14 @@ MAX_GRID = int(re.search(r"kPrefixMaxGrid = (\d+)", SRC).group(1))
 class Split:
     """PrefixSplit, with the units that the host makes of the batch's rows."""
 
-    def __init__(self, rows, kv_heads, tokens, own, own_tiles, grid):
+    def __init__(self, rows, kv_heads, tokens, own, own_cost, grid):
         self.tile = 128 if rows <= 128 else 256
         self.ways = 256 // self.tile
         self.head_tiles = -(-rows // self.tile)
         self.units = self.head_tiles * kv_heads
         self.pages = -(-tokens // 128)
         self.total = self.pages * self.units
-        mine, theirs = self.total * 2 // self.ways, own * own_tiles * kv_heads
+        mine, theirs = self.total * 2 // self.ways, own * own_cost * kv_heads // 8
         most = grid
         if mine > 0:
             most = max(1, (grid * mine + (mine + theirs) // 2) // (mine + theirs))
@@ -45,7 +45,7 @@ CASES = [(r, h, n, o, g) for r in (1, 16, 128, 129, 256, 1024, 2500) for h in (1
 
 @pytest.mark.parametrize("rows,kv_heads,tokens,own,grid", random.Random(4).sample(CASES, 120))
 def test_every_page_of_every_unit_has_one_owner(rows, kv_heads, tokens, own, grid):
-    s = Split(rows, kv_heads, tokens, own, 1, grid)
+    s = Split(rows, kv_heads, tokens, own, rows % 5 * 12 or 7, grid)
     assert 1 <= s.ctas <= grid <= MAX_GRID
     assert s.start(0) == 0 and s.start(s.ctas) == s.total
     slots = {}
