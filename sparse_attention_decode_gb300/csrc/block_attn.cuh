@@ -22,10 +22,13 @@
 // blocks (1.05 GB): 175-178 us, 0.87-0.88 of the copy rate.
 #pragma once
 
+#include <algorithm>
+#include <cmath>
+
+#include "attn_ptx.cuh"
 #include "host_util.cuh"
 #include "keys.cuh"
 #include "layout.cuh"
-#include "ptx.cuh"
 #include "tcgen05.cuh"
 
 #include "msa_attention.h"

@@ -1,9 +1,11 @@
 // Eviction from the paged cache by accumulated attention weight: the weights'
 // update and the choice of the pages that leave.
+#include <algorithm>
+
+#include "attn_ptx.cuh"
 #include "host_util.cuh"
 #include "keys.cuh"
 #include "layout.cuh"
-#include "ptx.cuh"
 
 #include "msa_attention.h"
 

@@ -15,10 +15,13 @@
 // are requests enough to fill the GPU, rows are therefore taken one at a time, each
 // decided before the next is read; a few requests take all rows at once, since a
 // decision (two cluster barriers) would cost more than the rows it could save.
+#include <algorithm>
+#include <cmath>
+
+#include "attn_ptx.cuh"
 #include "host_util.cuh"
 #include "keys.cuh"
 #include "layout.cuh"
-#include "ptx.cuh"
 #include "tcgen05.cuh"
 
 #include "msa_attention.h"
