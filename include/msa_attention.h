@@ -100,7 +100,8 @@ msa_status msa_attention_sparse_fp8(const void *q, int64_t q_stride, const void 
  * tokens of its own (none where that is negative).  Same formula, same out and
  * out_lse as msa_attention_sparse, over all of these tokens.
  *
- *   prefix_table   int32 [ceil(max_prefix_len / 128)]: the prefix's pages.
+ *   prefix_table   int32 [ceil(max_prefix_len / 128)]: the prefix's pages.  Pages x
+ *                  KV heads x tiles of 256 rows of a head are at most 2^30.
  *   prefix_len     device int32 [1], in [0, max_prefix_len] (outside: 0).
  *   block_table, seq_lens   each request's own pages and own tokens.
  *   workspace      at least msa_attention_prefix_workspace_bytes(batch * q_len,

@@ -58,6 +58,8 @@ constexpr int kAttnThreads = 32 * (kAttnWarps + 1);
 constexpr int kAttnMaxRows = 64;  // rows of one unit (query heads of a KV head): 1, 2 or 4 tiles of 16
 constexpr int kAttnOStride = kDim + 4;  // fp32 row stride of a partial O in shared memory (bank spread)
 
+__device__ __forceinline__ int pages_of(int tokens) { return tokens / kPage + (tokens % kPage != 0); }
+
 struct BlockAttnParams {
     CUtensorMap kmap, vmap;  // [page][head][token][dim], box 1 x 1 x 128 x (64 bf16 | 128 E4M3)
     const uint16_t *q;
@@ -248,12 +250,14 @@ __global__ void __launch_bounds__(kAttnThreads, 2) block_attn_kernel(const __gri
         fence_barrier_init();
     }
     if (warp == kAttnWarps) {
+        if (lane < 2)
+            prefetch_tensormap(lane ? &p.vmap : &p.kmap);
         if (OWN) {
-            const int nb = (len + kPage - 1) / kPage;
+            const int nb = pages_of(len);
             if (lane == 0)
                 ctl->count = nb > crank ? (nb - crank + S - 1) / S : 0;
         } else {
-            const int nb = (visible(position(0)) + kPage - 1) / kPage;
+            const int nb = pages_of(visible(position(0)));
             const int id = sel_id;
             int page = -1;
             bool ok = id >= 0;

@@ -55,37 +55,57 @@ struct PrefixParts {
     int rows;  // rows of a KV head: batch * q_len * group
     int tile_rows, ways, head_tiles, units;
     int own_cost;          // of an own page and KV head, in eighths of a 128-row tile's page of the prefix
+    int own_most;          // pages of one request that count in that comparison: their sum stays below 2^31
     int limit, seq_limit;  // bounds on the prefix's and a request's tokens
     int grid;              // CTAs prefix_attn_kernel is launched with
 };
 
 __device__ __forceinline__ int tokens_in(int n, int limit) { return n < 0 || n > limit ? 0 : n; }
-__device__ __forceinline__ int pages_of(int tokens) { return (tokens + kPage - 1) / kPage; }
 
 constexpr int kPrefixMinPages = 2;  // pages a CTA's range should have at least
 
+// 32-bit numbers (the host refuses more): quotients of 64 bits would be half the start of every kernel.
 struct PrefixSplit {
     int pages, ctas;
-    int64_t total;
+    int span, per;    // `per` CTAs share `span` pages: those of one unit, or of all
+    int range, more;  // pages of a CTA's range; the first `more` of the `per` have one more
     // own: the batch's own pages, which run beside the prefix on the SMs that are left
-    __device__ PrefixSplit(const PrefixParts &p, int prefix, int64_t own)
+    __device__ PrefixSplit(const PrefixParts &p, int prefix, int own)
     {
         pages = pages_of(prefix);
-        total = static_cast<int64_t>(pages) * p.units;
-        const int64_t mine = total * 2 / p.ways, theirs = own * p.own_cost * p.kv_heads / 8;
-        int most = p.grid;
-        if (mine > 0)
-            most = max(1, static_cast<int>((static_cast<int64_t>(p.grid) * mine + (mine + theirs) / 2) / (mine + theirs)));
-        ctas = static_cast<int>(min(static_cast<int64_t>(most), (total + kPrefixMinPages - 1) / kPrefixMinPages));
-        // the same number of CTAs for every unit where that leaves few out: no range then ends in a second unit, and
-        // the tiles of a head walk the same pages at the same time, from L2 but for the first
-        const int even = ctas / p.units * p.units;
-        if (even * 8 >= ctas * 7)
-            ctas = even;
+        const int total = pages * p.units;
+        // shares of the GPU: an estimate, in the same steps wherever it is made
+        const float mine = static_cast<float>(total) * (p.ways == 1 ? 2.0f : 1.0f);
+        const float all = __fadd_rn(mine, __fmul_rn(static_cast<float>(own), static_cast<float>(p.own_cost * p.kv_heads) * 0.125f));
+        const int most =
+            min(p.grid, max(1, __float2int_rn(__fmul_rn(static_cast<float>(p.grid), __fdividef(mine, all)))));
+        const int per_unit = (pages + kPrefixMinPages - 1) / kPrefixMinPages;
+        ctas = min(most, (total + kPrefixMinPages - 1) / kPrefixMinPages);
+        // The same number of CTAs for every unit where that leaves few out: no range then ends in a second unit, and
+        // the tiles of a head walk the same pages at the same time, from L2 but for the first.
+        const int each = min(most / p.units, per_unit);
+        if (each > 0 && each * p.units * 8 >= ctas * 7) {
+            span = pages;
+            per = each;
+            ctas = per * p.units;
+        } else {
+            span = total;
+            per = ctas;
+        }
+        range = per > 0 ? span / per : 0;
+        more = span - range * per;
     }
-    __device__ int64_t start(int g) const { return g * total / ctas; }
+    __device__ int start(int g) const
+    {
+        const int k = g / per, i = g - k * per;
+        return k * span + i * range + min(i, more);
+    }
     // the CTA whose range holds page x of the sequence
-    __device__ int owner(int64_t x) const { return static_cast<int>(((x + 1) * ctas - 1) / total); }
+    __device__ int owner(int x) const
+    {
+        const int k = x / span, y = x - k * span, longer = more * (range + 1);
+        return k * per + (y < longer ? y / (range + 1) : more + (y - longer) / range);
+    }
 };
 
 struct PrefixAttnParams {
@@ -104,17 +124,17 @@ struct PrefixAttnParams {
 // The batch's own pages, added up by a whole block (every thread gets the sum).
 // `sums`: shared, one entry a warp.
 template <int THREADS>
-__device__ __forceinline__ int64_t own_pages(const int32_t *seq_lens, int batch, int limit, int *sums)
+__device__ __forceinline__ int own_pages(const int32_t *seq_lens, const PrefixParts &p, int *sums)
 {
     const int tid = threadIdx.x;
     int n = 0;
-    for (int b = tid; b < batch; b += THREADS)
-        n += pages_of(tokens_in(seq_lens[b], limit));
+    for (int b = tid; b < p.batch; b += THREADS)
+        n += min(pages_of(tokens_in(seq_lens[b], p.seq_limit)), p.own_most);
     n = __reduce_add_sync(0xffffffffu, n);
     if ((tid & 31) == 0)
         sums[tid >> 5] = n;
     __syncthreads();
-    int64_t all = 0;
+    int all = 0;
     for (int w = 0; w < THREADS / 32; ++w)
         all += sums[w];
     return all;
@@ -248,7 +268,7 @@ __device__ __forceinline__ uint32_t umma_desc_v_lo(uint32_t saddr)
 // with V and the next page's scores.
 template <int t>
 __device__ __forceinline__ void issue_chain(const PrefixAttnParams &p, PrefixSmem *ctl, uint8_t *smem, uint8_t *kv,
-                                            uint32_t tmem, int64_t lo, int64_t hi, int P)
+                                            uint32_t tmem, int lo, int hi, int P)
 {
     constexpr uint32_t idesc_s = umma_idesc_bf16_f32(128, 128);
     constexpr uint32_t idesc_o = umma_idesc_bf16_f32(128, 128) | (1u << 16);  // B with N contiguous
@@ -289,7 +309,7 @@ __device__ __forceinline__ void issue_chain(const PrefixAttnParams &p, PrefixSme
         pass(0);
     bool alive = true;
     uint32_t it = 0, kp0 = 0, seg = 0;
-    int left = static_cast<int>(hi - lo), in_unit = P - static_cast<int>(lo % P);
+    int left = hi - lo, in_unit = P - lo % P;
     while (left > 0 && alive) {
         const int n = min(left, in_unit);
         left -= n;
@@ -356,20 +376,15 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_attn_kernel(const __
 
     griddep_launch_dependents();
     const int cta = blockIdx.x;
-    const int prefix = __shfl_sync(0xffffffffu, tokens_in(*p.prefix_len, p.parts.limit), 0);
-    if (cta == 0 && tid == 0 && prefix == 0 && *p.prefix_len != 0)
-        atomicOr(p.fault, MSA_FAULT_SEQ_LEN);
-    const PrefixSplit split(p.parts, prefix,
-                            own_pages<kPrefixThreads>(p.seq_lens, p.parts.batch, p.parts.seq_limit, ctl->warp_sums));
-    if (cta >= split.ctas)
-        return;
-    const int P = split.pages, ways = p.parts.ways;
-    const int64_t lo = split.start(cta), hi = split.start(cta + 1);
-
-    if (tid == 0) {
+    // set up while the lengths are on their way; tensor memory too, by CTAs that may turn out to have no part in it
+    // (an SM has no room for a second CTA that wants it)
+    const int given = *p.prefix_len;  // under way together with the lengths
+    if (tid == 8 * 32) {
+        prefetch_tensormap(&p.kmap);
+        prefetch_tensormap(&p.vmap);
         for (int s = 0; s < kPrefixStages; ++s) {
             mbar_init(smem_addr(&ctl->kv_full[s]), 1);
-            mbar_init(smem_addr(&ctl->kv_empty[s]), 2 / ways);
+            mbar_init(smem_addr(&ctl->kv_empty[s]), 2 / p.parts.ways);
         }
         for (int t = 0; t < 2; ++t) {
             mbar_init(smem_addr(&ctl->q_full[t]), 128);
@@ -387,21 +402,33 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_attn_kernel(const __
         tmem_relinquish_alloc_permit();
     }
     tc_fence_before_sync();
-    __syncthreads();
+    const int own = own_pages<kPrefixThreads>(p.seq_lens, p.parts, ctl->warp_sums);
+    const int prefix = __shfl_sync(0xffffffffu, tokens_in(given, p.parts.limit), 0);
+    if (cta == 0 && tid == 0 && prefix != given)
+        atomicOr(p.fault, MSA_FAULT_SEQ_LEN);
+    const PrefixSplit split(p.parts, prefix, own);
     tc_fence_after_sync();
+    if (cta >= split.ctas) {
+        if (warp == 9)
+            tmem_dealloc(ctl->tmem, 512);
+        return;
+    }
+    const int P = split.pages, ways = p.parts.ways;
+    const int lo = split.start(cta), hi = split.start(cta + 1);
     const uint32_t tmem = __shfl_sync(0xffffffffu, ctl->tmem, 0);  // columns 0, 128: S (and the weights); 256, 384: O
 
     if (warp == 8) {
         // ---- K and V tiles, page after page ----
         bool alive = true;
         uint32_t it = 0;
-        int pages = -1;
-        for (int64_t x = lo; x < hi && alive; ++x) {
-            const int i = static_cast<int>(x - lo);
+        int pages = -1;  // a lane's share of 32 entries of the table
+        int u = lo / P, at = lo - u * P;
+        const int n = hi - lo;
+        for (int i = 0; i < n && alive; ++i) {
             if ((i & 31) == 0) {
                 pages = -1;
-                if (x + lane < hi) {
-                    pages = p.prefix_table[(x + lane) % P];
+                if (i + lane < n) {
+                    pages = p.prefix_table[(at + lane) % P];
                     if (pages < 0 || pages >= p.num_pages) {
                         pages = -1;
                         atomicOr(p.fault, MSA_FAULT_PAGE_ID);
@@ -409,7 +436,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_attn_kernel(const __
                 }
             }
             const int page = __shfl_sync(0xffffffffu, pages, i & 31);
-            const int h = static_cast<int>(x / P) / p.parts.head_tiles;
+            const int h = u / p.parts.head_tiles;
             for (int kvi = 0; kvi < 2; ++kvi, ++it) {
                 const int s = static_cast<int>(it % kPrefixStages);
                 if (it >= kPrefixStages)
@@ -429,6 +456,10 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_attn_kernel(const __
                     }
                 }
             }
+            if (++at == P) {
+                at = 0;
+                ++u;
+            }
         }
         // the copies in flight land before the CTA may end, also where another role gave up
         for (uint32_t j = it >= kPrefixStages ? it - kPrefixStages : 0; j < it && !p.withhold; ++j)
@@ -445,9 +476,9 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_attn_kernel(const __
         const float c = p.scale_log2;
         bool alive = true;
         uint32_t it = 0, kp0 = 0;  // pages of this chain, pages of the CTA before the unit's
-        for (int64_t x = lo; x < hi; ) {
-            const int u = static_cast<int>(x / P), page0 = static_cast<int>(x % P);
-            const int n = static_cast<int>(min(hi - x, static_cast<int64_t>(P - page0)));
+        for (int x = lo; x < hi; ) {
+            const int u = x / P, page0 = x - u * P;
+            const int n = min(hi - x, P - page0);
             x += n;
             const int h = u / p.parts.head_tiles;
             const int nrow = (u % p.parts.head_tiles) * p.parts.tile_rows + (ways == 1 ? t * 128 : 0) + row;
@@ -460,16 +491,25 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_attn_kernel(const __
             // have been the other chain's, is over, and a chain without a page of a unit must not run ahead.
             asm volatile("bar.sync 2, 256;" ::: "memory");
             if (some) {
-                const uint16_t *src = p.q + static_cast<int64_t>(nrow / p.parts.group) * p.q_stride +
-                                      (h * p.parts.group + nrow % p.parts.group) * kDim;
-                uint4 v[16];
+                // the warp's 32 rows, two at a time: 16 lanes a row of 256 bytes
+                const int64_t src = have ? static_cast<int64_t>(nrow / p.parts.group) * p.q_stride +
+                                               (h * p.parts.group + nrow % p.parts.group) * kDim
+                                         : -1;
+                uint8_t *dst = smem + t * kPageBytes + ((lane >> 3) & 1) * kHalfPageBytes + (row & ~31) * 128;
+#pragma unroll 1
+                for (int r0 = lane >> 4; r0 < 32; r0 += 16) {
+                    uint4 v[8];
 #pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    v[i] = have ? reinterpret_cast<const uint4 *>(src)[i] : make_uint4(0u, 0u, 0u, 0u);
-                uint8_t *dst = smem + t * kPageBytes + row * 128;
+                    for (int i = 0; i < 8; ++i) {
+                        const int64_t from = __shfl_sync(0xffffffffu, src, r0 + 2 * i);
+                        v[i] = from >= 0 ? reinterpret_cast<const uint4 *>(p.q + from)[lane & 15] : make_uint4(0u, 0u, 0u, 0u);
+                    }
 #pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    *reinterpret_cast<uint4 *>(dst + (i >> 3) * kHalfPageBytes + (((i & 7) ^ (row & 7)) << 4)) = v[i];
+                    for (int i = 0; i < 8; ++i) {
+                        const int r = r0 + 2 * i;
+                        *reinterpret_cast<uint4 *>(dst + r * 128 + (((lane ^ r) & 7) << 4)) = v[i];
+                    }
+                }
                 fence_proxy_async_smem();
                 tc_fence_before_sync();
                 mbar_arrive(smem_addr(&ctl->q_full[t]));
@@ -670,15 +710,13 @@ struct JoinParams {
     float *lse;
 };
 
-constexpr int kJoinWarps = 8;
-
-template <int WPR>
-__global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_constant__ JoinParams p)
+template <int WPR, int WARPS>
+__global__ void __launch_bounds__(32 * WARPS, WPR == 1 ? 2 : WPR == 2 ? 3 : 5) join_kernel(const __grid_constant__ JoinParams p)
 {
-    constexpr int kRows = kJoinWarps / WPR;  // rows of a block
-    __shared__ float4 s_acc[kJoinWarps][32];
-    __shared__ float s_m[kJoinWarps], s_sum[kJoinWarps];
-    __shared__ int s_bad[kJoinWarps];
+    constexpr int kRows = WARPS / WPR;  // rows of a block
+    __shared__ float4 s_acc[WARPS][32];
+    __shared__ float s_m[WARPS], s_sum[WARPS];
+    __shared__ int s_bad[WARPS];
     const PrefixParts &a = p.parts;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, sub = warp % WPR;
     const int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + warp / WPR;  // (query row, KV head, head of the group)
@@ -687,53 +725,60 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_cons
     const int query = static_cast<int>(row / a.group / a.kv_heads);
     const int n = query * a.group + g;
     const PrefixSplit split(a, tokens_in(*p.prefix_len, a.limit),
-                            own_pages<32 * kJoinWarps>(p.seq_lens, a.batch, a.seq_limit, s_bad));
+                            own_pages<32 * WARPS>(p.seq_lens, a, s_bad));
     __syncthreads();
-    const float *o[2] = {a.o, a.own_o}, *e[2] = {a.lse, a.own_lse};
-    int64_t first[2] = {0, 0};  // row of the first part
-    const int step[2] = {256 / a.ways, 0};
-    int count[2] = {0, exists ? 1 : 0};
+    int64_t first = 0;  // row of the prefix's first part; its next one is `step` on
+    const int step = 256 / a.ways;
+    int count = 0;  // parts of the prefix; the request's own comes after them
     if (exists && split.pages > 0) {
-        const int64_t u = static_cast<int64_t>(h) * a.head_tiles + n / a.tile_rows;
+        const int u = h * a.head_tiles + n / a.tile_rows;
         const int g0 = split.owner(u * split.pages), g1 = split.owner((u + 1) * split.pages - 1) + 1;
-        count[0] = (g1 - g0) * a.ways;
-        first[0] = (g0 + u) * 256 + n % a.tile_rows;
+        count = (g1 - g0) * a.ways;
+        first = static_cast<int64_t>(g0 + u) * 256 + n % a.tile_rows;
     }
-    first[1] = exists ? (static_cast<int64_t>(query) * a.kv_heads + h) * a.group + g : 0;
+    const int64_t own_row = exists ? (static_cast<int64_t>(query) * a.kv_heads + h) * a.group + g : 0;
     griddep_wait();  // both kernels have ended
     float M = -INFINITY, sum = 0.0f;
     float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     bool bad = false;
+    const int all = exists ? count + 1 : 0, mine = all > sub ? (all - sub + WPR - 1) / WPR : 0;
+    for (int i0 = 0; i0 < mine; i0 += 32) {
+        const int end = min(32, mine - i0);
+        const int at = sub + i0 * WPR;  // the part of lane 0
+        const int l_at = at + lane * WPR;
+        const float x = lane >= end     ? -INFINITY
+                        : l_at == count ? __ldcg(a.own_lse + own_row)
+                                        : __ldcg(a.lse + first + static_cast<int64_t>(l_at) * step);
+        bad |= __any_sync(0xffffffffu, x == INFINITY);
+        float to = fmaxf(M, x);
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-        const int mine = count[k] > sub ? (count[k] - sub + WPR - 1) / WPR : 0;
-        for (int i0 = 0; i0 < mine; i0 += 32) {
-            const int end = min(32, mine - i0);
-            const int64_t at = first[k] + static_cast<int64_t>(sub + i0 * WPR) * step[k];
-            const float x = lane < end ? __ldcg(e[k] + at + static_cast<int64_t>(lane * WPR) * step[k]) : -INFINITY;
-            bad |= __any_sync(0xffffffffu, x == INFINITY);
-            float to = fmaxf(M, x);
+        for (int q = 16; q >= 1; q >>= 1)
+            to = fmaxf(to, __shfl_xor_sync(0xffffffffu, to, q));
+        const float old = rescale(M, to), f = x == -INFINITY ? 0.0f : rescale(x, to);
+        M = to;
+        sum *= old;
+        acc.x *= old;
+        acc.y *= old;
+        acc.z *= old;
+        acc.w *= old;
+        constexpr int kBatch = WPR == 2 ? 8 : 4;
+        for (int i = 0; i < end; i += kBatch) {
+            float4 v[kBatch];  // under way together, also where fewer are left
 #pragma unroll
-            for (int q = 16; q >= 1; q >>= 1)
-                to = fmaxf(to, __shfl_xor_sync(0xffffffffu, to, q));
-            const float old = rescale(M, to), f = x == -INFINITY ? 0.0f : rescale(x, to);
-            M = to;
-            sum *= old;
-            acc.x *= old;
-            acc.y *= old;
-            acc.z *= old;
-            acc.w *= old;
-#pragma unroll 8
-            for (int i = 0; i < end; ++i) {
-                const float fi = __shfl_sync(0xffffffffu, f, i);
-                // no branch, so that several loads go out together; what a part that holds nothing has there may be anything
-                const float4 v = __ldcg(reinterpret_cast<const float4 *>(o[k] + (at + static_cast<int64_t>(i * WPR) * step[k]) * kDim) + lane);
-                const bool some = fi != 0.0f;
+            for (int k = 0; k < kBatch; ++k) {
+                const int part = at + (i + k) * WPR;
+                const float *o = part == count ? a.own_o + own_row * kDim : a.o + (first + static_cast<int64_t>(part) * step) * kDim;
+                v[k] = i + k < end ? __ldcg(reinterpret_cast<const float4 *>(o) + lane) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            }
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) {
+                const float fi = __shfl_sync(0xffffffffu, f, i + k);  // 0 past the end
+                const bool some = fi != 0.0f;  // what a part that holds nothing has there may be anything
                 sum += fi;
-                acc.x += some ? fi * v.x : 0.0f;
-                acc.y += some ? fi * v.y : 0.0f;
-                acc.z += some ? fi * v.z : 0.0f;
-                acc.w += some ? fi * v.w : 0.0f;
+                acc.x += some ? fi * v[k].x : 0.0f;
+                acc.y += some ? fi * v[k].y : 0.0f;
+                acc.z += some ? fi * v[k].z : 0.0f;
+                acc.w += some ? fi * v[k].w : 0.0f;
             }
         }
     }

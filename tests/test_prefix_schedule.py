@@ -23,20 +23,26 @@ class Split:
         self.units = self.head_tiles * kv_heads
         self.pages = -(-tokens // 128)
         self.total = self.pages * self.units
-        mine, theirs = self.total * 2 // self.ways, own * own_cost * kv_heads // 8
-        most = grid
-        if mine > 0:
-            most = max(1, (grid * mine + (mine + theirs) // 2) // (mine + theirs))
+        mine, theirs = self.total * 2 // self.ways, own * own_cost * kv_heads / 8
+        most = min(grid, max(1, round(grid * mine / max(1, mine + theirs))))
         self.ctas = min(most, -(-self.total // MIN_PAGES))
-        even = self.ctas // self.units * self.units
-        if even * 8 >= self.ctas * 7:
-            self.ctas = even
+        each = min(most // self.units, -(-self.pages // MIN_PAGES))
+        if each > 0 and each * self.units * 8 >= self.ctas * 7:
+            self.span, self.per = self.pages, each
+            self.ctas = self.per * self.units
+        else:
+            self.span, self.per = self.total, self.ctas
+
+        self.range, self.more = divmod(self.span, self.per)
 
     def start(self, g):
-        return g * self.total // self.ctas
+        k, i = divmod(g, self.per)
+        return k * self.span + i * self.range + min(i, self.more)
 
     def owner(self, x):
-        return ((x + 1) * self.ctas - 1) // self.total
+        k, y = divmod(x, self.span)
+        longer = self.more * (self.range + 1)
+        return k * self.per + (y // (self.range + 1) if y < longer else self.more + (y - longer) // self.range)
 
 
 CASES = [(r, h, n, o, g) for r in (1, 16, 128, 129, 256, 1024, 2500) for h in (1, 4, 8) for n in (1, 128, 129, 4133, 32768)
