@@ -44,15 +44,46 @@ bool cache_ok(const void *base, const int64_t *strides, int64_t pages, int heads
 
 bool unaligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) != 0; }
 
-// CTAs of the cluster that walks one list: enough to fill two CTAs an SM, at
-// most one per block of the list.
-int block_attn_split(int64_t units, int pages, int sms)
+// Clusters of `size` CTAs (two an SM) that the device runs at the same time: those of 4 or 8 do not fill it, as a
+// cluster stays within one of its parts.  0 where the query fails.
+int resident_clusters(int dev, int size)
 {
+    static std::atomic<int> cache[kMaxDevices][9];
+    int v = dev >= 0 && dev < kMaxDevices ? cache[dev][size].load(std::memory_order_relaxed) : 0;
+    if (v > 0)
+        return v;
+    auto *kernel = block_attn_kernel<AttnBf16, 1, false>;
+    const size_t smem = block_attn_smem<AttnBf16>(0);
+    cudaLaunchConfig_t cfg;
+    std::memset(&cfg, 0, sizeof cfg);
+    cudaLaunchAttribute attr[1];
+    cfg.gridDim = dim3(static_cast<unsigned>(size));
+    cfg.blockDim = dim3(kAttnThreads);
+    cfg.dynamicSmemBytes = smem;
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = size;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&v, kernel, &cfg) != cudaSuccess)
+        return 0;
+    if (dev >= 0 && dev < kMaxDevices)
+        cache[dev][size].store(v, std::memory_order_relaxed);
+    return v;
+}
 
-    int s = 1;
-    while (s < 8 && 2 * s <= pages && units * s * 2 <= 2 * static_cast<int64_t>(sms))
-        s *= 2;
-    return s;
+// CTAs of the cluster that walks one list of at most `pages` pages: the most that still run all at once, and no more
+// than it takes to make the longest share as short.  16 blocks, 4 KV heads: 19 requests in clusters of 3 21.1 us (E4M3
+// 17.7), in clusters of 4 that do not all fit 27.4 (23.7); 24 requests 18.6 (E4M3) against 21.7 in clusters of 2.
+int block_attn_split(int64_t units, int pages, int dev)
+{
+    int s = 8;
+    while (s > 1 && (s > pages || units > resident_clusters(dev, s)))
+        --s;
+    const int longest = (pages + s - 1) / s;
+    return (pages + longest - 1) / longest;
 }
 
 template <class F, int MT, bool OWN>
@@ -139,7 +170,7 @@ static msa_status sparse_entry(const void *q, int64_t q_stride, const void *k, c
     p.scale_log2 = scale * kLog2e;
     p.withhold = test_withhold_pages();
     const int64_t units = static_cast<int64_t>(batch) * q_len * kv_heads;
-    const int split = block_attn_split(units, topk, sms);
+    const int split = block_attn_split(units, topk, dev);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (fp8)
         return group <= 16   ? launch_block_attn<AttnFp8, 1, false>(p, units, split, st)
@@ -290,7 +321,7 @@ static msa_status prefix_entry(const void *q, int64_t q_stride, const void *k, c
     // Clusters of up to 4 (16 requests x 4 positions x 16 heads over 8192 + 37000 tokens: 155 us unsplit, 88 with 2, 65
     // with 4, 68 with 8; 8 x 4 x 8 over 16384 + 8000: 46, 32, 30.5, 36).
     const int64_t units = static_cast<int64_t>(batch) * kv_heads * o.row_tiles;
-    const int split = block_attn_split(units, 4, sms), unit_rows = std::min(q_len * group, kAttnMaxRows);
+    const int split = block_attn_split(units, 4, dev), unit_rows = std::min(q_len * group, kAttnMaxRows);
     const msa_status own = unit_rows <= 16   ? launch_block_attn<AttnBf16, 1, true>(o, units, split, st)
                            : unit_rows <= 32 ? launch_block_attn<AttnBf16, 2, true>(o, units, split, st)
                                              : launch_block_attn<AttnBf16, 4, true>(o, units, split, st);
