@@ -212,8 +212,9 @@ static void prefix_parts(PrefixParts &a, int batch, int q_len, int group, int kv
     prefix_units(a, a.rows, kv_heads);
     // An own page takes an SM about as long as a 128-row tile's page of the prefix (1350 cycles) where the stream
     // bounds it (16 rows), and its share of the mma.sync rate where that does.  Measured on 11 batches: for 16 rows
-    // 6/8 to 7/8 are the fastest (64 requests over 32768 + 147000 tokens: 96 us, 101 at 8/8, 114 at 5/8), for 32 and
-    // 64 rows 12/8 a tile of 16 (8 x 4 x 8 over 16384 + 8000: 27 us, 31 at 8/8).
+    // 6/8 and 7/8 are the fastest (64 requests over 32768: 96 us, 99 at 8/8, 113 at 5/8), for 32 and 64 rows 12/8 a
+    // tile of 16 (8 x 4 x 8 over 16384 + 8000 tokens: 26 us, 27 at 10/8, 31 at 8/8; 16 x 4 x 16 over 8192 + 37000: 60,
+    // 62 and 66, 72 at 14/8).
     const int tiles = (q_len * group + 15) / 16;
     a.own_cost = tiles == 1 ? 7 : 12 * tiles;
     a.own_most = batch > 0 ? INT32_MAX / batch : 0;
@@ -318,8 +319,8 @@ static msa_status prefix_entry(const void *q, int64_t q_stride, const void *k, c
     o.row_tiles = (p.parts.q_len * group + kAttnMaxRows - 1) / kAttnMaxRows;
     o.scale_log2 = p.scale_log2;
     o.withhold = p.withhold;
-    // Clusters of up to 4 (16 requests x 4 positions x 16 heads over 8192 + 37000 tokens: 155 us unsplit, 88 with 2, 65
-    // with 4, 68 with 8; 8 x 4 x 8 over 16384 + 8000: 46, 32, 30.5, 36).
+    // Clusters of up to 4 (16 requests x 4 positions x 16 heads over 8192 + 37000 tokens, at that time: 155 us
+    // unsplit, 88 with 2, 65 with 4, 68 with 8; 8 x 4 x 8 over 16384 + 8000: 46, 32, 30.5, 36).
     const int64_t units = static_cast<int64_t>(batch) * kv_heads * o.row_tiles;
     const int split = block_attn_split(units, 4, dev), unit_rows = std::min(q_len * group, kAttnMaxRows);
     const msa_status own = unit_rows <= 16   ? launch_block_attn<AttnBf16, 1, true>(o, units, split, st)

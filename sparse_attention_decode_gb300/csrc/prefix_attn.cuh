@@ -13,9 +13,9 @@
 // stream.  So the two run side by side: this kernel takes as many SMs as its share
 // of the work by the live lengths (its other CTAs end at once), and the own pages'
 // CTAs, launched as its dependents, start on the rest and follow as its CTAs end.
-// (One after the other: 125 us for 64 requests over 32768 + 147000 tokens; own
-// pages as further units of this kernel: 193 us, a few microseconds of latency for
-// each of their short runs.)
+// (64 requests over 32768 + 147000 tokens: 87 us; one after the other 125; own pages
+// as further units of this kernel 193, a few microseconds of latency for each of
+// their short runs.)
 //
 // Per page and 128-row tile: S (128 x 128, fp32) in tensor memory; a warpgroup
 // with one thread a row takes the row's maximum, 2^(c s - m) and the sum, and
@@ -30,8 +30,11 @@
 // 1400) -> product (512), with a barrier between each.  Two chains run side by
 // side, each with an MMA warp of its own, and take turns at the tensor cores: the
 // two tiles of 256 rows, or the even and the odd pages of one tile, whose range
-// then leaves two parts.  2700 cycles a page of 256 rows, 3/4 of the MMA rate; one
-// issuing thread for both took 5000, two without turns 5000 as well.
+// then leaves two parts.  2700 to 3000 cycles a page of 256 rows (1.45-1.6 us), 0.7 to
+// 3/4 of the MMA rate; one issuing thread for both took 5000, two without turns 5000
+// as well.  Around the pages: 1.5 us until the split is known, 3 to 3.5 until the first
+// scores, 3 for the parts, 1.5 to 2 until the join knows that both kernels have ended,
+// 2 to 4 for the join.
 #pragma once
 
 #include "block_attn.cuh"
@@ -701,7 +704,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_attn_kernel(const __
 // out = sum 2^(e - M) o / sum 2^(e - M) over a row's parts (o, e), prefix first,
 // then own.  WPR warps a row take the parts in turn; each has the numbers of 32
 // parts in its lanes and asks for several vectors at once.  Bound by those reads
-// (L2): 4096 rows with 8 parts, 17 MB.
+// (L2): 4096 rows with 7 parts, 15 MB, take 4 us, 1024 rows with 26 parts 3.
 struct JoinParams {
     PrefixParts parts;
     const int32_t *prefix_len;
