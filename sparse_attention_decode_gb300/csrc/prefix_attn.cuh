@@ -32,9 +32,13 @@
 // two tiles of 256 rows, or the even and the odd pages of one tile, whose range
 // then leaves two parts.  2700 to 3000 cycles a page of 256 rows (1.45-1.6 us), 0.7 to
 // 3/4 of the MMA rate; one issuing thread for both took 5000, two without turns 5000
-// as well.  Around the pages: 1.5 us until the split is known, 3 to 3.5 until the first
-// scores, 3 for the parts, 1.5 to 2 until the join knows that both kernels have ended,
-// 2 to 4 for the join.
+// as well.  What is left is the MMAs' own: a turn's 16 take 1350 cycles where the pipe
+// alone would take 1024 (the scores read 8 KiB of shared memory each in 64 cycles, all
+// there is).  Without any loads of tiles a page takes 2850, with two threads a row in
+// the softmax, with three tiles of K and two of V, or with the turn passed earlier the
+// same as now.  Around the pages: 1.5 us until the split is known, 3 to 3.5 until the
+// first scores, 3 for the parts, 1.5 to 2 until the join knows that both kernels have
+// ended, 2 to 4 for the join.
 #pragma once
 
 #include "block_attn.cuh"
