@@ -271,6 +271,25 @@ __global__ void __launch_bounds__(T, 2) evict_kernel(const __grid_constant__ Evi
     }
     __syncthreads();
 
+    // Every read of a piece before its writes; the first piece's loads are under way beside those of the freed pages.
+    int from[kCopy];
+    int32_t page[kCopy];
+    float v[4][kCopy];
+    auto ask = [&](int i0, int h0) {
+#pragma unroll
+        for (int k = 0; k < kCopy; ++k) {
+            const int i = i0 + k * T + tid;
+            if (h0 == 0) {
+                from[k] = i < keep ? list[i] : -1;
+                page[k] = from[k] >= 0 ? table[from[k]] : -1;
+            }
+#pragma unroll
+            for (int h = 0; h < 4; ++h)
+                if (h0 + h < p.kv_heads && from[k] >= 0)
+                    v[h][k] = w[static_cast<int64_t>(h0 + h) * p.cols + from[k]];
+        }
+    };
+    ask(0, 0);
     int32_t *freed = p.freed + static_cast<int64_t>(b) * p.cols;
 #pragma unroll 4
     for (int i = tid; i < p.cols; i += T)
@@ -279,25 +298,13 @@ __global__ void __launch_bounds__(T, 2) evict_kernel(const __grid_constant__ Evi
         p.n_freed[b] = nb - keep;
         p.out_seq[b] = L - (nb - keep) * kPage;
     }
-    __syncthreads();  // the freed pages are read before any entry is overwritten
     for (int i0 = 0; i0 < keep; i0 += T * kCopy) {
-        int from[kCopy];
-        int32_t page[kCopy];
-#pragma unroll
-        for (int k = 0; k < kCopy; ++k) {
-            const int i = i0 + k * T + tid;
-            from[k] = i < keep ? list[i] : -1;
-            page[k] = from[k] >= 0 ? table[from[k]] : -1;
-        }
+        if (i0 > 0)
+            ask(i0, 0);
         for (int h0 = 0; h0 < p.kv_heads; h0 += 4) {
-            float v[4][kCopy];
-#pragma unroll
-            for (int h = 0; h < 4; ++h)
-#pragma unroll
-                for (int k = 0; k < kCopy; ++k)
-                    if (h0 + h < p.kv_heads && from[k] >= 0)
-                        v[h][k] = w[static_cast<int64_t>(h0 + h) * p.cols + from[k]];
-            __syncthreads();
+            if (h0 > 0)
+                ask(i0, h0);
+            __syncthreads();  // what the piece and, before the first, the freed list come from is read
 #pragma unroll
             for (int h = 0; h < 4; ++h)
 #pragma unroll
