@@ -114,24 +114,25 @@ __device__ __forceinline__ void block_sums(const float *w, int64_t cols, int hea
     }
 }
 
-// One CTA per request.  Keys in shared memory; the budget-th largest by four
-// 8-bit radix passes, the first one's counts taken as the keys are made (adding
-// up a warp's equal digits by match before they are counted was slower).  A warp
-// then takes a run of blocks, 32 at a time by ballot: how many lie above the
-// threshold and how many on it, one prefix sum over the warps, and the blocks'
-// places follow (blocks on the threshold stay in index order until it is met).
-// Table and weights are copied in increasing destination order, kCopy entries a
-// thread at a time: every read of a piece before its writes, and a source never
-// lies below its destination, so outputs may be the inputs.  VEC: rows start on 16
-// bytes.  T threads, two CTAs an SM: 1024 for long contexts, whose rounds over the
-// blocks are then few (with the first digit counted apart: 35 us against 38 with
-// 512), 256 for short ones.
+// One CTA per request.  Keys in shared memory; the budget-th largest by three
+// radix passes of 11, 11 and 10 bits, the first one's counts taken as the keys are
+// made (adding up a warp's equal digits by match before they are counted was
+// slower; four passes of 8 bits took 1 us more).  A warp then takes a run of
+// blocks, 32 at a time by ballot: how many lie above the threshold and how many on
+// it, one prefix sum over the warps, and the blocks' places follow (blocks on the
+// threshold stay in index order until it is met).  Table and weights are copied in
+// increasing destination order, kCopy entries a thread at a time: every read of a
+// piece before its writes, and a source never lies below its destination, so
+// outputs may be the inputs.  VEC: rows start on 16 bytes.  T threads, two CTAs an
+// SM: 1024 for long contexts, whose rounds over the blocks are then few (with the
+// first digit counted apart: 35 us against 38 with 512), 256 for short ones.
 //
-// Bound by latency: two rounds over the request's weights with the selection
-// between them.  What carries it are wide loads with several heads in flight and
-// few barriers (with a barrier every 512 entries and a load at a time: 62 us).
-// 256 x 8192 blocks x 4 heads, accumulation included: 31 us; 4 x 68: 5.
+// Bound by latency: 7 us for the keys, 1 to 2 a pass, 1.2 for the places, 5 for the
+// copies (256 requests x 8192 blocks x 4 heads).  What carries it are wide loads
+// with several heads in flight and few barriers (with a barrier every 512 entries
+// and a load at a time: 62 us).  Accumulation included: 29 us; 4 x 68 blocks: 4.8.
 constexpr int kCopy = 2;
+constexpr int kBins = 2048;  // of a radix pass: digits of 11, 11 and 10 bits
 
 template <bool VEC, int T>
 __global__ void __launch_bounds__(T, 2) evict_kernel(const __grid_constant__ EvictParams p)
@@ -140,7 +141,8 @@ __global__ void __launch_bounds__(T, 2) evict_kernel(const __grid_constant__ Evi
     extern __shared__ uint32_t evict_smem[];
     uint32_t *keys = evict_smem;
     uint16_t *list = reinterpret_cast<uint16_t *>(keys + (p.cols + 3) / 4 * 4);  // kept blocks, then the freed ones
-    __shared__ int hist[256];
+    __shared__ int2 hist2[kBins / 2];
+    int *hist = reinterpret_cast<int *>(hist2);
     __shared__ int above_of[kWarps], ties_of[kWarps];
     __shared__ uint32_t s_prefix;
     __shared__ int s_want;
@@ -181,7 +183,7 @@ __global__ void __launch_bounds__(T, 2) evict_kernel(const __grid_constant__ Evi
     int want = all ? 0 : keep;
     if (!all) {
         constexpr int N = VEC ? 4 : 1;
-        for (int i = tid; i < 256; i += T)
+        for (int i = tid; i < kBins; i += T)
             hist[i] = 0;
         __syncthreads();
 #pragma unroll 2
@@ -193,50 +195,56 @@ __global__ void __launch_bounds__(T, 2) evict_kernel(const __grid_constant__ Evi
                 const uint32_t key = j + k < p.n_sink || j + k >= nb - p.n_window ? 0xffffffffu : evict_key(sum[k]);
                 keys[j + k] = key;
                 if (j + k < nb)
-                    atomicAdd(&hist[key >> 24], 1);  // the first digit's count
+                    atomicAdd(&hist[key >> 21], 1);  // the first digit's count
             }
         }
         uint32_t mask = 0;
-        for (int shift = 24; shift >= 0; shift -= 8) {
-            if (shift < 24) {
-                for (int i = tid; i < 256; i += T)
-                    hist[i] = 0;
-                __syncthreads();
+#pragma unroll
+        for (int pass = 0; pass < 3; ++pass) {
+            const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
+            if (pass > 0) {
 #pragma unroll 4
                 for (int j = tid; j < nb; j += T)
                     if ((keys[j] & mask) == bound)
-                        atomicAdd(&hist[(keys[j] >> shift) & 255], 1);
+                        atomicAdd(&hist[(keys[j] >> shift) & (pass == 2 ? 1023 : 2047)], 1);
             }
             __syncthreads();
-            if (warp == 0) {
-                // the digit, from the top, in which the want-th largest lies: lane 0 has the 8 highest digits
-                int mine[8], sum = 0;
+            // the digit, from the top, in which the want-th largest lies: thread 0 has the highest ones
+            constexpr int kMine = kBins / T;
+            int mine[kMine], sum = 0;
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    mine[k] = hist[255 - lane * 8 - k];
-                    sum += mine[k];
-                }
-                int above = sum;
+            for (int k = 0; k < kMine; k += 2) {
+                const int at = (kBins - 2 - k) / 2 - tid * (kMine / 2);
+                const int2 two = hist2[at];
+                hist2[at] = make_int2(0, 0);  // for the next pass
+                mine[k] = two.y;
+                mine[k + 1] = two.x;
+                sum += two.x + two.y;
+            }
+            int above = sum;
 #pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const int y = __shfl_up_sync(0xffffffffu, above, o);
-                    if (lane >= o)
-                        above += y;
-                }
-                above -= sum;
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, above, o);
+                if (lane >= o)
+                    above += y;
+            }
+            if (lane == 31)
+                above_of[warp] = above;
+            above -= sum;
+            __syncthreads();
+            above += __reduce_add_sync(0xffffffffu, lane < warp ? above_of[lane] : 0);
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    if (above < want && above + mine[k] >= want) {
-                        s_prefix = bound | static_cast<uint32_t>(255 - lane * 8 - k) << shift;
-                        s_want = want - above;
-                    }
-                    above += mine[k];
+            for (int k = 0; k < kMine; ++k) {
+                if (above < want && above + mine[k] >= want) {
+                    s_prefix = bound | static_cast<uint32_t>(kBins - 1 - tid * kMine - k) << shift;
+                    s_want = want - above;
                 }
+                above += mine[k];
             }
             __syncthreads();
             bound = s_prefix;
             want = s_want;  // how many of the blocks that share the digits so far stay
-            mask |= 255u << shift;
+            mask |= (pass == 2 ? 1023u : 2047u) << shift;
         }
     }
     // a warp's run: rows of 32 blocks
