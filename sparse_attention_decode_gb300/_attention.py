@@ -69,10 +69,15 @@ def _layout(t):
     return None if t is None else (t.shape, t.stride(), t.dtype, t.get_device())
 
 
-def _one_device(*layouts):
-    """All tensors on one CUDA device: an address of another would be a fault."""
+def _place(workspace):
+    """Device number of a workspace; one with gaps has none."""
+    return workspace.get_device() if workspace.is_contiguous() else -1
+
+
+def _one_device(place, *layouts):
+    """All tensors and the workspace on one CUDA device: an address of another would be a fault."""
     devices = {x[3] for x in layouts if x is not None}
-    assert len(devices) == 1 and min(devices) >= 0, "all tensors on one CUDA device"
+    assert devices == {place} and place >= 0, "all tensors and a contiguous workspace on one CUDA device"
 
 
 def _stream(stream, t):
@@ -133,8 +138,8 @@ def _requests(block_table, seq_lens):
 
 
 @_shapes
-def _sparse_shapes(q, k, k_scale, v, v_scale, block_table, seq_lens, ids, out, lse, mass, q_len, max_model_len):
-    _one_device(q, k, k_scale, v, v_scale, block_table, seq_lens, ids, out, lse, mass)
+def _sparse_shapes(place, q, k, k_scale, v, v_scale, block_table, seq_lens, ids, out, lse, mass, q_len, max_model_len):
+    _one_device(place, q, k, k_scale, v, v_scale, block_table, seq_lens, ids, out, lse, mass)
     e4m3 = k_scale is not None
     ks, vs, pages, kv_heads = _caches(k, v, e4m3)
     batch, cols, bt_stride = _requests(block_table, seq_lens)
@@ -155,7 +160,7 @@ def _sparse_shapes(q, k, k_scale, v, v_scale, block_table, seq_lens, ids, out, l
 def _sparse(name, q, k, k_scale, v, v_scale, block_table, seq_lens, ids, out, workspace, scale, q_len, max_model_len,
             out_lse, out_mass, stream):
     q_stride, ks, vs, pages, bt_stride, sizes, sel, topk = _sparse_shapes(
-        _layout(q), _layout(k), _layout(k_scale), _layout(v), _layout(v_scale), _layout(block_table),
+        _place(workspace), _layout(q), _layout(k), _layout(k_scale), _layout(v), _layout(v_scale), _layout(block_table),
         _layout(seq_lens), _layout(ids), _layout(out), _layout(out_lse), _layout(out_mass), q_len, max_model_len)
     if k_scale is None:
         cache = (k.data_ptr(), ks, v.data_ptr(), vs)
@@ -188,8 +193,8 @@ def msa_attention_sparse_fp8(q, k, k_scale, v, v_scale, block_table, seq_lens, i
 
 
 @_shapes
-def _accumulate_shapes(weights, ids, mass, n_rows, q_len):
-    _one_device(weights, ids, mass, n_rows)
+def _accumulate_shapes(place, weights, ids, mass, n_rows, q_len):
+    _one_device(place, weights, ids, mass, n_rows)
     batch, kv_heads, cols = (int(x) for x in weights[0])
     rows, sel, topk = (int(x) for x in ids[0])
     assert rows == batch * q_len, "ids: batch * q_len rows"
@@ -206,7 +211,8 @@ def msa_cache_accumulate(weights, ids, mass, workspace, *, q_len: int = 1, n_row
     ``ids`` [batch * q_len, sel_heads, k] and ``mass`` [batch * q_len, kv_heads, k] as msa_attention_sparse takes and
     gives them.  See include/msa_attention.h.
     """
-    cols, sizes = _accumulate_shapes(_layout(weights), _layout(ids), _layout(mass), _layout(n_rows), q_len)
+    cols, sizes = _accumulate_shapes(
+        _place(workspace), _layout(weights), _layout(ids), _layout(mass), _layout(n_rows), q_len)
     st = _fn("msa_cache_accumulate")(weights.data_ptr(), cols, ids.data_ptr(), mass.data_ptr(), _ptr(n_rows), *sizes,
                                      workspace.data_ptr(), workspace.nbytes, _stream(stream, weights))
     if st:
@@ -214,9 +220,9 @@ def msa_cache_accumulate(weights, ids, mass, workspace, *, q_len: int = 1, n_row
 
 
 @_shapes
-def _evict_shapes(block_table, seq_lens, weights, out_table, out_seq_lens, out_weights, out_freed, out_n_freed,
+def _evict_shapes(place, block_table, seq_lens, weights, out_table, out_seq_lens, out_weights, out_freed, out_n_freed,
                   max_model_len):
-    _one_device(block_table, seq_lens, weights, out_table, out_seq_lens, out_weights, out_freed, out_n_freed)
+    _one_device(place, block_table, seq_lens, weights, out_table, out_seq_lens, out_weights, out_freed, out_n_freed)
     batch, cols, bt_stride = _requests(block_table, seq_lens)
     o_batch, o_cols, o_stride = _requests(out_table, out_seq_lens)
     assert o_batch == batch and o_cols == cols, "out_table, out_seq_lens: like the inputs"
@@ -237,6 +243,7 @@ def msa_cache_evict(block_table, seq_lens, weights, budget: int, n_sink: int, n_
     The new table, lengths and weights may be written over the old ones.  See include/msa_attention.h.
     """
     bt_stride, o_stride, sizes = _evict_shapes(
+        _place(workspace),
         _layout(block_table), _layout(seq_lens), _layout(weights), _layout(out_table), _layout(out_seq_lens),
         _layout(out_weights), _layout(out_freed), _layout(out_n_freed), max_model_len)
     st = _fn("msa_cache_evict")(
@@ -248,8 +255,8 @@ def msa_cache_evict(block_table, seq_lens, weights, budget: int, n_sink: int, n_
 
 
 @_shapes
-def _verify_shapes(logits, draft, tokens, uniforms, race, out, accepted, temperature, n_draft, logprobs):
-    _one_device(logits, draft, tokens, uniforms, race, out, accepted, temperature, n_draft, logprobs)
+def _verify_shapes(place, logits, draft, tokens, uniforms, race, out, accepted, temperature, n_draft, logprobs):
+    _one_device(place, logits, draft, tokens, uniforms, race, out, accepted, temperature, n_draft, logprobs)
     shape, stride, dtype, _ = logits
     assert len(shape) == 3 and dtype in (_F32, _BF16) and stride[2] == 1, \
         "logits: fp32 or bf16 [batch, drafts + 1, vocab], rows contiguous"
@@ -276,6 +283,7 @@ def msa_verify_draft(logits, draft_probs, draft_tokens, uniforms, race, out_toke
     vocab], ``race`` fp32 [batch, vocab] of Exp(1) draws.  See include/msa_attention.h.
     """
     kind, sizes = _verify_shapes(
+        _place(workspace),
         _layout(logits), _layout(draft_probs), _layout(draft_tokens), _layout(uniforms), _layout(race),
         _layout(out_tokens), _layout(out_accepted), _layout(temperature), _layout(n_draft), _layout(out_logprobs))
     st = _fn("msa_verify_draft")(
@@ -291,9 +299,9 @@ def msa_attention_prefix_workspace_bytes(max_rows: int, heads: int, kv_heads: in
 
 
 @_shapes
-def _prefix_shapes(q, k, v, prefix_table, prefix_len, block_table, seq_lens, out, lse, q_len, max_prefix_len,
+def _prefix_shapes(place, q, k, v, prefix_table, prefix_len, block_table, seq_lens, out, lse, q_len, max_prefix_len,
                    max_model_len):
-    _one_device(q, k, v, prefix_table, prefix_len, block_table, seq_lens, out, lse)
+    _one_device(place, q, k, v, prefix_table, prefix_len, block_table, seq_lens, out, lse)
     ks, vs, pages, kv_heads = _caches(k, v, False)
     batch, cols, bt_stride = _requests(block_table, seq_lens)
     rows = batch * q_len
@@ -317,6 +325,7 @@ def msa_attention_prefix(q, k, v, prefix_table, prefix_len, block_table, seq_len
     include/msa_attention.h.
     """
     q_stride, ks, vs, pages, bound, bt_stride, sizes = _prefix_shapes(
+        _place(workspace),
         _layout(q), _layout(k), _layout(v), _layout(prefix_table), _layout(prefix_len), _layout(block_table),
         _layout(seq_lens), _layout(out), _layout(out_lse), q_len, max_prefix_len, max_model_len)
     st = _fn("msa_attention_prefix")(

@@ -397,7 +397,9 @@ extern "C" msa_status msa_cache_evict(const int32_t *block_table, int64_t bt_str
     const bool wide = cols > 1024;
     auto *kernel = wide ? (vec ? evict_kernel<true, 1024> : evict_kernel<false, 1024>)
                         : (vec ? evict_kernel<true, 256> : evict_kernel<false, 256>);
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
+    // (up to 1024 blocks need 6 KiB, which is always granted)
+    if (wide && cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) !=
+                    cudaSuccess)
         return MSA_ERR_CUDA;
     cudaLaunchAttribute attr[1];
     const cudaLaunchConfig_t cfg =

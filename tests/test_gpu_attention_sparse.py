@@ -191,6 +191,8 @@ def test_refusals():
     for bad in (0.0, -1.0, float("nan"), float("inf")):
         assert status(scale=bad) == msa.MSA_ERR_INVALID_ARG
     assert status(ws=ws[:128]) == msa.MSA_ERR_WORKSPACE_TOO_SMALL
+    for bad in (ws.cpu(), torch.zeros(512, dtype=torch.uint8, device="cuda")[::2]):  # on the host; with gaps
+        assert status(ws=bad) == "refused"
     assert status(ids=torch.full((1, 2, 33), -1, dtype=torch.int32, device="cuda")) == msa.MSA_ERR_UNSUPPORTED
     assert status(k=kp[:1].expand(kp.shape[0], -1, -1, -1)) == msa.MSA_ERR_INVALID_ARG
     for kw in (dict(q=q.half()), dict(k=kp[..., :64]), dict(k=kp.float()), dict(ids=ids.long()), dict(out=out[:, :4]),
