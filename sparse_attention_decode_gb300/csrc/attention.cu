@@ -87,7 +87,7 @@ int block_attn_split(int64_t units, int pages, int dev)
 }
 
 template <class F, int MT, bool OWN>
-msa_status launch_block_attn(const BlockAttnParams &p, int64_t units, int split, cudaStream_t st)
+msa_status launch_block_attn(const BlockAttnParams &p, int64_t units, int split, cudaStream_t st, bool dependent = false)
 {
     const size_t smem = block_attn_smem<F>(p.mass ? (p.k + split - 1) / split : 0);
     auto *kernel = block_attn_kernel<F, MT, OWN>;
@@ -104,11 +104,11 @@ msa_status launch_block_attn(const BlockAttnParams &p, int64_t units, int split,
     attr[0].val.clusterDim.x = split;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
-    // beside prefix_attn_kernel: CTAs start where it leaves room
+    // dependent: beside prefix_attn_kernel, CTAs start where it leaves room
     attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = OWN ? 2 : 1;
+    cfg.numAttrs = dependent ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kernel, p) == cudaSuccess ? MSA_OK : MSA_ERR_CUDA;
 }
 
@@ -294,9 +294,6 @@ static msa_status prefix_entry(const void *q, int64_t q_stride, const void *k, c
     if (cudaFuncSetAttribute(prefix_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              static_cast<int>(kPrefixSmemBytes)) != cudaSuccess)
         return MSA_ERR_CUDA;
-    prefix_attn_kernel<<<p.parts.grid, kPrefixThreads, kPrefixSmemBytes, st>>>(p);
-    if (cudaGetLastError() != cudaSuccess)
-        return MSA_ERR_CUDA;
     BlockAttnParams o;
     std::memset(&o, 0, sizeof o);
     o.kmap = p.kmap;
@@ -320,14 +317,38 @@ static msa_status prefix_entry(const void *q, int64_t q_stride, const void *k, c
     o.scale_log2 = p.scale_log2;
     o.withhold = p.withhold;
     // Clusters of up to 4 (16 requests x 4 positions x 16 heads over 8192 + 37000 tokens, at that time: 155 us
-    // unsplit, 88 with 2, 65 with 4, 68 with 8; 8 x 4 x 8 over 16384 + 8000: 46, 32, 30.5, 36).
+    // unsplit, 88 with 2, 65 with 4, 68 with 8; 8 x 4 x 8 over 16384 + 8000: 46, 32, 30.5, 36), of fewer where a request
+    // cannot have as many pages (16 x 16 rows over 2048 + 300 tokens a request: 15.3 us, 17.3 with 4).
     const int64_t units = static_cast<int64_t>(batch) * kv_heads * o.row_tiles;
-    const int split = block_attn_split(units, 4, dev), unit_rows = std::min(q_len * group, kAttnMaxRows);
-    const msa_status own = unit_rows <= 16   ? launch_block_attn<AttnBf16, 1, true>(o, units, split, st)
-                           : unit_rows <= 32 ? launch_block_attn<AttnBf16, 2, true>(o, units, split, st)
-                                             : launch_block_attn<AttnBf16, 4, true>(o, units, split, st);
-    if (own != MSA_OK)
-        return own;
+    const int own_pages = p.parts.seq_limit / kPage + (p.parts.seq_limit % kPage != 0);  // at most
+    const int split = block_attn_split(units, own_pages >= 4 ? 4 : own_pages >= 2 ? 2 : 1, dev);
+    const int unit_rows = std::min(q_len * group, kAttnMaxRows);
+    auto launch_own = [&](bool dependent) {
+        return unit_rows <= 16   ? launch_block_attn<AttnBf16, 1, true>(o, units, split, st, dependent)
+               : unit_rows <= 32 ? launch_block_attn<AttnBf16, 2, true>(o, units, split, st, dependent)
+                                 : launch_block_attn<AttnBf16, 4, true>(o, units, split, st, dependent);
+    };
+    // Few own CTAs start first, on SMs kept free for them (a CTA may take one by itself), and the prefix as their
+    // dependent: it ends last, and the join waits for one grid's end instead of two in a row (2 requests over 4133
+    // tokens: 13.2 us against 13.5, over 8192: 15.9 and 16.5; 1 over 30000: 26.7 and 27.8).  Many would hold the
+    // prefix's CTAs up.
+    const bool own_first = units * split <= sms / 8;
+    if (own_first) {
+        p.parts.spare = static_cast<int>(units * split);
+        const msa_status own = launch_own(false);
+        if (own != MSA_OK)
+            return own;
+    }
+    cudaLaunchAttribute attr[1];
+    cudaLaunchConfig_t cfg = pdl_config(dim3(p.parts.grid), dim3(kPrefixThreads), kPrefixSmemBytes, st, attr);
+    cfg.numAttrs = own_first ? 1 : 0;
+    if (cudaLaunchKernelEx(&cfg, prefix_attn_kernel, p) != cudaSuccess)
+        return MSA_ERR_CUDA;
+    if (!own_first) {
+        const msa_status own = launch_own(true);
+        if (own != MSA_OK)
+            return own;
+    }
     JoinParams j;
     std::memset(&j, 0, sizeof j);
     j.parts = p.parts;

@@ -13,6 +13,7 @@
 // stream.  So the two run side by side: this kernel takes as many SMs as its share
 // of the work by the live lengths (its other CTAs end at once), and the own pages'
 // CTAs, launched as its dependents, start on the rest and follow as its CTAs end.
+// (Few own CTAs are launched first instead, and this kernel as their dependent.)
 // (64 requests over 32768 + 147000 tokens: 87 us; one after the other 125; own pages
 // as further units of this kernel 193, a few microseconds of latency for each of
 // their short runs.)
@@ -65,6 +66,7 @@ struct PrefixParts {
     int own_most;          // pages of one request that count in that comparison: their sum stays below 2^31
     int limit, seq_limit;  // bounds on the prefix's and a request's tokens
     int grid;              // CTAs prefix_attn_kernel is launched with
+    int spare;             // of them, so many take no part: their SMs are the own pages'
 };
 
 __device__ __forceinline__ int tokens_in(int n, int limit) { return n < 0 || n > limit ? 0 : n; }
@@ -87,7 +89,7 @@ struct PrefixSplit {
         const float mine = static_cast<float>(total) * (p.ways == 1 ? 2.0f : 1.0f);
         const float all = __fadd_rn(mine, __fmul_rn(static_cast<float>(own), static_cast<float>(p.own_cost * p.kv_heads) * 0.125f));
         const int most =
-            min(p.grid, max(1, __float2int_rn(__fmul_rn(static_cast<float>(p.grid), __fdividef(mine, all)))));
+            min(p.grid - p.spare, max(1, __float2int_rn(__fmul_rn(static_cast<float>(p.grid), __fdividef(mine, all)))));
         const int per_unit = (pages + kPrefixMinPages - 1) / kPrefixMinPages;
         ctas = min(most, (total + kPrefixMinPages - 1) / kPrefixMinPages);
         // The same number of CTAs for every unit where that leaves few out: no range then ends in a second unit, and
@@ -420,6 +422,8 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_attn_kernel(const __
     if (cta >= split.ctas) {
         if (warp == 9)
             tmem_dealloc(ctl->tmem, 512);
+        if (cta == 0)
+            griddep_wait();
         return;
     }
     const int P = split.pages, ways = p.parts.ways;
@@ -704,6 +708,8 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_attn_kernel(const __
     __syncthreads();
     if (warp == 9)
         tmem_dealloc(tmem, 512);
+    if (cta == 0)
+        griddep_wait();  // where the own pages' kernel was launched first: the join waits for this grid only
 }
 
 // ---------------------------------------------------------------------------
