@@ -1,8 +1,10 @@
 // Verification of drafted tokens against the target's probabilities.
 //
-// With c = log2 e / T, x = c max l as rounded and Z = sum 2^(c l - x):
-// p(v) = 2^(c l_v - x) / Z and ln p(v) = (c l_v - x - log2 Z) ln 2; x cancels, so
-// its rounding does no harm as long as every use takes the same one.  The draw is an
+// With c = log2 e / T, m = max l and Z = sum 2^(c (l - m)):
+// p(v) = 2^(c (l_v - m)) / Z and ln p(v) = (c (l_v - m) - log2 Z) ln 2.  m is a logit
+// itself, so the largest term is exactly 1 whatever c is: c l - c m in one fused
+// operation would leave the rounding of c m in the exponent, 1e-3 for l = 30000 and
+// more than an exponent holds at temperatures below 1e-7.  The draw is an
 // exponential race: the argmax of r(v) / e(v) over independent e ~ Exp(1) is v
 // with probability r(v) / sum r, so it needs no normalised cumulative sum, and
 // its argmax is the same however the vocabulary is split.
@@ -16,6 +18,7 @@
 // decided before the next is read; a few requests take all rows at once, since a
 // decision (two cluster barriers) would cost more than the rows it could save.
 #include <algorithm>
+#include <cfloat>
 #include <cmath>
 
 #include "attn_ptx.cuh"
@@ -124,30 +127,29 @@ struct Logits<uint16_t> {
     }
 };
 
-// A part of a row in log2 units: x = c max l and s = sum 2^(c l - x).  Greedy: the
-// largest logit itself (c = 1) and where it first occurs.
+// A part of a row: m = max l and s = sum 2^(c (l - m)).  Greedy: where the largest logit first occurs.
 struct RowPart {
-    float x, s;
+    float m, s;
     int i;
-    __device__ __forceinline__ void join(const RowPart &o)
+    __device__ __forceinline__ void join(const RowPart &o, float c)
     {
-        const float n = fmaxf(x, o.x);
+        const float n = fmaxf(m, o.m);
         if (n == -INFINITY)
             return;
-        i = x > o.x ? i : o.x > x ? o.i : min(i, o.i);
-        s = s * exp2_approx(x - n) + o.s * exp2_approx(o.x - n);
-        x = n;
+        i = m > o.m ? i : o.m > m ? o.i : min(i, o.i);
+        s = s * exp2_approx((m - n) * c) + o.s * exp2_approx((o.m - n) * c);
+        m = n;
     }
 };
 
 // The join of all lanes' parts, in lane order pairwise: the same for the same parts.
-__device__ __forceinline__ void warp_join(RowPart &r)
+__device__ __forceinline__ void warp_join(RowPart &r, float c)
 {
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const RowPart other{__shfl_xor_sync(0xffffffffu, r.x, o), __shfl_xor_sync(0xffffffffu, r.s, o),
+        const RowPart other{__shfl_xor_sync(0xffffffffu, r.m, o), __shfl_xor_sync(0xffffffffu, r.s, o),
                             __shfl_xor_sync(0xffffffffu, r.i, o)};
-        r.join(other);
+        r.join(other, c);
     }
 }
 
@@ -207,16 +209,16 @@ __device__ __forceinline__ float rcp_approx(float x)
 }
 
 // One CTA's best of max(p - q, 0) / e (Q) or p / e over its slice, as (value, lowest index); 0: none.
-// p = 2^(c l - x) * inv.
+// p = 2^(c (l - m)) * inv.
 template <bool ALIGNED, class T, bool Q>
 __device__ __forceinline__ uint64_t race_part(const T *row, const float *q, const float *e, int V, int rank, int ranks,
-                                              float x, float inv, float c)
+                                              float m, float inv, float c)
 {
     constexpr int N = Logits<T>::kVec;
     float best = 0.0f;
     int at = -1;
     auto value = [&](float l, float qv, float ev) {
-        const float pv = exp2_approx(fmaf(l, c, -x)) * inv;
+        const float pv = exp2_approx((l - m) * c) * inv;
         return (Q ? pv - qv : pv) * rcp_approx(ev);
     };
     const int nv = V / N;
@@ -292,7 +294,8 @@ __global__ void __launch_bounds__(kVerifyThreads, BLOCKS) verify_kernel(const __
     }
     const float temp = p.temperature ? p.temperature[b] : 1.0f;
     const bool greedy = !(temp > 0.0f);
-    const float c = greedy ? 1.0f : kVLog2e / temp;
+    // positive and finite, so that c times a difference of logits is 0 or of its sign, also at the ends of the range
+    const float c = greedy ? 1.0f : fminf(fmaxf(kVLog2e / temp, FLT_MIN), FLT_MAX);
     constexpr int N = Logits<T>::kVec;
     const int nv = V / N;
     // the drafts' tokens and numbers, on their way to shared memory beside the first rows
@@ -334,7 +337,7 @@ __global__ void __launch_bounds__(kVerifyThreads, BLOCKS) verify_kernel(const __
                         for (int e = 0; e < N; ++e)
                             top = fmaxf(top, l[w][e]);
                     }
-                    if (top * c > part.x) {  // rarer and rarer along the row
+                    if (top > part.m) {  // rarer and rarer along the row
                         if (greedy) {
 #pragma unroll
                             for (int w = H - 1; w >= 0; --w)
@@ -342,17 +345,22 @@ __global__ void __launch_bounds__(kVerifyThreads, BLOCKS) verify_kernel(const __
                                 for (int e = N - 1; e >= 0; --e)
                                     part.i = l[w][e] == top ? (v0 + (u0 + w) * ranks) * N + e : part.i;
                         }
-                        part.s *= exp2_approx(part.x - top * c);
-                        part.x = top * c;
+                        part.s *= exp2_approx((part.m - top) * c);
+                        part.m = top;
                     }
                     if (!greedy) {
-                        const float ref = part.x == -INFINITY ? 0.0f : part.x;
+                        const float ref = part.m == -INFINITY ? 0.0f : part.m;
+                        const uint64_t c2 = pack2(c, c), r2 = pack2(-ref, -ref);
                         float a[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
                         for (int w = 0; w < H; ++w)
 #pragma unroll
-                            for (int e = 0; e < N; ++e)
-                                a[(w * N + e) & 3] += exp2_approx(fmaf(l[w][e], c, -ref));
+                            for (int e = 0; e < N; e += 2) {
+                                float y, z;
+                                unpack2(mul2(add2(pack2(l[w][e], l[w][e + 1]), r2), c2), y, z);
+                                a[e & 3] += exp2_approx(y);
+                                a[(e + 1) & 3] += exp2_approx(z);
+                            }
                         part.s += (a[0] + a[1]) + (a[2] + a[3]);
                     }
                 }
@@ -371,12 +379,12 @@ __global__ void __launch_bounds__(kVerifyThreads, BLOCKS) verify_kernel(const __
             }
             const int v = nv * N + rank;  // the elements that fill no vector
             if (v < V) {
-                const float y = Logits<T>::one(row + v) * c;
-                part.join(RowPart{y, y > -INFINITY ? 1.0f : 0.0f, v});
+                const float y = Logits<T>::one(row + v);
+                part.join(RowPart{y, y > -INFINITY ? 1.0f : 0.0f, v}, c);
             }
-            warp_join(part);
+            warp_join(part, c);
             if (lane == 0) {
-                sm.wm[i][warp] = part.x;
+                sm.wm[i][warp] = part.m;
                 sm.ws[i][warp] = part.s;
                 sm.wi[i][warp] = part.i;
             }
@@ -396,9 +404,9 @@ __global__ void __launch_bounds__(kVerifyThreads, BLOCKS) verify_kernel(const __
             RowPart q{-INFINITY, 0.0f, 0x7fffffff};
             if (lane < kVerifyWarps)
                 q = RowPart{sm.wm[r][lane], sm.ws[r][lane], sm.wi[r][lane]};
-            warp_join(q);
+            warp_join(q, c);
             if (lane == 0) {
-                sm.m[r] = q.x;
+                sm.m[r] = q.m;
                 sm.s[r] = q.s;
                 sm.i[r] = q.i;
             }
@@ -412,22 +420,22 @@ __global__ void __launch_bounds__(kVerifyThreads, BLOCKS) verify_kernel(const __
                 q = RowPart{dsmem_ld_float(mapa_shared(smem_addr(&sm.m[r]), lane)),
                             dsmem_ld_float(mapa_shared(smem_addr(&sm.s[r]), lane)),
                             dsmem_ld_int(mapa_shared(smem_addr(&sm.i[r]), lane))};
-            warp_join(q);
+            warp_join(q, c);
             if (lane == 0) {
                 int ok = 0;
                 float lp = 0.0f;
-                if (r < n && sm.x[r] >= 0 && q.x > -INFINITY) {
+                if (r < n && sm.x[r] >= 0 && q.m > -INFINITY) {
                     if (greedy) {
                         ok = sm.x[r] == q.i;
                     } else {
-                        const float e = fmaf(sm.lx[r], c, -q.x);
+                        const float e = (sm.lx[r] - q.m) * c;
                         ok = sm.u[r] * sm.qx[r] < exp2_approx(e) / q.s;
                         lp = (e - log2f(q.s)) * kVLn2;
                     }
                 }
-                sm.gm[r] = q.x;
+                sm.gm[r] = q.m;
                 sm.gs[r] = q.s;
-                sm.gi[r] = q.x > -INFINITY ? q.i : -1;
+                sm.gi[r] = q.m > -INFINITY ? q.i : -1;
                 sm.ok[r] = ok;
                 sm.lp[r] = lp;
             }
@@ -442,14 +450,14 @@ __global__ void __launch_bounds__(kVerifyThreads, BLOCKS) verify_kernel(const __
     const int rank = crank * kVerifyThreads + tid, ranks = C * kVerifyThreads;
     const bool draws = !greedy && sm.gm[at] > -INFINITY;
     bool residual = draws && at < n;
-    const float x0 = sm.gm[at], inv = draws ? 1.0f / sm.gs[at] : 0.0f;
+    const float m0 = sm.gm[at], inv = draws ? 1.0f / sm.gs[at] : 0.0f;
     const T *row = logits + at * p.stride_i;
     uint64_t key = 0;
     for (int round = 0; draws && round < 2; ++round) {
         const float *q = residual ? p.draft + (static_cast<int64_t>(b) * S + at) * V : nullptr;
         const float *e = p.race + static_cast<int64_t>(b) * V;
-        uint64_t k = warp_max(residual ? race_part<ALIGNED, T, true>(row, q, e, V, rank, ranks, x0, inv, c)
-                                       : race_part<ALIGNED, T, false>(row, nullptr, e, V, rank, ranks, x0, inv, c));
+        uint64_t k = warp_max(residual ? race_part<ALIGNED, T, true>(row, q, e, V, rank, ranks, m0, inv, c)
+                                       : race_part<ALIGNED, T, false>(row, nullptr, e, V, rank, ranks, m0, inv, c));
         if (lane == 0)
             sm.wbest[warp] = k;
         __syncthreads();
@@ -469,7 +477,7 @@ __global__ void __launch_bounds__(kVerifyThreads, BLOCKS) verify_kernel(const __
         const int x = greedy ? sm.gi[at] : key ? static_cast<int>(0xffffffffu - static_cast<uint32_t>(key)) : -1;
         float lp = 0.0f;
         if (x >= 0 && !greedy)
-            lp = (fmaf(Logits<T>::one(row + x), c, -x0) - log2f(sm.gs[at])) * kVLn2;
+            lp = ((Logits<T>::one(row + x) - m0) * c - log2f(sm.gs[at])) * kVLn2;
         for (int i = lane; i <= S; i += 32) {
             const int64_t o = static_cast<int64_t>(b) * (S + 1) + i;
             p.out[o] = i < at ? p.tokens[static_cast<int64_t>(b) * S + i] : i == at ? x : -1;
