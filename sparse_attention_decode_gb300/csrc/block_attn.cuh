@@ -26,6 +26,7 @@
 #pragma once
 
 #include <algorithm>
+#include <cfloat>
 #include <cmath>
 
 #include "attn_ptx.cuh"
@@ -542,6 +543,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2) block_attn_kernel(const __gri
                     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
                     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
                     if (top > vref) {
+                        top = fmaxf(top, FLT_MIN);  // (the inverse of a subnormal scale may be infinite)
                         const float down = vref / top;
                         a0 *= down;
                         a1 *= down;
