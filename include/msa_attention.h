@@ -83,8 +83,9 @@ msa_status msa_attention_sparse(const void *q, int64_t q_stride, const void *k, 
  * The same on an E4M3 cache: K[t] = e4m3(code) * k_scale[page, head, t], V alike;
  * scales fp32 [num_pages, kv_heads, 128], contiguous, 16-byte aligned, finite
  * and >= 0.  Both products run in f16 with fp32 accumulation: codes convert
- * exactly, a query row is brought to [2^13, 2^14) by a power of two, and the
- * weights are multiplied by V's scales relative to the largest one met.
+ * exactly, a query row is brought to [2^13, 2^14) by a power of two, and a row's
+ * products of weight and V scale are held relative to the largest of them: at 11
+ * bits down to 2^-28 of it, at fewer down to 2^-38.
  */
 msa_status msa_attention_sparse_fp8(const void *q, int64_t q_stride, const void *k, const int64_t *k_strides,
                                     const float *k_scale, const void *v, const int64_t *v_strides,

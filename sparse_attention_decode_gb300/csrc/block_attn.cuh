@@ -7,8 +7,9 @@
 //     M = max_T c s,  L = sum_T 2^(c s - M),  c = log2 e,  lse_n = (M + log2 L) ln 2,
 // taken page by page with the running maximum and sum of a softmax: a part
 // (M1, L1, O1) joins another by O = 2^(M1-M) O1 + 2^(M2-M) O2 (L alike), with
-// M = max(M1, M2).  M, L and O stay in fp32; the weights 2^(c s - M) are rounded
-// once, to the operand type of the second product (bf16 beside a bf16 cache,
+// M = max(M1, M2).  (E4M3: as (M1, L1, O1 / L1), whose share is 2^(M1-M) L1 / L: no
+// larger than V itself, whatever the scales.)  M, L and O stay in fp32; the weights
+// 2^(c s - M) are rounded once, to the operand type of the second product (bf16 beside a bf16 cache,
 // f16 beside an E4M3 one), after L has taken them in full.
 //
 // What bounds it: every K and V byte is used by the 1..64 rows of one KV head
@@ -26,7 +27,6 @@
 #pragma once
 
 #include <algorithm>
-#include <cfloat>
 #include <cmath>
 
 #include "attn_ptx.cuh"
@@ -96,7 +96,7 @@ struct BlockAttnSmem {
     int abort_flag;
     float wm[kAttnWarps][16], wl[kAttnWarps][16];  // each warp's rows: running maximum (log2 units) and sum
     float cm[kAttnMaxRows], cl[kAttnMaxRows];      // the CTA's rows, read by the whole cluster
-    float rm[kAttnMaxRows], rinv[kAttnMaxRows];    // final maximum and 1 / sum
+    float rm[kAttnMaxRows], rinv[kAttnMaxRows];    // final maximum and 1 / sum (0: nothing)
     float fac[8][kAttnMaxRows];                    // what each rank's part of a row is multiplied by
 };
 
@@ -198,6 +198,14 @@ __device__ __forceinline__ float q_row_factor(float amax, float *undo)
     *undo = ldexpf(1.0f, -e);
     return ldexpf(1.0f, e);
 }
+
+// E4M3: the unit of a row's (weight x V scale) products, the largest power of two <= v, and its inverse; v within
+// [2^-112, 2^126] keeps both, and the inverse times kVTop, normal.  In f16 such a product is below 4 kVTop.
+constexpr float kVTop = 8192.0f;                   // 2^13
+constexpr float kVLeast = 1.925929944387236e-34f;  // 2^-112
+constexpr float kVMost = 8.507059173023462e37f;    // 2^126
+__device__ __forceinline__ float v_unit(float v) { return __uint_as_float(__float_as_uint(v) & 0x7f800000u); }
+__device__ __forceinline__ float v_unit_inverse(float v) { return __uint_as_float(0x7f000000u - (__float_as_uint(v) & 0x7f800000u)); }
 
 __device__ __forceinline__ float bf16_lo(uint32_t v) { return __uint_as_float(v << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
@@ -399,7 +407,9 @@ __global__ void __launch_bounds__(kAttnThreads, 2) block_attn_kernel(const __gri
             for (int e = 0; e < 4; ++e)
                 o[d][e] = 0.0f;
         float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.0f, l1 = 0.0f;
-        float vref = 0.0f, vinv = 0.0f;  // E4M3: o is held in units of vref, the largest V scale met so far; its inverse
+        // E4M3: a row's o is held in units of a power of two next to the largest (weight x V scale) met so far, at the
+        // running maximum; v0, v1 follow that product and the units their exponents
+        float v0 = kVLeast, v1 = kVLeast;
 
         bool alive = true;
         uint32_t it = 0;
@@ -528,36 +538,51 @@ __global__ void __launch_bounds__(kAttnThreads, 2) block_attn_kernel(const __gri
                         pa[j][3] = f32x2_to_bf16x2(s[2 * j + 1][2], s[2 * j + 1][3]);
                     }
                 } else {
-                    // weights times V's per-token scales, relative to the largest scale so far: at most 1 in f16
+                    // Weights times V's per-token scales in f16, relative to the largest such product of the row: in
+                    // [2^13, 2^14) at most, so that products down to 2^-28 of it keep f16's 11 bits (down to 2^-38 some).
+                    // Relative to the largest scale alone, a token with a large scale and no weight would take the bits
+                    // of all others.
                     const float *vsc = scales + s_v * kPage;
                     float2 sc[4];
-                    float top = 0.0f;
+#pragma unroll
+                    for (int f = 0; f < 4; ++f)
+                        sc[f] = *reinterpret_cast<const float2 *>(vsc + tok + f * 8 + 2 * t);
+                    if (vleft < 32) {
+#pragma unroll
+                        for (int f = 0; f < 4; ++f) {
+                            const int c = f * 8 + 2 * t;
+                            sc[f].x = c < vleft ? sc[f].x : 0.0f;
+                            sc[f].y = c + 1 < vleft ? sc[f].y : 0.0f;
+                        }
+                    }
+                    float x0 = 0.0f, x1 = 0.0f;
 #pragma unroll
                     for (int f = 0; f < 4; ++f) {
-                        const int c = f * 8 + 2 * t;
-                        sc[f] = *reinterpret_cast<const float2 *>(vsc + tok + c);
-                        sc[f].x = c < vleft ? sc[f].x : 0.0f;
-                        sc[f].y = c + 1 < vleft ? sc[f].y : 0.0f;
-                        top = fmaxf(top, fmaxf(fabsf(sc[f].x), fabsf(sc[f].y)));
-                    }
-                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                    if (top > vref) {
-                        top = fmaxf(top, FLT_MIN);  // (the inverse of a subnormal scale may be infinite)
-                        const float down = vref / top;
-                        a0 *= down;
-                        a1 *= down;
-                        vref = top;
-                        vinv = 1.0f / top;
+                        s[f][0] *= sc[f].x;
+                        s[f][1] *= sc[f].y;
+                        s[f][2] *= sc[f].x;
+                        s[f][3] *= sc[f].y;
+                        x0 = fmaxf(x0, fmaxf(fabsf(s[f][0]), fabsf(s[f][1])));
+                        x1 = fmaxf(x1, fmaxf(fabsf(s[f][2]), fabsf(s[f][3])));
                     }
 #pragma unroll
+                    for (int q = 1; q < 4; q <<= 1) {
+                        x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, q));
+                        x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, q));
+                    }
+                    const float y0 = v_unit(v0), y1 = v_unit(v1);
+                    v0 = fminf(fmaxf(fmaxf(v0 * a0, x0), kVLeast), kVMost);
+                    v1 = fminf(fmaxf(fmaxf(v1 * a1, x1), kVLeast), kVMost);
+                    const float i0 = v_unit_inverse(v0), i1 = v_unit_inverse(v1);
+                    a0 = a0 * y0 * i0;  // o from the units so far to the new ones
+                    a1 = a1 * y1 * i1;
+                    const float w0 = i0 * kVTop, w1 = i1 * kVTop;
+#pragma unroll
                     for (int j = 0; j < 2; ++j) {
-                        const float2 sa = make_float2(sc[2 * j].x * vinv, sc[2 * j].y * vinv);
-                        const float2 sb = make_float2(sc[2 * j + 1].x * vinv, sc[2 * j + 1].y * vinv);
-                        pa[j][0] = f32x2_to_f16x2(s[2 * j][0] * sa.x, s[2 * j][1] * sa.y);
-                        pa[j][1] = f32x2_to_f16x2(s[2 * j][2] * sa.x, s[2 * j][3] * sa.y);
-                        pa[j][2] = f32x2_to_f16x2(s[2 * j + 1][0] * sb.x, s[2 * j + 1][1] * sb.y);
-                        pa[j][3] = f32x2_to_f16x2(s[2 * j + 1][2] * sb.x, s[2 * j + 1][3] * sb.y);
+                        pa[j][0] = f32x2_to_f16x2(s[2 * j][0] * w0, s[2 * j][1] * w0);
+                        pa[j][1] = f32x2_to_f16x2(s[2 * j][2] * w1, s[2 * j][3] * w1);
+                        pa[j][2] = f32x2_to_f16x2(s[2 * j + 1][0] * w0, s[2 * j + 1][1] * w0);
+                        pa[j][3] = f32x2_to_f16x2(s[2 * j + 1][2] * w1, s[2 * j + 1][3] * w1);
                     }
                 }
                 if (__any_sync(0xffffffffu, a0 != 1.0f || a1 != 1.0f)) {
@@ -656,7 +681,17 @@ __global__ void __launch_bounds__(kAttnThreads, 2) block_attn_kernel(const __gri
         consumer_barrier();  // every warp has read its last tile
         float *wo = reinterpret_cast<float *>(smem);  // [warp][16][kAttnOStride]
         if (!ctl->abort_flag) {
-            const float unit_v = F::kFp8 ? vref : 1.0f;
+            const float u0 = v_unit(v0) * (1.0f / kVTop), u1 = v_unit(v1) * (1.0f / kVTop);  // E4M3
+            if (F::kFp8) {
+                const float i0 = l0 == 0.0f ? 0.0f : 1.0f / l0, i1 = l1 == 0.0f ? 0.0f : 1.0f / l1;
+#pragma unroll
+                for (int d = 0; d < 16; ++d) {
+                    o[d][0] *= i0;
+                    o[d][1] *= i0;
+                    o[d][2] *= i1;
+                    o[d][3] *= i1;
+                }
+            }
             float *at = wo + warp * 16 * kAttnOStride;
 #pragma unroll
             for (int d = 0; d < 16; d += 2) {
@@ -672,9 +707,9 @@ __global__ void __launch_bounds__(kAttnThreads, 2) block_attn_kernel(const __gri
                 } else {
                     const int col = d * 8 + 4 * t;
                     *reinterpret_cast<float4 *>(at + g * kAttnOStride + col) =
-                        make_float4(o[d][0] * unit_v, o[d + 1][0] * unit_v, o[d][1] * unit_v, o[d + 1][1] * unit_v);
+                        make_float4(o[d][0] * u0, o[d + 1][0] * u0, o[d][1] * u0, o[d + 1][1] * u0);
                     *reinterpret_cast<float4 *>(at + (g + 8) * kAttnOStride + col) =
-                        make_float4(o[d][2] * unit_v, o[d + 1][2] * unit_v, o[d][3] * unit_v, o[d + 1][3] * unit_v);
+                        make_float4(o[d][2] * u1, o[d + 1][2] * u1, o[d][3] * u1, o[d + 1][3] * u1);
                 }
             }
         }
@@ -687,12 +722,19 @@ __global__ void __launch_bounds__(kAttnThreads, 2) block_attn_kernel(const __gri
             for (int k = 0; k < KS; ++k)
                 M = fmaxf(M, ctl->wm[w0 + k * MT][r]);
             float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            float share[KS];
+#pragma unroll
+            for (int k = 0; k < KS; ++k) {
+                const float f = rescale(ctl->wm[w0 + k * MT][r], M), fl = f * ctl->wl[w0 + k * MT][r];
+                sum += fl;
+                share[k] = F::kFp8 ? fl : f;
+            }
+            const float inv = !F::kFp8 ? 1.0f : sum == 0.0f ? 0.0f : 1.0f / sum;
 #pragma unroll
             for (int k = 0; k < KS; ++k) {
                 const int w = w0 + k * MT;
-                const float f = rescale(ctl->wm[w][r], M);
+                const float f = share[k] * inv;
                 const float4 v = *reinterpret_cast<const float4 *>(wo + (w * 16 + r) * kAttnOStride + col);
-                sum += f * ctl->wl[w][r];
                 acc.x += f * v.x;
                 acc.y += f * v.y;
                 acc.z += f * v.z;
@@ -740,13 +782,21 @@ __global__ void __launch_bounds__(kAttnThreads, 2) block_attn_kernel(const __gri
 #pragma unroll
             for (int c = 0; c < 8; ++c) {
                 const float f = rescale(m[c], M);
-                sum += f * l[c];
-                ctl->fac[c][tid] = f;
+                l[c] *= f;
+                sum += l[c];
+                if (!F::kFp8)
+                    ctl->fac[c][tid] = f;
             }
             if (gave_up)
                 sum = 0.0f;
+            const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+            if (F::kFp8) {
+#pragma unroll
+                for (int c = 0; c < 8; ++c)
+                    ctl->fac[c][tid] = l[c] * inv;
+            }
             ctl->rm[tid] = M;
-            ctl->rinv[tid] = sum == 0.0f ? 0.0f : 1.0f / sum;
+            ctl->rinv[tid] = inv;
             if ((OWN || p.lse) && crank == 0) {
                 // OWN: +inf marks a part that is not whole
                 const float e = sum == 0.0f ? -INFINITY : M + log2f(sum);
@@ -771,8 +821,8 @@ __global__ void __launch_bounds__(kAttnThreads, 2) block_attn_kernel(const __gri
                     acc.z += f * v[c].z;
                     acc.w += f * v[c].w;
                 }
-            const float inv = ctl->rinv[n];
-            const bool none = inv == 0.0f;  // nothing visible: zeros
+            const bool none = ctl->rinv[n] == 0.0f;  // nothing visible: zeros
+            const float inv = F::kFp8 ? 1.0f : ctl->rinv[n];
             if (OWN) {
                 *reinterpret_cast<float4 *>(p.part + place(n) * kDim + lane * 4) =
                     make_float4(none ? 0.0f : acc.x * inv, none ? 0.0f : acc.y * inv, none ? 0.0f : acc.z * inv,
