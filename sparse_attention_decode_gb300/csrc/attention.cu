@@ -11,9 +11,6 @@ bool test_withhold_pages();  // msa_indexer_test_withhold_pages
 // (page, token, head).  The stride of an axis of length 1 is never used.
 bool make_cache_map(CUtensorMap *map, const void *base, const int64_t *strides, int64_t pages, int heads, bool fp8)
 {
-    EncodeTiledFn enc = encode_tiled();
-    if (!enc)
-        return false;
     const cuuint64_t size = fp8 ? 1 : 2;
     const cuuint64_t dims[4] = {static_cast<cuuint64_t>(kDim), static_cast<cuuint64_t>(kPage),
                                 static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(pages)};
@@ -22,9 +19,10 @@ bool make_cache_map(CUtensorMap *map, const void *base, const int64_t *strides, 
                                  static_cast<cuuint64_t>(pages > 1 ? strides[0] : kDim) * size};
     const cuuint32_t box[4] = {fp8 ? 128u : 64u, 128u, 1u, 1u};
     const cuuint32_t estr[4] = {1, 1, 1, 1};
-    return enc(map, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base),
-               dims, bytes, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    return encode_map(map, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+                      const_cast<void *>(base), dims, bytes, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                      CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
 // A cache's address and strides: 16-byte multiples, positive, within a tensor map's 2^40-byte strides.

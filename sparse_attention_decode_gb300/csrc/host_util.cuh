@@ -53,6 +53,22 @@ static EncodeTiledFn encode_tiled()
     return fn;
 }
 
+// Encodes a tensor map (the arguments of cuTensorMapEncodeTiled).  The encoder
+// wants a context that is current on the calling thread, and a thread whose first
+// CUDA call this is has none yet: the runtime's is bound then and the map encoded.
+template <class... Args>
+static bool encode_map(Args... args)
+{
+    EncodeTiledFn enc = encode_tiled();
+    if (!enc)
+        return false;
+    CUresult r = enc(args...);
+    int dev = 0;
+    if (r == CUDA_ERROR_INVALID_CONTEXT && cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess)
+        r = enc(args...);
+    return r == CUDA_SUCCESS;
+}
+
 constexpr int kMaxDevices = 64;
 
 static int device_sms(int dev)

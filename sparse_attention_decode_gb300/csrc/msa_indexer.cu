@@ -1280,19 +1280,16 @@ bool test_withhold_pages() { return g_withhold_pages.load(std::memory_order_rela
 template <class F>
 static bool make_pool_map(CUtensorMap *map, const void *pool, int64_t num_pages)
 {
-    EncodeTiledFn enc = encode_tiled();
-    if (!enc)
-        return false;
     const cuuint64_t elem = F::kFp8 ? 1 : 2;
     const cuuint64_t dims[2] = {static_cast<cuuint64_t>(kDim),
                                 static_cast<cuuint64_t>(num_pages) * kPage};
     const cuuint64_t strides[1] = {static_cast<cuuint64_t>(kDim) * elem};
     const cuuint32_t box[2] = {F::kFp8 ? 128u : 64u, static_cast<cuuint32_t>(kPage)};
     const cuuint32_t estr[2] = {1, 1};
-    return enc(map, F::kFp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
-               const_cast<void *>(pool), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    return encode_map(map, F::kFp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
+                      const_cast<void *>(pool), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                      CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
 template <int KMAX, class F, int NQ>
