@@ -42,6 +42,13 @@ bool cache_ok(const void *base, const int64_t *strides, int64_t pages, int heads
 
 bool unaligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) != 0; }
 
+template <class F, int MT, bool OWN>
+bool block_attn_allowed(int dev)
+{
+    static std::atomic<bool> done[kMaxDevices];
+    return allow_smem(block_attn_kernel<F, MT, OWN>, block_attn_smem<F>(MSA_MAX_TOPK), dev, done);
+}
+
 // Clusters of `size` CTAs (two an SM) that the device runs at the same time: those of 4 or 8 do not fill it, as a
 // cluster stays within one of its parts.  0 where the query fails.
 int resident_clusters(int dev, int size)
@@ -64,7 +71,7 @@ int resident_clusters(int dev, int size)
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess ||
+    if (!block_attn_allowed<AttnBf16, 1, false>(dev) ||
         cudaOccupancyMaxActiveClusters(&v, kernel, &cfg) != cudaSuccess)
         return 0;
     if (dev >= 0 && dev < kMaxDevices)
@@ -85,11 +92,12 @@ int block_attn_split(int64_t units, int pages, int dev)
 }
 
 template <class F, int MT, bool OWN>
-msa_status launch_block_attn(const BlockAttnParams &p, int64_t units, int split, cudaStream_t st, bool dependent = false)
+msa_status launch_block_attn(const BlockAttnParams &p, int64_t units, int split, int dev, cudaStream_t st,
+                             bool dependent = false)
 {
     const size_t smem = block_attn_smem<F>(p.mass ? (p.k + split - 1) / split : 0);
     auto *kernel = block_attn_kernel<F, MT, OWN>;
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
+    if (!block_attn_allowed<F, MT, OWN>(dev))
         return MSA_ERR_CUDA;
     cudaLaunchConfig_t cfg;
     std::memset(&cfg, 0, sizeof cfg);
@@ -171,12 +179,12 @@ static msa_status sparse_entry(const void *q, int64_t q_stride, const void *k, c
     const int split = block_attn_split(units, topk, dev);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (fp8)
-        return group <= 16   ? launch_block_attn<AttnFp8, 1, false>(p, units, split, st)
-               : group <= 32 ? launch_block_attn<AttnFp8, 2, false>(p, units, split, st)
-                             : launch_block_attn<AttnFp8, 4, false>(p, units, split, st);
-    return group <= 16   ? launch_block_attn<AttnBf16, 1, false>(p, units, split, st)
-           : group <= 32 ? launch_block_attn<AttnBf16, 2, false>(p, units, split, st)
-                         : launch_block_attn<AttnBf16, 4, false>(p, units, split, st);
+        return group <= 16   ? launch_block_attn<AttnFp8, 1, false>(p, units, split, dev, st)
+               : group <= 32 ? launch_block_attn<AttnFp8, 2, false>(p, units, split, dev, st)
+                             : launch_block_attn<AttnFp8, 4, false>(p, units, split, dev, st);
+    return group <= 16   ? launch_block_attn<AttnBf16, 1, false>(p, units, split, dev, st)
+           : group <= 32 ? launch_block_attn<AttnBf16, 2, false>(p, units, split, dev, st)
+                         : launch_block_attn<AttnBf16, 4, false>(p, units, split, dev, st);
 }
 
 // The units of a batch's rows (a tile of 128 rows of a KV head where they do not fill more).
@@ -289,8 +297,8 @@ static msa_status prefix_entry(const void *q, int64_t q_stride, const void *k, c
     p.parts.seq_limit = static_cast<int>(std::min<int64_t>(max_model_len, kPage * bt_stride));
     p.parts.grid = std::min(sms, kPrefixMaxGrid);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (cudaFuncSetAttribute(prefix_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             static_cast<int>(kPrefixSmemBytes)) != cudaSuccess)
+    static std::atomic<bool> allowed[kMaxDevices];
+    if (!allow_smem(prefix_attn_kernel, kPrefixSmemBytes, dev, allowed))
         return MSA_ERR_CUDA;
     BlockAttnParams o;
     std::memset(&o, 0, sizeof o);
@@ -322,9 +330,9 @@ static msa_status prefix_entry(const void *q, int64_t q_stride, const void *k, c
     const int split = block_attn_split(units, own_pages >= 4 ? 4 : own_pages >= 2 ? 2 : 1, dev);
     const int unit_rows = std::min(q_len * group, kAttnMaxRows);
     auto launch_own = [&](bool dependent) {
-        return unit_rows <= 16   ? launch_block_attn<AttnBf16, 1, true>(o, units, split, st, dependent)
-               : unit_rows <= 32 ? launch_block_attn<AttnBf16, 2, true>(o, units, split, st, dependent)
-                                 : launch_block_attn<AttnBf16, 4, true>(o, units, split, st, dependent);
+        return unit_rows <= 16   ? launch_block_attn<AttnBf16, 1, true>(o, units, split, dev, st, dependent)
+               : unit_rows <= 32 ? launch_block_attn<AttnBf16, 2, true>(o, units, split, dev, st, dependent)
+                                 : launch_block_attn<AttnBf16, 4, true>(o, units, split, dev, st, dependent);
     };
     // Few own CTAs start first, on SMs kept free for them (a CTA may take one by itself), and the prefix as their
     // dependent: it ends last, and the join waits for one grid's end instead of two in a row (2 requests over 4133

@@ -335,6 +335,9 @@ __global__ void __launch_bounds__(T, 2) evict_kernel(const __grid_constant__ Evi
 
 using namespace msa;
 
+// Keys of all blocks, then the list of their numbers.
+static size_t evict_smem_bytes(int64_t cols) { return (static_cast<size_t>(cols) + 3) / 4 * 16 + static_cast<size_t>(cols) * 2; }
+
 extern "C" msa_status msa_cache_accumulate(float *weights, int64_t cols, const int32_t *ids, const float *mass,
                                            const int32_t *n_rows, int batch, int q_len, int kv_heads, int sel_heads,
                                            int topk, void *workspace, size_t workspace_bytes, void *stream)
@@ -392,14 +395,16 @@ extern "C" msa_status msa_cache_evict(const int32_t *block_table, int64_t bt_str
     p.n_sink = n_sink;
     p.n_window = n_window;
     p.apart = out_table != block_table && out_weights != weights;
-    const size_t smem = (static_cast<size_t>(cols) + 3) / 4 * 16 + static_cast<size_t>(cols) * 2;
+    const size_t smem = evict_smem_bytes(cols);
     const bool vec = cols % 4 == 0 && ((reinterpret_cast<uintptr_t>(weights) | reinterpret_cast<uintptr_t>(out_weights)) & 15) == 0;
     const bool wide = cols > 1024;
     auto *kernel = wide ? (vec ? evict_kernel<true, 1024> : evict_kernel<false, 1024>)
                         : (vec ? evict_kernel<true, 256> : evict_kernel<false, 256>);
     // (up to 1024 blocks need 6 KiB, which is always granted)
-    if (wide && cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) !=
-                    cudaSuccess)
+    static std::atomic<bool> allowed[2][kMaxDevices];
+    int dev = 0;
+    if (wide && (cudaGetDevice(&dev) != cudaSuccess ||
+                 !allow_smem(kernel, evict_smem_bytes(MSA_MAX_CACHE_BLOCKS), dev, allowed[vec])))
         return MSA_ERR_CUDA;
     cudaLaunchAttribute attr[1];
     const cudaLaunchConfig_t cfg =

@@ -84,6 +84,23 @@ static int device_sms(int dev)
     return v;
 }
 
+// Lets `kernel` be launched with up to `most` bytes of dynamic shared memory on
+// device `dev`, once (`done`: the kernel's own flags).  The setting belongs to the
+// process: `most` is what the largest call asks for, whatever the call at hand
+// does, so that no thread's launch meets a smaller one set by another.
+template <class Kernel>
+static bool allow_smem(Kernel *kernel, size_t most, int dev, std::atomic<bool> (&done)[kMaxDevices])
+{
+    const bool known = dev >= 0 && dev < kMaxDevices;
+    if (known && done[dev].load(std::memory_order_acquire))
+        return true;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(most)) != cudaSuccess)
+        return false;
+    if (known)
+        done[dev].store(true, std::memory_order_release);
+    return true;
+}
+
 // L2 size of device `dev` in bytes (0 when the query fails).
 static int64_t device_l2_bytes(int dev)
 {
