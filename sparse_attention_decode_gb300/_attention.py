@@ -1,9 +1,10 @@
 """Binding of the serving operators declared in include/msa_attention.h (argument marshalling only).
 
 Like the indexer's calls: each function has the name of the C entry point it calls, takes torch CUDA tensors,
-enqueues on the current stream (or ``stream=``) and raises MsaError on a bad status.  A decode step makes these calls
-at the same shapes again and again, so what follows from shapes, strides and types alone (the checks, and the
-numbers handed to C) is worked out once per combination; addresses are read on every call.
+enqueues on the current stream (or ``stream=``) of the current device, which the tensors have to be on, and raises
+MsaError on a bad status.  A decode step makes these calls at the same shapes again and again, so what follows from
+shapes, strides and types alone (the checks, and the numbers handed to C) is worked out once per combination;
+addresses are read on every call.
 """
 
 from __future__ import annotations
@@ -69,15 +70,21 @@ def _layout(t):
     return None if t is None else (t.shape, t.stride(), t.dtype, t.get_device())
 
 
+def _current_device() -> int:
+    return torch._C._cuda_getDevice()
+
+
 def _place(workspace):
-    """Device number of a workspace; one with gaps has none."""
-    return workspace.get_device() if workspace.is_contiguous() else -1
+    """Device number of a workspace; one with gaps, or on a device that is not the current one, has none."""
+    place = workspace.get_device()
+    return place if place >= 0 and workspace.is_contiguous() and place == _current_device() else -1
 
 
 def _one_device(place, *layouts):
-    """All tensors and the workspace on one CUDA device: an address of another would be a fault."""
+    """All tensors and the workspace on the current CUDA device, where C launches: another's address would be a fault."""
     devices = {x[3] for x in layouts if x is not None}
-    assert devices == {place} and place >= 0, "all tensors and a contiguous workspace on one CUDA device"
+    assert devices == {place} and place >= 0, \
+        "all tensors and a contiguous workspace on one CUDA device, the current one"
 
 
 def _stream(stream, t):
