@@ -144,6 +144,12 @@ def _requests(block_table, seq_lens):
     return batch, cols, (s[0] if batch > 1 else cols)
 
 
+def _length_limit(cols: int, max_model_len: Optional[int]) -> int:
+    """Tokens a request may have: a row of the table given ends after its columns, also inside a wider table."""
+    tokens = MSA_PAGE_TOKENS * cols
+    return tokens if max_model_len is None else min(tokens, max_model_len)
+
+
 @_shapes
 def _sparse_shapes(place, q, k, k_scale, v, v_scale, block_table, seq_lens, ids, out, lse, mass, q_len, max_model_len):
     _one_device(place, q, k, k_scale, v, v_scale, block_table, seq_lens, ids, out, lse, mass)
@@ -160,7 +166,7 @@ def _sparse_shapes(place, q, k, k_scale, v, v_scale, block_table, seq_lens, ids,
             _whole(scale, _F32, (pages, kv_heads, MSA_PAGE_TOKENS), "scales")
     _whole(lse, _F32, (rows, heads), "out_lse", True)
     _whole(mass, _F32, (rows, kv_heads, topk), "out_mass", True)
-    limit = MSA_PAGE_TOKENS * cols if max_model_len is None else max_model_len
+    limit = _length_limit(cols, max_model_len)
     return q_stride, ks, vs, pages, bt_stride, (batch, q_len, kv_heads, heads // kv_heads, limit), sel, topk
 
 
@@ -238,7 +244,7 @@ def _evict_shapes(place, block_table, seq_lens, weights, out_table, out_seq_lens
     _whole(out_weights, _F32, shape, "out_weights")
     _whole(out_freed, _I32, (batch, cols), "out_freed")
     _whole(out_n_freed, _I32, (batch,), "out_n_freed")
-    limit = MSA_PAGE_TOKENS * cols if max_model_len is None else max_model_len
+    limit = _length_limit(cols, max_model_len)
     return bt_stride, o_stride, (cols, batch, shape[1], limit)
 
 
@@ -318,7 +324,7 @@ def _prefix_shapes(place, q, k, v, prefix_table, prefix_len, block_table, seq_le
     bound = MSA_PAGE_TOKENS * int(prefix_table[0][0])
     assert max_prefix_len is None or max_prefix_len <= bound, "max_prefix_len: within prefix_table"
     _whole(lse, _F32, (rows, heads), "out_lse", True)
-    limit = MSA_PAGE_TOKENS * cols if max_model_len is None else max_model_len
+    limit = _length_limit(cols, max_model_len)
     return (q_stride, ks, vs, pages, bound if max_prefix_len is None else max_prefix_len, bt_stride,
             (batch, q_len, kv_heads, heads // kv_heads, limit))
 

@@ -98,3 +98,16 @@ def test_tensors_on_a_gpu_that_is_not_current_are_refused(calls, monkeypatch, ca
     with pytest.raises(AssertionError, match="current"):
         call()
     assert len(calls) == 2
+
+
+@pytest.mark.parametrize("call,limit_at", [(sparse, 14), (prefix, 17), (evict, 7)])
+def test_a_request_is_no_longer_than_its_columns_of_the_table(calls, call, limit_at):
+    """A table that is some columns of a wider one: what lies behind them is not the request's, and past the last row no
+    one's."""
+    columns = {} if call is evict else dict(cols=8, stride=100)
+    for given, want in ((None, 1024), (700, 700), (1024, 1024), (12800, 1024), (1 << 20, 1024)):
+        calls.clear()
+        call(max_model_len=given, **columns)
+        assert calls[0][1][limit_at] == want
+    if columns:
+        assert 100 in calls[0][1]  # the rows' distance is passed on as it is
