@@ -5,13 +5,14 @@
  * Shared conventions.  Pointers are device memory of the caller unless said
  * otherwise; work is enqueued on `stream` (a cudaStream_t as void*) and can be
  * captured in a CUDA graph; nothing is allocated and nothing synchronised.
- * Argument errors are returned before anything is enqueued.  Bad device data
- * (a length, page id, block id or token out of range) never faults: the entry
- * counts as absent and a bit is set in the workspace fault word, read and
- * cleared by msa_indexer_get_error().  Every workspace is 256-byte aligned and
- * zero-filled once before its first use; an indexer workspace does where 256
- * bytes are asked for.  Calls that may overlap on the GPU need their own.
- * Results do not depend on the order in which thread blocks run.
+ * Argument errors are returned before anything is enqueued.  A batch of 0 does
+ * nothing and needs no pointers.  Bad device data (a length, page id, block id or
+ * token out of range) never faults: the entry counts as absent and a bit is set in
+ * the workspace fault word, read and cleared by msa_indexer_get_error().  Every
+ * workspace is 256-byte aligned and zero-filled once before its first use; an
+ * indexer workspace does where 256 bytes are asked for.  Calls that may overlap on
+ * the GPU need their own.  Results do not depend on the order in which thread
+ * blocks run.
  *
  * The paged K/V cache.  Pages of 128 tokens, `kv_heads` heads of dimension 128;
  * element (page, token, head, dim) of K lies at
@@ -101,8 +102,9 @@ msa_status msa_attention_sparse_fp8(const void *q, int64_t q_stride, const void 
  * tokens of its own (none where that is negative).  Same formula, same out and
  * out_lse as msa_attention_sparse, over all of these tokens.
  *
- *   prefix_table   int32 [ceil(max_prefix_len / 128)]: the prefix's pages.  Pages x
- *                  KV heads x tiles of 256 rows of a head are at most 2^30.
+ *   prefix_table   int32 [ceil(max_prefix_len / 128)]: the prefix's pages (NULL where
+ *                  max_prefix_len is 0).  Pages x KV heads x tiles of 256 rows of a head
+ *                  are at most 2^30.
  *   prefix_len     device int32 [1], in [0, max_prefix_len] (outside: 0).
  *   block_table, seq_lens   each request's own pages and own tokens.
  *   workspace      at least msa_attention_prefix_workspace_bytes(batch * q_len,

@@ -132,6 +132,8 @@ static msa_status sparse_entry(const void *q, int64_t q_stride, const void *k, c
     if (batch > MSA_MAX_BATCH || num_pages > (int64_t{1} << 24) || topk > MSA_MAX_TOPK || group > MSA_MAX_GROUP ||
         kv_heads > 1024 || q_len > 64 || static_cast<int64_t>(batch) * q_len * kv_heads > (int64_t{1} << 27))
         return MSA_ERR_UNSUPPORTED;
+    if (batch == 0)  // (an empty tensor has no address)
+        return MSA_OK;
     if (!q || !block_table || !seq_lens || !ids || !out || !workspace || !cache_ok(k, k_strides, num_pages, kv_heads, fp8) ||
         !cache_ok(v, v_strides, num_pages, kv_heads, fp8) || unaligned(q, 16) || q_stride % 8 ||
         q_stride < static_cast<int64_t>(kv_heads) * group * kDim || unaligned(out, 16) || unaligned(workspace, 256))
@@ -140,8 +142,6 @@ static msa_status sparse_entry(const void *q, int64_t q_stride, const void *k, c
         return MSA_ERR_INVALID_ARG;
     if (workspace_bytes < kHeaderBytes)
         return MSA_ERR_WORKSPACE_TOO_SMALL;
-    if (batch == 0)
-        return MSA_OK;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess)
         return MSA_ERR_CUDA;
@@ -262,7 +262,9 @@ static msa_status prefix_entry(const void *q, int64_t q_stride, const void *k, c
     if (batch > MSA_MAX_BATCH || num_pages > (int64_t{1} << 24) || group > MSA_MAX_GROUP || kv_heads > 1024 ||
         q_len > 64 || static_cast<int64_t>(batch) * q_len * kv_heads * group > (int64_t{1} << 27))
         return MSA_ERR_UNSUPPORTED;
-    if (!q || !block_table || !seq_lens || !prefix_table || !prefix_len || !out || !workspace ||
+    if (batch == 0)  // (an empty tensor has no address)
+        return MSA_OK;
+    if (!q || !block_table || !seq_lens || (!prefix_table && max_prefix_len > 0) || !prefix_len || !out || !workspace ||
         !cache_ok(k, k_strides, num_pages, kv_heads, false) || !cache_ok(v, v_strides, num_pages, kv_heads, false) ||
         unaligned(q, 16) || q_stride % 8 || q_stride < static_cast<int64_t>(kv_heads) * group * kDim ||
         unaligned(out, 16) || unaligned(workspace, 256))
@@ -274,8 +276,6 @@ static msa_status prefix_entry(const void *q, int64_t q_stride, const void *k, c
     prefix_parts(p.parts, batch, q_len, group, kv_heads, max_prefix_len, static_cast<uint8_t *>(workspace));
     if ((static_cast<int64_t>(max_prefix_len) + kPage - 1) / kPage * p.parts.units > (1 << 30))
         return MSA_ERR_UNSUPPORTED;
-    if (batch == 0)
-        return MSA_OK;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess)
         return MSA_ERR_CUDA;

@@ -342,15 +342,16 @@ extern "C" msa_status msa_cache_accumulate(float *weights, int64_t cols, const i
                                            const int32_t *n_rows, int batch, int q_len, int kv_heads, int sel_heads,
                                            int topk, void *workspace, size_t workspace_bytes, void *stream)
 {
-    if (batch < 0 || q_len < 1 || kv_heads < 1 || sel_heads < 1 || topk < 1 || cols < 1 || kv_heads % sel_heads ||
-        !weights || !ids || !mass || !workspace || (reinterpret_cast<uintptr_t>(workspace) & 255))
+    if (batch < 0 || q_len < 1 || kv_heads < 1 || sel_heads < 1 || topk < 1 || cols < 1 || kv_heads % sel_heads)
+        return MSA_ERR_INVALID_ARG;
+    if (batch > 0 && (!weights || !ids || !mass || !workspace || (reinterpret_cast<uintptr_t>(workspace) & 255)))
         return MSA_ERR_INVALID_ARG;
     if (batch > MSA_MAX_BATCH || topk > MSA_MAX_TOPK || kv_heads > 1024 || q_len > 64 || cols > (int64_t{1} << 30))
         return MSA_ERR_UNSUPPORTED;
+    if (batch == 0)  // (an empty tensor has no address)
+        return MSA_OK;
     if (workspace_bytes < kHeaderBytes)
         return MSA_ERR_WORKSPACE_TOO_SMALL;
-    if (batch == 0)
-        return MSA_OK;
     const int64_t warps = static_cast<int64_t>(batch) * kv_heads;
     accumulate_kernel<<<static_cast<unsigned>((warps + 3) / 4), 128, 0, static_cast<cudaStream_t>(stream)>>>(
         weights, cols, ids, mass, n_rows, batch, q_len, kv_heads, sel_heads, topk,
@@ -365,16 +366,17 @@ extern "C" msa_status msa_cache_evict(const int32_t *block_table, int64_t bt_str
                                       int32_t *out_n_freed, void *workspace, size_t workspace_bytes, void *stream)
 {
     if (batch < 0 || kv_heads < 1 || cols < 1 || max_model_len < 1 || n_sink < 0 || n_window < 1 ||
-        static_cast<int64_t>(n_sink) + n_window > budget || bt_stride < cols || out_stride < cols || !block_table ||
-        !seq_lens || !weights || !out_table || !out_seq_lens || !out_weights || !out_freed || !out_n_freed ||
-        !workspace || (reinterpret_cast<uintptr_t>(workspace) & 255))
+        static_cast<int64_t>(n_sink) + n_window > budget || bt_stride < cols || out_stride < cols)
+        return MSA_ERR_INVALID_ARG;
+    if (batch > 0 && (!block_table || !seq_lens || !weights || !out_table || !out_seq_lens || !out_weights ||
+                      !out_freed || !out_n_freed || !workspace || (reinterpret_cast<uintptr_t>(workspace) & 255)))
         return MSA_ERR_INVALID_ARG;
     if (batch > MSA_MAX_BATCH || kv_heads > 1024 || cols > MSA_MAX_CACHE_BLOCKS)
         return MSA_ERR_UNSUPPORTED;
-    if (workspace_bytes < kHeaderBytes)
-        return MSA_ERR_WORKSPACE_TOO_SMALL;
     if (batch == 0)
         return MSA_OK;
+    if (workspace_bytes < kHeaderBytes)
+        return MSA_ERR_WORKSPACE_TOO_SMALL;
     EvictParams p;
     std::memset(&p, 0, sizeof p);
     p.table = block_table;

@@ -520,9 +520,11 @@ extern "C" msa_status msa_verify_draft(const void *logits, int logits_bf16, int6
                                        int32_t *out_tokens, int32_t *out_accepted, float *out_logprobs,
                                        void *workspace, size_t workspace_bytes, void *stream)
 {
-    if (batch < 0 || max_draft < 0 || vocab < 1 || !logits || !race || !out_tokens || !out_accepted || !workspace ||
-        (max_draft > 0 && (!draft_probs || !draft_tokens || !uniforms)) || logits_stride_i < vocab ||
-        logits_stride_b < vocab || (reinterpret_cast<uintptr_t>(workspace) & 255))
+    if (batch < 0 || max_draft < 0 || vocab < 1 || logits_stride_i < vocab || logits_stride_b < vocab)
+        return MSA_ERR_INVALID_ARG;
+    if (batch > 0 && (!logits || !race || !out_tokens || !out_accepted || !workspace ||
+                      (max_draft > 0 && (!draft_probs || !draft_tokens || !uniforms)) ||
+                      (reinterpret_cast<uintptr_t>(workspace) & 255)))
         return MSA_ERR_INVALID_ARG;
     const uintptr_t size = logits_bf16 ? 2 : 4;
     if ((reinterpret_cast<uintptr_t>(logits) & (size - 1)) ||
@@ -530,10 +532,10 @@ extern "C" msa_status msa_verify_draft(const void *logits, int logits_bf16, int6
         return MSA_ERR_INVALID_ARG;
     if (batch > MSA_MAX_BATCH || max_draft > MSA_MAX_DRAFT || vocab > (1 << 24))
         return MSA_ERR_UNSUPPORTED;
+    if (batch == 0)  // (an empty tensor has no address)
+        return MSA_OK;
     if (workspace_bytes < kHeaderBytes)
         return MSA_ERR_WORKSPACE_TOO_SMALL;
-    if (batch == 0)
-        return MSA_OK;
     VerifyParams p;
     std::memset(&p, 0, sizeof p);
     p.logits = logits;
