@@ -273,10 +273,12 @@ __device__ __forceinline__ void async_word(void *dst, const void *src)
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
 }
 
-// ALIGNED: every row of every input starts on 16 bytes.  BLOCKS: CTAs an SM: 3
-// without spills where the work of one thread sets the time, 4 (64 registers, some
-// spills) where the number of loads in flight does (256 x 163840 fp32: 175 and
-// 147 us; 32 x 100003 bf16: 22 and 28 us).
+// ALIGNED: every row of every input starts on 16 bytes.  BLOCKS: CTAs an SM.  3, without
+// spills, where the work of one thread sets the time: few requests, and many whose bf16
+// rows are shifted into place (32 x 100003 bf16: 22 us, 29 with 4; 120: 67 and 81; 256:
+// 107 and 133).  4 (64 registers, some spills) where the number of loads in flight does:
+// many requests otherwise (256 x 163840 fp32: 143 us, 175 with 3; 256 x 100003 fp32: 118
+// and 128; 256 x 100000 bf16: 67 and 81).
 template <class T, bool ALIGNED, int BLOCKS>
 __global__ void __launch_bounds__(kVerifyThreads, BLOCKS) verify_kernel(const __grid_constant__ VerifyParams p)
 {
@@ -572,9 +574,10 @@ extern "C" msa_status msa_verify_draft(const void *logits, int logits_bf16, int6
                           15) == 0;
     const auto run = [&](auto one) {
         using T = decltype(one);
+        constexpr int kShifted = sizeof(T) == 2 ? 3 : 4;
         if (many)
             return aligned ? launch_verify<T, true, 4>(p, batch, cluster, st)
-                           : launch_verify<T, false, 4>(p, batch, cluster, st);
+                           : launch_verify<T, false, kShifted>(p, batch, cluster, st);
         return aligned ? launch_verify<T, true, 3>(p, batch, cluster, st)
                        : launch_verify<T, false, 3>(p, batch, cluster, st);
     };
