@@ -353,10 +353,15 @@ extern "C" msa_status msa_cache_accumulate(float *weights, int64_t cols, const i
     if (workspace_bytes < kHeaderBytes)
         return MSA_ERR_WORKSPACE_TOO_SMALL;
     const int64_t warps = static_cast<int64_t>(batch) * kv_heads;
-    accumulate_kernel<<<static_cast<unsigned>((warps + 3) / 4), 128, 0, static_cast<cudaStream_t>(stream)>>>(
-        weights, cols, ids, mass, n_rows, batch, q_len, kv_heads, sel_heads, topk,
-        &static_cast<WorkspaceHeader *>(workspace)->fault);
-    return cudaGetLastError() == cudaSuccess ? MSA_OK : MSA_ERR_CUDA;
+    cudaLaunchConfig_t cfg;
+    std::memset(&cfg, 0, sizeof cfg);
+    cfg.gridDim = dim3(static_cast<unsigned>((warps + 3) / 4));
+    cfg.blockDim = dim3(128);
+    cfg.stream = static_cast<cudaStream_t>(stream);
+    return cudaLaunchKernelEx(&cfg, accumulate_kernel, weights, cols, ids, mass, n_rows, batch, q_len, kv_heads, sel_heads,
+                              topk, &static_cast<WorkspaceHeader *>(workspace)->fault) == cudaSuccess
+               ? MSA_OK
+               : MSA_ERR_CUDA;
 }
 
 extern "C" msa_status msa_cache_evict(const int32_t *block_table, int64_t bt_stride, const int32_t *seq_lens,
