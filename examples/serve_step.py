@@ -41,9 +41,11 @@ def make_step(lens, prompt, vocab, seed=0):
     prompt_pages = -(-prompt // PAGE)
     pages = prompt_pages + B * cols
     order = torch.randperm(pages, device="cuda", generator=g).to(torch.int32)
+    held = torch.tensor([[j < -(-n // PAGE) for j in range(cols)] for n in lens], device="cuda")
+    table = torch.where(held, order[prompt_pages:].view(B, cols), torch.full((1,), -1, dtype=torch.int32, device="cuda"))
     s = dict(
         seq=torch.tensor(lens, dtype=torch.int32, device="cuda"),
-        table=order[prompt_pages:].view(B, cols).contiguous(),
+        table=table,
         prompt_table=order[:prompt_pages].contiguous(),
         prompt_len=torch.tensor([prompt], dtype=torch.int32, device="cuda"),
         # head-major pages: a page's tile of one KV head is contiguous
@@ -96,7 +98,8 @@ def step(s, budget):
                          temperature=s["temperature"], out_logprobs=logp)
 
     # 5. the mass of the positions that count (the one before the first draft, then the accepted drafts); the refused
-    # drafts' tokens leave the cache's end, the lightest pages of requests over their budget its middle
+    # drafts' tokens leave the cache's end, the lightest pages of requests over their budget its middle (a page that held
+    # refused drafts alone leaves the table unlisted: a server takes its number from the table before this call)
     msa.msa_cache_accumulate(s["weights"], ids, mass, ws, q_len=q_len, n_rows=accepted + 1)
     s["seq"] -= DRAFTS - accepted
     freed, n_freed = torch.empty_like(s["table"]), empty(B, dtype=torch.int32)

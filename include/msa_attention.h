@@ -152,7 +152,9 @@ msa_status msa_cache_accumulate(float *weights, int64_t cols, const int32_t *ids
  *   weights       fp32 [batch, kv_heads, cols], contiguous.
  *   budget        >= n_sink + n_window; n_window >= 1 (the last block, which is
  *                 being filled, stays).
- *   out_table     int32 [batch, out_stride]: the kept blocks' pages, then -1.
+ *   out_table     int32 [batch, out_stride]: the kept blocks' pages, then -1.  What lay
+ *                 past a request's last block (pages allocated ahead, or left by
+ *                 refused drafts) is in neither list: note it before writing in place.
  *   out_seq_lens  int32 [batch]: 128 less for each block that left.
  *   out_weights   fp32 [batch, kv_heads, cols]: the kept blocks' weights, then 0.
  *   out_freed     int32 [batch, cols]: the pages that left, in block order, then -1.
