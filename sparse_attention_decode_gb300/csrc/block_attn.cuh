@@ -39,9 +39,6 @@
 
 namespace msa {
 
-constexpr float kLn2 = 0.69314718055994531f;
-constexpr float kLog2e = 1.4426950408889634f;
-
 // Tiles of the cache: bf16 as two 16 KiB halves of 64 dims, E4M3 as one 16 KiB
 // tile and its 128 per-token scales; 128-byte rows in the TMA 128-byte swizzle.
 struct AttnBf16 {
@@ -110,33 +107,6 @@ __host__ __device__ constexpr size_t block_attn_smem(int mass_pages)
            block_attn_mass_bytes(mass_pages);
 }
 
-__device__ __forceinline__ float dsmem_ld_f32(uint32_t addr)
-{
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
-    return v;
-}
-__device__ __forceinline__ float4 dsmem_ld_f32x4(uint32_t addr)
-{
-    float4 v;
-    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                 : "r"(addr)
-                 : "memory");
-    return v;
-}
-__device__ __forceinline__ int dsmem_ld_s32(uint32_t addr)
-{
-    int v;
-    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
-    return v;
-}
-__device__ __forceinline__ uint32_t cluster_nctarank()
-{
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
-    return r;
-}
 __device__ __forceinline__ void consumer_barrier()
 {
     asm volatile("bar.sync 1, %0;" ::"n"(32 * kAttnWarps) : "memory");

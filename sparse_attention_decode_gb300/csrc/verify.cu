@@ -51,8 +51,6 @@ struct VerifyParams {
 constexpr int kVerifyThreads = 256;
 constexpr int kVerifyWarps = kVerifyThreads / 32;
 constexpr int kVerifyRows = MSA_MAX_DRAFT + 1;
-constexpr float kVLog2e = 1.4426950408889634f;
-constexpr float kVLn2 = 0.69314718055994531f;
 
 struct VerifySmem {
     float wm[kVerifyRows][kVerifyWarps], ws[kVerifyRows][kVerifyWarps];
@@ -68,31 +66,6 @@ struct VerifySmem {
     uint64_t best[2];  // the CTA's draw: from the residual, from p
     uint64_t wbest[kVerifyWarps];
 };
-
-__device__ __forceinline__ uint64_t dsmem_ld_u64(uint32_t addr)
-{
-    uint64_t v;
-    asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(addr) : "memory");
-    return v;
-}
-__device__ __forceinline__ float dsmem_ld_float(uint32_t addr)
-{
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
-    return v;
-}
-__device__ __forceinline__ int dsmem_ld_int(uint32_t addr)
-{
-    int v;
-    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
-    return v;
-}
-__device__ __forceinline__ uint32_t verify_cluster_size()
-{
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
-    return r;
-}
 
 // Logits in 16-byte vectors; NaN counts as -inf.
 template <class T>
@@ -284,7 +257,7 @@ __global__ void __launch_bounds__(kVerifyThreads, BLOCKS) verify_kernel(const __
 {
     __shared__ VerifySmem sm;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int C = static_cast<int>(verify_cluster_size()), crank = static_cast<int>(cluster_ctarank());
+    const int C = static_cast<int>(cluster_nctarank()), crank = static_cast<int>(cluster_ctarank());
     const int b = blockIdx.x / C;
     const int V = p.vocab, S = p.max_draft;
     const T *logits = static_cast<const T *>(p.logits) + b * p.stride_b;
@@ -297,7 +270,7 @@ __global__ void __launch_bounds__(kVerifyThreads, BLOCKS) verify_kernel(const __
     const float temp = p.temperature ? p.temperature[b] : 1.0f;
     const bool greedy = !(temp > 0.0f);
     // positive and finite, so that c times a difference of logits is 0 or of its sign, also at the ends of the range
-    const float c = greedy ? 1.0f : fminf(fmaxf(kVLog2e / temp, FLT_MIN), FLT_MAX);
+    const float c = greedy ? 1.0f : fminf(fmaxf(kLog2e / temp, FLT_MIN), FLT_MAX);
     constexpr int N = Logits<T>::kVec;
     const int nv = V / N;
     // the drafts' tokens and numbers, on their way to shared memory beside the first rows
@@ -419,9 +392,9 @@ __global__ void __launch_bounds__(kVerifyThreads, BLOCKS) verify_kernel(const __
         for (int r = i0 + warp; r < i1; r += kVerifyWarps) {
             RowPart q{-INFINITY, 0.0f, 0x7fffffff};
             if (lane < C)
-                q = RowPart{dsmem_ld_float(mapa_shared(smem_addr(&sm.m[r]), lane)),
-                            dsmem_ld_float(mapa_shared(smem_addr(&sm.s[r]), lane)),
-                            dsmem_ld_int(mapa_shared(smem_addr(&sm.i[r]), lane))};
+                q = RowPart{dsmem_ld_f32(mapa_shared(smem_addr(&sm.m[r]), lane)),
+                            dsmem_ld_f32(mapa_shared(smem_addr(&sm.s[r]), lane)),
+                            dsmem_ld_s32(mapa_shared(smem_addr(&sm.i[r]), lane))};
             warp_join(q, c);
             if (lane == 0) {
                 int ok = 0;
@@ -432,7 +405,7 @@ __global__ void __launch_bounds__(kVerifyThreads, BLOCKS) verify_kernel(const __
                     } else {
                         const float e = (sm.lx[r] - q.m) * c;
                         ok = sm.u[r] * sm.qx[r] < exp2_approx(e) / q.s;
-                        lp = (e - log2f(q.s)) * kVLn2;
+                        lp = (e - log2f(q.s)) * kLn2;
                     }
                 }
                 sm.gm[r] = q.m;
@@ -479,7 +452,7 @@ __global__ void __launch_bounds__(kVerifyThreads, BLOCKS) verify_kernel(const __
         const int x = greedy ? sm.gi[at] : key ? static_cast<int>(0xffffffffu - static_cast<uint32_t>(key)) : -1;
         float lp = 0.0f;
         if (x >= 0 && !greedy)
-            lp = ((Logits<T>::one(row + x) - m0) * c - log2f(sm.gs[at])) * kVLn2;
+            lp = ((Logits<T>::one(row + x) - m0) * c - log2f(sm.gs[at])) * kLn2;
         for (int i = lane; i <= S; i += 32) {
             const int64_t o = static_cast<int64_t>(b) * (S + 1) + i;
             p.out[o] = i < at ? p.tokens[static_cast<int64_t>(b) * S + i] : i == at ? x : -1;
