@@ -86,7 +86,8 @@ msa_status msa_attention_sparse(const void *q, int64_t q_stride, const void *k, 
  * and >= 0.  Both products run in f16 with fp32 accumulation: codes convert
  * exactly, a query row is brought to [2^13, 2^14) by a power of two, and a row's
  * products of weight and V scale are held relative to the largest of them: at 11
- * bits down to 2^-28 of it, at fewer down to 2^-38.
+ * bits down to 2^-28 of it, at fewer down to 2^-38 (a weight below 2^-126 of the
+ * row's largest is 0, whatever its scale).
  */
 msa_status msa_attention_sparse_fp8(const void *q, int64_t q_stride, const void *k, const int64_t *k_strides,
                                     const float *k_scale, const void *v, const int64_t *v_strides,

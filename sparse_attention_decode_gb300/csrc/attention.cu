@@ -50,7 +50,8 @@ bool block_attn_allowed(int dev)
 }
 
 // Clusters of `size` CTAs (two an SM) that the device runs at the same time: those of 4 or 8 do not fill it, as a
-// cluster stays within one of its parts.  0 where the query fails.
+// cluster stays within one of its parts.  0 where the query fails.  Asked of one kernel without the mass scratch: every
+// form of it gives the same counts for 2 to 8 CTAs, with any scratch (152, 97, 74, 58, 46, 38, 36 on a GB300).
 int resident_clusters(int dev, int size)
 {
     static std::atomic<int> cache[kMaxDevices][9];
@@ -196,7 +197,8 @@ static void prefix_units(PrefixParts &a, int64_t rows, int kv_heads)
     a.units = a.head_tiles * kv_heads;
 }
 
-// Bytes: rows of the prefix's slots and one own part a row and head, 516 each.
+// Bytes: rows of the prefix's slots and one own part a row and head, 516 each.  The slots (34 MB) do not shrink with the
+// batch or the prefix: how many CTAs share it is worked out on the device, from the live lengths.
 static size_t prefix_workspace(int max_rows, int group, int kv_heads)
 {
     PrefixParts a;
@@ -335,9 +337,9 @@ static msa_status prefix_entry(const void *q, int64_t q_stride, const void *k, c
                                  : launch_block_attn<AttnBf16, 4, true>(o, units, split, dev, st, dependent);
     };
     // Few own CTAs start first, on SMs kept free for them (a CTA may take one by itself), and the prefix as their
-    // dependent: it ends last, and the join waits for one grid's end instead of two in a row (2 requests over 4133
-    // tokens: 13.2 us against 13.5, over 8192: 15.9 and 16.5; 1 over 30000: 26.7 and 27.8).  Many would hold the
-    // prefix's CTAs up.
+    // dependent: it ends last, and the join waits for one grid's end instead of two in a row (2 requests over 1000
+    // tokens: 11.7 us against 11.95, over 4133: 13.3 and 13.6, over 16384: 18.5 and 20.7; 1 over 30000: 26.5 and 28.2).
+    // Many would hold the prefix's CTAs up (4 requests over 8192, already no gain: 18.8 both ways).
     const bool own_first = units * split <= sms / 8;
     if (own_first) {
         p.parts.spare = static_cast<int>(units * split);

@@ -20,10 +20,19 @@
 // cluster of up to 8 CTAs that splits one list when there are few: the parts
 // join through distributed shared memory, in cluster-rank order, so there is one
 // launch, no scratch, and the same result each time.  256 requests x 4 heads x 16
-// blocks (1.05 GB): 165-167 us, 0.93-0.94 of the copy rate.  Few requests are bound
-// by latency: of one request's 7.5 us, 1.3 are the length, ids and table, 1.3 the
-// first tile, 2 two pages (a page alone on an SM takes a CTA 1 us, two CTAs 1.28
-// each), 2.5 the parts' way to the output.
+// blocks (1.05 GB): 166-168 us, 0.93 of the copy rate.  Few requests are bound by
+// latency: of one request's 8 us, 1.3 are the length, ids and table, 1.3 the first
+// tile, 2 two pages (a page alone on an SM takes a CTA 1 us, two CTAs 1.28 each), 2.5
+// the parts' way to the output.
+//
+// Draft positions walk a list each: 32 requests x 4 positions x 4 x 16 heads read 537
+// MB of which 160 are distinct, 56 us (E4M3 66).  E4M3, 32 requests: 22.4 us for 69 MB;
+// neither the stream (0.36 of DRAM's cycles), the MMAs (0.14) nor the issue slots
+// (0.27) are full: 256 CTAs stand in 304 places, so that 104 SMs walk 16 pages and 48
+// walk 8, and the chain of one request is around them.  256 requests: 120 us, 0.67 of
+// the copy rate.  Groups of 17 to 64 rows keep more than their registers (spills of 20
+// to 52 bytes, E4M3 76 to 104): 64 requests x 4 x 32 heads 55 us (E4M3 67) for 266 MB
+// (139), x 4 x 64 heads 91 (115).
 #pragma once
 
 #include <algorithm>
@@ -97,7 +106,9 @@ struct BlockAttnSmem {
     float fac[8][kAttnMaxRows];                    // what each rank's part of a row is multiplied by
 };
 
-// Mass scratch: [page of this CTA][slice * rows] of (sum, maximum at that time); 64 entries a page.
+// Mass scratch: [page of this CTA][slice * rows] of (sum, maximum at that time); 64 entries a page.  Two CTAs fit on
+// an SM with 24 pages of it (E4M3: 18): an unsplit list of 32 blocks has one (160 requests x 4 heads: 241 us, without
+// the mass 208; E4M3 218 and 142).
 __host__ __device__ constexpr size_t block_attn_mass_bytes(int pages) { return static_cast<size_t>(pages) * 64 * 8; }
 
 template <class F>

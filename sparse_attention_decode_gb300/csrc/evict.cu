@@ -127,10 +127,16 @@ __device__ __forceinline__ void block_sums(const float *w, int64_t cols, int hea
 // SM: 1024 for long contexts, whose rounds over the blocks are then few (with the
 // first digit counted apart: 35 us against 38 with 512), 256 for short ones.
 //
-// Bound by latency: 7 us for the keys, 1 to 2 a pass, 1.2 for the places, 5 for the
-// copies (256 requests x 8192 blocks x 4 heads).  What carries it are wide loads
-// with several heads in flight and few barriers (with a barrier every 512 entries
-// and a load at a time: 62 us).  Accumulation included: 29 us; 4 x 68 blocks: 4.8.
+// Bound by latency.  256 requests x 8192 blocks x 4 heads, accumulation included: 29
+// us.  By the clock, from accumulation's start: 2.3 until it has ended; then, in the
+// slowest CTA (in the median one), 11 us for the keys (7), 6 for the three passes (3.6),
+// 1 for the counts, 1.9 for the places, 1.7 for the freed pages and 1.1 for the copies,
+// 25 in all; the launch and the end are the rest.  104 SMs carry two requests, 48 one.
+// DRAM is busy for 14 % of the time, the issue slots for 36; stalls are loads (4.1 a
+// issued instruction), barriers (3.8) and turns not got (3.3); 32 registers a thread
+// spill 28 bytes.  What carries it are wide loads with several heads in flight and few
+// barriers (with a barrier every 512 entries and a load at a time: 62 us).
+// 4 x 68 blocks: 4.9.
 constexpr int kCopy = 2;
 constexpr int kBins = 2048;  // of a radix pass: digits of 11, 11 and 10 bits
 

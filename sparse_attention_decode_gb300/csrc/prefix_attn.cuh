@@ -14,7 +14,7 @@
 // of the work by the live lengths (its other CTAs end at once), and the own pages'
 // CTAs, launched as its dependents, start on the rest and follow as its CTAs end.
 // (Few own CTAs are launched first instead, and this kernel as their dependent.)
-// (64 requests over 32768 + 147000 tokens: 87 us; one after the other 125; own pages
+// (64 requests over 32768 + 147000 tokens: 88 us; one after the other 125; own pages
 // as further units of this kernel 193, a few microseconds of latency for each of
 // their short runs.)
 //
@@ -71,8 +71,10 @@ struct PrefixParts {
 
 __device__ __forceinline__ int tokens_in(int n, int limit) { return n < 0 || n > limit ? 0 : n; }
 
-// Pages a CTA's range should have at least: one for each chain of a small tile.  Fewer pages are more parts to join
-// (2 requests over 4133 tokens: 13.2 us, 16.2 with 1, 15.1 with 3; over 8192: 16.8, 18.6, 15.0).
+// Pages a CTA's range should have at least: one for each chain of a small tile.  Fewer pages are more parts to join,
+// more of them a longer range: 2 requests over 4133 tokens take 13.3 us (15.8 with 1, 14.6 with 3, 14.5 with 4), over
+// 8192 15.9 (16.5, 15.0, 15.6: 64 parts a row cost more there than a third page), over 16384 18.3 with any, and larger
+// batches have more pages a CTA anyway.
 constexpr int kPrefixMinPages = 2;
 
 // 32-bit numbers (the host refuses more): quotients of 64 bits would be half the start of every kernel.

@@ -10,7 +10,12 @@
 // its argmax is the same however the vocabulary is split.
 //
 // What bounds it: the stream of logits (every one is read once for m and Z, those
-// of one row again, from L2, for the draw).  One cluster a request: its CTAs take
+// of one row again for the draw).  256 requests x 163840 fp32, 3 drafts of which 1.5
+// are accepted: 670 MB that have to be read and 170 of the drawn rows again, which L2
+// no longer holds: 840 MB in 143 us, 0.87 of the copy rate.  Rows off 16 bytes are
+// bound by their loads' shape: each thread reads its vector word by word, so that a
+// warp's load touches 21 sectors where 4 would hold the data (32 x 100003 bf16: 22 us
+// for 38 MB; aligned, 32 x 100000: 15.8).  One cluster a request: its CTAs take
 // slices of the vocabulary in 16-byte loads, several in flight a thread, exchange
 // (m, Z) and the best key through distributed shared memory and decide alike; one
 // launch.  A row past the first refusal has no part in the result.  Where there
