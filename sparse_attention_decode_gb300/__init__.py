@@ -1,9 +1,10 @@
 """Decode-time MSA lightning indexer for GB300 (sm_103a).
 
 The compute lives in ``libmsa_indexer.so`` (hand-written CUDA kernels behind
-a C ABI, declared in ``include/msa_indexer.h`` and, for the operators that read
-the indexer's blocks, ``include/msa_attention.h``); this package only builds and
-binds it.  PyTorch supplies device memory and streams.
+a C ABI, declared in ``include/msa_indexer.h``, for the operators that read the
+indexer's blocks in ``include/msa_attention.h``, and for what a serving step runs
+around them in ``include/msa_serving.h``); this package only builds and binds it.
+PyTorch supplies device memory and streams.
 """
 
 from ._binding import (  # noqa: F401
@@ -63,4 +64,16 @@ from ._attention import (  # noqa: E402,F401
     msa_cache_accumulate,
     msa_cache_evict,
     msa_verify_draft,
+)
+
+from ._serving import (  # noqa: E402,F401
+    MSA_MAX_ALTERNATIVES,
+    MSA_MAX_GIVEN_TOKENS,
+    SERVING_EXPORTED,
+    msa_attention_paged,
+    msa_attention_paged_fp8,
+    msa_attention_paged_workspace_bytes,
+    msa_cache_append,
+    msa_cache_append_fp8,
+    msa_token_logprobs,
 )
