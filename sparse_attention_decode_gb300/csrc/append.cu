@@ -73,12 +73,6 @@ __device__ __forceinline__ void turn(uint64_t f, int position, float &cs, float 
     sincospif(static_cast<float>(part) * 4.656612873077393e-10f, &sn, &cs);
 }
 
-__device__ __forceinline__ uint16_t e4m3_pair(float lo, float hi)
-{
-    uint16_t r;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
-    return r;
-}
 
 __device__ __forceinline__ float half_warp_sum(float x)
 {

@@ -45,6 +45,13 @@ __device__ __forceinline__ uint32_t f32x2_to_bf16x2(float lo, float hi)
     return r;
 }
 
+// Two fp32 values to E4M3 codes (lo -> low byte), to the nearest, at most 448.
+__device__ __forceinline__ uint16_t e4m3_pair(float lo, float hi)
+{
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    return r;
+}
 // 2^x (the special-function unit's; +-2 ulp, 2^-inf = 0).
 __device__ __forceinline__ float exp2_approx(float x)
 {

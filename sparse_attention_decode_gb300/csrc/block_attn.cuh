@@ -38,6 +38,7 @@
 #include <algorithm>
 #include <cmath>
 
+#include "attn_common.cuh"
 #include "attn_ptx.cuh"
 #include "host_util.cuh"
 #include "keys.cuh"
@@ -67,8 +68,6 @@ constexpr int kAttnWarps = 4;  // consumer warps; one producer warp after them
 constexpr int kAttnThreads = 32 * (kAttnWarps + 1);
 constexpr int kAttnMaxRows = 64;  // rows of one unit (query heads of a KV head): 1, 2 or 4 tiles of 16
 constexpr int kAttnOStride = kDim + 4;  // fp32 row stride of a partial O in shared memory (bank spread)
-
-__device__ __forceinline__ int pages_of(int tokens) { return tokens / kPage + (tokens % kPage != 0); }
 
 struct BlockAttnParams {
     CUtensorMap kmap, vmap;  // [page][head][token][dim], box 1 x 1 x 128 x (64 bf16 | 128 E4M3)
@@ -123,63 +122,6 @@ __device__ __forceinline__ void consumer_barrier()
     asm volatile("bar.sync 1, %0;" ::"n"(32 * kAttnWarps) : "memory");
 }
 
-__device__ __forceinline__ bool mbar_test_wait(uint32_t bar, uint32_t parity)
-{
-    uint32_t done;
-    asm volatile(
-        "{\n"
-        "  .reg .pred p;\n"
-        "  mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
-        "  selp.u32 %0, 1, 0, p;\n"
-        "}\n"
-        : "=r"(done)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    return done != 0;
-}
-
-// Bounded wait of a whole warp; false, with the CTA's abort flag and the fault
-// bit set, when it ran out or another warp gave up before.  A phase that is
-// complete already, the common case in a page loop that the cache stream does not
-// hold up, costs one test.  `withhold`: the test of the bounded waits, with far
-// fewer polls.
-constexpr uint32_t kWithheldPolls = 1u << 14;
-
-__device__ __forceinline__ bool attn_wait(int *abort_flag, uint32_t *fault, uint32_t bar, uint32_t parity, int withhold)
-{
-    if (__all_sync(0xffffffffu, mbar_test_wait(bar, parity)))
-        return true;
-    bool ok = false;
-    if (!*reinterpret_cast<volatile int *>(abort_flag)) {
-        const uint32_t polls = withhold ? kWithheldPolls : kSpinLimit;
-        for (uint32_t i = 0; i < polls && !ok; ++i)
-            ok = mbar_try_wait(bar, parity);
-        if (!ok) {
-            atomicOr(fault, MSA_FAULT_TIMEOUT);
-            *reinterpret_cast<volatile int *>(abort_flag) = 1;
-        }
-    }
-    return __all_sync(0xffffffffu, ok);
-}
-
-// The factor 2^(a - b) that moves a part from maximum a to b >= a; 1 for an empty part (-inf both).
-__device__ __forceinline__ float rescale(float a, float b) { return a == b ? 1.0f : exp2_approx(a - b); }
-
-// One query row in the lane's fragments: rows g and g + 8 of a 16-row tile.
-// E4M3: f16 after a power of two that puts the row's largest |q| in [2^13, 2^14)
-// (exact for values within 2^-14 .. 2^14 of it), undone through *undo.
-__device__ __forceinline__ float q_row_factor(float amax, float *undo)
-{
-    int e = 0;
-    if (amax > 0.0f && amax < INFINITY) {
-        frexpf(amax, &e);  // amax in [2^(e-1), 2^e)
-        e = 14 - e;
-        e = max(-100, min(100, e));
-    }
-    *undo = ldexpf(1.0f, -e);
-    return ldexpf(1.0f, e);
-}
-
 // E4M3: the unit of a row's (weight x V scale) products, the largest power of two <= v, and its inverse; v within
 // [2^-112, 2^126] keeps both, and the inverse times kVTop, normal.  In f16 such a product is below 4 kVTop.
 constexpr float kVTop = 8192.0f;                   // 2^13
@@ -187,9 +129,6 @@ constexpr float kVLeast = 1.925929944387236e-34f;  // 2^-112
 constexpr float kVMost = 8.507059173023462e37f;    // 2^126
 __device__ __forceinline__ float v_unit(float v) { return __uint_as_float(__float_as_uint(v) & 0x7f800000u); }
 __device__ __forceinline__ float v_unit_inverse(float v) { return __uint_as_float(0x7f000000u - (__float_as_uint(v) & 0x7f800000u)); }
-
-__device__ __forceinline__ float bf16_lo(uint32_t v) { return __uint_as_float(v << 16); }
-__device__ __forceinline__ float bf16_hi(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
 
 // MT: 16-row tiles of a unit (the four warps are MT tiles x 4 / MT slices of a
 // page's tokens).  A unit is (query row, KV head) with its group's rows, or, OWN,

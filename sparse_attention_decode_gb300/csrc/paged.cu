@@ -1,100 +1,49 @@
 // Attention over all of a request's tokens: argument checks and launches.
-#include <cuda_fp16.h>
-
-#include "block_attn.cuh"
-
-#include "msa_serving.h"
+#include "paged_attn.cuh"
 
 namespace msa {
 
 bool test_withhold_pages();  // msa_indexer_test_withhold_pages
-bool cache_ok(const void *base, const int64_t *strides, int64_t pages, int heads, bool fp8);  // attention.cu
+bool make_cache_map(CUtensorMap *map, const void *base, const int64_t *strides, int64_t pages, int heads, bool fp8);  // attention.cu
+bool cache_ok(const void *base, const int64_t *strides, int64_t pages, int heads, bool fp8);
 bool unaligned(const void *p, uintptr_t a);
 
-struct PagedParams {
-    const uint16_t *q;
-    const uint8_t *k, *v;
-    const float *kscale, *vscale;
-    const int32_t *block_table, *seq_lens;
-    uint16_t *out;
-    float *lse;
-    uint32_t *fault;
-    int64_t q_stride, bt_stride, num_pages;
-    int64_t ks[3], vs[3];
-    int batch, q_len, kv_heads, group, seq_limit;
-    float scale_log2;
-};
+// Rows of a unit: a chain's 16 or 32, or both chains' 32.
+static int paged_tile_rows(int64_t rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : kPagedMaxRows; }
 
-__device__ __forceinline__ float e4m3_value(uint8_t c)
+// Two parts a CTA: a row of each is 516 bytes.
+static size_t paged_workspace(int64_t max_rows, int group)
 {
-    return static_cast<float>(__half2float(__ushort_as_half(static_cast<unsigned short>(e4m3x2_to_f16x2(c) & 0xffffu))));
+    return kHeaderBytes + 2 * kPagedMaxGrid * static_cast<size_t>(paged_tile_rows(max_rows * group)) * (kDim + 1) * sizeof(float);
 }
 
-// A block a query head: thread t a token of the page, then a dim.
-template <bool FP8>
-__global__ void __launch_bounds__(128) paged_kernel(const __grid_constant__ PagedParams p)
+template <class F, int N, int WAYS>
+static msa_status launch_paged(const PagedParams &p, int dev, cudaStream_t st)
 {
-    __shared__ float s_q[kDim], s_p[kPage], s_w[4];
-    const int tid = threadIdx.x;
-    const int heads = p.kv_heads * p.group;
-    const int64_t row = blockIdx.x / heads;
-    const int head = blockIdx.x % heads, h = head / p.group, b = static_cast<int>(row / p.q_len), i = static_cast<int>(row % p.q_len);
-    const int L = p.seq_lens[b];
-    const bool bad = L < 0 || L > p.seq_limit;
-    if (bad && tid == 0)
-        atomicOr(p.fault, MSA_FAULT_SEQ_LEN);
-    const int len = bad ? 0 : L, sees = max(0, len - (p.q_len - 1 - i));
-    s_q[tid] = __uint_as_float(static_cast<uint32_t>(p.q[row * p.q_stride + head * kDim + tid]) << 16);
-    __syncthreads();
-    float m = -INFINITY, l = 0.0f, o = 0.0f;
-    for (int base = 0; base < sees; base += kPage) {
-        const int page = p.block_table[b * p.bt_stride + base / kPage];
-        if (page < 0 || page >= p.num_pages) {
-            if (tid == 0)
-                atomicOr(p.fault, MSA_FAULT_PAGE_ID);
-            continue;
-        }
-        const bool seen = base + tid < sees;
-        const int64_t at = (static_cast<int64_t>(page) * p.kv_heads + h) * kPage;
-        float s = -INFINITY;
-        if (seen) {
-            s = 0.0f;
-            const int64_t from = page * p.ks[0] + tid * p.ks[1] + h * p.ks[2];
-            for (int d = 0; d < kDim; ++d)
-                s += s_q[d] * (FP8 ? e4m3_value(p.k[from + d])
-                                   : __uint_as_float(static_cast<uint32_t>(reinterpret_cast<const uint16_t *>(p.k)[from + d]) << 16));
-            s *= p.scale_log2 * (FP8 ? p.kscale[at + tid] : 1.0f);
-        }
-        float top = s;
-        for (int q = 16; q >= 1; q >>= 1)
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, q));
-        if ((tid & 31) == 0)
-            s_w[tid >> 5] = top;
-        __syncthreads();
-        const float n = fmaxf(m, fmaxf(fmaxf(s_w[0], s_w[1]), fmaxf(s_w[2], s_w[3])));
-        const float f = rescale(m, n);
-        m = n;
-        s_p[tid] = seen ? exp2_approx(s - n) : 0.0f;
-        __syncthreads();
-        float sum = 0.0f, acc = 0.0f;
-        const int64_t from = page * p.vs[0] + h * p.vs[2] + tid;
-        for (int t = 0; t < min(kPage, sees - base); ++t) {
-            sum += s_p[t];
-            acc += s_p[t] * (FP8 ? e4m3_value(p.v[from + t * p.vs[1]]) * p.vscale[at + t]
-                                 : __uint_as_float(static_cast<uint32_t>(reinterpret_cast<const uint16_t *>(p.v)[from + t * p.vs[1]]) << 16));
-        }
-        l = l * f + sum;
-        o = o * f + acc;
-    }
-    p.out[(row * heads + head) * kDim + tid] = static_cast<uint16_t>(f32x2_to_bf16x2(l > 0.0f ? o / l : 0.0f, 0.0f));
-    if (tid == 0 && p.lse)
-        p.lse[row * heads + head] = l > 0.0f ? (m + log2f(l)) * kLn2 : -INFINITY;
+    static std::atomic<bool> allowed[kMaxDevices];
+    auto *kernel = paged_attn_kernel<F, N, WAYS>;
+    constexpr size_t smem = PagedLayout<F, N, WAYS>::kBytes;
+    if (!allow_smem(kernel, smem, dev, allowed))
+        return MSA_ERR_CUDA;
+    kernel<<<static_cast<unsigned>(p.grid), kPagedThreads, smem, st>>>(p);
+    if (cudaGetLastError() != cudaSuccess)
+        return MSA_ERR_CUDA;
+    if (p.grid < 2)
+        return MSA_OK;
+    constexpr int kWarpsARow = 4;
+    const int rows = std::min(p.tile_rows, p.q_len * p.group);
+    cudaLaunchAttribute attr[1];
+    const cudaLaunchConfig_t cfg =
+        pdl_config(dim3(static_cast<unsigned>(p.grid - 1), static_cast<unsigned>((rows * kWarpsARow + 7) / 8)), dim3(256), 0, st, attr);
+    return cudaLaunchKernelEx(&cfg, paged_join_kernel<kWarpsARow>, p) == cudaSuccess ? MSA_OK : MSA_ERR_CUDA;
 }
 
-static size_t paged_workspace(int64_t max_rows, int group, int kv_heads)
+template <class F>
+static msa_status launch_paged_rows(const PagedParams &p, int dev, cudaStream_t st)
 {
-    (void)max_rows, (void)group, (void)kv_heads;
-    return kHeaderBytes;
+    return p.tile_rows == 16   ? launch_paged<F, 16, 2>(p, dev, st)
+           : p.tile_rows == 32 ? launch_paged<F, 32, 2>(p, dev, st)
+                               : launch_paged<F, 32, 1>(p, dev, st);
 }
 
 static msa_status paged_entry(const void *q, int64_t q_stride, const void *k, const int64_t *k_strides,
@@ -117,13 +66,24 @@ static msa_status paged_entry(const void *q, int64_t q_stride, const void *k, co
         return MSA_ERR_INVALID_ARG;
     if (fp8 && (!k_scale || !v_scale || unaligned(k_scale, 16) || unaligned(v_scale, 16)))
         return MSA_ERR_INVALID_ARG;
-    if (workspace_bytes < paged_workspace(static_cast<int64_t>(batch) * q_len, group, kv_heads))
+    if (workspace_bytes < paged_workspace(static_cast<int64_t>(batch) * q_len, group))
         return MSA_ERR_WORKSPACE_TOO_SMALL;
     PagedParams p;
     std::memset(&p, 0, sizeof p);
+    p.tile_rows = paged_tile_rows(static_cast<int64_t>(q_len) * group);
+    p.row_tiles = (q_len * group + p.tile_rows - 1) / p.tile_rows;
+    p.seq_limit = static_cast<int>(std::min<int64_t>(max_model_len, kPage * bt_stride));
+    // the pages of all units are counted in 32 bits
+    if ((static_cast<int64_t>(p.seq_limit) + kPage - 1) / kPage * batch * p.row_tiles * kv_heads > (1 << 30))
+        return MSA_ERR_UNSUPPORTED;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess)
+        return MSA_ERR_CUDA;
+    const int sms = device_sms(dev);
+    if (sms <= 0 || !make_cache_map(&p.kmap, k, k_strides, num_pages, kv_heads, fp8) ||
+        !make_cache_map(&p.vmap, v, v_strides, num_pages, kv_heads, fp8))
+        return MSA_ERR_CUDA;
     p.q = static_cast<const uint16_t *>(q);
-    p.k = static_cast<const uint8_t *>(k);
-    p.v = static_cast<const uint8_t *>(v);
     p.kscale = k_scale;
     p.vscale = v_scale;
     p.block_table = block_table;
@@ -134,23 +94,17 @@ static msa_status paged_entry(const void *q, int64_t q_stride, const void *k, co
     p.q_stride = q_stride;
     p.bt_stride = bt_stride;
     p.num_pages = num_pages;
-    for (int i = 0; i < 3; ++i) {
-        p.ks[i] = k_strides[i];
-        p.vs[i] = v_strides[i];
-    }
     p.batch = batch;
     p.q_len = q_len;
     p.kv_heads = kv_heads;
     p.group = group;
-    p.seq_limit = static_cast<int>(std::min<int64_t>(max_model_len, kPage * bt_stride));
+    p.grid = std::min(sms, kPagedMaxGrid);
+    p.part_lse = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + kHeaderBytes);
+    p.part_o = p.part_lse + 2 * kPagedMaxGrid * p.tile_rows;
     p.scale_log2 = scale * kLog2e;
-    const unsigned grid = static_cast<unsigned>(static_cast<int64_t>(batch) * q_len * kv_heads * group);
+    p.withhold = test_withhold_pages();
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (fp8)
-        paged_kernel<true><<<grid, 128, 0, st>>>(p);
-    else
-        paged_kernel<false><<<grid, 128, 0, st>>>(p);
-    return cudaGetLastError() == cudaSuccess ? MSA_OK : MSA_ERR_CUDA;
+    return fp8 ? launch_paged_rows<PagedFp8>(p, dev, st) : launch_paged_rows<PagedBf16>(p, dev, st);
 }
 
 }  // namespace msa
@@ -161,7 +115,7 @@ extern "C" size_t msa_attention_paged_workspace_bytes(int max_rows, int heads, i
 {
     if (max_rows < 0 || kv_heads < 1 || heads < kv_heads || heads % kv_heads)
         return 0;
-    return paged_workspace(max_rows, heads / kv_heads, kv_heads);
+    return paged_workspace(max_rows, heads / kv_heads);
 }
 
 extern "C" msa_status msa_attention_paged(const void *q, int64_t q_stride, const void *k, const int64_t *k_strides,

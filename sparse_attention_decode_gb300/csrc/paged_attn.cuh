@@ -1,0 +1,1010 @@
+// Attention of a few query rows over all pages of their request, on the
+// 5th-generation tensor cores with the tokens as the rows of both products.
+//
+// Mathematics: the softmax over a row's tokens and the join of its parts as in
+// block_attn.cuh.  A unit is (request, tile of up to 64 of its query rows, KV head);
+// the pages of all units, one after the other, are cut into one equal range a CTA,
+// so a context of any length keeps every SM busy to the end.  A unit inside one range
+// goes straight to the output; the parts of one that a range's end cuts go to the
+// workspace in fp32 and are joined, always in page order, by paged_join_kernel.
+//
+// Why tokens as rows: a tcgen05 product has 128 rows, a request's query rows are 1 to
+// 64, a page is 128 tokens.  S^T = K Q^T (128 tokens x N rows) and O^T = V^T P^T
+// (128 dims x N rows) fill the 128 rows with what there is, read K and V where TMA put
+// them, and cost one pass of the operand through shared memory each, whatever N is
+// (256 cycles of an SM's 2700 a bf16 page at the copy rate).  A thread has one token: the
+// scale of an E4M3 token is one number for all its weights.
+//
+// A row's maximum would be a reduction over the lanes for every page.  The reference m
+// of a row need not be the maximum: it is kept until a score passes it by more than
+// 2^8 (weights then stay below 2^8, which costs fp32 sums and bf16 operands nothing), so
+// that a page asks one vote of its 128 threads, and the reductions, and the rescaling of
+// O in tensor memory, follow only where somebody has passed it: once a unit as a rule.
+//
+// E4M3: the codes go into the products as they are (kind::f8f6f4), so the other operand
+// has to be E4M3 as well.  A query row, brought to [2^7, 2^8) by a power of two, is the
+// sum of two E4M3 numbers, exactly where it is within 2^-9 of the row's largest (4 bits
+// each, the second 2^-5 on), and to 2^-23 of that largest below.  A weight times its
+// token's V scale is the sum of three (12 bits), held relative to the row's largest such
+// product: to 2^-12 of itself, or 2^-28 of that largest.  The terms stand side by side as
+// further rows of the product, so K and V still pass once.
+#pragma once
+
+#include "attn_common.cuh"
+#include "host_util.cuh"
+#include "tcgen05.cuh"
+
+#include "msa_serving.h"
+
+namespace msa {
+
+struct PagedBf16 {
+    static constexpr bool kFp8 = false;
+    static constexpr int kTileBytes = kPageBytes;
+    static constexpr int kScaleBytes = 0;
+    static constexpr int kQTerms = 1, kPTerms = 1;
+};
+struct PagedFp8 {
+    static constexpr bool kFp8 = true;
+    static constexpr int kTileBytes = kPage * kDim;
+    static constexpr int kScaleBytes = kPage * 4;
+    static constexpr int kQTerms = 2, kPTerms = 3;
+};
+
+constexpr int kPagedThreads = 352;  // two softmax warpgroups, a TMA warp, two MMA warps
+constexpr int kPagedMaxGrid = 256;
+constexpr int kPagedMaxRows = 64;   // of a unit: one chain's 16 or 32, or both chains' 32
+constexpr float kPagedLag = 8.0f;
+constexpr float kPagedTermUp = 32.0f;                  // an E4M3 term over the next
+constexpr float kPagedTermDown = 1.0f / kPagedTermUp;
+
+struct PagedParams {
+    CUtensorMap kmap, vmap;
+    const uint16_t *q;
+    const float *kscale, *vscale;
+    const int32_t *block_table, *seq_lens;
+    uint16_t *out;
+    float *lse;
+    float *part_o, *part_lse;  // [2 a CTA][tile_rows] rows, lse in log2 units; -inf: nothing, +inf: not whole
+    uint32_t *fault;
+    int64_t q_stride, bt_stride, num_pages;
+    int batch, q_len, kv_heads, group, seq_limit;
+    int tile_rows, row_tiles;  // rows of a unit at most; units of a request and KV head
+    int grid;                  // CTAs of paged_attn_kernel
+    float scale_log2;
+    int withhold;  // test of the bounded waits: the producer loads and signals no page
+};
+
+__device__ __forceinline__ int paged_len(const PagedParams &p, int b)
+{
+    const int n = p.seq_lens[b];
+    return n < 0 || n > p.seq_limit ? 0 : n;
+}
+
+// Pages a CTA's range should have at least: one for each chain.
+constexpr int kPagedMinPages = 2;
+
+// The ranges: CTA g has [start(g), start(g + 1)) of the units' pages.
+struct PagedSplit {
+    int total, ctas, range, more;
+    __device__ PagedSplit(int total_, int grid) : total(total_)
+    {
+        ctas = min(grid, (total + kPagedMinPages - 1) / kPagedMinPages);
+        range = ctas > 0 ? total / ctas : 0;
+        more = total - range * ctas;
+    }
+    __device__ int start(int g) const { return g * range + min(g, more); }
+};
+
+// A place in the sequence of the units' pages.
+struct PagedAt {
+    int b, u, j;  // request, its unit, the unit's page
+};
+
+struct PagedScan {
+    int warp_sums[32];
+    PagedAt at;
+};
+
+// The batch's pages and the place of page `want(total)` of the sequence, by a whole block.
+template <int THREADS, class Want>
+__device__ __forceinline__ int paged_find(const PagedParams &p, PagedScan *sc, Want want)
+{
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int units = p.row_tiles * p.kv_heads;
+    const int each = (p.batch + THREADS - 1) / THREADS;
+    const int b0 = min(p.batch, tid * each), b1 = min(p.batch, b0 + each);
+    int mine = 0;
+    for (int b = b0; b < b1; ++b)
+        mine += pages_of(paged_len(p, b)) * units;
+    int upto = mine;  // inclusive over the warp
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, upto, o);
+        upto += lane >= o ? x : 0;
+    }
+    if (lane == 31)
+        sc->warp_sums[warp] = upto;
+    if (tid == 0)
+        sc->at = PagedAt{p.batch, 0, 0};
+    __syncthreads();
+    int before = 0, total = 0;
+    for (int w = 0; w < THREADS / 32; ++w) {
+        before += w < warp ? sc->warp_sums[w] : 0;
+        total += sc->warp_sums[w];
+    }
+    const int x = want(total);
+    int from = before + upto - mine;
+    if (x >= from && x < from + mine) {
+        for (int b = b0; b < b1; ++b) {
+            const int P = pages_of(paged_len(p, b)), n = P * units;
+            if (x < from + n) {
+                const int u = (x - from) / P;
+                sc->at = PagedAt{b, u, x - from - u * P};
+                break;
+            }
+            from += n;
+        }
+    }
+    __syncthreads();
+    return total;
+}
+
+// Runs through a range unit by unit.
+struct PagedWalk {
+    int b, u, j, left;  // the next page, and pages left
+    int len, P;         // of request b
+    __device__ PagedWalk(const PagedParams &p, const PagedAt &at, int n) : b(at.b), u(at.u), j(at.j), left(n), len(0), P(0)
+    {
+        if (left > 0) {
+            len = paged_len(p, b);
+            P = pages_of(len);
+        }
+    }
+    __device__ int run() const { return min(left, P - j); }
+    __device__ void next(const PagedParams &p)
+    {
+        left -= run();
+        j = 0;
+        if (++u == p.row_tiles * p.kv_heads && left > 0) {
+            u = 0;
+            do {
+                if (++b >= p.batch) {  // not while the lengths stay as they are
+                    left = 0;
+                    return;
+                }
+                len = paged_len(p, b);
+                P = pages_of(len);
+            } while (P == 0);
+        }
+    }
+};
+
+template <int N, int STAGES>
+struct PagedSmem {
+    uint64_t kv_full[STAGES], kv_empty[STAGES];
+    uint64_t q_full, q_taken, s_full[2], p_full[2], o_done[2], drained[2];
+    int page_ok[STAGES];
+    PagedScan scan;
+    uint32_t tmem;
+    int abort_flag;
+    float4 row[2][N];       // a chain's rows: undo of the query row (E4M3), reference (log2 units), unit of the weights (E4M3)
+    float fac[2][N];        // what a moved reference multiplies a row's O by
+    float lfac[2][N];       // and its sum
+    float vtop[2][N];       // E4M3: the row's largest weight x V scale at its reference
+    int wmax[2][4][N];      // the warps' maxima, in an order of integers
+    float wsum[2][4][N];
+    int sees[2 * N];        // tokens a row sees
+    float undo[2 * N];      // E4M3: the query row's power of two, undone
+    float share[2][2 * N];  // what a chain's part of a row is multiplied by at the end
+};
+
+// Shared memory: query rows, the chains' weights, as many tiles of K and V as there is room for, their scales.
+template <class F, int N, int WAYS>
+struct PagedLayout {
+    static constexpr int kRows = WAYS == 2 ? N : 2 * N;                  // of a unit
+    static constexpr int kQBytes = kRows * kDim * 2;                     // (E4M3: two terms of a byte)
+    static constexpr int kPBytes = F::kPTerms * N * kPage * (F::kFp8 ? 1 : 2);  // of a chain
+    static constexpr int kKv = kQBytes + 2 * kPBytes;                    // 1024-byte aligned
+    static constexpr int kRoom = 232448 - 1024 - kKv - static_cast<int>(sizeof(PagedSmem<N, 12>));
+    static constexpr int kStages = kRoom / (F::kTileBytes + F::kScaleBytes);
+    using Smem = PagedSmem<N, kStages>;
+    static constexpr int kScales = kKv + kStages * F::kTileBytes;
+    static constexpr int kCtl = kScales + kStages * F::kScaleBytes;
+    static constexpr size_t kBytes = 1024 + kCtl + sizeof(Smem);
+    static constexpr int kSCols = F::kQTerms * N, kOCols = F::kPTerms * N, kChainCols = kSCols + kOCols;
+    static constexpr uint32_t kTmem = 2 * kChainCols <= 64 ? 64 : 2 * kChainCols <= 128 ? 128 : 2 * kChainCols <= 256 ? 256 : 512;
+    // WAYS 2: a ring for each chain, so that a stage's phases, which a wait tells by their parity, are all one chain's
+    static constexpr int kDepth = WAYS == 2 ? kStages / 2 : kStages;
+    static __device__ __forceinline__ int stage(int chain, uint32_t tile)
+    {
+        return static_cast<int>(tile % kDepth) + (WAYS == 2 ? chain * kDepth : 0);
+    }
+    static __device__ __forceinline__ uint32_t phase(uint32_t tile) { return (tile / kDepth) & 1; }
+    static_assert(kKv % 1024 == 0 && kStages >= 4 && kStages <= 12 && kBytes <= 232448 && 2 * kChainCols <= 512,
+                  "shared and tensor memory");
+};
+
+// D[tmem] (+)= A B, by the elected lane; both operands in shared memory, the high words of their descriptors given.
+template <bool FP8>
+__device__ __forceinline__ void umma_small(uint32_t one, uint32_t d_tmem, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo,
+                                           uint32_t b_hi, uint32_t idesc, uint32_t acc)
+{
+    if (FP8)
+        asm volatile(
+            "{\n"
+            "  .reg .pred p, q;\n"
+            "  .reg .b64 ad, bd;\n"
+            "  setp.ne.u32 p, %6, 0;\n"
+            "  setp.ne.u32 q, %7, 0;\n"
+            "  mov.b64 ad, {%1, %4};\n"
+            "  mov.b64 bd, {%2, %5};\n"
+            "  @p tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], ad, bd, %3, q;\n"
+            "}\n" ::"r"(d_tmem),
+            "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(a_hi), "r"(b_hi), "r"(one), "r"(acc)
+            : "memory");
+    else
+        asm volatile(
+            "{\n"
+            "  .reg .pred p, q;\n"
+            "  .reg .b64 ad, bd;\n"
+            "  setp.ne.u32 p, %6, 0;\n"
+            "  setp.ne.u32 q, %7, 0;\n"
+            "  mov.b64 ad, {%1, %4};\n"
+            "  mov.b64 bd, {%2, %5};\n"
+            "  @p tcgen05.mma.cta_group::1.kind::f16 [%0], ad, bd, %3, q;\n"
+            "}\n" ::"r"(d_tmem),
+            "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(a_hi), "r"(b_hi), "r"(one), "r"(acc)
+            : "memory");
+}
+
+// 16 (or 8) consecutive 32-bit columns of one TMEM lane per thread; valid after a wait (tmem_wait_all).
+__device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t (&r)[16])
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st_cols(uint32_t taddr, const uint32_t (&r)[16])
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};" ::"r"(r[0]),
+        "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+        "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(taddr)
+        : "memory");
+}
+
+// A barrier of `threads` threads that tells all of them whether one of them says so.
+__device__ __forceinline__ bool barrier_any(int id, int threads, bool say)
+{
+    uint32_t r;
+    __syncwarp();
+    asm volatile(
+        "{\n"
+        "  .reg .pred p, q;\n"
+        "  setp.ne.u32 p, %3, 0;\n"
+        "  barrier.cta.red.or.pred.aligned q, %1, %2, p;\n"
+        "  selp.u32 %0, 1, 0, q;\n"
+        "}\n"
+        : "=r"(r)
+        : "r"(id), "r"(threads), "r"(static_cast<uint32_t>(say))
+        : "memory");
+    return r != 0;
+}
+__device__ __forceinline__ void barrier_sync(int id, int threads)
+{
+    __syncwarp();
+    asm volatile("barrier.cta.sync.aligned %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
+// fp32 in an order of signed integers, and back.
+__device__ __forceinline__ int float_int(float x)
+{
+    const int i = __float_as_int(x);
+    return i ^ ((i >> 31) & 0x7fffffff);
+}
+__device__ __forceinline__ float int_float(int i) { return __int_as_float(i ^ ((i >> 31) & 0x7fffffff)); }
+
+__device__ __forceinline__ void f16x2_floats(uint32_t v, float &lo, float &hi)
+{
+    asm("{\n  .reg .b16 a, b;\n  mov.b32 {a, b}, %2;\n  cvt.f32.f16 %0, a;\n  cvt.f32.f16 %1, b;\n}\n" : "=f"(lo), "=f"(hi) : "r"(v));
+}
+// x, y as sums of E4M3 numbers t[0] + t[1] / 32 + .., two codes each; |x|, |y| <= 448.
+template <int TERMS>
+__device__ __forceinline__ void e4m3_terms(float x, float y, uint32_t (&t)[TERMS])
+{
+#pragma unroll
+    for (int i = 0; i < TERMS; ++i) {
+        t[i] = e4m3_pair(x, y);
+        if (i + 1 < TERMS) {
+            float a, b;
+            f16x2_floats(e4m3x2_to_f16x2(static_cast<uint16_t>(t[i])), a, b);
+            x = (x - a) * kPagedTermUp;
+            y = (y - b) * kPagedTermUp;
+        }
+    }
+}
+
+// The sums over a warp's lanes of N values a thread: lane r (modulo N) gets value r's.
+template <int N>
+__device__ __forceinline__ float lanes_sum(const float (&l)[N], int lane)
+{
+    float v[16];
+    if (N == 32) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const float keep = lane & 16 ? l[(i + 16) % N] : l[i], give = lane & 16 ? l[i] : l[(i + 16) % N];
+            v[i] = keep + __shfl_xor_sync(0xffffffffu, give, 16);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            v[i] = l[i] + __shfl_xor_sync(0xffffffffu, l[i], 16);
+    }
+#pragma unroll
+    for (int o = 8; o >= 1; o >>= 1)
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < o) {
+                const float keep = lane & o ? v[i + o] : v[i], give = lane & o ? v[i] : v[i + o];
+                v[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+            }
+    return v[0];
+}
+
+// N: query rows of a chain (16 or 32).  WAYS 2: the chains have the same rows and take a unit's pages in turn; 1: each
+// has rows of its own and takes every page.
+template <class F, int N, int WAYS>
+__global__ void __launch_bounds__(kPagedThreads, 1) paged_attn_kernel(const __grid_constant__ PagedParams p)
+{
+    using L = PagedLayout<F, N, WAYS>;
+    constexpr int R = L::kRows;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t *kv = smem + L::kKv;
+    float *scales = reinterpret_cast<float *>(smem + L::kScales);
+    auto *ctl = reinterpret_cast<typename L::Smem *>(smem + L::kCtl);
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // the same in all lanes, and known to be
+    const int cta = blockIdx.x;
+
+    griddep_launch_dependents();
+    if (tid == 8 * 32) {
+        prefetch_tensormap(&p.kmap);
+        prefetch_tensormap(&p.vmap);
+        for (int s = 0; s < L::kStages; ++s) {
+            mbar_init(smem_addr(&ctl->kv_full[s]), 1);
+            mbar_init(smem_addr(&ctl->kv_empty[s]), WAYS == 2 ? 5 : 10);  // a chain's product and four warps
+        }
+        mbar_init(smem_addr(&ctl->q_full), 8);
+        mbar_init(smem_addr(&ctl->q_taken), 2);
+        for (int t = 0; t < 2; ++t) {
+            mbar_init(smem_addr(&ctl->s_full[t]), 1);
+            mbar_init(smem_addr(&ctl->p_full[t]), 4);
+            mbar_init(smem_addr(&ctl->o_done[t]), 1);
+            mbar_init(smem_addr(&ctl->drained[t]), 1);
+        }
+        ctl->abort_flag = 0;
+        fence_barrier_init();
+    }
+    if (warp == 9) {
+        tmem_alloc(smem_addr(&ctl->tmem), L::kTmem);
+        tmem_relinquish_alloc_permit();
+    }
+    tc_fence_before_sync();
+    if (cta == 0)
+        for (int b = tid; b < p.batch; b += kPagedThreads)
+            if (p.seq_lens[b] != paged_len(p, b))
+                atomicOr(p.fault, MSA_FAULT_SEQ_LEN);
+    const int total = paged_find<kPagedThreads>(p, &ctl->scan, [&](int all) {
+        const PagedSplit s(all, p.grid);
+        return cta < s.ctas ? s.start(cta) : -1;
+    });
+    const PagedSplit split(total, p.grid);
+    const int count = cta < split.ctas ? split.start(cta + 1) - split.start(cta) : 0;
+    tc_fence_after_sync();
+    const uint32_t tmem = __shfl_sync(0xffffffffu, ctl->tmem, 0);
+    const int heads = p.kv_heads * p.group, unit_rows = p.q_len * p.group;
+    PagedWalk walk(p, ctl->scan.at, count);
+
+    if (warp == 8) {
+        // ---- K and V tiles, page after page ----
+        bool alive = true;
+        uint32_t tiles[2] = {0, 0};  // of the chains' rings
+        uint32_t done = 0;
+        for (; walk.left > 0 && alive; walk.next(p)) {
+            const int n = walk.run(), h = walk.u % p.kv_heads;
+            const int32_t *table = p.block_table + walk.b * p.bt_stride + walk.j;
+            int pages = -1;  // a lane's share of 32 entries of the table
+            for (int i = 0; i < n && alive; ++i, ++done) {
+                if ((i & 31) == 0) {
+                    pages = -1;
+                    if (i + lane < n) {
+                        pages = table[i + lane];
+                        if (pages < 0 || pages >= p.num_pages) {
+                            pages = -1;
+                            atomicOr(p.fault, MSA_FAULT_PAGE_ID);
+                        }
+                    }
+                }
+                const int page = __shfl_sync(0xffffffffu, pages, i & 31);
+                const int chain = WAYS == 2 ? done & 1 : 0;
+                for (int kvi = 0; kvi < 2; ++kvi) {
+                    const uint32_t tile = chain ? tiles[1]++ : tiles[0]++;
+                    const int s = L::stage(chain, tile);
+                    if (tile >= L::kDepth)
+                        alive = attn_wait(&ctl->abort_flag, p.fault, smem_addr(&ctl->kv_empty[s]), L::phase(tile) ^ 1, p.withhold);
+                    if (!alive) {
+                        chain ? --tiles[1] : --tiles[0];
+                        break;
+                    }
+                    if (lane == 0 && !p.withhold) {
+                        const uint32_t bar = smem_addr(&ctl->kv_full[s]), dst = smem_addr(kv) + s * F::kTileBytes;
+                        ctl->page_ok[s] = page >= 0;
+                        if (page < 0) {
+                            mbar_arrive(bar);
+                        } else {
+                            const CUtensorMap *map = kvi ? &p.vmap : &p.kmap;
+                            mbar_arrive_expect_tx(bar, F::kTileBytes + F::kScaleBytes);
+                            tma_load_4d(dst, map, 0, 0, h, page, bar);
+                            if (F::kFp8)
+                                bulk_load(smem_addr(scales + s * kPage),
+                                          (kvi ? p.vscale : p.kscale) + (static_cast<int64_t>(page) * p.kv_heads + h) * kPage,
+                                          F::kScaleBytes, bar);
+                            else
+                                tma_load_4d(dst + kHalfPageBytes, map, 64, 0, h, page, bar);
+                        }
+                    }
+                    __syncwarp();
+                }
+            }
+        }
+        // the copies in flight land before the CTA may end, also where another role gave up
+        for (int chain = 0; chain < WAYS && !p.withhold; ++chain)
+            for (uint32_t j = tiles[chain] >= L::kDepth ? tiles[chain] - L::kDepth : 0; j < tiles[chain]; ++j)
+                mbar_wait(smem_addr(&ctl->kv_full[L::stage(chain, j)]), L::phase(j));
+    } else if (warp >= 9) {
+        // ---- a chain's products ----
+        const int t = warp - 9;
+        const uint32_t one = elect_one();
+        constexpr uint32_t kTypes = (1u << 4) | (F::kFp8 ? 0u : (1u << 7) | (1u << 10)) | ((128u >> 4) << 24);
+        constexpr uint32_t idesc_s = kTypes | (static_cast<uint32_t>(L::kSCols >> 3) << 17);
+        constexpr uint32_t idesc_o = kTypes | (static_cast<uint32_t>(L::kOCols >> 3) << 17) | (1u << 15) | (1u << 16);  // both with their rows contiguous
+        constexpr int kSteps = F::kFp8 ? 4 : 8;
+        constexpr uint32_t kPlainHi = (2048u >> 4) | (1u << 14);  // no swizzle: 16 bytes of rows x 128 tokens, 2 KiB to the next rows
+        const uint32_t d_s = tmem + t * L::kChainCols, d_o = d_s + L::kSCols;
+        // query rows: bf16 in two halves of 64 dims, E4M3 in one, a chain's terms one after the other
+        const uint32_t q_desc = umma_desc_lo(smem_addr(smem) + (WAYS == 2 ? 0 : t * L::kSCols * 128));
+        const uint32_t p_desc = ((smem_addr(smem + L::kQBytes + t * L::kPBytes) >> 4) & 0x3FFFu) | ((128u >> 4) << 16);
+        const uint32_t kv_addr = smem_addr(kv);
+        auto wait = [&](uint64_t *bar, uint32_t parity) {
+            return attn_wait(&ctl->abort_flag, p.fault, smem_addr(bar), parity, p.withhold);
+        };
+        auto landed = [&](uint32_t tile) { return wait(&ctl->kv_full[L::stage(t, tile)], L::phase(tile)); };
+        bool alive = true;
+        uint32_t it = 0, done = 0, seg = 0;
+        for (; walk.left > 0 && alive; walk.next(p)) {
+            const int n = walk.run();
+            alive = wait(&ctl->q_full, seg++ & 1);
+            if (one)
+                mbar_arrive(smem_addr(&ctl->q_taken));
+            for (int j = WAYS == 2 ? (t ^ done) & 1 : 0; j < n && alive; j += WAYS, ++it) {
+                const uint32_t tile = 2 * it;
+                alive = landed(tile);
+                if (!alive)
+                    break;
+                tc_fence_after_sync();
+                const int sk = L::stage(t, tile), sv = L::stage(t, tile + 1);
+                const uint32_t a = umma_desc_lo(kv_addr + sk * F::kTileBytes);
+#pragma unroll
+                for (int ks = 0; ks < kSteps; ++ks) {
+                    const uint32_t off = F::kFp8 ? ks * 32 : (ks >> 2) * kHalfPageBytes + (ks & 3) * 32;
+                    const uint32_t boff = F::kFp8 ? ks * 32 : (ks >> 2) * (R * 128) + (ks & 3) * 32;
+                    umma_small<F::kFp8>(one, d_s, a + (off >> 4), kUmmaDescHi, q_desc + (boff >> 4), kUmmaDescHi, idesc_s, ks > 0);
+                }
+                umma_commit_one(one, smem_addr(&ctl->s_full[t]));
+                umma_commit_one(one, smem_addr(&ctl->kv_empty[sk]));
+                alive = landed(tile + 1) && wait(&ctl->p_full[t], it & 1);
+                if (!alive)
+                    break;
+                tc_fence_after_sync();
+                const uint32_t v = umma_desc_v_lo(kv_addr + sv * F::kTileBytes);
+#pragma unroll
+                for (int ks = 0; ks < kSteps; ++ks)
+                    umma_small<F::kFp8>(one, d_o, v + ((ks * 1024 * (F::kFp8 ? 4 : 2)) >> 4), kUmmaDescHi,
+                                        p_desc + ((ks * (F::kFp8 ? 512 : 256)) >> 4), kPlainHi, idesc_o, ks > 0 || j >= WAYS);
+                umma_commit_one(one, smem_addr(&ctl->o_done[t]));
+                umma_commit_one(one, smem_addr(&ctl->kv_empty[sv]));
+            }
+            done += n;
+        }
+        umma_commit_one(one, smem_addr(&ctl->drained[t]));  // nothing in flight when the tensor memory is freed
+        mbar_wait(smem_addr(&ctl->drained[t]), 0);
+        __syncwarp();
+    } else {
+        // ---- softmax: a thread a token ----
+        const int t = warp >> 2, tau = tid & 127;
+        const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // (32 * (warp % 4)) << 16
+        const uint32_t ts = tmem + t * L::kChainCols + lanes, to = ts + L::kSCols;
+        uint8_t *pbuf = smem + L::kQBytes + t * L::kPBytes + tau * 16;
+        auto wait = [&](uint64_t *bar, uint32_t parity) {
+            return attn_wait(&ctl->abort_flag, p.fault, smem_addr(bar), parity, p.withhold);
+        };
+        // requests without tokens: their rows are empty
+        for (int b = cta; b < p.batch; b += gridDim.x) {
+            if (paged_len(p, b) > 0)
+                continue;
+            const int64_t row0 = static_cast<int64_t>(b) * p.q_len * heads;
+            for (int i = tid; i < p.q_len * heads * (kDim / 8); i += 256)
+                reinterpret_cast<uint4 *>(p.out + row0 * kDim)[i] = make_uint4(0u, 0u, 0u, 0u);
+            if (p.lse)
+                for (int i = tid; i < p.q_len * heads; i += 256)
+                    p.lse[row0 + i] = -INFINITY;
+        }
+        bool dead = false;
+        uint32_t it = 0, done = 0;
+        int seg = 0;
+        for (; walk.left > 0; walk.next(p), ++seg) {
+            const int n = walk.run(), h = walk.u % p.kv_heads, row0 = walk.u / p.kv_heads * p.tile_rows;
+            const int rows = min(p.tile_rows, unit_rows - row0), len = walk.len, j0 = walk.j;
+            const bool whole = n == walk.P;
+            const int64_t slot = static_cast<int64_t>(2 * cta + (seg > 0)) * p.tile_rows;
+            // the place of row r among [query rows, query heads]
+            auto place = [&](int r) {
+                return (static_cast<int64_t>(walk.b) * p.q_len + (row0 + r) / p.group) * heads + h * p.group + (row0 + r) % p.group;
+            };
+            const int begins = WAYS == 2 ? done & 1 : 0;  // the chain that has the run's first page
+            if (!dead) {
+                // both chains, and who issues their products, are through with the unit before: its query rows, and the
+                // numbers of its rows
+                const bool ok = seg == 0 || wait(&ctl->q_taken, (seg - 1) & 1);
+                dead = barrier_any(2, 256, !ok);
+            }
+            if (!dead) {
+                // 16 lanes a query row
+                for (int r = tid >> 4; r < R; r += 16) {
+                    const bool have = r < rows;
+                    const int c = tid & 15;
+                    const int64_t q_row = static_cast<int64_t>(walk.b) * p.q_len + (row0 + r) / p.group;
+                    const uint4 v = have ? reinterpret_cast<const uint4 *>(p.q + q_row * p.q_stride +
+                                                                           (h * p.group + (row0 + r) % p.group) * kDim)[c]
+                                         : make_uint4(0u, 0u, 0u, 0u);
+                    if (!F::kFp8) {
+                        *reinterpret_cast<uint4 *>(smem + (c >> 3) * (R * 128) + r * 128 + (((c ^ r) & 7) << 4)) = v;
+                    } else {
+                        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                        float top = 0.0f;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            top = fmaxf(top, fmaxf(fabsf(bf16_lo(w[i])), fabsf(bf16_hi(w[i]))));
+#pragma unroll
+                        for (int o = 8; o >= 1; o >>= 1)
+                            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                        float undo;
+                        const float f = q_row_factor(top, &undo) * (1.0f / 64);  // [2^13, 2^14) to [2^7, 2^8)
+                        uint32_t term[4][F::kQTerms];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            e4m3_terms(bf16_lo(w[i]) * f, bf16_hi(w[i]) * f, term[i]);
+#pragma unroll
+                        for (int k = 0; k < F::kQTerms; ++k) {
+                            const int at = (r / N) * L::kSCols + k * N + r % N;
+                            *reinterpret_cast<uint2 *>(smem + at * 128 + ((((c >> 1) ^ at) & 7) << 4) + (c & 1) * 8) =
+                                make_uint2(term[0][k] | term[1][k] << 16, term[2][k] | term[3][k] << 16);
+                        }
+                        if (c == 0)
+                            ctl->undo[r] = undo * 64.0f;
+                    }
+                    if (c == 0)
+                        ctl->sees[r] = have ? max(0, len - (p.q_len - 1 - (row0 + r) / p.group)) : 0;
+                }
+                if (tau < N) {
+                    ctl->row[t][tau] = make_float4(1.0f, -INFINITY, 1.0f, 0.0f);
+                    ctl->vtop[t][tau] = 0.0f;
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(smem_addr(&ctl->q_full));
+                barrier_sync(2, 256);
+            }
+            float l[N];
+#pragma unroll
+            for (int r = 0; r < N; ++r)
+                l[r] = 0.0f;
+            bool bad = false, stop = false;
+            const int *sees = ctl->sees + (WAYS == 2 ? 0 : t * N);
+            const float *undo = ctl->undo + (WAYS == 2 ? 0 : t * N);
+            const int open = len - (p.q_len - 1);  // tokens that every row sees
+            const int first = WAYS == 2 ? t ^ begins : 0;
+            for (int j = first; j < n && !dead; j += WAYS, ++it) {
+                const uint32_t tile = 2 * it;
+                const int sk = L::stage(t, tile), sv = L::stage(t, tile + 1);
+                const int base = (j0 + j) * kPage;
+                bad |= !wait(&ctl->kv_full[sk], L::phase(tile));
+                const int valid = ctl->page_ok[sk] ? min(kPage, len - base) : 0;  // tokens of the page that are data
+                const float ks = F::kFp8 ? scales[sk * kPage + tau] : 1.0f;
+                bad |= !wait(&ctl->s_full[t], it & 1);
+                tc_fence_after_sync();
+                uint32_t raw[F::kQTerms * N / 16][16];
+#pragma unroll
+                for (int i = 0; i < F::kQTerms * N / 16; ++i)
+                    tmem_ld_cols(ts + i * 16, raw[i]);
+                tmem_wait_ld(raw[0]);
+#pragma unroll
+                for (int i = 1; i < F::kQTerms * N / 16; ++i)
+                    tmem_regs_ready(raw[i]);
+                float s[N];  // the token's scores, before the row's factor
+#pragma unroll
+                for (int r = 0; r < N; ++r) {
+                    s[r] = __uint_as_float(raw[r / 16][r % 16]);
+                    if (F::kFp8)
+                        s[r] = fmaf(__uint_as_float(raw[(N + r) / 16 % (F::kQTerms * N / 16)][r % 16]), kPagedTermDown, s[r]) * (ks * undo[r]);
+                }
+                const bool masks = base + kPage > open || valid < kPage;
+                if (masks) {
+#pragma unroll
+                    for (int r = 0; r < N; ++r)
+                        s[r] = tau < valid && base + tau < sees[r] ? s[r] : -INFINITY;
+                }
+                // V's page: its scales, and what lies past the tokens is no data: zero it (0 x NaN is NaN)
+                float vs = 1.0f;
+                if (F::kFp8 || valid < kPage) {
+                    bad |= !wait(&ctl->kv_full[sv], L::phase(tile + 1));
+                    if (F::kFp8)
+                        vs = tau < valid ? scales[sv * kPage + tau] : 0.0f;
+                    if (tau >= valid) {
+                        uint8_t *at = kv + sv * F::kTileBytes + tau * 128;
+#pragma unroll
+                        for (int i = 0; i < F::kTileBytes / kPage / 16; ++i)
+                            *reinterpret_cast<uint4 *>(at + (i >> 3) * kHalfPageBytes + (i & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+                    }
+                }
+                // weights at the references so far; passed by somebody: again at new ones
+                float w[N], ls[N];
+                for (bool moved = false;; moved = true) {
+                    float top = 0.0f, most = 0.0f;
+#pragma unroll
+                    for (int r = 0; r < N; ++r) {
+                        const float4 row = ctl->row[t][r];
+                        float x = fmaf(s[r], p.scale_log2, -row.y);
+                        if (masks)
+                            x = s[r] == -INFINITY ? -INFINITY : x;
+                        top = fmaxf(top, x);
+                        ls[r] = exp2_approx(x);
+                        w[r] = ls[r];
+                        if (F::kFp8) {
+                            w[r] = ls[r] * vs * row.z;
+                            most = fmaxf(most, w[r]);
+                        }
+                    }
+                    if (moved)
+                        break;
+                    if (!barrier_any(3 + t, 128, top > kPagedLag || most > 448.0f || bad))
+                        break;
+                    stop = barrier_any(3 + t, 128, bad);  // (what one warp saw alone is no reason to leave the others)
+                    if (stop)
+                        break;
+                    // new references: the largest scores
+#pragma unroll
+                    for (int r = 0; r < N; ++r) {
+                        const int m = __reduce_max_sync(0xffffffffu, float_int(s[r] * p.scale_log2));
+                        if (lane == r)
+                            ctl->wmax[t][warp & 3][r] = m;
+                    }
+                    barrier_sync(3 + t, 128);
+                    if (tau < N) {
+                        const float old = ctl->row[t][tau].y;
+                        const float m = fmaxf(old, int_float(max(max(ctl->wmax[t][0][tau], ctl->wmax[t][1][tau]),
+                                                                 max(ctl->wmax[t][2][tau], ctl->wmax[t][3][tau]))));
+                        const float f = rescale(old, m);
+                        ctl->row[t][tau].y = m;
+                        ctl->lfac[t][tau] = f;
+                        ctl->fac[t][tau] = f;
+                    }
+                    barrier_sync(3 + t, 128);
+                    if (F::kFp8) {
+                        // and the weights' units, by the largest weight x V scale
+#pragma unroll
+                        for (int r = 0; r < N; ++r) {
+                            const float m = ctl->row[t][r].y;
+                            const float x = s[r] == -INFINITY ? 0.0f : exp2_approx(fmaf(s[r], p.scale_log2, -m)) * vs;
+                            const int q = __reduce_max_sync(0xffffffffu, __float_as_int(x));
+                            if (lane == r)
+                                ctl->wmax[t][warp & 3][r] = q;
+                        }
+                        barrier_sync(3 + t, 128);
+                        if (tau < N) {
+                            const float before = ctl->vtop[t][tau], f = ctl->lfac[t][tau], unit = ctl->row[t][tau].z;
+                            const float now = __int_as_float(max(max(ctl->wmax[t][0][tau], ctl->wmax[t][1][tau]),
+                                                                 max(ctl->wmax[t][2][tau], ctl->wmax[t][3][tau])));
+                            const float most = fmaxf(before * f, now);
+                            // the power of two that brings it to [2^6, 2^7)
+                            const int e = static_cast<int>(__float_as_uint(most) >> 23);
+                            const float to = most > 0.0f ? __int_as_float(max(10, min(244, 260 - e)) << 23) : 1.0f;
+                            ctl->vtop[t][tau] = most;
+                            ctl->row[t][tau].z = to;
+                            ctl->fac[t][tau] = before * f > 0.0f ? f * to * (1.0f / unit) : 0.0f;
+                        }
+                        barrier_sync(3 + t, 128);
+                    }
+#pragma unroll
+                    for (int r = 0; r < N; ++r)
+                        l[r] *= ctl->lfac[t][r];
+                    if (j >= WAYS) {  // what the pages before left in O
+                        bad |= !wait(&ctl->o_done[t], (it - 1) & 1);
+                        tc_fence_after_sync();
+#pragma unroll 1
+                        for (int i = 0; i < L::kOCols; i += 16) {
+                            uint32_t o[16];
+                            tmem_ld_cols(to + i, o);
+                            tmem_wait_ld(o);
+#pragma unroll
+                            for (int k = 0; k < 16; ++k)
+                                o[k] = __float_as_uint(__uint_as_float(o[k]) * ctl->fac[t][i % N + k]);
+                            tmem_st_cols(to + i, o);
+                        }
+                        tmem_wait_st();
+                    }
+                }
+                if (stop)
+                    break;
+                // (the product with the weights before has to be over)
+                if (it > 0)
+                    bad |= !wait(&ctl->o_done[t], (it - 1) & 1);
+#pragma unroll
+                for (int r = 0; r < N; ++r)
+                    l[r] += ls[r];
+                if (!F::kFp8) {
+#pragma unroll
+                    for (int r = 0; r < N; r += 8)
+                        *reinterpret_cast<uint4 *>(pbuf + (r / 8) * 2048) =
+                            make_uint4(f32x2_to_bf16x2(w[r], w[r + 1]), f32x2_to_bf16x2(w[r + 2], w[r + 3]),
+                                       f32x2_to_bf16x2(w[r + 4], w[r + 5]), f32x2_to_bf16x2(w[r + 6], w[r + 7]));
+                } else {
+#pragma unroll
+                    for (int r = 0; r < N; r += 16) {
+                        uint32_t c[F::kPTerms][4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            uint32_t a[F::kPTerms], b[F::kPTerms];
+                            e4m3_terms(w[r + 4 * i], w[r + 4 * i + 1], a);
+                            e4m3_terms(w[r + 4 * i + 2], w[r + 4 * i + 3], b);
+#pragma unroll
+                            for (int k = 0; k < F::kPTerms; ++k)
+                                c[k][i] = a[k] | b[k] << 16;
+                        }
+#pragma unroll
+                        for (int k = 0; k < F::kPTerms; ++k)
+                            *reinterpret_cast<uint4 *>(pbuf + ((k * N + r) / 16) * 2048) = make_uint4(c[k][0], c[k][1], c[k][2], c[k][3]);
+                    }
+                }
+                fence_proxy_async_smem();
+                tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(smem_addr(&ctl->p_full[t]));
+                    mbar_arrive(smem_addr(&ctl->kv_empty[sk]));
+                    mbar_arrive(smem_addr(&ctl->kv_empty[sv]));
+                }
+            }
+            done += n;
+            // ---- the run's part of the unit ----
+            if (!dead) {
+                bad |= stop;
+                if (first < n && !bad)
+                    bad |= !wait(&ctl->o_done[t], (it - 1) & 1);
+                const float sum = lanes_sum<N>(l, lane);
+                if (lane < N)
+                    ctl->wsum[t][warp & 3][lane] = sum;
+                dead = barrier_any(2, 256, bad);
+            }
+            if (dead) {
+                for (int r = tid >> 5; r < rows; r += 8) {
+                    if (!whole) {
+                        if (lane == 0)
+                            p.part_lse[slot + r] = INFINITY;
+                        continue;
+                    }
+                    reinterpret_cast<uint2 *>(p.out + place(r) * kDim)[lane] = make_uint2(0u, 0u);
+                    if (p.lse && lane == 0)
+                        p.lse[place(r)] = -INFINITY;
+                }
+                continue;
+            }
+            if (tid < R) {
+                float m[2], sum[2];
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    const bool mine = WAYS == 2 || c == tid / N;
+                    const float *x = &ctl->wsum[c][0][tid % N];
+                    m[c] = mine ? ctl->row[c][tid % N].y : -INFINITY;
+                    sum[c] = mine ? (x[0] + x[N]) + (x[2 * N] + x[3 * N]) : 0.0f;
+                }
+                const float M = fmaxf(m[0], m[1]);
+                float all = 0.0f;
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    m[c] = sum[c] > 0.0f ? rescale(m[c], M) : 0.0f;
+                    all += m[c] * sum[c];
+                }
+#pragma unroll
+                for (int c = 0; c < 2; ++c)  // 0: nothing, and what stands in O may be anything
+                    ctl->share[c][tid] = sum[c] > 0.0f ? m[c] / (all * ctl->row[c][tid % N].z) : 0.0f;
+                if (tid < rows) {
+                    const float e = all > 0.0f ? M + log2f(all) : -INFINITY;
+                    if (!whole)
+                        p.part_lse[slot + tid] = e;
+                    else if (p.lse)
+                        p.lse[place(tid)] = e * kLn2;
+                }
+            }
+            barrier_sync(2, 256);
+            tc_fence_after_sync();
+            // a thread a dim: 8 rows at a time, both chains' shares of them; WAYS 2: the chains' warps take turns
+            for (int r0 = WAYS == 2 ? t * 8 : t * N; r0 < (WAYS == 2 ? N : t * N + N) && r0 < rows; r0 += WAYS * 8) {
+                float acc[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    acc[k] = 0.0f;
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    if (WAYS == 1 && c != t)
+                        continue;
+                    if (WAYS == 2 && (c ^ begins) >= n)  // a chain without a page
+                        continue;
+                    const uint32_t from = tmem + c * L::kChainCols + L::kSCols + lanes + r0 % N;
+                    uint32_t o[F::kPTerms][8];
+#pragma unroll
+                    for (int k = 0; k < F::kPTerms; ++k)
+                        asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                                     : "=r"(o[k][0]), "=r"(o[k][1]), "=r"(o[k][2]), "=r"(o[k][3]), "=r"(o[k][4]),
+                                       "=r"(o[k][5]), "=r"(o[k][6]), "=r"(o[k][7])
+                                     : "r"(from + k * N));
+#pragma unroll
+                    for (int k = 0; k < F::kPTerms; ++k)
+                        asm volatile("tcgen05.wait::ld.sync.aligned;"
+                                     : "+r"(o[k][0]), "+r"(o[k][1]), "+r"(o[k][2]), "+r"(o[k][3]), "+r"(o[k][4]),
+                                       "+r"(o[k][5]), "+r"(o[k][6]), "+r"(o[k][7])::"memory");
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        float x = __uint_as_float(o[0][k]);
+                        if (F::kFp8)
+                            x += kPagedTermDown * (__uint_as_float(o[F::kPTerms / 2][k]) +
+                                                   kPagedTermDown * __uint_as_float(o[F::kPTerms - 1][k]));
+                        const float share = ctl->share[c][r0 + k];
+                        acc[k] += share != 0.0f ? share * x : 0.0f;
+                    }
+                }
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const int r = r0 + k;
+                    if (r < rows) {
+                        if (whole)
+                            p.out[place(r) * kDim + tau] = static_cast<uint16_t>(f32x2_to_bf16x2(acc[k], 0.0f));
+                        else
+                            p.part_o[(slot + r) * kDim + tau] = acc[k];
+                    }
+                }
+            }
+            tc_fence_before_sync();
+        }
+        tc_fence_before_sync();
+    }
+    __syncthreads();
+    if (warp == 9)
+        tmem_dealloc(tmem, L::kTmem);
+}
+
+// ---------------------------------------------------------------------------
+// The units that a range's end cuts: block (c - 1, i) takes the one that CTA c is the first to go on with, and of its rows
+// those from 8 / WPR i on; WPR warps a row take its parts in turn.
+template <int WPR>
+__global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__ PagedParams p)
+{
+    constexpr int kRows = 8 / WPR;
+    __shared__ PagedScan scan;
+    __shared__ float4 s_acc[8][32];
+    __shared__ float s_m[8], s_sum[8];
+    __shared__ int s_bad[8];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, sub = warp % WPR;
+    const int c = blockIdx.x + 1;
+    const int total = paged_find<256>(p, &scan, [&](int all) {
+        const PagedSplit s(all, p.grid);
+        return c < s.ctas ? s.start(c) : -1;
+    });
+    const PagedSplit split(total, p.grid);
+    const PagedAt at = scan.at;
+    griddep_wait();  // also where there is nothing to do: who waits for this grid reads what both have written
+    if (c >= split.ctas || at.j == 0 || at.j > split.start(c) - split.start(c - 1))
+        return;  // no unit goes on there, or another block has it
+    const int P = pages_of(paged_len(p, at.b)), from = split.start(c) - at.j;
+    int parts = 2;
+    while (c + parts - 1 < split.ctas && split.start(c + parts - 1) < from + P)
+        ++parts;
+    // slot of part i: the CTA's first run, but for the unit's first part where the CTA has others before it
+    const int slot0 = 2 * (c - 1) + (split.start(c - 1) < from);
+    const int h = at.u % p.kv_heads, row0 = at.u / p.kv_heads * p.tile_rows;
+    const int rows = min(p.tile_rows, p.q_len * p.group - row0);
+    const int r = blockIdx.y * kRows + warp / WPR;
+    auto slot = [&](int i) { return static_cast<int64_t>(i == 0 ? slot0 : 2 * (c - 1 + i)) * p.tile_rows + r; };
+    float M = -INFINITY, sum = 0.0f;
+    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    bool bad = false;
+    const bool exists = r < rows;
+    const int mine = exists && parts > sub ? (parts - sub + WPR - 1) / WPR : 0;
+    for (int i0 = 0; i0 < mine; i0 += 32) {
+        const int end = min(32, mine - i0);
+        const float x = lane < end ? __ldcg(p.part_lse + slot(sub + (i0 + lane) * WPR)) : -INFINITY;
+        bad |= __any_sync(0xffffffffu, x == INFINITY);
+        float to = fmaxf(M, x);
+#pragma unroll
+        for (int q = 16; q >= 1; q >>= 1)
+            to = fmaxf(to, __shfl_xor_sync(0xffffffffu, to, q));
+        const float old = rescale(M, to), f = x == -INFINITY ? 0.0f : rescale(x, to);
+        M = to;
+        sum *= old;
+        acc.x *= old;
+        acc.y *= old;
+        acc.z *= old;
+        acc.w *= old;
+        for (int i = 0; i < end; i += 4) {
+            float4 v[4];  // under way together
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                v[k] = i + k < end ? __ldcg(reinterpret_cast<const float4 *>(p.part_o + slot(sub + (i0 + i + k) * WPR) * kDim) + lane)
+                                   : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float fi = __shfl_sync(0xffffffffu, f, i + k);
+                const bool some = fi != 0.0f;
+                sum += fi;
+                acc.x += some ? fi * v[k].x : 0.0f;
+                acc.y += some ? fi * v[k].y : 0.0f;
+                acc.z += some ? fi * v[k].z : 0.0f;
+                acc.w += some ? fi * v[k].w : 0.0f;
+            }
+        }
+    }
+    if (WPR > 1) {
+        s_acc[warp][lane] = acc;
+        if (lane == 0) {
+            s_m[warp] = M;
+            s_sum[warp] = sum;
+            s_bad[warp] = bad;
+        }
+        __syncthreads();
+        if (sub != 0)
+            return;
+#pragma unroll
+        for (int w = 1; w < WPR; ++w) {
+            const float m = s_m[warp + w], to = fmaxf(M, m), fa = rescale(M, to), fb = rescale(m, to);
+            const float4 v = s_acc[warp + w][lane];
+            sum = sum * fa + s_sum[warp + w] * fb;
+            acc.x = acc.x * fa + v.x * fb;
+            acc.y = acc.y * fa + v.y * fb;
+            acc.z = acc.z * fa + v.z * fb;
+            acc.w = acc.w * fa + v.w * fb;
+            M = to;
+            bad |= s_bad[warp + w] != 0;
+        }
+    }
+    if (!exists)
+        return;
+    const bool none = bad || sum == 0.0f;
+    const float inv = none ? 0.0f : 1.0f / sum;
+    const int64_t to = (static_cast<int64_t>(at.b) * p.q_len + (row0 + r) / p.group) * p.kv_heads * p.group + h * p.group +
+                       (row0 + r) % p.group;
+    uint2 w;
+    w.x = none ? 0u : f32x2_to_bf16x2(acc.x * inv, acc.y * inv);
+    w.y = none ? 0u : f32x2_to_bf16x2(acc.z * inv, acc.w * inv);
+    *reinterpret_cast<uint2 *>(p.out + to * kDim + lane * 4) = w;
+    if (p.lse && lane == 0)
+        p.lse[to] = none ? -INFINITY : (M + log2f(sum)) * kLn2;
+}
+
+}  // namespace msa

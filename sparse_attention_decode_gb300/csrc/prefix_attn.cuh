@@ -166,23 +166,6 @@ struct PrefixSmem {
 
 constexpr size_t kPrefixSmemBytes = 1024 + (2 + kPrefixStages) * kPageBytes + sizeof(PrefixSmem);
 
-// The MMA warps run their whole loop converged, with one elected lane behind a
-// predicate: descriptors and addresses are then the warp's, not a thread's, and an
-// instruction needs no moves from thread to uniform registers.  (Issued from inside
-// `if (lane == 0)`, an instruction of 64 cycles took about 110.)
-__device__ __forceinline__ uint32_t elect_one()
-{
-    uint32_t one;
-    asm volatile(
-        "{\n"
-        "  .reg .pred p;\n"
-        "  elect.sync _|p, 0xffffffff;\n"
-        "  selp.u32 %0, 1, 0, p;\n"
-        "}\n"
-        : "=r"(one));
-    return one;
-}
-
 // D[tmem] (+)= A[smem] * B[smem]^T, by the elected lane.
 template <bool ACC>
 __device__ __forceinline__ void umma_ss_one(uint32_t one, uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t idesc)
@@ -216,18 +199,6 @@ __device__ __forceinline__ void umma_ts_one(uint32_t one, uint32_t d_tmem, uint3
         : "memory");
 }
 
-__device__ __forceinline__ void umma_commit_one(uint32_t one, uint32_t bar)
-{
-    asm volatile(
-        "{\n"
-        "  .reg .pred p;\n"
-        "  setp.ne.u32 p, %1, 0;\n"
-        "  @p tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n"
-        "}\n" ::"r"(bar),
-        "r"(one)
-        : "memory");
-}
-
 // The maximum of three.
 __device__ __forceinline__ float max3(float a, float b, float c)
 {
@@ -248,14 +219,6 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32
         "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
         "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(taddr)
         : "memory");
-}
-__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-
-// V as B operand: N (the dims) contiguous in the 128-byte swizzle.  64 dims x 8 tokens make an atom of 1024 bytes;
-// the next 64 dims are one half tile (16 KiB) on, the next 8 tokens one atom on.
-__device__ __forceinline__ uint32_t umma_desc_v_lo(uint32_t saddr)
-{
-    return ((saddr >> 4) & 0x3FFFu) | (static_cast<uint32_t>(kHalfPageBytes >> 4) << 16);
 }
 
 // Chain t's MMAs, by one warp: for each of its pages the product of the weights

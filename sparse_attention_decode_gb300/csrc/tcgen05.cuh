@@ -111,6 +111,42 @@ __device__ __forceinline__ void umma_commit(uint32_t bar)
                  : "memory");
 }
 
+// Issue by one lane of a converged warp.  The MMA warps run their whole loop converged, with one elected lane behind a
+// predicate: descriptors and addresses are then the warp's, not a thread's, and an
+// instruction needs no moves from thread to uniform registers.  (Issued from inside
+// `if (lane == 0)`, an instruction of 64 cycles took about 110.)
+__device__ __forceinline__ uint32_t elect_one()
+{
+    uint32_t one;
+    asm volatile(
+        "{\n"
+        "  .reg .pred p;\n"
+        "  elect.sync _|p, 0xffffffff;\n"
+        "  selp.u32 %0, 1, 0, p;\n"
+        "}\n"
+        : "=r"(one));
+    return one;
+}
+
+__device__ __forceinline__ void umma_commit_one(uint32_t one, uint32_t bar)
+{
+    asm volatile(
+        "{\n"
+        "  .reg .pred p;\n"
+        "  setp.ne.u32 p, %1, 0;\n"
+        "  @p tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n"
+        "}\n" ::"r"(bar),
+        "r"(one)
+        : "memory");
+}
+
+// V as an operand whose rows (the dims) are contiguous, in the 128-byte swizzle.  64 dims x 8 tokens make an atom of 1024 bytes;
+// the next 64 dims are one half tile (16 KiB) on, the next 8 tokens one atom on.
+__device__ __forceinline__ uint32_t umma_desc_v_lo(uint32_t saddr)
+{
+    return ((saddr >> 4) & 0x3FFFu) | ((16384u >> 4) << 16);
+}
+
 // 32 consecutive fp32 columns of one TMEM lane per thread (shape 32x32b: warp
 // w reads lanes 32*(w%4) .. 32*(w%4)+31, lane i of the warp gets lane 32*(w%4)+i).
 // The values are valid after tmem_wait_ld(r).
@@ -152,6 +188,9 @@ __device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[16])
                    "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
                    "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]));
 }
+
+// Waits for all of this thread's TMEM stores.
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // Marks r as written here: placed after a tmem_wait_ld that also covered r's
 // load, it keeps r's uses after that wait.

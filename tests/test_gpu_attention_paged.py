@@ -236,3 +236,23 @@ def test_refusals():
     for kw in (dict(q=q.half()), dict(k=kp[..., :64]), dict(k=kp.float()), dict(out=out[:, :4]), dict(seq=seq.long()),
                dict(k=kp[:2]), dict(ws=ws.cpu()), dict(q=q[:, :3])):
         assert status(**kw) == "refused", kw
+
+
+@pytest.mark.parametrize("e4m3", [False, True], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("group", [16, 32, 64])
+def test_waits_that_run_out_empty_the_rows(e4m3, group):
+    """The producer withholds every page: bounded waits give up, the rows are empty, the next call is exact."""
+    import sparse_attention_decode_gb300 as msa
+    w = make(50, [9000, 0, 300, 2000], 1, 4, group, "hnd", e4m3)
+    ws = torch.zeros(msa.msa_attention_paged_workspace_bytes(4, 4 * group, 4), dtype=torch.uint8, device="cuda")
+    whole = call(msa, w, ws=ws)
+    assert whole[2] == 0
+    msa.msa_indexer_test_withhold_pages(1)
+    try:
+        out, lse, fault = call(msa, w, ws=ws)
+    finally:
+        msa.msa_indexer_test_withhold_pages(0)
+    assert fault == msa.MSA_FAULT_TIMEOUT
+    assert not bool(out.any()) and bool((lse == -float("inf")).all())
+    again = call(msa, w, ws=ws)
+    assert again[2] == 0 and all(torch.equal(a, b) for a, b in zip(again[:2], whole[:2]))
