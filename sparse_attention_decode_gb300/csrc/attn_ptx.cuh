@@ -60,6 +60,14 @@ __device__ __forceinline__ float exp2_approx(float x)
     return y;
 }
 
+// The maximum of three.
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
 // CTAs of this CTA's cluster, and loads from another one's shared memory.
 __device__ __forceinline__ uint32_t cluster_nctarank()
 {

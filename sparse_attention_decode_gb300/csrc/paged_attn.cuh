@@ -55,6 +55,7 @@ constexpr int kPagedThreads = 352;  // two softmax warpgroups, a TMA warp, two M
 constexpr int kPagedMaxGrid = 256;
 constexpr int kPagedMaxRows = 64;   // of a unit: one chain's 16 or 32, or both chains' 32
 constexpr float kPagedLag = 8.0f;
+constexpr float kPagedMost = 256.0f;  // of an E4M3 weight: what is left of it after a term is then at most 256 as well
 constexpr float kPagedTermUp = 32.0f;                  // an E4M3 term over the next
 constexpr float kPagedTermDown = 1.0f / kPagedTermUp;
 
@@ -183,20 +184,23 @@ struct PagedWalk {
 template <int N, int STAGES>
 struct PagedSmem {
     uint64_t kv_full[STAGES], kv_empty[STAGES];
-    uint64_t q_full, q_taken, s_full[2], p_full[2], o_done[2], drained[2];
+    uint64_t q_full, q_taken, s_full[2], s_free[2], p_full[2], o_done[2], drained[2];
     int page_ok[STAGES];
     PagedScan scan;
     uint32_t tmem;
     int abort_flag;
-    float4 row[2][N];       // a chain's rows: undo of the query row (E4M3), reference (log2 units), unit of the weights (E4M3)
-    float fac[2][N];        // what a moved reference multiplies a row's O by
-    float lfac[2][N];       // and its sum
-    float vtop[2][N];       // E4M3: the row's largest weight x V scale at its reference
-    int wmax[2][4][N];      // the warps' maxima, in an order of integers
+    int64_t q_at[2 * N];             // the unit's rows: where their queries lie, from the request's and head's on,
+    int at[2 * N], hidden[2 * N];    // their places among [query rows, query heads], the last tokens they do not see
+    int sees[2 * N];                 // and those they do, of the request at hand
+    alignas(16) float coef[2 * N];   // E4M3: the score scale and the query row's power of two, undone
+    alignas(16) float nref[2][N];    // a chain's rows: the reference (log2 units), negative
+    alignas(16) float unit[2][N];    // E4M3: what weights x V scale are multiplied by
+    alignas(16) float fac[2][N];     // what a moved reference multiplies a row's O by,
+    alignas(16) float lfac[2][N];    // and its sum
+    float vtop[2][N];                // E4M3: the row's largest weight x V scale at its reference
+    int wmax[2][4][N];               // the warps' maxima, in an order of integers
     float wsum[2][4][N];
-    int sees[2 * N];        // tokens a row sees
-    float undo[2 * N];      // E4M3: the query row's power of two, undone
-    float share[2][2 * N];  // what a chain's part of a row is multiplied by at the end
+    float share[2][2 * N];           // what a chain's part of a row is multiplied by at the end
 };
 
 // Shared memory: query rows, the chains' weights, as many tiles of K and V as there is room for, their scales.
@@ -221,7 +225,7 @@ struct PagedLayout {
         return static_cast<int>(tile % kDepth) + (WAYS == 2 ? chain * kDepth : 0);
     }
     static __device__ __forceinline__ uint32_t phase(uint32_t tile) { return (tile / kDepth) & 1; }
-    static_assert(kKv % 1024 == 0 && kStages >= 4 && kStages <= 12 && kBytes <= 232448 && 2 * kChainCols <= 512,
+    static_assert(kKv % 1024 == 0 && kDepth >= 3 && kStages <= 12 && kBytes <= 232448 && 2 * kChainCols <= 512,
                   "shared and tensor memory");
 };
 
@@ -384,6 +388,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attn_kernel(const __gr
         mbar_init(smem_addr(&ctl->q_taken), 2);
         for (int t = 0; t < 2; ++t) {
             mbar_init(smem_addr(&ctl->s_full[t]), 1);
+            mbar_init(smem_addr(&ctl->s_free[t]), 4);
             mbar_init(smem_addr(&ctl->p_full[t]), 4);
             mbar_init(smem_addr(&ctl->o_done[t]), 1);
             mbar_init(smem_addr(&ctl->drained[t]), 1);
@@ -485,6 +490,19 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attn_kernel(const __gr
             return attn_wait(&ctl->abort_flag, p.fault, smem_addr(bar), parity, p.withhold);
         };
         auto landed = [&](uint32_t tile) { return wait(&ctl->kv_full[L::stage(t, tile)], L::phase(tile)); };
+        auto test = [&](uint64_t *bar, uint32_t parity) { return __all_sync(0xffffffffu, mbar_test_wait(smem_addr(bar), parity)); };
+        auto scores = [&](uint32_t tile) {
+            const int sk = L::stage(t, tile);
+            const uint32_t a = umma_desc_lo(kv_addr + sk * F::kTileBytes);
+#pragma unroll
+            for (int ks = 0; ks < kSteps; ++ks) {
+                const uint32_t off = F::kFp8 ? ks * 32 : (ks >> 2) * kHalfPageBytes + (ks & 3) * 32;
+                const uint32_t boff = F::kFp8 ? ks * 32 : (ks >> 2) * (R * 128) + (ks & 3) * 32;
+                umma_small<F::kFp8>(one, d_s, a + (off >> 4), kUmmaDescHi, q_desc + (boff >> 4), kUmmaDescHi, idesc_s, ks > 0);
+            }
+            umma_commit_one(one, smem_addr(&ctl->s_full[t]));
+            umma_commit_one(one, smem_addr(&ctl->kv_empty[sk]));
+        };
         bool alive = true;
         uint32_t it = 0, done = 0, seg = 0;
         for (; walk.left > 0 && alive; walk.next(p)) {
@@ -492,26 +510,31 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attn_kernel(const __gr
             alive = wait(&ctl->q_full, seg++ & 1);
             if (one)
                 mbar_arrive(smem_addr(&ctl->q_taken));
+            bool ahead = false;  // the page's scores have been asked for
             for (int j = WAYS == 2 ? (t ^ done) & 1 : 0; j < n && alive; j += WAYS, ++it) {
-                const uint32_t tile = 2 * it;
-                alive = landed(tile);
-                if (!alive)
-                    break;
-                tc_fence_after_sync();
-                const int sk = L::stage(t, tile), sv = L::stage(t, tile + 1);
-                const uint32_t a = umma_desc_lo(kv_addr + sk * F::kTileBytes);
-#pragma unroll
-                for (int ks = 0; ks < kSteps; ++ks) {
-                    const uint32_t off = F::kFp8 ? ks * 32 : (ks >> 2) * kHalfPageBytes + (ks & 3) * 32;
-                    const uint32_t boff = F::kFp8 ? ks * 32 : (ks >> 2) * (R * 128) + (ks & 3) * 32;
-                    umma_small<F::kFp8>(one, d_s, a + (off >> 4), kUmmaDescHi, q_desc + (boff >> 4), kUmmaDescHi, idesc_s, ks > 0);
+                if (!ahead) {
+                    alive = landed(2 * it);
+                    if (!alive)
+                        break;
+                    tc_fence_after_sync();
+                    scores(2 * it);
                 }
-                umma_commit_one(one, smem_addr(&ctl->s_full[t]));
-                umma_commit_one(one, smem_addr(&ctl->kv_empty[sk]));
-                alive = landed(tile + 1) && wait(&ctl->p_full[t], it & 1);
+                ahead = false;
+                // the next page's scores as soon as its keys are there and this page's have been read, so that they run
+                // beside the softmax; its weights otherwise
+                for (uint32_t i = 0; j + WAYS < n && !ahead && i < kSpinLimit && !test(&ctl->p_full[t], it & 1) &&
+                                     !*reinterpret_cast<volatile int *>(&ctl->abort_flag);
+                     ++i)
+                    if (test(&ctl->s_free[t], it & 1) && test(&ctl->kv_full[L::stage(t, 2 * it + 2)], L::phase(2 * it + 2))) {
+                        tc_fence_after_sync();
+                        scores(2 * it + 2);
+                        ahead = true;
+                    }
+                alive = landed(2 * it + 1) && wait(&ctl->p_full[t], it & 1);
                 if (!alive)
                     break;
                 tc_fence_after_sync();
+                const int sv = L::stage(t, 2 * it + 1);
                 const uint32_t v = umma_desc_v_lo(kv_addr + sv * F::kTileBytes);
 #pragma unroll
                 for (int ks = 0; ks < kSteps; ++ks)
@@ -545,18 +568,27 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attn_kernel(const __gr
                 for (int i = tid; i < p.q_len * heads; i += 256)
                     p.lse[row0 + i] = -INFINITY;
         }
+        // the rows of tile `row0` on: the same for every request and head
+        auto lay_rows = [&](int row0) {
+            if (tid < R) {
+                const int i = (row0 + tid) / p.group, g = row0 + tid - i * p.group;
+                ctl->q_at[tid] = i * p.q_stride + g * kDim;
+                ctl->at[tid] = i * heads + g;
+                ctl->hidden[tid] = row0 + tid < unit_rows ? p.q_len - 1 - i : 0x3fffffff;
+            }
+            barrier_sync(2, 256);
+        };
+        if (p.row_tiles == 1)
+            lay_rows(0);
         bool dead = false;
         uint32_t it = 0, done = 0;
         int seg = 0;
         for (; walk.left > 0; walk.next(p), ++seg) {
-            const int n = walk.run(), h = walk.u % p.kv_heads, row0 = walk.u / p.kv_heads * p.tile_rows;
-            const int rows = min(p.tile_rows, unit_rows - row0), len = walk.len, j0 = walk.j;
+            const int n = walk.run(), tile_at = walk.u / p.kv_heads, h = walk.u - tile_at * p.kv_heads;
+            const int rows = min(p.tile_rows, unit_rows - tile_at * p.tile_rows), len = walk.len, j0 = walk.j;
             const bool whole = n == walk.P;
             const int64_t slot = static_cast<int64_t>(2 * cta + (seg > 0)) * p.tile_rows;
-            // the place of row r among [query rows, query heads]
-            auto place = [&](int r) {
-                return (static_cast<int64_t>(walk.b) * p.q_len + (row0 + r) / p.group) * heads + h * p.group + (row0 + r) % p.group;
-            };
+            const int64_t place0 = static_cast<int64_t>(walk.b) * p.q_len * heads + h * p.group;  // the first row's, ctl->at from there
             const int begins = WAYS == 2 ? done & 1 : 0;  // the chain that has the run's first page
             if (!dead) {
                 // both chains, and who issues their products, are through with the unit before: its query rows, and the
@@ -565,45 +597,53 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attn_kernel(const __gr
                 dead = barrier_any(2, 256, !ok);
             }
             if (!dead) {
+                if (p.row_tiles > 1)
+                    lay_rows(tile_at * p.tile_rows);
                 // 16 lanes a query row
-                for (int r = tid >> 4; r < R; r += 16) {
-                    const bool have = r < rows;
-                    const int c = tid & 15;
-                    const int64_t q_row = static_cast<int64_t>(walk.b) * p.q_len + (row0 + r) / p.group;
-                    const uint4 v = have ? reinterpret_cast<const uint4 *>(p.q + q_row * p.q_stride +
-                                                                           (h * p.group + (row0 + r) % p.group) * kDim)[c]
-                                         : make_uint4(0u, 0u, 0u, 0u);
+                const uint16_t *q = p.q + static_cast<int64_t>(walk.b) * p.q_len * p.q_stride + h * p.group * kDim;
+                const int c = tid & 15;
+                uint4 v[R / 16];
+#pragma unroll
+                for (int i = 0; i < R / 16; ++i) {
+                    const int r = (tid >> 4) + 16 * i;
+                    v[i] = r < rows ? reinterpret_cast<const uint4 *>(q + ctl->q_at[r])[c] : make_uint4(0u, 0u, 0u, 0u);
+                }
+#pragma unroll
+                for (int i = 0; i < R / 16; ++i) {
+                    const int r = (tid >> 4) + 16 * i;
                     if (!F::kFp8) {
-                        *reinterpret_cast<uint4 *>(smem + (c >> 3) * (R * 128) + r * 128 + (((c ^ r) & 7) << 4)) = v;
-                    } else {
-                        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-                        float top = 0.0f;
+                        *reinterpret_cast<uint4 *>(smem + (c >> 3) * (R * 128) + r * 128 + (((c ^ r) & 7) << 4)) = v[i];
+                        continue;
+                    }
+                    const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+                    float top = 0.0f;
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            top = fmaxf(top, fmaxf(fabsf(bf16_lo(w[i])), fabsf(bf16_hi(w[i]))));
+                    for (int k = 0; k < 4; ++k)
+                        top = max3(top, fabsf(bf16_lo(w[k])), fabsf(bf16_hi(w[k])));
 #pragma unroll
-                        for (int o = 8; o >= 1; o >>= 1)
-                            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-                        float undo;
-                        const float f = q_row_factor(top, &undo) * (1.0f / 64);  // [2^13, 2^14) to [2^7, 2^8)
-                        uint32_t term[4][F::kQTerms];
+                    for (int o = 8; o >= 1; o >>= 1)
+                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                    // the power of two that brings it to [2^7, 2^8)
+                    const int e = max(15, min(246, static_cast<int>(__float_as_uint(top) >> 23)));
+                    const float f = __int_as_float((261 - e) << 23);
+                    uint32_t term[4][F::kQTerms];
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            e4m3_terms(bf16_lo(w[i]) * f, bf16_hi(w[i]) * f, term[i]);
+                    for (int k = 0; k < 4; ++k)
+                        e4m3_terms(bf16_lo(w[k]) * f, bf16_hi(w[k]) * f, term[k]);
 #pragma unroll
-                        for (int k = 0; k < F::kQTerms; ++k) {
-                            const int at = (r / N) * L::kSCols + k * N + r % N;
-                            *reinterpret_cast<uint2 *>(smem + at * 128 + ((((c >> 1) ^ at) & 7) << 4) + (c & 1) * 8) =
-                                make_uint2(term[0][k] | term[1][k] << 16, term[2][k] | term[3][k] << 16);
-                        }
-                        if (c == 0)
-                            ctl->undo[r] = undo * 64.0f;
+                    for (int k = 0; k < F::kQTerms; ++k) {
+                        const int at = (r / N) * L::kSCols + k * N + r % N;
+                        *reinterpret_cast<uint2 *>(smem + at * 128 + ((((c >> 1) ^ at) & 7) << 4) + (c & 1) * 8) =
+                            make_uint2(term[0][k] | term[1][k] << 16, term[2][k] | term[3][k] << 16);
                     }
                     if (c == 0)
-                        ctl->sees[r] = have ? max(0, len - (p.q_len - 1 - (row0 + r) / p.group)) : 0;
+                        ctl->coef[r] = __int_as_float((e - 7) << 23) * p.scale_log2;
                 }
+                if (tid < R)
+                    ctl->sees[tid] = max(0, len - ctl->hidden[tid]);
                 if (tau < N) {
-                    ctl->row[t][tau] = make_float4(1.0f, -INFINITY, 1.0f, 0.0f);
+                    ctl->nref[t][tau] = INFINITY;
+                    ctl->unit[t][tau] = 1.0f;
                     ctl->vtop[t][tau] = 0.0f;
                 }
                 fence_proxy_async_smem();
@@ -612,13 +652,13 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attn_kernel(const __gr
                     mbar_arrive(smem_addr(&ctl->q_full));
                 barrier_sync(2, 256);
             }
-            float l[N];
+            uint64_t l2[N / 2];  // sums of the token's weights, two rows each
 #pragma unroll
-            for (int r = 0; r < N; ++r)
-                l[r] = 0.0f;
+            for (int r = 0; r < N / 2; ++r)
+                l2[r] = 0;
             bool bad = false, stop = false;
             const int *sees = ctl->sees + (WAYS == 2 ? 0 : t * N);
-            const float *undo = ctl->undo + (WAYS == 2 ? 0 : t * N);
+            const float *coef = ctl->coef + (WAYS == 2 ? 0 : t * N);
             const int open = len - (p.q_len - 1);  // tokens that every row sees
             const int first = WAYS == 2 ? t ^ begins : 0;
             for (int j = first; j < n && !dead; j += WAYS, ++it) {
@@ -630,20 +670,33 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attn_kernel(const __gr
                 const float ks = F::kFp8 ? scales[sk * kPage + tau] : 1.0f;
                 bad |= !wait(&ctl->s_full[t], it & 1);
                 tc_fence_after_sync();
-                uint32_t raw[F::kQTerms * N / 16][16];
+                float s[N];  // the token's scores: E4M3 in log2 units, bf16 before the scale
+                {
+                    uint32_t raw[F::kQTerms * N / 16][16];
 #pragma unroll
-                for (int i = 0; i < F::kQTerms * N / 16; ++i)
-                    tmem_ld_cols(ts + i * 16, raw[i]);
-                tmem_wait_ld(raw[0]);
+                    for (int i = 0; i < F::kQTerms * N / 16; ++i)
+                        tmem_ld_cols(ts + i * 16, raw[i]);
+                    tmem_wait_ld(raw[0]);
 #pragma unroll
-                for (int i = 1; i < F::kQTerms * N / 16; ++i)
-                    tmem_regs_ready(raw[i]);
-                float s[N];  // the token's scores, before the row's factor
+                    for (int i = 1; i < F::kQTerms * N / 16; ++i)
+                        tmem_regs_ready(raw[i]);
+                    tc_fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(smem_addr(&ctl->s_free[t]));
+                    const uint64_t down = pack2(kPagedTermDown, kPagedTermDown), ks2 = pack2(ks, ks);
 #pragma unroll
-                for (int r = 0; r < N; ++r) {
-                    s[r] = __uint_as_float(raw[r / 16][r % 16]);
-                    if (F::kFp8)
-                        s[r] = fmaf(__uint_as_float(raw[(N + r) / 16 % (F::kQTerms * N / 16)][r % 16]), kPagedTermDown, s[r]) * (ks * undo[r]);
+                    for (int r = 0; r < N; r += 2) {
+                        s[r] = __uint_as_float(raw[r / 16][r % 16]);
+                        s[r + 1] = __uint_as_float(raw[r / 16][r % 16 + 1]);
+                        if (F::kFp8) {
+                            const uint32_t(&low)[16] = raw[(N + r) / 16 % (F::kQTerms * N / 16)];
+                            const float2 cf = *reinterpret_cast<const float2 *>(coef + r);
+                            const uint64_t x = fma2(pack2(__uint_as_float(low[r % 16]), __uint_as_float(low[r % 16 + 1])), down,
+                                                    pack2(s[r], s[r + 1]));
+                            unpack2(mul2(x, mul2(ks2, pack2(cf.x, cf.y))), s[r], s[r + 1]);
+                        }
+                    }
                 }
                 const bool masks = base + kPage > open || valid < kPage;
                 if (masks) {
@@ -657,34 +710,42 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attn_kernel(const __gr
                     bad |= !wait(&ctl->kv_full[sv], L::phase(tile + 1));
                     if (F::kFp8)
                         vs = tau < valid ? scales[sv * kPage + tau] : 0.0f;
-                    if (tau >= valid) {
-                        uint8_t *at = kv + sv * F::kTileBytes + tau * 128;
-#pragma unroll
-                        for (int i = 0; i < F::kTileBytes / kPage / 16; ++i)
-                            *reinterpret_cast<uint4 *>(at + (i >> 3) * kHalfPageBytes + (i & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
-                    }
+                    // neighbouring lanes neighbouring 16 bytes (a row a thread: 1.2 us a page)
+                    for (int half = 0; half < F::kTileBytes / (kPage * 128); ++half)
+                        for (int i = valid * 8 + tau; i < kPage * 8; i += 128)
+                            *reinterpret_cast<uint4 *>(kv + sv * F::kTileBytes + half * kHalfPageBytes + i * 16) = make_uint4(0u, 0u, 0u, 0u);
                 }
                 // weights at the references so far; passed by somebody: again at new ones
-                float w[N], ls[N];
+                const float to_log2 = F::kFp8 ? 1.0f : p.scale_log2;
+                const uint64_t c2 = pack2(to_log2, to_log2), vs2 = pack2(vs, vs);
+                float w[N];
+                uint64_t ls2[N / 2];
                 for (bool moved = false;; moved = true) {
                     float top = 0.0f, most = 0.0f;
 #pragma unroll
-                    for (int r = 0; r < N; ++r) {
-                        const float4 row = ctl->row[t][r];
-                        float x = fmaf(s[r], p.scale_log2, -row.y);
-                        if (masks)
+                    for (int r = 0; r < N; r += 2) {
+                        const float2 nr = *reinterpret_cast<const float2 *>(&ctl->nref[t][r]);
+                        float x, y;
+                        unpack2(F::kFp8 ? add2(pack2(s[r], s[r + 1]), pack2(nr.x, nr.y))
+                                        : fma2(pack2(s[r], s[r + 1]), c2, pack2(nr.x, nr.y)),
+                                x, y);
+                        if (masks) {
                             x = s[r] == -INFINITY ? -INFINITY : x;
-                        top = fmaxf(top, x);
-                        ls[r] = exp2_approx(x);
-                        w[r] = ls[r];
+                            y = s[r + 1] == -INFINITY ? -INFINITY : y;
+                        }
+                        top = max3(top, x, y);
+                        w[r] = exp2_approx(x);
+                        w[r + 1] = exp2_approx(y);
+                        ls2[r / 2] = pack2(w[r], w[r + 1]);
                         if (F::kFp8) {
-                            w[r] = ls[r] * vs * row.z;
-                            most = fmaxf(most, w[r]);
+                            const float2 un = *reinterpret_cast<const float2 *>(&ctl->unit[t][r]);
+                            unpack2(mul2(ls2[r / 2], mul2(vs2, pack2(un.x, un.y))), w[r], w[r + 1]);
+                            most = max3(most, w[r], w[r + 1]);
                         }
                     }
                     if (moved)
                         break;
-                    if (!barrier_any(3 + t, 128, top > kPagedLag || most > 448.0f || bad))
+                    if (!barrier_any(3 + t, 128, top > kPagedLag || most > kPagedMost || bad))
                         break;
                     stop = barrier_any(3 + t, 128, bad);  // (what one warp saw alone is no reason to leave the others)
                     if (stop)
@@ -692,49 +753,47 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attn_kernel(const __gr
                     // new references: the largest scores
 #pragma unroll
                     for (int r = 0; r < N; ++r) {
-                        const int m = __reduce_max_sync(0xffffffffu, float_int(s[r] * p.scale_log2));
+                        const int m = __reduce_max_sync(0xffffffffu, float_int(s[r] * to_log2));
                         if (lane == r)
                             ctl->wmax[t][warp & 3][r] = m;
                     }
                     barrier_sync(3 + t, 128);
                     if (tau < N) {
-                        const float old = ctl->row[t][tau].y;
+                        const float old = -ctl->nref[t][tau];
                         const float m = fmaxf(old, int_float(max(max(ctl->wmax[t][0][tau], ctl->wmax[t][1][tau]),
                                                                  max(ctl->wmax[t][2][tau], ctl->wmax[t][3][tau]))));
-                        const float f = rescale(old, m);
-                        ctl->row[t][tau].y = m;
-                        ctl->lfac[t][tau] = f;
-                        ctl->fac[t][tau] = f;
+                        ctl->nref[t][tau] = -m;
+                        ctl->lfac[t][tau] = ctl->fac[t][tau] = rescale(old, m);
                     }
                     barrier_sync(3 + t, 128);
                     if (F::kFp8) {
                         // and the weights' units, by the largest weight x V scale
 #pragma unroll
                         for (int r = 0; r < N; ++r) {
-                            const float m = ctl->row[t][r].y;
-                            const float x = s[r] == -INFINITY ? 0.0f : exp2_approx(fmaf(s[r], p.scale_log2, -m)) * vs;
+                            const float x = s[r] == -INFINITY ? 0.0f : exp2_approx(s[r] + ctl->nref[t][r]) * vs;
                             const int q = __reduce_max_sync(0xffffffffu, __float_as_int(x));
                             if (lane == r)
                                 ctl->wmax[t][warp & 3][r] = q;
                         }
                         barrier_sync(3 + t, 128);
                         if (tau < N) {
-                            const float before = ctl->vtop[t][tau], f = ctl->lfac[t][tau], unit = ctl->row[t][tau].z;
-                            const float now = __int_as_float(max(max(ctl->wmax[t][0][tau], ctl->wmax[t][1][tau]),
-                                                                 max(ctl->wmax[t][2][tau], ctl->wmax[t][3][tau])));
-                            const float most = fmaxf(before * f, now);
-                            // the power of two that brings it to [2^6, 2^7)
-                            const int e = static_cast<int>(__float_as_uint(most) >> 23);
-                            const float to = most > 0.0f ? __int_as_float(max(10, min(244, 260 - e)) << 23) : 1.0f;
-                            ctl->vtop[t][tau] = most;
-                            ctl->row[t][tau].z = to;
-                            ctl->fac[t][tau] = before * f > 0.0f ? f * to * (1.0f / unit) : 0.0f;
+                            const float before = ctl->vtop[t][tau] * ctl->lfac[t][tau], unit = ctl->unit[t][tau];
+                            const float most_now = fmaxf(before, __int_as_float(max(max(ctl->wmax[t][0][tau], ctl->wmax[t][1][tau]),
+                                                                                    max(ctl->wmax[t][2][tau], ctl->wmax[t][3][tau]))));
+                            // the power of two that brings it to [2^4, 2^5): room for 2^3 of growth until the next time
+                            const int e = static_cast<int>(__float_as_uint(most_now) >> 23);
+                            const float to_unit = most_now > 0.0f ? __int_as_float(max(10, min(244, 258 - e)) << 23) : 1.0f;
+                            ctl->vtop[t][tau] = most_now;
+                            ctl->unit[t][tau] = to_unit;
+                            ctl->fac[t][tau] = before > 0.0f ? ctl->lfac[t][tau] * to_unit * (1.0f / unit) : 0.0f;
                         }
                         barrier_sync(3 + t, 128);
                     }
 #pragma unroll
-                    for (int r = 0; r < N; ++r)
-                        l[r] *= ctl->lfac[t][r];
+                    for (int r = 0; r < N; r += 2) {
+                        const float2 f = *reinterpret_cast<const float2 *>(&ctl->lfac[t][r]);
+                        l2[r / 2] = mul2(l2[r / 2], pack2(f.x, f.y));
+                    }
                     if (j >= WAYS) {  // what the pages before left in O
                         bad |= !wait(&ctl->o_done[t], (it - 1) & 1);
                         tc_fence_after_sync();
@@ -756,9 +815,6 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attn_kernel(const __gr
                 // (the product with the weights before has to be over)
                 if (it > 0)
                     bad |= !wait(&ctl->o_done[t], (it - 1) & 1);
-#pragma unroll
-                for (int r = 0; r < N; ++r)
-                    l[r] += ls[r];
                 if (!F::kFp8) {
 #pragma unroll
                     for (int r = 0; r < N; r += 8)
@@ -791,16 +847,23 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attn_kernel(const __gr
                     mbar_arrive(smem_addr(&ctl->kv_empty[sk]));
                     mbar_arrive(smem_addr(&ctl->kv_empty[sv]));
                 }
+#pragma unroll
+                for (int r = 0; r < N / 2; ++r)
+                    l2[r] = add2(l2[r], ls2[r]);
             }
             done += n;
             // ---- the run's part of the unit ----
             if (!dead) {
-                bad |= stop;
-                if (first < n && !bad)
-                    bad |= !wait(&ctl->o_done[t], (it - 1) & 1);
+                float l[N];
+#pragma unroll
+                for (int r = 0; r < N; r += 2)
+                    unpack2(l2[r / 2], l[r], l[r + 1]);
                 const float sum = lanes_sum<N>(l, lane);
                 if (lane < N)
                     ctl->wsum[t][warp & 3][lane] = sum;
+                bad |= stop;
+                if (first < n && !bad)
+                    bad |= !wait(&ctl->o_done[t], (it - 1) & 1);
                 dead = barrier_any(2, 256, bad);
             }
             if (dead) {
@@ -810,9 +873,11 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attn_kernel(const __gr
                             p.part_lse[slot + r] = INFINITY;
                         continue;
                     }
-                    reinterpret_cast<uint2 *>(p.out + place(r) * kDim)[lane] = make_uint2(0u, 0u);
+                    const int i = (tile_at * p.tile_rows + r) / p.group, g = tile_at * p.tile_rows + r - i * p.group;
+                    const int64_t at = place0 + i * heads + g;
+                    reinterpret_cast<uint2 *>(p.out + at * kDim)[lane] = make_uint2(0u, 0u);
                     if (p.lse && lane == 0)
-                        p.lse[place(r)] = -INFINITY;
+                        p.lse[at] = -INFINITY;
                 }
                 continue;
             }
@@ -822,7 +887,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attn_kernel(const __gr
                 for (int c = 0; c < 2; ++c) {
                     const bool mine = WAYS == 2 || c == tid / N;
                     const float *x = &ctl->wsum[c][0][tid % N];
-                    m[c] = mine ? ctl->row[c][tid % N].y : -INFINITY;
+                    m[c] = mine ? -ctl->nref[c][tid % N] : -INFINITY;
                     sum[c] = mine ? (x[0] + x[N]) + (x[2 * N] + x[3 * N]) : 0.0f;
                 }
                 const float M = fmaxf(m[0], m[1]);
@@ -834,13 +899,13 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attn_kernel(const __gr
                 }
 #pragma unroll
                 for (int c = 0; c < 2; ++c)  // 0: nothing, and what stands in O may be anything
-                    ctl->share[c][tid] = sum[c] > 0.0f ? m[c] / (all * ctl->row[c][tid % N].z) : 0.0f;
+                    ctl->share[c][tid] = sum[c] > 0.0f ? m[c] / (F::kFp8 ? all * ctl->unit[c][tid % N] : all) : 0.0f;
                 if (tid < rows) {
                     const float e = all > 0.0f ? M + log2f(all) : -INFINITY;
                     if (!whole)
                         p.part_lse[slot + tid] = e;
                     else if (p.lse)
-                        p.lse[place(tid)] = e * kLn2;
+                        p.lse[place0 + ctl->at[tid]] = e * kLn2;
                 }
             }
             barrier_sync(2, 256);
@@ -880,15 +945,18 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attn_kernel(const __gr
                         acc[k] += share != 0.0f ? share * x : 0.0f;
                     }
                 }
+                if (whole) {
+                    uint16_t *out = p.out + place0 * kDim + tau;
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const int r = r0 + k;
-                    if (r < rows) {
-                        if (whole)
-                            p.out[place(r) * kDim + tau] = static_cast<uint16_t>(f32x2_to_bf16x2(acc[k], 0.0f));
-                        else
-                            p.part_o[(slot + r) * kDim + tau] = acc[k];
-                    }
+                    for (int k = 0; k < 8; ++k)
+                        if (r0 + k < rows)
+                            out[static_cast<int64_t>(ctl->at[r0 + k]) * kDim] = static_cast<uint16_t>(f32x2_to_bf16x2(acc[k], 0.0f));
+                } else {
+                    float *out = p.part_o + (slot + r0) * kDim + tau;
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        if (r0 + k < rows)
+                            out[k * kDim] = acc[k];
                 }
             }
             tc_fence_before_sync();

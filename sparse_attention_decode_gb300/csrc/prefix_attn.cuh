@@ -199,14 +199,6 @@ __device__ __forceinline__ void umma_ts_one(uint32_t one, uint32_t d_tmem, uint3
         : "memory");
 }
 
-// The maximum of three.
-__device__ __forceinline__ float max3(float a, float b, float c)
-{
-    float r;
-    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-    return r;
-}
-
 // 32 consecutive 32-bit columns of one TMEM lane per thread (shape 32x32b).
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32])
 {
