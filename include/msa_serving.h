@@ -59,8 +59,8 @@ extern "C" {
  *   total_rows   batch * q_len, or, with cu_seqlens_q, rows of the tensors.
  *   cu_seqlens_q optional int32 [batch + 1], non-decreasing from 0 on,
  *                cu_seqlens_q[batch] <= total_rows; no request has more rows than
- *                tokens.  (A request that breaks this is passed over, with
- *                MSA_FAULT_SEQ_LEN.)  q_len is not used with it.
+ *                tokens.  (Where they break this MSA_FAULT_SEQ_LEN is set, and a row that is
+ *                not within its request's is passed over.)  q_len is not used with it.
  *   workspace    at least 256 bytes (the fault word).
  *
  * A slot is written by one row: the pages that get new tokens are not shared.

@@ -16,6 +16,7 @@
 #include <algorithm>
 #include <cmath>
 
+#include "attn_common.cuh"
 #include "attn_ptx.cuh"
 #include "host_util.cuh"
 #include "layout.cuh"
@@ -42,8 +43,9 @@ struct AppendParams {
     float eps;
 };
 
-constexpr int kAppendThreads = 256;
+constexpr int kAppendThreads = 128;
 constexpr int kAppendHeads = kAppendThreads / 16;  // heads at a time: 16 lanes a head, 8 values a lane
+constexpr int kAppendBatch = 5;                    // heads of a lane under way together
 constexpr uint64_t kInverseTurn = 11743562013128004906ull;  // 2^66 / (2 pi)
 
 // inv_freq in units of 2^-64 turns a position, modulo a turn: m 2^e with an integer m of 24 bits.
@@ -89,147 +91,381 @@ __device__ __forceinline__ float half_warp_max(float x)
     return x;
 }
 
-// A row a block (or a share of its heads, blockIdx.y of gridDim.y): query heads, then key heads, then value heads, 16
-// at a time.
+// Where a row goes: its request's token, or nowhere (live false; page -1: its key and value).
+struct RowPlace {
+    bool live;
+    int position, page, slot;
+};
+
+// Row `row` of request b, whose rows are [lo, lo + n).
+__device__ __forceinline__ RowPlace row_place(const AppendParams &p, int64_t row, int b, int lo, int n, bool bad)
+{
+    const int len = p.seq_lens[b];
+    bad |= len < 0 || len > p.seq_limit || (p.cu && n > len);
+    RowPlace x{false, 0, -1, 0};
+    if (bad) {
+        atomicOr(p.fault, MSA_FAULT_SEQ_LEN);
+        return x;
+    }
+    const int token = len - n + static_cast<int>(row - lo);
+    if (token < 0)
+        return x;
+    x.live = true;
+    x.position = p.positions ? p.positions[row] : token;
+    x.page = p.block_table[b * p.bt_stride + token / kPage];
+    x.slot = token % kPage;
+    if (x.page < 0 || x.page >= p.num_pages) {
+        atomicOr(p.fault, MSA_FAULT_PAGE_ID);
+        x.page = -1;
+    }
+    return x;
+}
+
+// Rows of requests that do not follow one another.
+__device__ __forceinline__ void check_rows(const AppendParams &p)  // by one block
+{
+    if (p.cu)
+        for (int b = threadIdx.x; b < p.batch; b += blockDim.x)
+            if (p.cu[b + 1] < p.cu[b] || p.cu[b + 1] > p.rows)
+                atomicOr(p.fault, MSA_FAULT_SEQ_LEN);
+}
+
+// The row's request looked up; cu: the first b with cu[b + 1] > row.
+__device__ __forceinline__ RowPlace row_place(const AppendParams &p, int64_t row)
+{
+    if (!p.cu) {
+        const int b = static_cast<int>(static_cast<uint32_t>(row) / static_cast<uint32_t>(p.q_len));  // (rows are below 2^27)
+        return row_place(p, row, b, b * p.q_len, p.q_len, false);
+    }
+    int b = 0, end = p.batch;
+    while (b < end) {
+        const int mid = (b + end) >> 1;
+        if (p.cu[mid + 1] > row)
+            end = mid;
+        else
+            b = mid + 1;
+    }
+    if (b == p.batch)
+        return RowPlace{false, 0, -1, 0};
+    const int lo = p.cu[b], hi = p.cu[b + 1];
+    return row_place(p, row, b, lo, hi - lo, lo < 0 || lo > row || hi > p.rows);
+}
+
+// A lane's part in heads: the row's line of heads (queries, keys, values), the lane's coefficients of one kind of them.
+template <bool FP8, bool INTER>
+struct HeadLane {
+    const AppendParams &p;
+    int nq, nk, all;   // heads before the keys, before the values, and all
+    int sub, lane;
+    int half, partner; // lanes of a head that hold a first half of the rotated dims (pairs apart); who holds the others
+    int kind = -1;
+    bool norm = false;
+    uint64_t A[4], B[4];  // two values each
+
+    __device__ __forceinline__ explicit HeadLane(const AppendParams &p_) : p(p_)
+    {
+        nq = p.q ? p.q_heads : 0;
+        nk = nq + p.kv_heads;
+        all = p.v ? nk + p.kv_heads : nk;
+        lane = threadIdx.x & 31;
+        sub = lane & 15;
+        half = p.rot / 16;
+        partner = INTER ? sub : sub < half ? sub + half : sub < 2 * half ? sub - half : sub;
+    }
+    // the lane's weights of kind `is`, and its partner's
+    __device__ __forceinline__ void weights(int is, float (&w)[8], float (&wp)[8]) const
+    {
+        const float *weight = is == 0 ? p.q_weight : is == 1 ? p.k_weight : nullptr;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            w[j] = weight ? weight[sub * 8 + j] : 1.0f;
+            wp[j] = weight ? weight[INTER ? sub * 8 + (j ^ 1) : partner * 8 + j] : 1.0f;
+        }
+    }
+    __device__ __forceinline__ void coefficients(int is, const float (&w)[8], const float (&wp)[8], const float *cosines,
+                                                 const float *sines)
+    {
+        kind = is;
+        norm = (is == 0 ? p.q_weight : is == 1 ? p.k_weight : nullptr) != nullptr;
+        const bool turns = is < 2 && sub < 2 * half;
+#pragma unroll
+        for (int j = 0; j < 8; j += 2) {
+            float a[2], c[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int pair = INTER ? sub * 4 + j / 2 : (turns && sub >= half ? sub - half : sub) * 8 + j + e;
+                const bool first = INTER ? e == 0 : sub < half;
+                a[e] = turns ? w[j + e] * cosines[pair] : w[j + e];
+                c[e] = turns ? wp[j + e] * (first ? -sines[pair] : sines[pair]) : 0.0f;
+            }
+            A[j / 2] = pack2(a[0], a[1]);
+            B[j / 2] = pack2(c[0], c[1]);
+        }
+    }
+    // the lane's 8 values of a head of the kind at hand, normalised and rotated; all lanes of the warp together
+    __device__ __forceinline__ void turned(const uint4 &raw, float (&f)[8]) const
+    {
+        const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+        uint64_t x[4], sum2 = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            x[j] = pack2(__uint_as_float(w[j] << 16), __uint_as_float(w[j] & 0xffff0000u));
+            sum2 = fma2(x[j], x[j], sum2);
+        }
+        float inv = 1.0f;
+        if (p.q_weight || p.k_weight) {
+            float s0, s1;
+            unpack2(sum2, s0, s1);
+            const float r = rsqrtf(half_warp_sum(s0 + s1) * (1.0f / kDim) + p.eps);
+            inv = norm ? r : 1.0f;
+        }
+        const uint64_t inv2 = pack2(inv, inv);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            uint64_t t = 0;
+            if (p.rot) {
+                const uint32_t o = INTER ? __byte_perm(w[j], 0, 0x1032) : __shfl_sync(0xffffffffu, w[j], (lane & 16) | partner);
+                t = mul2(pack2(__uint_as_float(o << 16), __uint_as_float(o & 0xffff0000u)), B[j]);
+            }
+            unpack2(mul2(fma2(x[j], A[j], t), inv2), f[2 * j], f[2 * j + 1]);
+        }
+    }
+    static __device__ __forceinline__ uint4 packed(const float (&f)[8])
+    {
+        return make_uint4(f32x2_to_bf16x2(f[0], f[1]), f32x2_to_bf16x2(f[2], f[3]), f32x2_to_bf16x2(f[4], f[5]),
+                          f32x2_to_bf16x2(f[6], f[7]));
+    }
+    // head `at` of the line, of any kind
+    __device__ __forceinline__ void head(int at, const uint4 &raw, int64_t row, int page, int slot, const float *cosines,
+                                         const float *sines)
+    {
+        const bool have = at < all;
+        const int is = at < nq ? 0 : at < nk ? 1 : 2;
+        float f[8];
+        if (is != kind) {
+            float wp[8];
+            weights(is, f, wp);
+            coefficients(is, f, wp, cosines, sines);
+        }
+        turned(raw, f);
+        const bool write = have && (is == 0 || page >= 0);
+        if ((!FP8 || is == 0) && write) {
+            uint16_t *dst;
+            if (is == 0) {
+                dst = p.out_q + row * p.out_q_stride + at * kDim;
+            } else {
+                const int64_t *st = is == 1 ? p.kc_stride : p.vc_stride;
+                dst = reinterpret_cast<uint16_t *>(is == 1 ? p.k_cache : p.v_cache) + page * st[0] + slot * st[1] +
+                      (at - (is == 1 ? nq : nk)) * st[2];
+            }
+            *reinterpret_cast<uint4 *>(dst + sub * 8) = is == 2 ? raw : packed(f);
+        }
+        if (!FP8 || !__any_sync(0xffffffffu, is != 0))
+            return;
+        float top = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 8; j += 2)
+            top = max3(top, fabsf(f[j]), fabsf(f[j + 1]));
+        top = half_warp_max(top);
+        const float unit = top < 6.018531076210112e-36f ? 0.0f : top / 448.0f;  // 2^-117: the quotient is normal
+        const float up = unit > 0.0f ? 1.0f / unit : 0.0f;
+        if (write && is != 0) {
+            const int64_t *st = is == 1 ? p.kc_stride : p.vc_stride;
+            const int g = at - (is == 1 ? nq : nk);
+            uint32_t c[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                c[j] = e4m3_pair(f[4 * j] * up, f[4 * j + 1] * up) |
+                       static_cast<uint32_t>(e4m3_pair(f[4 * j + 2] * up, f[4 * j + 3] * up)) << 16;
+            *reinterpret_cast<uint2 *>((is == 1 ? p.k_cache : p.v_cache) + page * st[0] + slot * st[1] + g * st[2] + sub * 8) =
+                unit > 0.0f ? make_uint2(c[0], c[1]) : make_uint2(0u, 0u);
+            if (sub == 0)
+                (is == 1 ? p.k_scale : p.v_scale)[(static_cast<int64_t>(page) * p.kv_heads + g) * kPage + slot] = unit;
+        }
+    }
+};
+
+// Few rows: a row a block (or a share of its heads, blockIdx.y of gridDim.y).  The heads go to the half warps in turn; a
+// lane's first ones are asked for before the row's place is looked up.
 template <bool FP8, bool INTER>
 __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_constant__ AppendParams p)
 {
     __shared__ float s_cos[kDim / 2], s_sin[kDim / 2];
-    const int tid = threadIdx.x, lane = tid & 31, sub = tid & 15;
+    const int tid = threadIdx.x;
     const int64_t row = blockIdx.x;
-    // the row's request and token (every warp for itself)
-    int b, n, i;
-    bool bad = false, live = true;
-    if (p.cu) {
-        int before = 0;  // requests that end at or before the row
-        for (int at = lane; at < p.batch; at += 32)
-            before += p.cu[at + 1] <= row;
-        b = __reduce_add_sync(0xffffffffu, before);
-        live = b < p.batch;
-        const int lo = live ? p.cu[b] : 0, hi = live ? p.cu[b + 1] : 0;
-        n = hi - lo;
-        i = static_cast<int>(row) - lo;
-        bad = live && (lo < 0 || lo > row || hi <= row || hi > p.rows);
-    } else {
-        b = static_cast<int>(row / p.q_len);
-        n = p.q_len;
-        i = static_cast<int>(row - static_cast<int64_t>(b) * n);
-    }
-    const int len = live ? p.seq_lens[b] : 0;
-    bad |= live && (len < 0 || len > p.seq_limit || (p.cu && n > len));
-    const int token = len - n + i;
-    if (bad && tid == 0)
-        atomicOr(p.fault, MSA_FAULT_SEQ_LEN);
-    if (!live || bad || token < 0)
+    HeadLane<FP8, INTER> x(p);
+    const int step = gridDim.y * kAppendHeads, first = blockIdx.y * kAppendHeads, h0 = first + tid / 16;
+    auto load = [&](int h) {
+        const uint16_t *from = h < x.nq   ? p.q + row * p.q_stride + h * kDim
+                               : h < x.nk ? p.k + row * p.k_stride + (h - x.nq) * kDim
+                                          : p.v + row * p.v_stride + (h - x.nk) * kDim;
+        return h < x.all ? reinterpret_cast<const uint4 *>(from)[x.sub] : make_uint4(0u, 0u, 0u, 0u);
+    };
+    uint4 in[kAppendBatch];
+#pragma unroll
+    for (int i = 0; i < kAppendBatch; ++i)
+        in[i] = load(h0 + i * step);
+    if (blockIdx.x == 0 && blockIdx.y == 0)
+        check_rows(p);
+    const RowPlace at = row_place(p, row);  // (every thread: one address, one answer)
+    if (!at.live)
         return;
-    const int position = p.positions ? p.positions[row] : token;
-    int page = p.block_table[b * p.bt_stride + token / kPage];
-    if (page < 0 || page >= p.num_pages) {
-        if (tid == 0)
-            atomicOr(p.fault, MSA_FAULT_PAGE_ID);
-        page = -1;
-    }
-    const int slot = token % kPage;
-    const int pairs = p.rot / 2;
-    if (tid < pairs)
-        turn(turns_of(p.inv_freq[tid]), position, s_cos[tid], s_sin[tid]);
+    if (tid < p.rot / 2)
+        turn(turns_of(p.inv_freq[tid]), at.position, s_cos[tid], s_sin[tid]);
     __syncthreads();
-
-    // kinds one after the other: a lane's coefficients are a kind's
-    const int half = p.rot / 16;  // lanes of a head that hold a first half of the rotated dims (pairs apart)
-    const int partner = INTER ? sub : sub < half ? sub + half : sub < 2 * half ? sub - half : sub;
-    for (int kind = 0; kind < 3; ++kind) {
-        const int heads = kind == 0 ? (p.q ? p.q_heads : 0) : kind == 1 ? p.kv_heads : (p.v ? p.kv_heads : 0);
-        if (!heads || (kind > 0 && page < 0))
-            continue;
-        const uint16_t *src = (kind == 0 ? p.q : kind == 1 ? p.k : p.v) +
-                              row * (kind == 0 ? p.q_stride : kind == 1 ? p.k_stride : p.v_stride) + sub * 8;
-        const float *weight = kind == 0 ? p.q_weight : kind == 1 ? p.k_weight : nullptr;
-        float A[8], B[8];
+    for (int h = 0; first + h < x.all; h += kAppendBatch * step) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            A[j] = weight ? weight[sub * 8 + j] : 1.0f;
-            B[j] = 0.0f;
-        }
-        if (kind < 2 && sub < 2 * half) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int at = INTER ? sub * 4 + j / 2 : (sub % half) * 8 + j;
-                const float wp = weight ? weight[INTER ? sub * 8 + (j ^ 1) : partner * 8 + j] : 1.0f;
-                const bool first = INTER ? j % 2 == 0 : sub < half;
-                A[j] *= s_cos[at];
-                B[j] = first ? -wp * s_sin[at] : wp * s_sin[at];
-            }
-        }
-        for (int h0 = blockIdx.y * kAppendHeads; h0 < heads; h0 += gridDim.y * kAppendHeads) {
-            const int h = h0 + tid / 16;
-            const bool have = h < heads;
-            const uint4 raw = have ? *reinterpret_cast<const uint4 *>(src + h * kDim) : make_uint4(0u, 0u, 0u, 0u);
-            const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
-            float y[8];
-            if (kind < 2) {
-                float x[8], xp[8];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    x[2 * j] = __uint_as_float(w[j] << 16);
-                    x[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
-                    const uint32_t o = INTER ? (w[j] << 16) | (w[j] >> 16)
-                                             : __shfl_sync(0xffffffffu, w[j], (lane & 16) | partner);
-                    xp[2 * j] = __uint_as_float(o << 16);
-                    xp[2 * j + 1] = __uint_as_float(o & 0xffff0000u);
-                }
-                float inv = 1.0f;
-                if (weight) {
-                    float sum = 0.0f;
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        sum = fmaf(x[j], x[j], sum);
-                    inv = rsqrtf(half_warp_sum(sum) * (1.0f / kDim) + p.eps);
-                }
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    y[j] = fmaf(x[j], A[j], xp[j] * B[j]) * inv;
-            } else {
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    y[2 * j] = __uint_as_float(w[j] << 16);
-                    y[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
-                }
-            }
-            if (kind == 0 || !FP8) {
-                if (!have)
-                    continue;
-                uint16_t *dst = kind == 0 ? p.out_q + row * p.out_q_stride + h * kDim
-                                          : reinterpret_cast<uint16_t *>(kind == 1 ? p.k_cache : p.v_cache) +
-                                                page * (kind == 1 ? p.kc_stride : p.vc_stride)[0] +
-                                                slot * (kind == 1 ? p.kc_stride : p.vc_stride)[1] +
-                                                h * (kind == 1 ? p.kc_stride : p.vc_stride)[2];
-                *reinterpret_cast<uint4 *>(dst + sub * 8) =
-                    make_uint4(f32x2_to_bf16x2(y[0], y[1]), f32x2_to_bf16x2(y[2], y[3]), f32x2_to_bf16x2(y[4], y[5]),
-                               f32x2_to_bf16x2(y[6], y[7]));
-            } else {
-                float top = 0.0f;
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    top = fmaxf(top, fabsf(y[j]));
-                top = half_warp_max(top);
-                const float unit = top < 6.018531076210112e-36f ? 0.0f : top / 448.0f;  // 2^-117: the quotient is normal
-                const float inv = unit > 0.0f ? 1.0f / unit : 0.0f;
-                if (!have)
-                    continue;
-                const int64_t *st = kind == 1 ? p.kc_stride : p.vc_stride;
-                uint8_t *dst = (kind == 1 ? p.k_cache : p.v_cache) + page * st[0] + slot * st[1] + h * st[2];
-                uint32_t c[2];
-#pragma unroll
-                for (int j = 0; j < 2; ++j)
-                    c[j] = e4m3_pair(y[4 * j] * inv, y[4 * j + 1] * inv) |
-                           static_cast<uint32_t>(e4m3_pair(y[4 * j + 2] * inv, y[4 * j + 3] * inv)) << 16;
-                *reinterpret_cast<uint2 *>(dst + sub * 8) = unit > 0.0f ? make_uint2(c[0], c[1]) : make_uint2(0u, 0u);
-                if (sub == 0)
-                    (kind == 1 ? p.k_scale : p.v_scale)[(static_cast<int64_t>(page) * p.kv_heads + h) * kPage + slot] = unit;
-            }
+        for (int u = 0; u < kAppendBatch; ++u) {
+            if (first + h + u * step >= x.all)
+                break;
+            const uint4 raw = in[u];
+            in[u] = load(h0 + h + (u + kAppendBatch) * step);
+            x.head(h0 + h + u * step, raw, row, at.page, at.slot, s_cos, s_sin);
         }
     }
+}
+
+// Many rows: blocks that stay, and take rows in turn.  A warp looks up the places of the block's next 32 rows at a time,
+// a lane a row, has the rows copied into a ring in shared memory and works out their sines and cosines; four warps turn
+// the heads.  What has to be on its way for the copy rate does not depend on registers then.
+struct AppendRow {
+    float cosines[kDim / 2], sines[kDim / 2];
+    int live, page, slot, pad;
+};
+constexpr int kAppendStages = 3;
+constexpr int kAppendBlocks = 4;  // an SM
+constexpr int kAppendSmBytes = 233472;
+constexpr int append_block_bytes(int row_bytes)  // with the static shared memory and what the system takes
+{
+    return kAppendStages * (row_bytes + static_cast<int>(sizeof(AppendRow))) + 128 + 1024;
+}
+
+template <bool FP8, bool INTER>
+__global__ void __launch_bounds__(kAppendThreads + 32, kAppendBlocks) append_rows_kernel(const __grid_constant__ AppendParams p, int row_bytes)
+{
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ uint64_t full[kAppendStages], empty[kAppendStages];
+    __shared__ AppendRow places[kAppendStages];
+    __shared__ int abort_flag;
+    uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 15) & ~uintptr_t(15));
+    const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+    if (tid == 0) {
+        for (int s = 0; s < kAppendStages; ++s) {
+            mbar_init(smem_addr(&full[s]), 2);  // the copies, and the row's place
+            mbar_init(smem_addr(&empty[s]), kAppendThreads / 32);
+        }
+        abort_flag = 0;
+        fence_barrier_init();
+    }
+    __syncthreads();
+    HeadLane<FP8, INTER> x(p);
+    const int64_t step = gridDim.x;
+    if (blockIdx.x == 0)
+        check_rows(p);
+    if (warp == kAppendThreads / 32) {
+        const uint64_t turns[2] = {lane < p.rot / 2 ? turns_of(p.inv_freq[lane]) : 0,
+                                   lane + 32 < p.rot / 2 ? turns_of(p.inv_freq[lane + 32]) : 0};
+        uint32_t it = 0;
+        bool alive = true;
+        for (int64_t r0 = blockIdx.x; r0 < p.rows && alive; r0 += 32 * step) {
+            RowPlace mine{false, 0, -1, 0};
+            bool looked = false;
+            for (int i = 0; i < 32 && r0 + i * step < p.rows && alive; ++i, ++it) {
+                const int64_t row = r0 + i * step;
+                const int s = static_cast<int>(it % kAppendStages);
+                if (it >= kAppendStages)
+                    alive = attn_wait(&abort_flag, p.fault, smem_addr(&empty[s]), (it / kAppendStages + 1) & 1, 0);
+                if (!alive)
+                    break;
+                if (lane == 0) {
+                    const uint32_t bar = smem_addr(&full[s]), to = smem_addr(ring + s * row_bytes);
+                    mbar_arrive_expect_tx(bar, x.all * kDim * 2);
+                    if (x.nq)
+                        bulk_load(to, p.q + row * p.q_stride, x.nq * kDim * 2, bar);
+                    bulk_load(to + x.nq * kDim * 2, p.k + row * p.k_stride, p.kv_heads * kDim * 2, bar);
+                    if (p.v)
+                        bulk_load(to + x.nk * kDim * 2, p.v + row * p.v_stride, p.kv_heads * kDim * 2, bar);
+                }
+                __syncwarp();
+                if (!looked) {  // beside the first copies
+                    if (r0 + lane * step < p.rows)
+                        mine = row_place(p, r0 + lane * step);
+                    looked = true;
+                }
+                AppendRow &to = places[s];
+                const int position = __shfl_sync(0xffffffffu, mine.position, i);
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+                    if (lane + 32 * k < p.rot / 2)
+                        turn(turns[k], position, to.cosines[lane + 32 * k], to.sines[lane + 32 * k]);
+                if (lane == i) {
+                    to.live = mine.live;
+                    to.page = mine.page;
+                    to.slot = mine.slot;
+                }
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(smem_addr(&full[s]));
+            }
+        }
+        // the copies in flight land before the block may end
+        for (uint32_t j = it >= kAppendStages ? it - kAppendStages : 0; j < it; ++j)
+            mbar_wait(smem_addr(&full[j % kAppendStages]), (j / kAppendStages) & 1);
+        return;
+    }
+    float w[8], wp[8];  // the queries' weights
+    x.weights(0, w, wp);
+    uint32_t it = 0;
+    for (int64_t row = blockIdx.x; row < p.rows; row += step, ++it) {
+        const int s = static_cast<int>(it % kAppendStages);
+        if (!attn_wait(&abort_flag, p.fault, smem_addr(&full[s]), (it / kAppendStages) & 1, 0))
+            return;
+        const AppendRow &at = places[s];
+        if (at.live) {
+            const uint4 *from = reinterpret_cast<const uint4 *>(ring + s * row_bytes) + x.sub;
+            x.kind = -1;
+            int h = 0;
+            if (x.nq >= kAppendHeads) {  // queries, as far as every half warp has one
+                x.coefficients(0, w, wp, at.cosines, at.sines);
+                uint16_t *dst = p.out_q + row * p.out_q_stride + (tid / 16) * kDim + x.sub * 8;
+                const uint4 *src = from + (tid / 16) * 16;
+#pragma unroll 2
+                for (; h + kAppendHeads <= x.nq; h += kAppendHeads) {
+                    float f[8];
+                    x.turned(src[h * 16], f);
+                    *reinterpret_cast<uint4 *>(dst + h * kDim) = x.packed(f);
+                }
+            }
+            for (; h < x.all; h += kAppendHeads) {
+                const int mine = h + tid / 16;
+                x.head(mine, mine < x.all ? from[mine * 16] : make_uint4(0u, 0u, 0u, 0u), row, at.page, at.slot, at.cosines, at.sines);
+            }
+        }
+        __syncwarp();
+        if (lane == 0)
+            mbar_arrive(smem_addr(&empty[s]));
+    }
+}
+
+template <bool FP8, bool INTER>
+static msa_status launch_append(const AppendParams &p, int sms, int dev, cudaStream_t st)
+{
+    const int heads = (p.q ? p.q_heads : 0) + (p.v ? 2 : 1) * p.kv_heads;
+    const int64_t bytes = static_cast<int64_t>(heads) * kDim * 2;
+    const int blocks = bytes < kAppendSmBytes / 4 ? std::min(kAppendBlocks, kAppendSmBytes / append_block_bytes(static_cast<int>(bytes))) : 0;
+    if (p.rows > sms && blocks >= 2) {
+        static std::atomic<bool> allowed[kMaxDevices];
+        auto *kernel = append_rows_kernel<FP8, INTER>;
+        if (!allow_smem(kernel, kAppendSmBytes / 2 - 1024 - kAppendStages * sizeof(AppendRow) - 128, dev, allowed))
+            return MSA_ERR_CUDA;
+        const unsigned grid = static_cast<unsigned>(std::min<int64_t>(p.rows, blocks * sms));
+        kernel<<<grid, kAppendThreads + 32, static_cast<size_t>(kAppendStages * bytes + 16), st>>>(p, static_cast<int>(bytes));
+    } else {
+        const int shares = (heads + kAppendHeads - 1) / kAppendHeads;
+        const dim3 grid(static_cast<unsigned>(p.rows), static_cast<unsigned>(p.rows * 2 <= sms ? std::min(shares, 64) : 1));
+        append_kernel<FP8, INTER><<<grid, kAppendThreads, 0, st>>>(p);
+    }
+    return cudaGetLastError() == cudaSuccess ? MSA_OK : MSA_ERR_CUDA;
 }
 
 static msa_status append_entry(AppendParams &p, const int64_t *k_strides, const int64_t *v_strides, int interleaved,
@@ -273,17 +509,10 @@ static msa_status append_entry(AppendParams &p, const int64_t *k_strides, const 
     p.rows = total_rows;
     p.batch = batch;
     p.seq_limit = static_cast<int>(std::min<int64_t>(max_model_len, kPage * p.bt_stride));
-    const int heads = std::max(p.q ? p.q_heads : 0, p.kv_heads);
-    const int shares = (heads + kAppendHeads - 1) / kAppendHeads;
-    const dim3 grid(static_cast<unsigned>(total_rows), static_cast<unsigned>(total_rows * 2 <= sms ? std::min(shares, 64) : 1));
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (fp8)
-        interleaved ? append_kernel<true, true><<<grid, kAppendThreads, 0, st>>>(p)
-                    : append_kernel<true, false><<<grid, kAppendThreads, 0, st>>>(p);
-    else
-        interleaved ? append_kernel<false, true><<<grid, kAppendThreads, 0, st>>>(p)
-                    : append_kernel<false, false><<<grid, kAppendThreads, 0, st>>>(p);
-    return cudaGetLastError() == cudaSuccess ? MSA_OK : MSA_ERR_CUDA;
+        return interleaved ? launch_append<true, true>(p, sms, dev, st) : launch_append<true, false>(p, sms, dev, st);
+    return interleaved ? launch_append<false, true>(p, sms, dev, st) : launch_append<false, false>(p, sms, dev, st);
 }
 
 static AppendParams append_params(const void *q, int64_t q_stride, int q_heads, void *out_q, int64_t out_q_stride,
