@@ -44,8 +44,7 @@ struct AppendParams {
 };
 
 constexpr int kAppendThreads = 128;
-constexpr int kAppendHeads = kAppendThreads / 16;  // heads at a time: 16 lanes a head, 8 values a lane
-constexpr int kAppendBatch = 5;                    // heads of a lane under way together
+constexpr int kAppendBatch = 4;                    // heads of a lane under way together
 constexpr uint64_t kInverseTurn = 11743562013128004906ull;  // 2^66 / (2 pi)
 
 // inv_freq in units of 2^-64 turns a position, modulo a turn: m 2^e with an integer m of 24 bits.
@@ -285,16 +284,20 @@ struct HeadLane {
     }
 };
 
-// Few rows: a row a block (or a share of its heads, blockIdx.y of gridDim.y).  The heads go to the half warps in turn; a
-// lane's first ones are asked for before the row's place is looked up.
+// Few rows, or short ones: a row a warp, or a share of its heads (`shares` warps a row, which take its heads two at a time
+// in turn).  A lane's first heads are asked for before the row's place is looked up.
 template <bool FP8, bool INTER>
-__global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_constant__ AppendParams p)
+__global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_constant__ AppendParams p, int shares)
 {
-    __shared__ float s_cos[kDim / 2], s_sin[kDim / 2];
-    const int tid = threadIdx.x;
-    const int64_t row = blockIdx.x;
+    __shared__ float s_cos[kAppendThreads / 32][kDim / 2], s_sin[kAppendThreads / 32][kDim / 2];
+    const int warp = threadIdx.x >> 5;
+    const int64_t at_warp = static_cast<int64_t>(blockIdx.x) * (kAppendThreads / 32) + warp, row = at_warp / shares;
+    if (blockIdx.x == 0)
+        check_rows(p);
+    if (row >= p.rows)
+        return;
     HeadLane<FP8, INTER> x(p);
-    const int step = gridDim.y * kAppendHeads, first = blockIdx.y * kAppendHeads, h0 = first + tid / 16;
+    const int first = static_cast<int>(at_warp - row * shares) * 2, h0 = first + (x.lane >> 4), step = 2 * shares;
     auto load = [&](int h) {
         const uint16_t *from = h < x.nq   ? p.q + row * p.q_stride + h * kDim
                                : h < x.nk ? p.k + row * p.k_stride + (h - x.nq) * kDim
@@ -305,14 +308,14 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
 #pragma unroll
     for (int i = 0; i < kAppendBatch; ++i)
         in[i] = load(h0 + i * step);
-    if (blockIdx.x == 0 && blockIdx.y == 0)
-        check_rows(p);
-    const RowPlace at = row_place(p, row);  // (every thread: one address, one answer)
+    const RowPlace at = row_place(p, row);  // (every lane: one address, one answer)
     if (!at.live)
         return;
-    if (tid < p.rot / 2)
-        turn(turns_of(p.inv_freq[tid]), at.position, s_cos[tid], s_sin[tid]);
-    __syncthreads();
+#pragma unroll
+    for (int i = x.lane; i < kDim / 2; i += 32)
+        if (i < p.rot / 2)
+            turn(turns_of(p.inv_freq[i]), at.position, s_cos[warp][i], s_sin[warp][i]);
+    __syncwarp();
     for (int h = 0; first + h < x.all; h += kAppendBatch * step) {
 #pragma unroll
         for (int u = 0; u < kAppendBatch; ++u) {
@@ -320,7 +323,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
                 break;
             const uint4 raw = in[u];
             in[u] = load(h0 + h + (u + kAppendBatch) * step);
-            x.head(h0 + h + u * step, raw, row, at.page, at.slot, s_cos, s_sin);
+            x.head(h0 + h + u * step, raw, row, at.page, at.slot, s_cos[warp], s_sin[warp]);
         }
     }
 }
@@ -332,8 +335,10 @@ struct AppendRow {
     float cosines[kDim / 2], sines[kDim / 2];
     int live, page, slot, pad;
 };
-constexpr int kAppendStages = 3;
-constexpr int kAppendBlocks = 4;  // an SM
+constexpr int kRowsThreads = 128;
+constexpr int kRowsHeads = kRowsThreads / 16;
+constexpr int kAppendStages = 2;
+constexpr int kAppendBlocks = 5;  // an SM (4 with 3 rows each: 48.8 us for 237 MB, 43.2)
 constexpr int kAppendSmBytes = 233472;
 constexpr int append_block_bytes(int row_bytes)  // with the static shared memory and what the system takes
 {
@@ -341,7 +346,7 @@ constexpr int append_block_bytes(int row_bytes)  // with the static shared memor
 }
 
 template <bool FP8, bool INTER>
-__global__ void __launch_bounds__(kAppendThreads + 32, kAppendBlocks) append_rows_kernel(const __grid_constant__ AppendParams p, int row_bytes)
+__global__ void __launch_bounds__(kRowsThreads + 32, kAppendBlocks) append_rows_kernel(const __grid_constant__ AppendParams p, int row_bytes)
 {
     extern __shared__ uint8_t smem_raw[];
     __shared__ uint64_t full[kAppendStages], empty[kAppendStages];
@@ -352,7 +357,7 @@ __global__ void __launch_bounds__(kAppendThreads + 32, kAppendBlocks) append_row
     if (tid == 0) {
         for (int s = 0; s < kAppendStages; ++s) {
             mbar_init(smem_addr(&full[s]), 2);  // the copies, and the row's place
-            mbar_init(smem_addr(&empty[s]), kAppendThreads / 32);
+            mbar_init(smem_addr(&empty[s]), kRowsThreads / 32);
         }
         abort_flag = 0;
         fence_barrier_init();
@@ -362,7 +367,7 @@ __global__ void __launch_bounds__(kAppendThreads + 32, kAppendBlocks) append_row
     const int64_t step = gridDim.x;
     if (blockIdx.x == 0)
         check_rows(p);
-    if (warp == kAppendThreads / 32) {
+    if (warp == kRowsThreads / 32) {
         const uint64_t turns[2] = {lane < p.rot / 2 ? turns_of(p.inv_freq[lane]) : 0,
                                    lane + 32 < p.rot / 2 ? turns_of(p.inv_freq[lane + 32]) : 0};
         uint32_t it = 0;
@@ -425,18 +430,18 @@ __global__ void __launch_bounds__(kAppendThreads + 32, kAppendBlocks) append_row
             const uint4 *from = reinterpret_cast<const uint4 *>(ring + s * row_bytes) + x.sub;
             x.kind = -1;
             int h = 0;
-            if (x.nq >= kAppendHeads) {  // queries, as far as every half warp has one
+            if (x.nq >= kRowsHeads) {  // queries, as far as every half warp has one
                 x.coefficients(0, w, wp, at.cosines, at.sines);
                 uint16_t *dst = p.out_q + row * p.out_q_stride + (tid / 16) * kDim + x.sub * 8;
                 const uint4 *src = from + (tid / 16) * 16;
 #pragma unroll 2
-                for (; h + kAppendHeads <= x.nq; h += kAppendHeads) {
+                for (; h + kRowsHeads <= x.nq; h += kRowsHeads) {
                     float f[8];
                     x.turned(src[h * 16], f);
                     *reinterpret_cast<uint4 *>(dst + h * kDim) = x.packed(f);
                 }
             }
-            for (; h < x.all; h += kAppendHeads) {
+            for (; h < x.all; h += kRowsHeads) {
                 const int mine = h + tid / 16;
                 x.head(mine, mine < x.all ? from[mine * 16] : make_uint4(0u, 0u, 0u, 0u), row, at.page, at.slot, at.cosines, at.sines);
             }
@@ -453,17 +458,17 @@ static msa_status launch_append(const AppendParams &p, int sms, int dev, cudaStr
     const int heads = (p.q ? p.q_heads : 0) + (p.v ? 2 : 1) * p.kv_heads;
     const int64_t bytes = static_cast<int64_t>(heads) * kDim * 2;
     const int blocks = bytes < kAppendSmBytes / 4 ? std::min(kAppendBlocks, kAppendSmBytes / append_block_bytes(static_cast<int>(bytes))) : 0;
-    if (p.rows > sms && blocks >= 2) {
+    if (p.rows > sms && heads >= 24 && blocks >= 2) {
         static std::atomic<bool> allowed[kMaxDevices];
         auto *kernel = append_rows_kernel<FP8, INTER>;
         if (!allow_smem(kernel, kAppendSmBytes / 2 - 1024 - kAppendStages * sizeof(AppendRow) - 128, dev, allowed))
             return MSA_ERR_CUDA;
         const unsigned grid = static_cast<unsigned>(std::min<int64_t>(p.rows, blocks * sms));
-        kernel<<<grid, kAppendThreads + 32, static_cast<size_t>(kAppendStages * bytes + 16), st>>>(p, static_cast<int>(bytes));
+        kernel<<<grid, kRowsThreads + 32, static_cast<size_t>(kAppendStages * bytes + 16), st>>>(p, static_cast<int>(bytes));
     } else {
-        const int shares = (heads + kAppendHeads - 1) / kAppendHeads;
-        const dim3 grid(static_cast<unsigned>(p.rows), static_cast<unsigned>(p.rows * 2 <= sms ? std::min(shares, 64) : 1));
-        append_kernel<FP8, INTER><<<grid, kAppendThreads, 0, st>>>(p);
+        const int shares = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>((heads + 1) / 2, (16 * sms + p.rows - 1) / p.rows)));
+        const int64_t blocks_of = (p.rows * shares + kAppendThreads / 32 - 1) / (kAppendThreads / 32);
+        append_kernel<FP8, INTER><<<static_cast<unsigned>(blocks_of), kAppendThreads, 0, st>>>(p, shares);
     }
     return cudaGetLastError() == cudaSuccess ? MSA_OK : MSA_ERR_CUDA;
 }
