@@ -30,12 +30,18 @@ static msa_status launch_paged(const PagedParams &p, int dev, cudaStream_t st)
         return MSA_ERR_CUDA;
     if (p.grid < 2)
         return MSA_OK;
-    constexpr int kWarpsARow = 4;
+    // Few units have many parts each: a block a unit and row.  Else at most one unit for each range's end, of 2 or 3 parts.
     const int rows = std::min(p.tile_rows, p.q_len * p.group);
+    const int64_t units = static_cast<int64_t>(p.batch) * p.row_tiles * p.kv_heads;
     cudaLaunchAttribute attr[1];
-    const cudaLaunchConfig_t cfg =
-        pdl_config(dim3(static_cast<unsigned>(p.grid - 1), static_cast<unsigned>((rows * kWarpsARow + 7) / 8)), dim3(256), 0, st, attr);
-    return cudaLaunchKernelEx(&cfg, paged_join_kernel<kWarpsARow>, p) == cudaSuccess ? MSA_OK : MSA_ERR_CUDA;
+    auto join = [&](auto *k, int64_t x, int wpr) {
+        const cudaLaunchConfig_t cfg =
+            pdl_config(dim3(static_cast<unsigned>(x), static_cast<unsigned>((rows * wpr + 7) / 8)), dim3(256), 0, st, attr);
+        return cudaLaunchKernelEx(&cfg, k, p) == cudaSuccess ? MSA_OK : MSA_ERR_CUDA;
+    };
+    return units * 8 <= p.grid    ? join(paged_join_kernel<8, true>, units, 8)
+           : units < p.grid ? join(paged_join_kernel<2, true>, units, 2)
+                            : join(paged_join_kernel<1, false>, p.grid - 1, 1);
 }
 
 template <class F>

@@ -25,8 +25,8 @@
 // has to be E4M3 as well.  A query row, brought to [2^7, 2^8) by a power of two, is the
 // sum of two E4M3 numbers, exactly where it is within 2^-9 of the row's largest (4 bits
 // each, the second 2^-5 on), and to 2^-23 of that largest below.  A weight times its
-// token's V scale is the sum of three (12 bits), held relative to the row's largest such
-// product: to 2^-12 of itself, or 2^-28 of that largest.  The terms stand side by side as
+// token's V scale is the sum of three, after one rounding to f16 (11 bits), and held
+// relative to the row's largest such product so far: down to 2^-24 of it.  The terms stand side by side as
 // further rows of the product, so K and V still pass once.
 #pragma once
 
@@ -82,19 +82,29 @@ __device__ __forceinline__ int paged_len(const PagedParams &p, int b)
     return n < 0 || n > p.seq_limit ? 0 : n;
 }
 
-// Pages a CTA's range should have at least: one for each chain.
-constexpr int kPagedMinPages = 2;
+// The batch's work: pages of all units, and units that have some.
+struct PagedWork {
+    int pages, units;
+};
 
-// The ranges: CTA g has [start(g), start(g + 1)) of the units' pages.
+// The ranges: CTA g has [start(g), start(g + 1)) of the units' pages: two pages at least, one for each chain, but no fewer
+// ranges than units.
 struct PagedSplit {
-    int total, ctas, range, more;
-    __device__ PagedSplit(int total_, int grid) : total(total_)
+    int ctas, range, more;
+    __device__ PagedSplit(const PagedWork &work, int grid)
     {
-        ctas = min(grid, (total + kPagedMinPages - 1) / kPagedMinPages);
+        const int total = work.pages;
+        ctas = min(grid, max((total + 1) / 2, work.units));
         range = ctas > 0 ? total / ctas : 0;
         more = total - range * ctas;
     }
     __device__ int start(int g) const { return g * range + min(g, more); }
+    // the CTA whose range holds page x
+    __device__ int owner(int x) const
+    {
+        const int longer = more * (range + 1);
+        return x < longer ? x / (range + 1) : more + (x - longer) / range;
+    }
 };
 
 // A place in the sequence of the units' pages.
@@ -103,39 +113,53 @@ struct PagedAt {
 };
 
 struct PagedScan {
-    int warp_sums[32];
+    int pages[32], requests[32], early[32];  // the warps' sums
     PagedAt at;
 };
 
-// The batch's pages and the place of page `want(total)` of the sequence, by a whole block.
+// The batch's work, the pages of requests before `request` (in `before`) and the place of page `want(work)` of the sequence
+// (request `batch`: there is none), by a whole block.
 template <int THREADS, class Want>
-__device__ __forceinline__ int paged_find(const PagedParams &p, PagedScan *sc, Want want)
+__device__ __forceinline__ PagedWork paged_find(const PagedParams &p, PagedScan *sc, int request, int &before, Want want)
 {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int units = p.row_tiles * p.kv_heads;
     const int each = (p.batch + THREADS - 1) / THREADS;
     const int b0 = min(p.batch, tid * each), b1 = min(p.batch, b0 + each);
-    int mine = 0;
-    for (int b = b0; b < b1; ++b)
-        mine += pages_of(paged_len(p, b)) * units;
+    int mine = 0, some = 0, early = 0;
+    for (int b = b0; b < b1; ++b) {
+        const int n = pages_of(paged_len(p, b)) * units;
+        mine += n;
+        some += n > 0;
+        early += b < request ? n : 0;
+    }
     int upto = mine;  // inclusive over the warp
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const int x = __shfl_up_sync(0xffffffffu, upto, o);
         upto += lane >= o ? x : 0;
     }
-    if (lane == 31)
-        sc->warp_sums[warp] = upto;
+    some = __reduce_add_sync(0xffffffffu, some);
+    early = __reduce_add_sync(0xffffffffu, early);
+    if (lane == 31) {
+        sc->pages[warp] = upto;
+        sc->requests[warp] = some;
+        sc->early[warp] = early;
+    }
     if (tid == 0)
         sc->at = PagedAt{p.batch, 0, 0};
     __syncthreads();
-    int before = 0, total = 0;
+    int prior = 0;
+    PagedWork work{0, 0};
+    before = 0;
     for (int w = 0; w < THREADS / 32; ++w) {
-        before += w < warp ? sc->warp_sums[w] : 0;
-        total += sc->warp_sums[w];
+        prior += w < warp ? sc->pages[w] : 0;
+        work.pages += sc->pages[w];
+        work.units += sc->requests[w] * units;
+        before += sc->early[w];
     }
-    const int x = want(total);
-    int from = before + upto - mine;
+    const int x = want(work);
+    int from = prior + upto - mine;
     if (x >= from && x < from + mine) {
         for (int b = b0; b < b1; ++b) {
             const int P = pages_of(paged_len(p, b)), n = P * units;
@@ -148,7 +172,7 @@ __device__ __forceinline__ int paged_find(const PagedParams &p, PagedScan *sc, W
         }
     }
     __syncthreads();
-    return total;
+    return work;
 }
 
 // Runs through a range unit by unit.
@@ -313,23 +337,19 @@ __device__ __forceinline__ int float_int(float x)
 }
 __device__ __forceinline__ float int_float(int i) { return __int_as_float(i ^ ((i >> 31) & 0x7fffffff)); }
 
-__device__ __forceinline__ void f16x2_floats(uint32_t v, float &lo, float &hi)
-{
-    asm("{\n  .reg .b16 a, b;\n  mov.b32 {a, b}, %2;\n  cvt.f32.f16 %0, a;\n  cvt.f32.f16 %1, b;\n}\n" : "=f"(lo), "=f"(hi) : "r"(v));
-}
-// x, y as sums of E4M3 numbers t[0] + t[1] / 32 + .., two codes each; |x|, |y| <= 448.
+// x, y (at most 256) as sums of E4M3 numbers t[0] + t[1] / 32 + .., two codes each, after one rounding to f16.  What a term
+// leaves is exact in f16.
 template <int TERMS>
 __device__ __forceinline__ void e4m3_terms(float x, float y, uint32_t (&t)[TERMS])
 {
+    uint32_t left = f32x2_to_f16x2(x, y);
 #pragma unroll
     for (int i = 0; i < TERMS; ++i) {
-        t[i] = e4m3_pair(x, y);
-        if (i + 1 < TERMS) {
-            float a, b;
-            f16x2_floats(e4m3x2_to_f16x2(static_cast<uint16_t>(t[i])), a, b);
-            x = (x - a) * kPagedTermUp;
-            y = (y - b) * kPagedTermUp;
-        }
+        uint16_t code;
+        asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(code) : "r"(left));
+        t[i] = code;
+        if (i + 1 < TERMS)
+            asm("{\n  .reg .b32 a;\n  sub.f16x2 a, %0, %1;\n  mul.f16x2 %0, a, %2;\n}\n" : "+r"(left) : "r"(e4m3x2_to_f16x2(code)), "r"(0x50005000u));
     }
 }
 
@@ -405,8 +425,9 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attn_kernel(const __gr
         for (int b = tid; b < p.batch; b += kPagedThreads)
             if (p.seq_lens[b] != paged_len(p, b))
                 atomicOr(p.fault, MSA_FAULT_SEQ_LEN);
-    const int total = paged_find<kPagedThreads>(p, &ctl->scan, [&](int all) {
-        const PagedSplit s(all, p.grid);
+    int unused;
+    const PagedWork total = paged_find<kPagedThreads>(p, &ctl->scan, 0, unused, [&](const PagedWork &work) {
+        const PagedSplit s(work, p.grid);
         return cta < s.ctas ? s.start(cta) : -1;
     });
     const PagedSplit split(total, p.grid);
@@ -580,77 +601,90 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attn_kernel(const __gr
         };
         if (p.row_tiles == 1)
             lay_rows(0);
+        // The query rows of the unit at `w` on their way to registers, 16 lanes a row, and from there to shared memory; then the
+        // chains' products may begin, beside what is left to do for the unit before.
+        auto load_rows = [&](const PagedWalk &w, uint4 (&v)[R / 16]) {
+            const int tile_at = w.u / p.kv_heads, h = w.u - tile_at * p.kv_heads;
+            const int rows = min(p.tile_rows, unit_rows - tile_at * p.tile_rows);
+            const uint16_t *q = p.q + static_cast<int64_t>(w.b) * p.q_len * p.q_stride + h * p.group * kDim;
+#pragma unroll
+            for (int i = 0; i < R / 16; ++i) {
+                const int r = (tid >> 4) + 16 * i;
+                v[i] = w.left > 0 && r < rows ? reinterpret_cast<const uint4 *>(q + ctl->q_at[r])[tid & 15] : make_uint4(0u, 0u, 0u, 0u);
+            }
+        };
+        auto put_rows = [&](const PagedWalk &w, const uint4 (&v)[R / 16]) {
+            const int c = tid & 15;
+#pragma unroll
+            for (int i = 0; i < R / 16; ++i) {
+                const int r = (tid >> 4) + 16 * i;
+                if (!F::kFp8) {
+                    *reinterpret_cast<uint4 *>(smem + (c >> 3) * (R * 128) + r * 128 + (((c ^ r) & 7) << 4)) = v[i];
+                    continue;
+                }
+                const uint32_t x[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+                float top = 0.0f;
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    top = max3(top, fabsf(bf16_lo(x[k])), fabsf(bf16_hi(x[k])));
+#pragma unroll
+                for (int o = 8; o >= 1; o >>= 1)
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                // the power of two that brings it to [2^7, 2^8)
+                const int e = max(15, min(246, static_cast<int>(__float_as_uint(top) >> 23)));
+                const float f = __int_as_float((261 - e) << 23);
+                uint32_t term[4][F::kQTerms];
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    e4m3_terms(bf16_lo(x[k]) * f, bf16_hi(x[k]) * f, term[k]);
+#pragma unroll
+                for (int k = 0; k < F::kQTerms; ++k) {
+                    const int at = (r / N) * L::kSCols + k * N + r % N;
+                    *reinterpret_cast<uint2 *>(smem + at * 128 + ((((c >> 1) ^ at) & 7) << 4) + (c & 1) * 8) =
+                        make_uint2(term[0][k] | term[1][k] << 16, term[2][k] | term[3][k] << 16);
+                }
+                if (c == 0)
+                    ctl->coef[r] = __int_as_float((e - 7) << 23) * p.scale_log2;
+            }
+            if (tid < R)
+                ctl->sees[tid] = max(0, w.len - ctl->hidden[tid]);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(smem_addr(&ctl->q_full));
+        };
+        auto start_rows = [&] {
+            if (tau < N) {
+                ctl->nref[t][tau] = INFINITY;
+                ctl->unit[t][tau] = 1.0f;
+                ctl->vtop[t][tau] = 0.0f;
+            }
+        };
         bool dead = false;
         uint32_t it = 0, done = 0;
         int seg = 0;
-        for (; walk.left > 0; walk.next(p), ++seg) {
+        PagedWalk walk_next = walk;
+        uint4 q_next[R / 16];
+        if (walk.left > 0) {
+            if (p.row_tiles > 1)
+                lay_rows(walk.u / p.kv_heads * p.tile_rows);
+            load_rows(walk, q_next);
+            start_rows();
+            put_rows(walk, q_next);
+        }
+        for (; walk.left > 0; walk = walk_next, ++seg) {
             const int n = walk.run(), tile_at = walk.u / p.kv_heads, h = walk.u - tile_at * p.kv_heads;
             const int rows = min(p.tile_rows, unit_rows - tile_at * p.tile_rows), len = walk.len, j0 = walk.j;
             const bool whole = n == walk.P;
             const int64_t slot = static_cast<int64_t>(2 * cta + (seg > 0)) * p.tile_rows;
             const int64_t place0 = static_cast<int64_t>(walk.b) * p.q_len * heads + h * p.group;  // the first row's, ctl->at from there
             const int begins = WAYS == 2 ? done & 1 : 0;  // the chain that has the run's first page
+            walk_next = walk;
+            walk_next.next(p);
             if (!dead) {
-                // both chains, and who issues their products, are through with the unit before: its query rows, and the
-                // numbers of its rows
-                const bool ok = seg == 0 || wait(&ctl->q_taken, (seg - 1) & 1);
-                dead = barrier_any(2, 256, !ok);
-            }
-            if (!dead) {
-                if (p.row_tiles > 1)
-                    lay_rows(tile_at * p.tile_rows);
-                // 16 lanes a query row
-                const uint16_t *q = p.q + static_cast<int64_t>(walk.b) * p.q_len * p.q_stride + h * p.group * kDim;
-                const int c = tid & 15;
-                uint4 v[R / 16];
-#pragma unroll
-                for (int i = 0; i < R / 16; ++i) {
-                    const int r = (tid >> 4) + 16 * i;
-                    v[i] = r < rows ? reinterpret_cast<const uint4 *>(q + ctl->q_at[r])[c] : make_uint4(0u, 0u, 0u, 0u);
-                }
-#pragma unroll
-                for (int i = 0; i < R / 16; ++i) {
-                    const int r = (tid >> 4) + 16 * i;
-                    if (!F::kFp8) {
-                        *reinterpret_cast<uint4 *>(smem + (c >> 3) * (R * 128) + r * 128 + (((c ^ r) & 7) << 4)) = v[i];
-                        continue;
-                    }
-                    const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-                    float top = 0.0f;
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        top = max3(top, fabsf(bf16_lo(w[k])), fabsf(bf16_hi(w[k])));
-#pragma unroll
-                    for (int o = 8; o >= 1; o >>= 1)
-                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-                    // the power of two that brings it to [2^7, 2^8)
-                    const int e = max(15, min(246, static_cast<int>(__float_as_uint(top) >> 23)));
-                    const float f = __int_as_float((261 - e) << 23);
-                    uint32_t term[4][F::kQTerms];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        e4m3_terms(bf16_lo(w[k]) * f, bf16_hi(w[k]) * f, term[k]);
-#pragma unroll
-                    for (int k = 0; k < F::kQTerms; ++k) {
-                        const int at = (r / N) * L::kSCols + k * N + r % N;
-                        *reinterpret_cast<uint2 *>(smem + at * 128 + ((((c >> 1) ^ at) & 7) << 4) + (c & 1) * 8) =
-                            make_uint2(term[0][k] | term[1][k] << 16, term[2][k] | term[3][k] << 16);
-                    }
-                    if (c == 0)
-                        ctl->coef[r] = __int_as_float((e - 7) << 23) * p.scale_log2;
-                }
-                if (tid < R)
-                    ctl->sees[tid] = max(0, len - ctl->hidden[tid]);
-                if (tau < N) {
-                    ctl->nref[t][tau] = INFINITY;
-                    ctl->unit[t][tau] = 1.0f;
-                    ctl->vtop[t][tau] = 0.0f;
-                }
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(smem_addr(&ctl->q_full));
-                barrier_sync(2, 256);
+                if (p.row_tiles == 1)
+                    load_rows(walk_next, q_next);
+                barrier_sync(2, 256);  // the rows' numbers are all there
             }
             uint64_t l2[N / 2];  // sums of the token's weights, two rows each
 #pragma unroll
@@ -864,6 +898,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attn_kernel(const __gr
                 bad |= stop;
                 if (first < n && !bad)
                     bad |= !wait(&ctl->o_done[t], (it - 1) & 1);
+                bad |= !wait(&ctl->q_taken, seg & 1);  // (who issues the products has seen this unit's rows)
                 dead = barrier_any(2, 256, bad);
             }
             if (dead) {
@@ -881,6 +916,10 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attn_kernel(const __gr
                 }
                 continue;
             }
+            // the scores of this unit have all been read: the next one's rows may take the place of its
+            if (p.row_tiles == 1 && walk_next.left > 0)
+                put_rows(walk_next, q_next);
+            float top = 0.0f, all = 0.0f;
             if (tid < R) {
                 float m[2], sum[2];
 #pragma unroll
@@ -891,7 +930,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attn_kernel(const __gr
                     sum[c] = mine ? (x[0] + x[N]) + (x[2 * N] + x[3 * N]) : 0.0f;
                 }
                 const float M = fmaxf(m[0], m[1]);
-                float all = 0.0f;
+                all = 0.0f;
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
                     m[c] = sum[c] > 0.0f ? rescale(m[c], M) : 0.0f;
@@ -899,17 +938,21 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attn_kernel(const __gr
                 }
 #pragma unroll
                 for (int c = 0; c < 2; ++c)  // 0: nothing, and what stands in O may be anything
-                    ctl->share[c][tid] = sum[c] > 0.0f ? m[c] / (F::kFp8 ? all * ctl->unit[c][tid % N] : all) : 0.0f;
-                if (tid < rows) {
-                    const float e = all > 0.0f ? M + log2f(all) : -INFINITY;
-                    if (!whole)
-                        p.part_lse[slot + tid] = e;
-                    else if (p.lse)
-                        p.lse[place0 + ctl->at[tid]] = e * kLn2;
-                }
+                    ctl->share[c][tid] =
+                        sum[c] > 0.0f ? __fdividef(m[c], all) * (F::kFp8 ? 1.0f / ctl->unit[c][tid % N] : 1.0f) : 0.0f;
+                top = M;
             }
             barrier_sync(2, 256);
             tc_fence_after_sync();
+            if (p.row_tiles == 1)
+                start_rows();
+            if (tid < rows) {
+                const float e = all > 0.0f ? top + log2f(all) : -INFINITY;
+                if (!whole)
+                    p.part_lse[slot + tid] = e;
+                else if (p.lse)
+                    p.lse[place0 + ctl->at[tid]] = e * kLn2;
+            }
             // a thread a dim: 8 rows at a time, both chains' shares of them; WAYS 2: the chains' warps take turns
             for (int r0 = WAYS == 2 ? t * 8 : t * N; r0 < (WAYS == 2 ? N : t * N + N) && r0 < rows; r0 += WAYS * 8) {
                 float acc[8];
@@ -960,6 +1003,13 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attn_kernel(const __gr
                 }
             }
             tc_fence_before_sync();
+            if (p.row_tiles > 1 && walk_next.left > 0) {  // tiles of rows: where they lie changes with the unit
+                barrier_sync(2, 256);
+                lay_rows(walk_next.u / p.kv_heads * p.tile_rows);
+                load_rows(walk_next, q_next);
+                start_rows();
+                put_rows(walk_next, q_next);
+            }
         }
         tc_fence_before_sync();
     }
@@ -969,10 +1019,10 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attn_kernel(const __gr
 }
 
 // ---------------------------------------------------------------------------
-// The units that a range's end cuts: block (c - 1, i) takes the one that CTA c is the first to go on with, and of its rows
-// those from 8 / WPR i on; WPR warps a row take its parts in turn.
-template <int WPR>
-__global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__ PagedParams p)
+// The units that a range's end cuts, 8 / WPR of their rows a block, WPR warps a row that take its parts in turn.  UNITS:
+// block x takes unit x, if it is cut; else the one that CTA x + 1 is the first to go on with.
+template <int WPR, bool UNITS>
+__global__ void __launch_bounds__(256, 6) paged_join_kernel(const __grid_constant__ PagedParams p)
 {
     constexpr int kRows = 8 / WPR;
     __shared__ PagedScan scan;
@@ -980,26 +1030,30 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__
     __shared__ float s_m[8], s_sum[8];
     __shared__ int s_bad[8];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, sub = warp % WPR;
-    const int c = blockIdx.x + 1;
-    const int total = paged_find<256>(p, &scan, [&](int all) {
+    const int units = p.row_tiles * p.kv_heads, x = blockIdx.x;
+    int before;
+    const PagedWork work = paged_find<256>(p, &scan, UNITS ? x / units : 0, before, [&](const PagedWork &all) {
         const PagedSplit s(all, p.grid);
-        return c < s.ctas ? s.start(c) : -1;
+        return !UNITS && x + 1 < s.ctas ? s.start(x + 1) : -1;
     });
-    const PagedSplit split(total, p.grid);
-    const PagedAt at = scan.at;
+    const PagedSplit split(work, p.grid);
+    const PagedAt at = UNITS ? PagedAt{x / units, x % units, 0} : scan.at;
+    const int P = at.b < p.batch ? pages_of(paged_len(p, at.b)) : 0;
+    // the unit's pages [from, from + P), and the CTA that has the first
+    const int from = UNITS ? before + at.u * P : (x + 1 < split.ctas ? split.start(x + 1) : 0) - at.j;
+    const int c = UNITS ? (P > 0 ? split.owner(from) : 0) : x;
     griddep_wait();  // also where there is nothing to do: who waits for this grid reads what both have written
-    if (c >= split.ctas || at.j == 0 || at.j > split.start(c) - split.start(c - 1))
+    if (P == 0 || (!UNITS && (at.j == 0 || split.start(c) > from)))
         return;  // no unit goes on there, or another block has it
-    const int P = pages_of(paged_len(p, at.b)), from = split.start(c) - at.j;
-    int parts = 2;
-    while (c + parts - 1 < split.ctas && split.start(c + parts - 1) < from + P)
-        ++parts;
+    const int parts = split.owner(from + P - 1) - c + 1;
+    if (parts == 1)
+        return;
     // slot of part i: the CTA's first run, but for the unit's first part where the CTA has others before it
-    const int slot0 = 2 * (c - 1) + (split.start(c - 1) < from);
+    const int slot0 = 2 * c + (split.start(c) < from);
     const int h = at.u % p.kv_heads, row0 = at.u / p.kv_heads * p.tile_rows;
     const int rows = min(p.tile_rows, p.q_len * p.group - row0);
     const int r = blockIdx.y * kRows + warp / WPR;
-    auto slot = [&](int i) { return static_cast<int64_t>(i == 0 ? slot0 : 2 * (c - 1 + i)) * p.tile_rows + r; };
+    auto slot = [&](int i) { return static_cast<int64_t>(i == 0 ? slot0 : 2 * (c + i)) * p.tile_rows + r; };
     float M = -INFINITY, sum = 0.0f;
     float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     bool bad = false;
