@@ -1022,7 +1022,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attn_kernel(const __gr
 // The units that a range's end cuts, 8 / WPR of their rows a block, WPR warps a row that take its parts in turn.  UNITS:
 // block x takes unit x, if it is cut; else the one that CTA x + 1 is the first to go on with.
 template <int WPR, bool UNITS>
-__global__ void __launch_bounds__(256, 6) paged_join_kernel(const __grid_constant__ PagedParams p)
+__global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__ PagedParams p)
 {
     constexpr int kRows = 8 / WPR;
     __shared__ PagedScan scan;
@@ -1074,14 +1074,14 @@ __global__ void __launch_bounds__(256, 6) paged_join_kernel(const __grid_constan
         acc.y *= old;
         acc.z *= old;
         acc.w *= old;
-        for (int i = 0; i < end; i += 4) {
-            float4 v[4];  // under way together
+        for (int i = 0; i < end; i += 8) {
+            float4 v[8];  // under way together
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
+            for (int k = 0; k < 8; ++k)
                 v[k] = i + k < end ? __ldcg(reinterpret_cast<const float4 *>(p.part_o + slot(sub + (i0 + i + k) * WPR) * kDim) + lane)
                                    : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
+            for (int k = 0; k < 8; ++k) {
                 const float fi = __shfl_sync(0xffffffffu, f, i + k);
                 const bool some = fi != 0.0f;
                 sum += fi;
