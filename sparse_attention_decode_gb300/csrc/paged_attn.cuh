@@ -22,12 +22,12 @@
 // O in tensor memory, follow only where somebody has passed it: once a unit as a rule.
 //
 // E4M3: the codes go into the products as they are (kind::f8f6f4), so the other operand
-// has to be E4M3 as well.  A query row, brought to [2^7, 2^8) by a power of two, is the
-// sum of two E4M3 numbers, exactly where it is within 2^-9 of the row's largest (4 bits
-// each, the second 2^-5 on), and to 2^-23 of that largest below.  A weight times its
+// has to be E4M3 as well.  A query row, brought to [2^3, 2^4) by a power of two, is the
+// sum of two E4M3 numbers, the second 2^-9 on: exactly where it is within 2^-9 of the
+// row's largest (4 bits each), and to 2^-23 of that largest below.  A weight times its
 // token's V scale is the sum of three, after one rounding to f16 (11 bits), and held
-// relative to the row's largest such product so far: down to 2^-24 of it.  The terms stand side by side as
-// further rows of the product, so K and V still pass once.
+// relative to the row's largest such product so far: down to 2^-26 of it.  The terms
+// stand side by side as further rows of the product, so K and V still pass once.
 #pragma once
 
 #include "attn_common.cuh"
@@ -55,9 +55,8 @@ constexpr int kPagedThreads = 352;  // two softmax warpgroups, a TMA warp, two M
 constexpr int kPagedMaxGrid = 256;
 constexpr int kPagedMaxRows = 64;   // of a unit: one chain's 16 or 32, or both chains' 32
 constexpr float kPagedLag = 8.0f;
-constexpr float kPagedMost = 256.0f;  // of an E4M3 weight: what is left of it after a term is then at most 256 as well
-constexpr float kPagedTermUp = 32.0f;                  // an E4M3 term over the next
-constexpr float kPagedTermDown = 1.0f / kPagedTermUp;
+constexpr float kPagedMost = 32768.0f;  // of an E4M3 weight, in units of 2^-11 (what its terms are taken from)
+constexpr float kPagedTermDown = 1.0f / 512.0f;  // an E4M3 term's unit over the one before
 
 struct PagedParams {
     CUtensorMap kmap, vmap;
@@ -337,19 +336,22 @@ __device__ __forceinline__ int float_int(float x)
 }
 __device__ __forceinline__ float int_float(int i) { return __int_as_float(i ^ ((i >> 31) & 0x7fffffff)); }
 
-// x, y (at most 256) as sums of E4M3 numbers t[0] + t[1] / 32 + .., two codes each, after one rounding to f16.  What a term
-// leaves is exact in f16.
+// x, y (at most 16, times 2^11) as sums of E4M3 numbers t[0] + t[1] / 2^9 + t[2] / 2^18, two codes each, after one rounding
+// to f16.  What a term leaves is exact in f16: half a unit in the last of 4 bits, 256 at most for the second term.  The third
+// can be asked for up to 2^12 where x passes 1, and ends at 448: 8 bits are left then, 11 below.
 template <int TERMS>
 __device__ __forceinline__ void e4m3_terms(float x, float y, uint32_t (&t)[TERMS])
 {
     uint32_t left = f32x2_to_f16x2(x, y);
 #pragma unroll
     for (int i = 0; i < TERMS; ++i) {
+        constexpr uint32_t kDown[3] = {0x10001000u, 0x34003400u, 0x58005800u};  // 2^-11, 2^-2, 2^7, two each
+        constexpr uint32_t kBack[3] = {0xe800e800u, 0xc400c400u, 0xa000a000u};  // -2^11, -2^2, -2^-7
         uint16_t code;
-        asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(code) : "r"(left));
+        asm("{\n  .reg .b32 a;\n  mul.f16x2 a, %1, %2;\n  cvt.rn.satfinite.e4m3x2.f16x2 %0, a;\n}\n" : "=h"(code) : "r"(left), "r"(kDown[i]));
         t[i] = code;
         if (i + 1 < TERMS)
-            asm("{\n  .reg .b32 a;\n  sub.f16x2 a, %0, %1;\n  mul.f16x2 %0, a, %2;\n}\n" : "+r"(left) : "r"(e4m3x2_to_f16x2(code)), "r"(0x50005000u));
+            asm("fma.rn.f16x2 %0, %1, %2, %0;" : "+r"(left) : "r"(e4m3x2_to_f16x2(code)), "r"(kBack[i]));
     }
 }
 
@@ -630,9 +632,9 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attn_kernel(const __gr
 #pragma unroll
                 for (int o = 8; o >= 1; o >>= 1)
                     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-                // the power of two that brings it to [2^7, 2^8)
-                const int e = max(15, min(246, static_cast<int>(__float_as_uint(top) >> 23)));
-                const float f = __int_as_float((261 - e) << 23);
+                // the power of two that brings it to [2^14, 2^15)
+                const int e = max(22, min(240, static_cast<int>(__float_as_uint(top) >> 23)));
+                const float f = __int_as_float((268 - e) << 23);
                 uint32_t term[4][F::kQTerms];
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
@@ -644,7 +646,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attn_kernel(const __gr
                         make_uint2(term[0][k] | term[1][k] << 16, term[2][k] | term[3][k] << 16);
                 }
                 if (c == 0)
-                    ctl->coef[r] = __int_as_float((e - 7) << 23) * p.scale_log2;
+                    ctl->coef[r] = __int_as_float((e - 3) << 23) * p.scale_log2;  // (2^-11 is in the terms)
             }
             if (tid < R)
                 ctl->sees[tid] = max(0, w.len - ctl->hidden[tid]);
@@ -720,15 +722,20 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attn_kernel(const __gr
                         mbar_arrive(smem_addr(&ctl->s_free[t]));
                     const uint64_t down = pack2(kPagedTermDown, kPagedTermDown), ks2 = pack2(ks, ks);
 #pragma unroll
-                    for (int r = 0; r < N; r += 2) {
-                        s[r] = __uint_as_float(raw[r / 16][r % 16]);
-                        s[r + 1] = __uint_as_float(raw[r / 16][r % 16 + 1]);
-                        if (F::kFp8) {
-                            const uint32_t(&low)[16] = raw[(N + r) / 16 % (F::kQTerms * N / 16)];
-                            const float2 cf = *reinterpret_cast<const float2 *>(coef + r);
-                            const uint64_t x = fma2(pack2(__uint_as_float(low[r % 16]), __uint_as_float(low[r % 16 + 1])), down,
-                                                    pack2(s[r], s[r + 1]));
-                            unpack2(mul2(x, mul2(ks2, pack2(cf.x, cf.y))), s[r], s[r + 1]);
+                    for (int r = 0; r < N; r += 4) {
+                        float cf[4];
+                        if (F::kFp8)
+                            *reinterpret_cast<float4 *>(cf) = *reinterpret_cast<const float4 *>(coef + r);
+#pragma unroll
+                        for (int e = 0; e < 4; e += 2) {
+                            s[r + e] = __uint_as_float(raw[r / 16][r % 16 + e]);
+                            s[r + e + 1] = __uint_as_float(raw[r / 16][r % 16 + e + 1]);
+                            if (F::kFp8) {
+                                const uint32_t(&low)[16] = raw[(N + r) / 16 % (F::kQTerms * N / 16)];
+                                const uint64_t x = fma2(pack2(__uint_as_float(low[r % 16 + e]), __uint_as_float(low[r % 16 + e + 1])),
+                                                        down, pack2(s[r + e], s[r + e + 1]));
+                                unpack2(mul2(x, mul2(ks2, pack2(cf[e], cf[e + 1]))), s[r + e], s[r + e + 1]);
+                            }
                         }
                     }
                 }
@@ -754,33 +761,42 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attn_kernel(const __gr
                 const uint64_t c2 = pack2(to_log2, to_log2), vs2 = pack2(vs, vs);
                 float w[N];
                 uint64_t ls2[N / 2];
-                for (bool moved = false;; moved = true) {
-                    float top = 0.0f, most = 0.0f;
+                float top = 0.0f, most = 0.0f;
+                auto weigh = [&] {
 #pragma unroll
-                    for (int r = 0; r < N; r += 2) {
-                        const float2 nr = *reinterpret_cast<const float2 *>(&ctl->nref[t][r]);
-                        float x, y;
-                        unpack2(F::kFp8 ? add2(pack2(s[r], s[r + 1]), pack2(nr.x, nr.y))
-                                        : fma2(pack2(s[r], s[r + 1]), c2, pack2(nr.x, nr.y)),
-                                x, y);
-                        if (masks) {
-                            x = s[r] == -INFINITY ? -INFINITY : x;
-                            y = s[r + 1] == -INFINITY ? -INFINITY : y;
-                        }
-                        top = max3(top, x, y);
-                        w[r] = exp2_approx(x);
-                        w[r + 1] = exp2_approx(y);
-                        ls2[r / 2] = pack2(w[r], w[r + 1]);
-                        if (F::kFp8) {
-                            const float2 un = *reinterpret_cast<const float2 *>(&ctl->unit[t][r]);
-                            unpack2(mul2(ls2[r / 2], mul2(vs2, pack2(un.x, un.y))), w[r], w[r + 1]);
-                            most = max3(most, w[r], w[r + 1]);
+                    for (int r = 0; r < N; r += 4) {
+                        float nr[4], un[4];
+                        *reinterpret_cast<float4 *>(nr) = *reinterpret_cast<const float4 *>(&ctl->nref[t][r]);
+                        if (F::kFp8)
+                            *reinterpret_cast<float4 *>(un) = *reinterpret_cast<const float4 *>(&ctl->unit[t][r]);
+#pragma unroll
+                        for (int e = 0; e < 4; e += 2) {
+                            const int k = r + e;
+                            float x, y;
+                            unpack2(F::kFp8 ? add2(pack2(s[k], s[k + 1]), pack2(nr[e], nr[e + 1]))
+                                            : fma2(pack2(s[k], s[k + 1]), c2, pack2(nr[e], nr[e + 1])),
+                                    x, y);
+                            if (masks) {
+                                x = s[k] == -INFINITY ? -INFINITY : x;
+                                y = s[k + 1] == -INFINITY ? -INFINITY : y;
+                            }
+                            top = max3(top, x, y);
+                            w[k] = exp2_approx(x);
+                            w[k + 1] = exp2_approx(y);
+                            ls2[k / 2] = pack2(w[k], w[k + 1]);
+                            if (F::kFp8) {
+                                unpack2(mul2(ls2[k / 2], mul2(vs2, pack2(un[e], un[e + 1]))), w[k], w[k + 1]);
+                                most = max3(most, w[k], w[k + 1]);
+                            }
                         }
                     }
-                    if (moved)
-                        break;
-                    if (!barrier_any(3 + t, 128, top > kPagedLag || most > kPagedMost || bad))
-                        break;
+                };
+                bool moves = j < WAYS;  // a unit's first page: no references yet
+                if (!moves) {
+                    weigh();
+                    moves = barrier_any(3 + t, 128, top > kPagedLag || most > kPagedMost || bad);
+                }
+                if (moves) {
                     stop = barrier_any(3 + t, 128, bad);  // (what one warp saw alone is no reason to leave the others)
                     if (stop)
                         break;
@@ -814,9 +830,9 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attn_kernel(const __gr
                             const float before = ctl->vtop[t][tau] * ctl->lfac[t][tau], unit = ctl->unit[t][tau];
                             const float most_now = fmaxf(before, __int_as_float(max(max(ctl->wmax[t][0][tau], ctl->wmax[t][1][tau]),
                                                                                     max(ctl->wmax[t][2][tau], ctl->wmax[t][3][tau]))));
-                            // the power of two that brings it to [2^4, 2^5): room for 2^3 of growth until the next time
+                            // the power of two that brings it to [2^9, 2^10): room for 2^5 of growth until the next time
                             const int e = static_cast<int>(__float_as_uint(most_now) >> 23);
-                            const float to_unit = most_now > 0.0f ? __int_as_float(max(10, min(244, 258 - e)) << 23) : 1.0f;
+                            const float to_unit = most_now > 0.0f ? __int_as_float(max(10, min(244, 263 - e)) << 23) : 1.0f;
                             ctl->vtop[t][tau] = most_now;
                             ctl->unit[t][tau] = to_unit;
                             ctl->fac[t][tau] = before > 0.0f ? ctl->lfac[t][tau] * to_unit * (1.0f / unit) : 0.0f;
@@ -843,6 +859,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attn_kernel(const __gr
                         }
                         tmem_wait_st();
                     }
+                    weigh();
                 }
                 if (stop)
                     break;
@@ -939,7 +956,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attn_kernel(const __gr
 #pragma unroll
                 for (int c = 0; c < 2; ++c)  // 0: nothing, and what stands in O may be anything
                     ctl->share[c][tid] =
-                        sum[c] > 0.0f ? __fdividef(m[c], all) * (F::kFp8 ? 1.0f / ctl->unit[c][tid % N] : 1.0f) : 0.0f;
+                        sum[c] > 0.0f ? __fdividef(m[c], all) * (F::kFp8 ? 2048.0f / ctl->unit[c][tid % N] : 1.0f) : 0.0f;
                 top = M;
             }
             barrier_sync(2, 256);
