@@ -23,7 +23,7 @@
 // that reach it become 64-bit keys that order equal logits by the lower token; a key's
 // place is the number of larger ones.  The bound comes from the lanes' running maxima,
 // which are logits of their own: the n-th of the warps' four largest each.  It is brought
-// up to date after 1, 2, 4, .. stages, without a barrier: old numbers make a bound as well.
+// up to date after stages 1, 3, 11, .., without a barrier: old numbers make a bound as well.
 // (Where logits rise along a row, every place is noted for a while: 64 of them are then
 // read at once, and 32 keys at a time sorted and merged into a list of the warp's 32
 // largest, which raises the bound.)
@@ -242,14 +242,24 @@ __device__ __forceinline__ Candidates push_group(Candidates c, uint64_t *buffer,
 #pragma unroll
     for (int w = 0; w < 16 / N; ++w)
         raw_logits(in[w], x[w]);
+    for (;;) {  // each lane its largest, as long as one has one that counts
+        float top = -INFINITY;
+        int at = 0;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        const float l = x[i / N][i % N];
-        if (__any_sync(0xffffffffu, l >= c.at_least)) {
-            c.push(buffer, l >= c.at_least ? logit_key(l, v + i / N * stride + i % N) : 0, lane);
-            if (c.fill >= 32)
-                c = merge_candidates(c, buffer, list, keep, lane);
+        for (int i = 15; i >= 0; --i) {
+            const bool larger = x[i / N][i % N] >= top;  // (the first of equal ones; NaN never)
+            top = larger ? x[i / N][i % N] : top;
+            at = larger ? i : at;
         }
+        const bool counts = top >= c.at_least && top > -INFINITY;
+        if (!__any_sync(0xffffffffu, counts))
+            break;
+        c.push(buffer, counts ? logit_key(top, v + at / N * stride + at % N) : 0, lane);
+        if (c.fill >= 32)
+            c = merge_candidates(c, buffer, list, keep, lane);
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            x[i / N][i % N] = i == at ? -INFINITY : x[i / N][i % N];
     }
     return c;
 }
@@ -395,7 +405,7 @@ __global__ void __launch_bounds__(kLpThreads + 32, kLpBlocks) logprobs_kernel(co
         uint32_t least2 = 0xff80ff80u;
         bool far = true;  // (no reference yet)
         float run = -INFINITY;  // the lane's largest logit
-        int stage = 0, noted = 0;
+        int stage = 0, noted = 0, update = 0;
         const uint4 *vectors = reinterpret_cast<const uint4 *>(x.row + x.head);
         // the CTA's bound by the lanes' largest logits so far
         auto raise = [&](float top, bool together) {
@@ -423,7 +433,8 @@ __global__ void __launch_bounds__(kLpThreads + 32, kLpBlocks) logprobs_kernel(co
             auto vector = [&](int i) { return i < left ? ring[i] : make_uint4(none, none, none, none); };
             if (left > 0)
                 attn_wait(&sm.abort_flag, p.fault, smem_addr(&sm.full[s]), (it / kLpStages) & 1, 0);
-            if (keep > 0 && (stage & (stage + 1)) == 0) {
+                if (keep > 0 && stage == update) {
+                update = 4 * stage + 2;
                 float top = run;
 #pragma unroll
                 for (int u = 0; u < kLpVectors / kLpThreads; ++u)
