@@ -261,6 +261,87 @@ def test_bad_device_data_is_absent_and_reported():
         assert got["fault"] == (msa.MSA_FAULT_SEQ_LEN if broken else 0), bad
 
 
+MANY = [
+    # more rows than the GPU has SMs, lines of 24 heads and more (and of fewer): lens, new, kv heads, query heads, ...
+    ([50 + 9 * i for i in range(9)], [40] * 9, 3, 26, 64, True, "wide"),
+    ([400, 3, 0, 170], [200, 3, 0, 170], 24, 0, 48, False, "nhd"),
+    ([160], [160], 8, 207, 128, False, "hnd"),   # the longest line that fits twice an SM
+    ([160], [160], 8, 208, 128, True, "hnd"),    # and one more
+    ([130, 180], [100, 77], 1, 21, 0, True, "hnd"),
+    ([200], [200], 5, 13, 32, False, "hnd"),
+]
+
+
+@pytest.mark.parametrize("e4m3", [False, True], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("case", MANY, ids=lambda c: f"{sum(c[1])}h{c[2]}q{c[3]}r{c[4]}{'i' * c[5]}{c[6]}")
+def test_many_rows(case, e4m3):
+    import sparse_attention_decode_gb300 as msa
+    lens, new, H, Hq, rot, inter, layout = case
+    w = make(29, lens, new, H, Hq, rot, inter, True, layout, e4m3, shift=5)
+    got = call(msa, w, ragged=True, q=Hq > 0)
+    assert got["fault"] == 0
+    verify(w, got, q=Hq > 0)
+
+
+@pytest.mark.parametrize("e4m3", [False, True], ids=["bf16", "e4m3"])
+def test_many_rows_of_keys_alone(e4m3):
+    import sparse_attention_decode_gb300 as msa
+    w = make(30, [60] * 4, [41] * 4, 25, 0, 32, False, True, "hnd", e4m3, values=False)
+    got = call(msa, w, q=False)
+    assert got["fault"] == 0
+    verify(w, got, q=False)
+
+
+@pytest.mark.parametrize("inter", [False, True], ids=["halves", "interleaved"])
+def test_many_rows_padded_in_place_and_captured(inter):
+    """Requests shorter than q_len, rows behind the last request, queries prepared where they are."""
+    import sparse_attention_decode_gb300 as msa
+    w = make(31, [90, 7, 0, 40], [45] * 4, 2, 24, 64, inter, True, "hnd", False)
+    got = call(msa, w)
+    assert got["fault"] == 0
+    verify(w, got)
+    x = w["x"].cuda()
+    kp, vp, ws = ref.to_cuda(w["kp"]), ref.to_cuda(w["vp"]), torch.zeros(256, dtype=torch.uint8, device="cuda")
+    seq, table = torch.tensor(w["lens"], dtype=torch.int32, device="cuda"), w["table"].cuda()
+    more = dict(q_weight=w["qw"].cuda(), k_weight=w["kw"].cuda(), eps=1e-5, inv_freq=w["inv"].cuda(), q_len=45,
+                interleaved=inter)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        msa.msa_cache_append(x[:, 24:26], x[:, 26:], kp, vp, table, seq, ws, q=x[:, :24], out_q=x[:, :24], **more)
+    graph.replay()
+    torch.cuda.synchronize()
+    live = [r for r, t in enumerate(w["token"]) if t >= 0]
+    assert same(x[live, :24].cpu(), got["q"][live]) and same(kp.cpu(), got["kp"]) and same(vp.cpu(), got["vp"])
+    left = [r for r, t in enumerate(w["token"]) if t < 0]
+    assert same(x[left].cpu(), w["x"][left]) and same(x[:, 24:].cpu(), w["x"][:, 24:])
+    w = make(32, [100, 120], [95, 90], 2, 24, 64, inter, True, "hnd", False)
+    cu = torch.tensor([0, 90, 180], dtype=torch.int32, device="cuda")  # of 185 rows
+    w["owner"] = [0] * 90 + [1] * 95
+    w["token"] = list(range(10, 100)) + list(range(30, 120)) + [-1] * 5
+    got = call(msa, w, ragged=True, cu_seqlens_q=cu)
+    assert got["fault"] == 0
+    verify(w, got)
+
+
+def test_many_rows_with_bad_device_data():
+    import sparse_attention_decode_gb300 as msa
+    w = make(33, [300, 40, 129, 60], [40] * 4, 2, 24, 64, False, True, "hnd", False)
+    w["table"][0, 2] = 10 ** 6
+    w["lens"] = [300, -1, 10 ** 6, 60]
+    got = call(msa, w)
+    assert got["fault"] == msa.MSA_FAULT_PAGE_ID | msa.MSA_FAULT_SEQ_LEN
+    at = torch.tensor(w["token"])
+    y, tol = plain(w["x"][:, :24], w["qw"], 1e-5, at, w["inv"], False)
+    live = list(range(40)) + list(range(120, 160))
+    assert bool(((got["q"].double() - y).abs() <= tol + 2.0 ** -8 * y.abs())[live].all())
+    assert bool((got["q"][40:120] == 7.0).all())
+    for bad in ([0, 90, 30, 160, 160], [0, 40, 80, 120, 9000], [-3, 40, 80, 120, 160], [0, 160, 160, 160, 160]):
+        cu = torch.tensor(bad, dtype=torch.int32, device="cuda")
+        w["lens"] = [300, 40, 129, 60]
+        assert call(msa, w, ragged=True, cu_seqlens_q=cu)["fault"] & msa.MSA_FAULT_SEQ_LEN == \
+            (msa.MSA_FAULT_SEQ_LEN if bad != [0, 160, 160, 160, 160] else 0), bad
+
+
 def test_refusals():
     import sparse_attention_decode_gb300 as msa
     z = lambda *s, dtype=torch.bfloat16: torch.zeros(*s, dtype=dtype, device="cuda")  # noqa: E731

@@ -178,6 +178,26 @@ def test_optional_outputs_streams_and_graphs():
     assert near(out, want[0], want[4]) and torch.equal(ids.cpu(), want[2]) and near(top, want[3], want[4])
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["fp32", "bf16"])
+@pytest.mark.parametrize("shape", [(7, 300007), (45, 120011), (100, 33333), (420, 20003)], ids=lambda s: f"{s[0]}x{s[1]}")
+def test_rows_of_many_stages(shape, dtype):
+    """Rows of each share of a row's blocks, long enough to go round the ring; largest logits anywhere and masked runs."""
+    import sparse_attention_decode_gb300 as msa
+    R, V = shape
+    g = torch.Generator(device="cuda").manual_seed(37)
+    x = (torch.randn(R, V, device="cuda", generator=g) * 2).to(dtype)
+    x[0, V - 60:] = 9.0  # ties at the end
+    x[1 % R, :V // 2] = -INF
+    x[2 % R, V // 3:] = torch.finfo(dtype).min
+    x[3 % R] = -INF
+    x[4 % R] = torch.linspace(-20, 20, V, device="cuda").to(dtype)
+    x[5 % R] = torch.linspace(20, -20, V, device="cuda").to(dtype)
+    tokens = torch.randint(0, V, (R, 3), dtype=torch.int32, generator=torch.Generator().manual_seed(38))
+    temp = torch.full((R,), 0.8)
+    temp[6 % R] = 0.0
+    assert verify(msa, x, tokens, temp, 20) == 0
+
+
 def test_tokens_outside_the_vocabulary_are_reported():
     import sparse_attention_decode_gb300 as msa
     x = torch.zeros(2, 100, device="cuda")
