@@ -17,6 +17,11 @@ static size_t paged_workspace(int64_t max_rows, int group)
     return kHeaderBytes + 2 * kPagedMaxGrid * static_cast<size_t>(paged_tile_rows(max_rows * group)) * (kDim + 1) * sizeof(float);
 }
 
+// What a unit costs beside its pages (its query rows, its first page's references, its epilogue), in pages of the same type:
+// bf16, E4M3.  64 requests of 1 to 3000 tokens, 4 heads: 16 rows 52.8 us without, 44.4 with 2 to 4, 45.2 with 8; 64 rows 90.2,
+// 56.0 with 4, 57.3 with 8; E4M3 64.4, 37.5 with 4, 34.3 with 8, 37.5 with 16.
+constexpr int kPagedLead[2] = {4, 8};
+
 template <class F, int N, int WAYS>
 static msa_status launch_paged(const PagedParams &p, int dev, cudaStream_t st)
 {
@@ -79,8 +84,9 @@ static msa_status paged_entry(const void *q, int64_t q_stride, const void *k, co
     p.tile_rows = paged_tile_rows(static_cast<int64_t>(q_len) * group);
     p.row_tiles = (q_len * group + p.tile_rows - 1) / p.tile_rows;
     p.seq_limit = static_cast<int>(std::min<int64_t>(max_model_len, kPage * bt_stride));
-    // the pages of all units are counted in 32 bits
-    if ((static_cast<int64_t>(p.seq_limit) + kPage - 1) / kPage * batch * p.row_tiles * kv_heads > (1 << 30))
+    p.lead = fp8 ? kPagedLead[1] : kPagedLead[0];
+    // the slots of all units are counted in 32 bits
+    if (((static_cast<int64_t>(p.seq_limit) + kPage - 1) / kPage + p.lead) * batch * p.row_tiles * kv_heads > (1 << 30))
         return MSA_ERR_UNSUPPORTED;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess)

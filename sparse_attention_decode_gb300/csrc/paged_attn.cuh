@@ -71,6 +71,7 @@ struct PagedParams {
     int batch, q_len, kv_heads, group, seq_limit;
     int tile_rows, row_tiles;  // rows of a unit at most; units of a request and KV head
     int grid;                  // CTAs of paged_attn_kernel
+    int lead;                  // what a unit costs beside its pages, in pages
     float scale_log2;
     int withhold;  // test of the bounded waits: the producer loads and signals no page
 };
@@ -81,24 +82,24 @@ __device__ __forceinline__ int paged_len(const PagedParams &p, int b)
     return n < 0 || n > p.seq_limit ? 0 : n;
 }
 
-// The batch's work: pages of all units, and units that have some.
+// The batch's work: slots of all units, and units that have some.  A unit of P pages has `lead` slots, in which there is
+// nothing to do and which stand for its start and its end, and then a slot a page.
 struct PagedWork {
-    int pages, units;
+    int slots, units;
 };
 
-// The ranges: CTA g has [start(g), start(g + 1)) of the units' pages: two pages at least, one for each chain, but no fewer
+// The ranges: CTA g has [start(g), start(g + 1)) of the units' slots, two pages at least, one for each chain, but no fewer
 // ranges than units.
 struct PagedSplit {
     int ctas, range, more;
-    __device__ PagedSplit(const PagedWork &work, int grid)
+    __device__ PagedSplit(const PagedWork &work, const PagedParams &p)
     {
-        const int total = work.pages;
-        ctas = min(grid, max((total + 1) / 2, work.units));
-        range = ctas > 0 ? total / ctas : 0;
-        more = total - range * ctas;
+        ctas = min(p.grid, max((work.slots - work.units * p.lead + 1) / 2, work.units));
+        range = ctas > 0 ? work.slots / ctas : 0;
+        more = work.slots - range * ctas;
     }
     __device__ int start(int g) const { return g * range + min(g, more); }
-    // the CTA whose range holds page x
+    // the CTA whose range holds slot x
     __device__ int owner(int x) const
     {
         const int longer = more * (range + 1);
@@ -106,17 +107,17 @@ struct PagedSplit {
     }
 };
 
-// A place in the sequence of the units' pages.
+// A place in the sequence of the units' slots.
 struct PagedAt {
-    int b, u, j;  // request, its unit, the unit's page
+    int b, u, j;  // request, its unit, the unit's page (negative: its lead)
 };
 
 struct PagedScan {
-    int pages[32], requests[32], early[32];  // the warps' sums
+    int slots[32], requests[32], early[32];  // the warps' sums
     PagedAt at;
 };
 
-// The batch's work, the pages of requests before `request` (in `before`) and the place of page `want(work)` of the sequence
+// The batch's work, the slots of requests before `request` (in `before`) and the place of slot `want(work)` of the sequence
 // (request `batch`: there is none), by a whole block.
 template <int THREADS, class Want>
 __device__ __forceinline__ PagedWork paged_find(const PagedParams &p, PagedScan *sc, int request, int &before, Want want)
@@ -127,7 +128,7 @@ __device__ __forceinline__ PagedWork paged_find(const PagedParams &p, PagedScan 
     const int b0 = min(p.batch, tid * each), b1 = min(p.batch, b0 + each);
     int mine = 0, some = 0, early = 0;
     for (int b = b0; b < b1; ++b) {
-        const int n = pages_of(paged_len(p, b)) * units;
+        const int P = pages_of(paged_len(p, b)), n = P > 0 ? (P + p.lead) * units : 0;
         mine += n;
         some += n > 0;
         early += b < request ? n : 0;
@@ -141,7 +142,7 @@ __device__ __forceinline__ PagedWork paged_find(const PagedParams &p, PagedScan 
     some = __reduce_add_sync(0xffffffffu, some);
     early = __reduce_add_sync(0xffffffffu, early);
     if (lane == 31) {
-        sc->pages[warp] = upto;
+        sc->slots[warp] = upto;
         sc->requests[warp] = some;
         sc->early[warp] = early;
     }
@@ -152,8 +153,8 @@ __device__ __forceinline__ PagedWork paged_find(const PagedParams &p, PagedScan 
     PagedWork work{0, 0};
     before = 0;
     for (int w = 0; w < THREADS / 32; ++w) {
-        prior += w < warp ? sc->pages[w] : 0;
-        work.pages += sc->pages[w];
+        prior += w < warp ? sc->slots[w] : 0;
+        work.slots += sc->slots[w];
         work.units += sc->requests[w] * units;
         before += sc->early[w];
     }
@@ -161,10 +162,10 @@ __device__ __forceinline__ PagedWork paged_find(const PagedParams &p, PagedScan 
     int from = prior + upto - mine;
     if (x >= from && x < from + mine) {
         for (int b = b0; b < b1; ++b) {
-            const int P = pages_of(paged_len(p, b)), n = P * units;
+            const int P = pages_of(paged_len(p, b)), each_unit = P > 0 ? P + p.lead : 0, n = each_unit * units;
             if (x < from + n) {
-                const int u = (x - from) / P;
-                sc->at = PagedAt{b, u, x - from - u * P};
+                const int u = (x - from) / each_unit;
+                sc->at = PagedAt{b, u, x - from - u * each_unit - p.lead};
                 break;
             }
             from += n;
@@ -176,10 +177,12 @@ __device__ __forceinline__ PagedWork paged_find(const PagedParams &p, PagedScan 
 
 // Runs through a range unit by unit.
 struct PagedWalk {
-    int b, u, j, left;  // the next page, and pages left
+    int b, u, j, left;  // the next page, and slots left from there on
     int len, P;         // of request b
     __device__ PagedWalk(const PagedParams &p, const PagedAt &at, int n) : b(at.b), u(at.u), j(at.j), left(n), len(0), P(0)
     {
+        left += min(j, 0);
+        j = max(j, 0);
         if (left > 0) {
             len = paged_len(p, b);
             P = pages_of(len);
@@ -188,7 +191,7 @@ struct PagedWalk {
     __device__ int run() const { return min(left, P - j); }
     __device__ void next(const PagedParams &p)
     {
-        left -= run();
+        left -= run() + p.lead;
         j = 0;
         if (++u == p.row_tiles * p.kv_heads && left > 0) {
             u = 0;
@@ -429,10 +432,10 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attn_kernel(const __gr
                 atomicOr(p.fault, MSA_FAULT_SEQ_LEN);
     int unused;
     const PagedWork total = paged_find<kPagedThreads>(p, &ctl->scan, 0, unused, [&](const PagedWork &work) {
-        const PagedSplit s(work, p.grid);
+        const PagedSplit s(work, p);
         return cta < s.ctas ? s.start(cta) : -1;
     });
-    const PagedSplit split(total, p.grid);
+    const PagedSplit split(total, p);
     const int count = cta < split.ctas ? split.start(cta + 1) - split.start(cta) : 0;
     tc_fence_after_sync();
     const uint32_t tmem = __shfl_sync(0xffffffffu, ctl->tmem, 0);
@@ -1050,23 +1053,23 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__
     const int units = p.row_tiles * p.kv_heads, x = blockIdx.x;
     int before;
     const PagedWork work = paged_find<256>(p, &scan, UNITS ? x / units : 0, before, [&](const PagedWork &all) {
-        const PagedSplit s(all, p.grid);
+        const PagedSplit s(all, p);
         return !UNITS && x + 1 < s.ctas ? s.start(x + 1) : -1;
     });
-    const PagedSplit split(work, p.grid);
+    const PagedSplit split(work, p);
     const PagedAt at = UNITS ? PagedAt{x / units, x % units, 0} : scan.at;
     const int P = at.b < p.batch ? pages_of(paged_len(p, at.b)) : 0;
-    // the unit's pages [from, from + P), and the CTA that has the first
-    const int from = UNITS ? before + at.u * P : (x + 1 < split.ctas ? split.start(x + 1) : 0) - at.j;
+    // the slots of the unit's pages [from, from + P), and the CTA that has the first
+    const int from = UNITS ? before + at.u * (P + p.lead) + p.lead : (x + 1 < split.ctas ? split.start(x + 1) : 0) - at.j;
     const int c = UNITS ? (P > 0 ? split.owner(from) : 0) : x;
     griddep_wait();  // also where there is nothing to do: who waits for this grid reads what both have written
-    if (P == 0 || (!UNITS && (at.j == 0 || split.start(c) > from)))
+    if (P == 0 || (!UNITS && (at.j <= 0 || split.start(c) > from)))
         return;  // no unit goes on there, or another block has it
     const int parts = split.owner(from + P - 1) - c + 1;
     if (parts == 1)
         return;
     // slot of part i: the CTA's first run, but for the unit's first part where the CTA has others before it
-    const int slot0 = 2 * c + (split.start(c) < from);
+    const int slot0 = 2 * c + (split.start(c) < from - p.lead);
     const int h = at.u % p.kv_heads, row0 = at.u / p.kv_heads * p.tile_rows;
     const int rows = min(p.tile_rows, p.q_len * p.group - row0);
     const int r = blockIdx.y * kRows + warp / WPR;
