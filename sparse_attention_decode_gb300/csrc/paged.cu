@@ -22,15 +22,16 @@ static size_t paged_workspace(int64_t max_rows, int group)
 // 56.0 with 4, 57.3 with 8; E4M3 64.4, 37.5 with 4, 34.3 with 8, 37.5 with 16.
 constexpr int kPagedLead[2] = {4, 8};
 
-template <class F, int N, int WAYS>
+template <class F, int N, int WAYS, int GROUPS>
 static msa_status launch_paged(const PagedParams &p, int dev, cudaStream_t st)
 {
     static std::atomic<bool> allowed[kMaxDevices];
-    auto *kernel = paged_attn_kernel<F, N, WAYS>;
-    constexpr size_t smem = PagedLayout<F, N, WAYS>::kBytes;
+    auto *kernel = paged_attn_kernel<F, N, WAYS, GROUPS>;
+    using L = PagedLayout<F, N, WAYS, GROUPS>;
+    constexpr size_t smem = L::kBytes;
     if (!allow_smem(kernel, smem, dev, allowed))
         return MSA_ERR_CUDA;
-    kernel<<<static_cast<unsigned>(p.grid), kPagedThreads, smem, st>>>(p);
+    kernel<<<static_cast<unsigned>(p.grid), L::kThreads, smem, st>>>(p);
     if (cudaGetLastError() != cudaSuccess)
         return MSA_ERR_CUDA;
     if (p.grid < 2)
@@ -52,9 +53,12 @@ static msa_status launch_paged(const PagedParams &p, int dev, cudaStream_t st)
 template <class F>
 static msa_status launch_paged_rows(const PagedParams &p, int dev, cudaStream_t st)
 {
-    return p.tile_rows == 16   ? launch_paged<F, 16, 2>(p, dev, st)
-           : p.tile_rows == 32 ? launch_paged<F, 32, 2>(p, dev, st)
-                               : launch_paged<F, 32, 1>(p, dev, st);
+    if (p.tile_rows == 16)
+        return launch_paged<F, 16, 2, 1>(p, dev, st);
+    if constexpr (F::kFp8)
+        return p.tile_rows == 32 ? launch_paged<F, 16, 2, 2>(p, dev, st) : launch_paged<F, 16, 1, 4>(p, dev, st);
+    else
+        return p.tile_rows == 32 ? launch_paged<F, 32, 2, 1>(p, dev, st) : launch_paged<F, 32, 1, 2>(p, dev, st);
 }
 
 static msa_status paged_entry(const void *q, int64_t q_stride, const void *k, const int64_t *k_strides,

@@ -51,9 +51,8 @@ struct PagedFp8 {
     static constexpr int kQTerms = 2, kPTerms = 3;
 };
 
-constexpr int kPagedThreads = 352;  // two softmax warpgroups, a TMA warp, two MMA warps
 constexpr int kPagedMaxGrid = 256;
-constexpr int kPagedMaxRows = 64;   // of a unit: one chain's 16 or 32, or both chains' 32
+constexpr int kPagedMaxRows = 64;   // of a unit
 constexpr float kPagedLag = 8.0f;
 constexpr float kPagedMost = 32768.0f;  // of an E4M3 weight, in units of 2^-11 (what its terms are taken from)
 constexpr float kPagedTermDown = 1.0f / 512.0f;  // an E4M3 term's unit over the one before
@@ -207,51 +206,56 @@ struct PagedWalk {
     }
 };
 
-template <int N, int STAGES>
+template <int N, int WAYS, int GROUPS, int STAGES>
 struct PagedSmem {
+    static constexpr int kChains = WAYS * GROUPS, kRows = N * GROUPS;
     uint64_t kv_full[STAGES], kv_empty[STAGES];
-    uint64_t q_full, q_taken, s_full[2], s_free[2], p_full[2], o_done[2], drained[2];
+    uint64_t q_full, q_taken, s_full[WAYS], s_free[WAYS], p_full[WAYS], o_done[WAYS], drained[WAYS];
     int page_ok[STAGES];
     PagedScan scan;
     uint32_t tmem;
     int abort_flag;
-    int64_t q_at[2 * N];             // the unit's rows: where their queries lie, from the request's and head's on,
-    int at[2 * N], hidden[2 * N];    // their places among [query rows, query heads], the last tokens they do not see
-    int sees[2 * N];                 // and those they do, of the request at hand
-    alignas(16) float coef[2 * N];   // E4M3: the score scale and the query row's power of two, undone
-    alignas(16) float nref[2][N];    // a chain's rows: the reference (log2 units), negative
-    alignas(16) float unit[2][N];    // E4M3: what weights x V scale are multiplied by
-    alignas(16) float fac[2][N];     // what a moved reference multiplies a row's O by,
-    alignas(16) float lfac[2][N];    // and its sum
-    float vtop[2][N];                // E4M3: the row's largest weight x V scale at its reference
-    int wmax[2][4][N];               // the warps' maxima, in an order of integers
-    float wsum[2][4][N];
-    float share[2][2 * N];           // what a chain's part of a row is multiplied by at the end
+    int64_t q_at[kRows];             // the unit's rows: where their queries lie, from the request's and head's on,
+    int at[kRows], hidden[kRows];    // their places among [query rows, query heads], the last tokens they do not see
+    int sees[kRows];                 // and those they do, of the request at hand
+    alignas(16) float coef[kRows];   // E4M3: the score scale and the query row's power of two, undone
+    alignas(16) float nref[kChains][N];    // a chain's rows: the reference (log2 units), negative
+    alignas(16) float unit[kChains][N];    // E4M3: what weights x V scale are multiplied by
+    alignas(16) float fac[kChains][N];     // what a moved reference multiplies a row's O by,
+    alignas(16) float lfac[kChains][N];    // and its sum
+    float vtop[kChains][N];                // E4M3: the row's largest weight x V scale at its reference
+    int wmax[kChains][4][N];               // the warps' maxima, in an order of integers
+    float wsum[kChains][4][N];
+    float share[WAYS][kRows];        // what a way's part of a row is multiplied by at the end
 };
 
 // Shared memory: query rows, the chains' weights, as many tiles of K and V as there is room for, their scales.
-template <class F, int N, int WAYS>
+template <class F, int N, int WAYS, int GROUPS>
 struct PagedLayout {
-    static constexpr int kRows = WAYS == 2 ? N : 2 * N;                  // of a unit
+    static constexpr int kChains = WAYS * GROUPS;
+    static constexpr int kThreads = kChains * 128 + 32 + WAYS * 32;      // softmax warpgroups, a TMA warp, MMA warps
+    static constexpr int kRows = N * GROUPS;                             // of a unit
     static constexpr int kQBytes = kRows * kDim * 2;                     // (E4M3: two terms of a byte)
     static constexpr int kPBytes = F::kPTerms * N * kPage * (F::kFp8 ? 1 : 2);  // of a chain
-    static constexpr int kKv = kQBytes + 2 * kPBytes;                    // 1024-byte aligned
-    static constexpr int kRoom = 232448 - 1024 - kKv - static_cast<int>(sizeof(PagedSmem<N, 12>));
+    static constexpr int kKv = kQBytes + kChains * kPBytes;                    // 1024-byte aligned
+    static constexpr int kRoom = 232448 - 1024 - kKv - static_cast<int>(sizeof(PagedSmem<N, WAYS, GROUPS, 12>));
     static constexpr int kStages = kRoom / (F::kTileBytes + F::kScaleBytes);
-    using Smem = PagedSmem<N, kStages>;
+    using Smem = PagedSmem<N, WAYS, GROUPS, kStages>;
     static constexpr int kScales = kKv + kStages * F::kTileBytes;
     static constexpr int kCtl = kScales + kStages * F::kScaleBytes;
     static constexpr size_t kBytes = 1024 + kCtl + sizeof(Smem);
-    static constexpr int kSCols = F::kQTerms * N, kOCols = F::kPTerms * N, kChainCols = kSCols + kOCols;
-    static constexpr uint32_t kTmem = 2 * kChainCols <= 64 ? 64 : 2 * kChainCols <= 128 ? 128 : 2 * kChainCols <= 256 ? 256 : 512;
-    // WAYS 2: a ring for each chain, so that a stage's phases, which a wait tells by their parity, are all one chain's
-    static constexpr int kDepth = WAYS == 2 ? kStages / 2 : kStages;
-    static __device__ __forceinline__ int stage(int chain, uint32_t tile)
+    static constexpr int kSCols = F::kQTerms * N, kOCols = F::kPTerms * N;  // of a chain
+    static constexpr int kWayCols = GROUPS * (kSCols + kOCols);
+    static constexpr int kCols = WAYS * kWayCols;
+    static constexpr uint32_t kTmem = kCols <= 64 ? 64 : kCols <= 128 ? 128 : kCols <= 256 ? 256 : 512;
+    // a ring for each way, so that a stage's phases, which a wait tells by their parity, are all one way's
+    static constexpr int kDepth = kStages / WAYS;
+    static __device__ __forceinline__ int stage(int way, uint32_t tile)
     {
-        return static_cast<int>(tile % kDepth) + (WAYS == 2 ? chain * kDepth : 0);
+        return static_cast<int>(tile % kDepth) + way * kDepth;
     }
     static __device__ __forceinline__ uint32_t phase(uint32_t tile) { return (tile / kDepth) & 1; }
-    static_assert(kKv % 1024 == 0 && kDepth >= 3 && kStages <= 12 && kBytes <= 232448 && 2 * kChainCols <= 512,
+    static_assert(kKv % 1024 == 0 && kDepth >= 3 && kStages <= 12 && kBytes <= 232448 && kCols <= 512,
                   "shared and tensor memory");
 };
 
@@ -385,13 +389,13 @@ __device__ __forceinline__ float lanes_sum(const float (&l)[N], int lane)
     return v[0];
 }
 
-// N: query rows of a chain (16 or 32).  WAYS 2: the chains have the same rows and take a unit's pages in turn; 1: each
-// has rows of its own and takes every page.
-template <class F, int N, int WAYS>
-__global__ void __launch_bounds__(kPagedThreads, 1) paged_attn_kernel(const __grid_constant__ PagedParams p)
+// A way is a line of pages: all of the unit's (WAYS 1), or every second (2).  One warp issues its products, for all rows of
+// the unit at once; GROUPS chains, a warpgroup each, take N of the rows (16 or 32) through the softmax.
+template <class F, int N, int WAYS, int GROUPS>
+__global__ void __launch_bounds__(PagedLayout<F, N, WAYS, GROUPS>::kThreads, 1) paged_attn_kernel(const __grid_constant__ PagedParams p)
 {
-    using L = PagedLayout<F, N, WAYS>;
-    constexpr int R = L::kRows;
+    using L = PagedLayout<F, N, WAYS, GROUPS>;
+    constexpr int R = L::kRows, C = L::kChains, kSoft = C * 128;  // threads of the softmax
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t *kv = smem + L::kKv;
@@ -402,36 +406,36 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attn_kernel(const __gr
     const int cta = blockIdx.x;
 
     griddep_launch_dependents();
-    if (tid == 8 * 32) {
+    if (tid == kSoft) {
         prefetch_tensormap(&p.kmap);
         prefetch_tensormap(&p.vmap);
         for (int s = 0; s < L::kStages; ++s) {
             mbar_init(smem_addr(&ctl->kv_full[s]), 1);
-            mbar_init(smem_addr(&ctl->kv_empty[s]), WAYS == 2 ? 5 : 10);  // a chain's product and four warps
+            mbar_init(smem_addr(&ctl->kv_empty[s]), 1 + 4 * GROUPS);  // a product and the chains' warps
         }
-        mbar_init(smem_addr(&ctl->q_full), 8);
-        mbar_init(smem_addr(&ctl->q_taken), 2);
-        for (int t = 0; t < 2; ++t) {
+        mbar_init(smem_addr(&ctl->q_full), 4 * C);
+        mbar_init(smem_addr(&ctl->q_taken), WAYS);
+        for (int t = 0; t < WAYS; ++t) {
             mbar_init(smem_addr(&ctl->s_full[t]), 1);
-            mbar_init(smem_addr(&ctl->s_free[t]), 4);
-            mbar_init(smem_addr(&ctl->p_full[t]), 4);
+            mbar_init(smem_addr(&ctl->s_free[t]), 4 * GROUPS);
+            mbar_init(smem_addr(&ctl->p_full[t]), 4 * GROUPS);
             mbar_init(smem_addr(&ctl->o_done[t]), 1);
             mbar_init(smem_addr(&ctl->drained[t]), 1);
         }
         ctl->abort_flag = 0;
         fence_barrier_init();
     }
-    if (warp == 9) {
+    if (warp == 4 * C + 1) {
         tmem_alloc(smem_addr(&ctl->tmem), L::kTmem);
         tmem_relinquish_alloc_permit();
     }
     tc_fence_before_sync();
     if (cta == 0)
-        for (int b = tid; b < p.batch; b += kPagedThreads)
+        for (int b = tid; b < p.batch; b += L::kThreads)
             if (p.seq_lens[b] != paged_len(p, b))
                 atomicOr(p.fault, MSA_FAULT_SEQ_LEN);
     int unused;
-    const PagedWork total = paged_find<kPagedThreads>(p, &ctl->scan, 0, unused, [&](const PagedWork &work) {
+    const PagedWork total = paged_find<L::kThreads>(p, &ctl->scan, 0, unused, [&](const PagedWork &work) {
         const PagedSplit s(work, p);
         return cta < s.ctas ? s.start(cta) : -1;
     });
@@ -442,10 +446,10 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attn_kernel(const __gr
     const int heads = p.kv_heads * p.group, unit_rows = p.q_len * p.group;
     PagedWalk walk(p, ctl->scan.at, count);
 
-    if (warp == 8) {
+    if (warp == 4 * C) {
         // ---- K and V tiles, page after page ----
         bool alive = true;
-        uint32_t tiles[2] = {0, 0};  // of the chains' rings
+        uint32_t tiles[2] = {0, 0};  // of the ways' rings
         uint32_t done = 0;
         for (; walk.left > 0 && alive; walk.next(p)) {
             const int n = walk.run(), h = walk.u % p.kv_heads;
@@ -463,14 +467,14 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attn_kernel(const __gr
                     }
                 }
                 const int page = __shfl_sync(0xffffffffu, pages, i & 31);
-                const int chain = WAYS == 2 ? done & 1 : 0;
+                const int way = WAYS == 2 ? done & 1 : 0;
                 for (int kvi = 0; kvi < 2; ++kvi) {
-                    const uint32_t tile = chain ? tiles[1]++ : tiles[0]++;
-                    const int s = L::stage(chain, tile);
+                    const uint32_t tile = way ? tiles[1]++ : tiles[0]++;
+                    const int s = L::stage(way, tile);
                     if (tile >= L::kDepth)
                         alive = attn_wait(&ctl->abort_flag, p.fault, smem_addr(&ctl->kv_empty[s]), L::phase(tile) ^ 1, p.withhold);
                     if (!alive) {
-                        chain ? --tiles[1] : --tiles[0];
+                        way ? --tiles[1] : --tiles[0];
                         break;
                     }
                     if (lane == 0 && !p.withhold) {
@@ -495,30 +499,30 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attn_kernel(const __gr
             }
         }
         // the copies in flight land before the CTA may end, also where another role gave up
-        for (int chain = 0; chain < WAYS && !p.withhold; ++chain)
-            for (uint32_t j = tiles[chain] >= L::kDepth ? tiles[chain] - L::kDepth : 0; j < tiles[chain]; ++j)
-                mbar_wait(smem_addr(&ctl->kv_full[L::stage(chain, j)]), L::phase(j));
-    } else if (warp >= 9) {
-        // ---- a chain's products ----
-        const int t = warp - 9;
+        for (int way = 0; way < WAYS && !p.withhold; ++way)
+            for (uint32_t j = tiles[way] >= L::kDepth ? tiles[way] - L::kDepth : 0; j < tiles[way]; ++j)
+                mbar_wait(smem_addr(&ctl->kv_full[L::stage(way, j)]), L::phase(j));
+    } else if (warp > 4 * C) {
+        // ---- a way's products ----
+        const int way = warp - 4 * C - 1;
         const uint32_t one = elect_one();
         constexpr uint32_t kTypes = (1u << 4) | (F::kFp8 ? 0u : (1u << 7) | (1u << 10)) | ((128u >> 4) << 24);
-        constexpr uint32_t idesc_s = kTypes | (static_cast<uint32_t>(L::kSCols >> 3) << 17);
-        constexpr uint32_t idesc_o = kTypes | (static_cast<uint32_t>(L::kOCols >> 3) << 17) | (1u << 15) | (1u << 16);  // both with their rows contiguous
+        constexpr uint32_t idesc_s = kTypes | (static_cast<uint32_t>(GROUPS * L::kSCols >> 3) << 17);
+        constexpr uint32_t idesc_o = kTypes | (static_cast<uint32_t>(GROUPS * L::kOCols >> 3) << 17) | (1u << 15) | (1u << 16);  // both with their rows contiguous
         constexpr int kSteps = F::kFp8 ? 4 : 8;
         constexpr uint32_t kPlainHi = (2048u >> 4) | (1u << 14);  // no swizzle: 16 bytes of rows x 128 tokens, 2 KiB to the next rows
-        const uint32_t d_s = tmem + t * L::kChainCols, d_o = d_s + L::kSCols;
+        const uint32_t d_s = tmem + way * L::kWayCols, d_o = d_s + GROUPS * L::kSCols;
         // query rows: bf16 in two halves of 64 dims, E4M3 in one, a chain's terms one after the other
-        const uint32_t q_desc = umma_desc_lo(smem_addr(smem) + (WAYS == 2 ? 0 : t * L::kSCols * 128));
-        const uint32_t p_desc = ((smem_addr(smem + L::kQBytes + t * L::kPBytes) >> 4) & 0x3FFFu) | ((128u >> 4) << 16);
+        const uint32_t q_desc = umma_desc_lo(smem_addr(smem));
+        const uint32_t p_desc = ((smem_addr(smem + L::kQBytes + way * GROUPS * L::kPBytes) >> 4) & 0x3FFFu) | ((128u >> 4) << 16);
         const uint32_t kv_addr = smem_addr(kv);
         auto wait = [&](uint64_t *bar, uint32_t parity) {
             return attn_wait(&ctl->abort_flag, p.fault, smem_addr(bar), parity, p.withhold);
         };
-        auto landed = [&](uint32_t tile) { return wait(&ctl->kv_full[L::stage(t, tile)], L::phase(tile)); };
+        auto landed = [&](uint32_t tile) { return wait(&ctl->kv_full[L::stage(way, tile)], L::phase(tile)); };
         auto test = [&](uint64_t *bar, uint32_t parity) { return __all_sync(0xffffffffu, mbar_test_wait(smem_addr(bar), parity)); };
         auto scores = [&](uint32_t tile) {
-            const int sk = L::stage(t, tile);
+            const int sk = L::stage(way, tile);
             const uint32_t a = umma_desc_lo(kv_addr + sk * F::kTileBytes);
 #pragma unroll
             for (int ks = 0; ks < kSteps; ++ks) {
@@ -526,7 +530,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attn_kernel(const __gr
                 const uint32_t boff = F::kFp8 ? ks * 32 : (ks >> 2) * (R * 128) + (ks & 3) * 32;
                 umma_small<F::kFp8>(one, d_s, a + (off >> 4), kUmmaDescHi, q_desc + (boff >> 4), kUmmaDescHi, idesc_s, ks > 0);
             }
-            umma_commit_one(one, smem_addr(&ctl->s_full[t]));
+            umma_commit_one(one, smem_addr(&ctl->s_full[way]));
             umma_commit_one(one, smem_addr(&ctl->kv_empty[sk]));
         };
         bool alive = true;
@@ -537,7 +541,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attn_kernel(const __gr
             if (one)
                 mbar_arrive(smem_addr(&ctl->q_taken));
             bool ahead = false;  // the page's scores have been asked for
-            for (int j = WAYS == 2 ? (t ^ done) & 1 : 0; j < n && alive; j += WAYS, ++it) {
+            for (int j = WAYS == 2 ? (way ^ done) & 1 : 0; j < n && alive; j += WAYS, ++it) {
                 if (!ahead) {
                     alive = landed(2 * it);
                     if (!alive)
@@ -548,37 +552,38 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attn_kernel(const __gr
                 ahead = false;
                 // the next page's scores as soon as its keys are there and this page's have been read, so that they run
                 // beside the softmax; its weights otherwise
-                for (uint32_t i = 0; j + WAYS < n && !ahead && i < kSpinLimit && !test(&ctl->p_full[t], it & 1) &&
+                for (uint32_t i = 0; j + WAYS < n && !ahead && i < kSpinLimit && !test(&ctl->p_full[way], it & 1) &&
                                      !*reinterpret_cast<volatile int *>(&ctl->abort_flag);
                      ++i)
-                    if (test(&ctl->s_free[t], it & 1) && test(&ctl->kv_full[L::stage(t, 2 * it + 2)], L::phase(2 * it + 2))) {
+                    if (test(&ctl->s_free[way], it & 1) && test(&ctl->kv_full[L::stage(way, 2 * it + 2)], L::phase(2 * it + 2))) {
                         tc_fence_after_sync();
                         scores(2 * it + 2);
                         ahead = true;
                     }
-                alive = landed(2 * it + 1) && wait(&ctl->p_full[t], it & 1);
+                alive = landed(2 * it + 1) && wait(&ctl->p_full[way], it & 1);
                 if (!alive)
                     break;
                 tc_fence_after_sync();
-                const int sv = L::stage(t, 2 * it + 1);
+                const int sv = L::stage(way, 2 * it + 1);
                 const uint32_t v = umma_desc_v_lo(kv_addr + sv * F::kTileBytes);
 #pragma unroll
                 for (int ks = 0; ks < kSteps; ++ks)
                     umma_small<F::kFp8>(one, d_o, v + ((ks * 1024 * (F::kFp8 ? 4 : 2)) >> 4), kUmmaDescHi,
                                         p_desc + ((ks * (F::kFp8 ? 512 : 256)) >> 4), kPlainHi, idesc_o, ks > 0 || j >= WAYS);
-                umma_commit_one(one, smem_addr(&ctl->o_done[t]));
+                umma_commit_one(one, smem_addr(&ctl->o_done[way]));
                 umma_commit_one(one, smem_addr(&ctl->kv_empty[sv]));
             }
             done += n;
         }
-        umma_commit_one(one, smem_addr(&ctl->drained[t]));  // nothing in flight when the tensor memory is freed
-        mbar_wait(smem_addr(&ctl->drained[t]), 0);
+        umma_commit_one(one, smem_addr(&ctl->drained[way]));  // nothing in flight when the tensor memory is freed
+        mbar_wait(smem_addr(&ctl->drained[way]), 0);
         __syncwarp();
     } else {
         // ---- softmax: a thread a token ----
-        const int t = warp >> 2, tau = tid & 127;
+        const int t = warp >> 2, tau = tid & 127, way = t / GROUPS, rows0 = t % GROUPS * N;
         const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // (32 * (warp % 4)) << 16
-        const uint32_t ts = tmem + t * L::kChainCols + lanes, to = ts + L::kSCols;
+        const uint32_t ts = tmem + way * L::kWayCols + t % GROUPS * L::kSCols + lanes;
+        const uint32_t to = tmem + way * L::kWayCols + GROUPS * L::kSCols + t % GROUPS * L::kOCols + lanes;
         uint8_t *pbuf = smem + L::kQBytes + t * L::kPBytes + tau * 16;
         auto wait = [&](uint64_t *bar, uint32_t parity) {
             return attn_wait(&ctl->abort_flag, p.fault, smem_addr(bar), parity, p.withhold);
@@ -588,10 +593,10 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attn_kernel(const __gr
             if (paged_len(p, b) > 0)
                 continue;
             const int64_t row0 = static_cast<int64_t>(b) * p.q_len * heads;
-            for (int i = tid; i < p.q_len * heads * (kDim / 8); i += 256)
+            for (int i = tid; i < p.q_len * heads * (kDim / 8); i += kSoft)
                 reinterpret_cast<uint4 *>(p.out + row0 * kDim)[i] = make_uint4(0u, 0u, 0u, 0u);
             if (p.lse)
-                for (int i = tid; i < p.q_len * heads; i += 256)
+                for (int i = tid; i < p.q_len * heads; i += kSoft)
                     p.lse[row0 + i] = -INFINITY;
         }
         // the rows of tile `row0` on: the same for every request and head
@@ -602,27 +607,27 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attn_kernel(const __gr
                 ctl->at[tid] = i * heads + g;
                 ctl->hidden[tid] = row0 + tid < unit_rows ? p.q_len - 1 - i : 0x3fffffff;
             }
-            barrier_sync(2, 256);
+            barrier_sync(2, kSoft);
         };
         if (p.row_tiles == 1)
             lay_rows(0);
         // The query rows of the unit at `w` on their way to registers, 16 lanes a row, and from there to shared memory; then the
         // chains' products may begin, beside what is left to do for the unit before.
-        auto load_rows = [&](const PagedWalk &w, uint4 (&v)[R / 16]) {
+        auto load_rows = [&](const PagedWalk &w, uint4 (&v)[R / (8 * C)]) {
             const int tile_at = w.u / p.kv_heads, h = w.u - tile_at * p.kv_heads;
             const int rows = min(p.tile_rows, unit_rows - tile_at * p.tile_rows);
             const uint16_t *q = p.q + static_cast<int64_t>(w.b) * p.q_len * p.q_stride + h * p.group * kDim;
 #pragma unroll
-            for (int i = 0; i < R / 16; ++i) {
-                const int r = (tid >> 4) + 16 * i;
+            for (int i = 0; i < R / (8 * C); ++i) {
+                const int r = (tid >> 4) + 8 * C * i;
                 v[i] = w.left > 0 && r < rows ? reinterpret_cast<const uint4 *>(q + ctl->q_at[r])[tid & 15] : make_uint4(0u, 0u, 0u, 0u);
             }
         };
-        auto put_rows = [&](const PagedWalk &w, const uint4 (&v)[R / 16]) {
+        auto put_rows = [&](const PagedWalk &w, const uint4 (&v)[R / (8 * C)]) {
             const int c = tid & 15;
 #pragma unroll
-            for (int i = 0; i < R / 16; ++i) {
-                const int r = (tid >> 4) + 16 * i;
+            for (int i = 0; i < R / (8 * C); ++i) {
+                const int r = (tid >> 4) + 8 * C * i;
                 if (!F::kFp8) {
                     *reinterpret_cast<uint4 *>(smem + (c >> 3) * (R * 128) + r * 128 + (((c ^ r) & 7) << 4)) = v[i];
                     continue;
@@ -669,7 +674,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attn_kernel(const __gr
         uint32_t it = 0, done = 0;
         int seg = 0;
         PagedWalk walk_next = walk;
-        uint4 q_next[R / 16];
+        uint4 q_next[R / (8 * C)];
         if (walk.left > 0) {
             if (p.row_tiles > 1)
                 lay_rows(walk.u / p.kv_heads * p.tile_rows);
@@ -683,31 +688,31 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attn_kernel(const __gr
             const bool whole = n == walk.P;
             const int64_t slot = static_cast<int64_t>(2 * cta + (seg > 0)) * p.tile_rows;
             const int64_t place0 = static_cast<int64_t>(walk.b) * p.q_len * heads + h * p.group;  // the first row's, ctl->at from there
-            const int begins = WAYS == 2 ? done & 1 : 0;  // the chain that has the run's first page
+            const int begins = WAYS == 2 ? done & 1 : 0;  // the way that has the run's first page
             walk_next = walk;
             walk_next.next(p);
             if (!dead) {
                 if (p.row_tiles == 1)
                     load_rows(walk_next, q_next);
-                barrier_sync(2, 256);  // the rows' numbers are all there
+                barrier_sync(2, kSoft);  // the rows' numbers are all there
             }
             uint64_t l2[N / 2];  // sums of the token's weights, two rows each
 #pragma unroll
             for (int r = 0; r < N / 2; ++r)
                 l2[r] = 0;
             bool bad = false, stop = false;
-            const int *sees = ctl->sees + (WAYS == 2 ? 0 : t * N);
-            const float *coef = ctl->coef + (WAYS == 2 ? 0 : t * N);
+            const int *sees = ctl->sees + rows0;
+            const float *coef = ctl->coef + rows0;
             const int open = len - (p.q_len - 1);  // tokens that every row sees
-            const int first = WAYS == 2 ? t ^ begins : 0;
+            const int first = WAYS == 2 ? way ^ begins : 0;
             for (int j = first; j < n && !dead; j += WAYS, ++it) {
                 const uint32_t tile = 2 * it;
-                const int sk = L::stage(t, tile), sv = L::stage(t, tile + 1);
+                const int sk = L::stage(way, tile), sv = L::stage(way, tile + 1);
                 const int base = (j0 + j) * kPage;
                 bad |= !wait(&ctl->kv_full[sk], L::phase(tile));
                 const int valid = ctl->page_ok[sk] ? min(kPage, len - base) : 0;  // tokens of the page that are data
                 const float ks = F::kFp8 ? scales[sk * kPage + tau] : 1.0f;
-                bad |= !wait(&ctl->s_full[t], it & 1);
+                bad |= !wait(&ctl->s_full[way], it & 1);
                 tc_fence_after_sync();
                 float s[N];  // the token's scores: E4M3 in log2 units, bf16 before the scale
                 {
@@ -722,7 +727,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attn_kernel(const __gr
                     tc_fence_before_sync();
                     __syncwarp();
                     if (lane == 0)
-                        mbar_arrive(smem_addr(&ctl->s_free[t]));
+                        mbar_arrive(smem_addr(&ctl->s_free[way]));
                     const uint64_t down = pack2(kPagedTermDown, kPagedTermDown), ks2 = pack2(ks, ks);
 #pragma unroll
                     for (int r = 0; r < N; r += 4) {
@@ -848,7 +853,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attn_kernel(const __gr
                         l2[r / 2] = mul2(l2[r / 2], pack2(f.x, f.y));
                     }
                     if (j >= WAYS) {  // what the pages before left in O
-                        bad |= !wait(&ctl->o_done[t], (it - 1) & 1);
+                        bad |= !wait(&ctl->o_done[way], (it - 1) & 1);
                         tc_fence_after_sync();
 #pragma unroll 1
                         for (int i = 0; i < L::kOCols; i += 16) {
@@ -868,7 +873,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attn_kernel(const __gr
                     break;
                 // (the product with the weights before has to be over)
                 if (it > 0)
-                    bad |= !wait(&ctl->o_done[t], (it - 1) & 1);
+                    bad |= !wait(&ctl->o_done[way], (it - 1) & 1);
                 if (!F::kFp8) {
 #pragma unroll
                     for (int r = 0; r < N; r += 8)
@@ -897,7 +902,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attn_kernel(const __gr
                 tc_fence_before_sync();
                 __syncwarp();
                 if (lane == 0) {
-                    mbar_arrive(smem_addr(&ctl->p_full[t]));
+                    mbar_arrive(smem_addr(&ctl->p_full[way]));
                     mbar_arrive(smem_addr(&ctl->kv_empty[sk]));
                     mbar_arrive(smem_addr(&ctl->kv_empty[sv]));
                 }
@@ -917,12 +922,12 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attn_kernel(const __gr
                     ctl->wsum[t][warp & 3][lane] = sum;
                 bad |= stop;
                 if (first < n && !bad)
-                    bad |= !wait(&ctl->o_done[t], (it - 1) & 1);
+                    bad |= !wait(&ctl->o_done[way], (it - 1) & 1);
                 bad |= !wait(&ctl->q_taken, seg & 1);  // (who issues the products has seen this unit's rows)
-                dead = barrier_any(2, 256, bad);
+                dead = barrier_any(2, kSoft, bad);
             }
             if (dead) {
-                for (int r = tid >> 5; r < rows; r += 8) {
+                for (int r = tid >> 5; r < rows; r += 4 * C) {
                     if (!whole) {
                         if (lane == 0)
                             p.part_lse[slot + r] = INFINITY;
@@ -941,28 +946,27 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attn_kernel(const __gr
                 put_rows(walk_next, q_next);
             float top = 0.0f, all = 0.0f;
             if (tid < R) {
-                float m[2], sum[2];
+                float m[WAYS], sum[WAYS], M = -INFINITY;
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    const bool mine = WAYS == 2 || c == tid / N;
-                    const float *x = &ctl->wsum[c][0][tid % N];
-                    m[c] = mine ? -ctl->nref[c][tid % N] : -INFINITY;
-                    sum[c] = mine ? (x[0] + x[N]) + (x[2 * N] + x[3 * N]) : 0.0f;
+                for (int c = 0; c < WAYS; ++c) {
+                    const int chain = c * GROUPS + tid / N;
+                    const float *x = &ctl->wsum[chain][0][tid % N];
+                    m[c] = -ctl->nref[chain][tid % N];
+                    sum[c] = (x[0] + x[N]) + (x[2 * N] + x[3 * N]);
+                    M = fmaxf(M, m[c]);
                 }
-                const float M = fmaxf(m[0], m[1]);
-                all = 0.0f;
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
+                for (int c = 0; c < WAYS; ++c) {
                     m[c] = sum[c] > 0.0f ? rescale(m[c], M) : 0.0f;
                     all += m[c] * sum[c];
                 }
 #pragma unroll
-                for (int c = 0; c < 2; ++c)  // 0: nothing, and what stands in O may be anything
+                for (int c = 0; c < WAYS; ++c)  // 0: nothing, and what stands in O may be anything
                     ctl->share[c][tid] =
-                        sum[c] > 0.0f ? __fdividef(m[c], all) * (F::kFp8 ? 2048.0f / ctl->unit[c][tid % N] : 1.0f) : 0.0f;
+                        sum[c] > 0.0f ? __fdividef(m[c], all) * (F::kFp8 ? 2048.0f / ctl->unit[c * GROUPS + tid / N][tid % N] : 1.0f) : 0.0f;
                 top = M;
             }
-            barrier_sync(2, 256);
+            barrier_sync(2, kSoft);
             tc_fence_after_sync();
             if (p.row_tiles == 1)
                 start_rows();
@@ -973,19 +977,17 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attn_kernel(const __gr
                 else if (p.lse)
                     p.lse[place0 + ctl->at[tid]] = e * kLn2;
             }
-            // a thread a dim: 8 rows at a time, both chains' shares of them; WAYS 2: the chains' warps take turns
-            for (int r0 = WAYS == 2 ? t * 8 : t * N; r0 < (WAYS == 2 ? N : t * N + N) && r0 < rows; r0 += WAYS * 8) {
+            // a thread a dim: the warpgroups take 8 rows at a time in turn, with all ways' shares of them
+            for (int r0 = t * 8; r0 < rows; r0 += C * 8) {
                 float acc[8];
 #pragma unroll
                 for (int k = 0; k < 8; ++k)
                     acc[k] = 0.0f;
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    if (WAYS == 1 && c != t)
+                for (int c = 0; c < WAYS; ++c) {
+                    if (WAYS == 2 && (c ^ begins) >= n)  // a way without a page
                         continue;
-                    if (WAYS == 2 && (c ^ begins) >= n)  // a chain without a page
-                        continue;
-                    const uint32_t from = tmem + c * L::kChainCols + L::kSCols + lanes + r0 % N;
+                    const uint32_t from = tmem + c * L::kWayCols + GROUPS * L::kSCols + r0 / N * L::kOCols + lanes + r0 % N;
                     uint32_t o[F::kPTerms][8];
 #pragma unroll
                     for (int k = 0; k < F::kPTerms; ++k)
@@ -1024,7 +1026,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attn_kernel(const __gr
             }
             tc_fence_before_sync();
             if (p.row_tiles > 1 && walk_next.left > 0) {  // tiles of rows: where they lie changes with the unit
-                barrier_sync(2, 256);
+                barrier_sync(2, kSoft);
                 lay_rows(walk_next.u / p.kv_heads * p.tile_rows);
                 load_rows(walk_next, q_next);
                 start_rows();
@@ -1034,7 +1036,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attn_kernel(const __gr
         tc_fence_before_sync();
     }
     __syncthreads();
-    if (warp == 9)
+    if (warp == 4 * C + 1)
         tmem_dealloc(tmem, L::kTmem);
 }
 
