@@ -12,9 +12,13 @@
 // instruction), where 2^y is 0: -inf times 0 would be NaN.  A warp's reference is the
 // largest logit of its first ones, and moves when one passes it by 2^8.
 //
-// What bounds it: the stream of logits.  Slices of a row come into a ring in shared memory
-// by bulk copies, so that a thread's registers hold one group of 16 logits and the loop is
-// short: 4.5 instructions a bf16 logit.
+// What bounds it: the stream of logits (1024 x 163840 fp32, 671 MB, one alternative: 117 us,
+// 5.7 TB/s; bf16 the instructions: 71 us, 4.7 TB/s).  Slices of a row come into a ring in
+// shared memory by bulk copies, so that a thread's registers hold one group of 16 logits and
+// the loop is short: 4.5 instructions a bf16 logit.  Where a CTA has one slice of a row, what
+// follows one after the other: 128 x 100003 bf16, 20 alternatives, take 15 us, of which the
+// stream is 4; first stage 2, the others 4, noted places 0.7, order in the CTA 1.2, clusters'
+// barrier and lists 1.2, what is left 1 and the launch.
 //
 // Alternatives.  16 logits a lane cost one comparison of their maximum with a bound that n
 // logits of the CTA are known to reach; where it passes, the lane's place is noted (a
@@ -433,7 +437,7 @@ __global__ void __launch_bounds__(kLpThreads + 32, kLpBlocks) logprobs_kernel(co
             auto vector = [&](int i) { return i < left ? ring[i] : make_uint4(none, none, none, none); };
             if (left > 0)
                 attn_wait(&sm.abort_flag, p.fault, smem_addr(&sm.full[s]), (it / kLpStages) & 1, 0);
-                if (keep > 0 && stage == update) {
+            if (keep > 0 && stage == update) {
                 update = 4 * stage + 2;
                 float top = run;
 #pragma unroll
@@ -736,8 +740,11 @@ extern "C" msa_status msa_token_logprobs(const void *logits, int logits_bf16, in
     p.top_n = top_n;
     p.keep = std::max(top_n, temperature && given > 0 ? 1 : 0);
     p.rows = rows;
+    // CTAs a row: as many as there is room for, two an SM for pairs, one an SM for larger clusters, which do not fit so densely.
+    // fp32, 5 alternatives, with 8 / 4 / 2 / 1 of them: 1 x 163840 9.2 / 10.9 / 15.0 / 21.4 us, 16 x 131072 9.9 / 10.7 / 14.2 /
+    // 19.1, 38 rows 18.3 / 11.7 / 14.3 / 19.2, 76 - / 23.5 / 16.4 / 20.3, 152 - / - / 21.6 / 21.8.
     int cluster = 8;
-    while (cluster > 1 && rows * cluster > 2 * sms)
+    while (cluster > 1 && rows * cluster > (cluster > 2 ? sms : 2 * sms))
         cluster /= 2;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     return logits_bf16 ? launch_logprobs<uint16_t>(p, cluster, sms, dev, st)

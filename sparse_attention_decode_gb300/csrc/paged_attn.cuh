@@ -9,11 +9,18 @@
 // workspace in fp32 and are joined, always in page order, by paged_join_kernel.
 //
 // Why tokens as rows: a tcgen05 product has 128 rows, a request's query rows are 1 to
-// 64, a page is 128 tokens.  S^T = K Q^T (128 tokens x N rows) and O^T = V^T P^T
-// (128 dims x N rows) fill the 128 rows with what there is, read K and V where TMA put
-// them, and cost one pass of the operand through shared memory each, whatever N is
-// (256 cycles of an SM's 2700 a bf16 page at the copy rate).  A thread has one token: the
-// scale of an E4M3 token is one number for all its weights.
+// 64, a page is 128 tokens.  S^T = K Q^T (128 tokens x rows) and O^T = V^T P^T
+// (128 dims x rows) fill the 128 rows with what there is, read K and V where TMA put
+// them, and cost one pass of the operand through shared memory each, however many query
+// rows there are: one product for all of them.  A thread has one token: the scale of an
+// E4M3 token is one number for all its weights.
+//
+// What bounds it: the stream of pages, where a unit has many and its rows are 16 to 32
+// (256 requests of 8000 to 8704 tokens, 4.4 GB: 627 us, 7.0 TB/s; E4M3, 32 of 30000 to
+// 32768: 162 us, 6.5 TB/s; 64 bf16 rows, 8 of 32768: 92.5 us, 5.8 TB/s).  On one E4M3
+// request of 131072 (30.6 us for a floor of 20.5) and below, what a unit costs once: its
+// rows, the first page's references, the epilogue, the join, one after the other.  With
+// 64 E4M3 rows the weights' arithmetic: 1.5 us a page for 0.8 of the stream.
 //
 // A row's maximum would be a reduction over the lanes for every page.  The reference m
 // of a row need not be the maximum: it is kept until a score passes it by more than
@@ -26,8 +33,10 @@
 // sum of two E4M3 numbers, the second 2^-9 on: exactly where it is within 2^-9 of the
 // row's largest (4 bits each), and to 2^-23 of that largest below.  A weight times its
 // token's V scale is the sum of three, after one rounding to f16 (11 bits), and held
-// relative to the row's largest such product so far: down to 2^-26 of it.  The terms
-// stand side by side as further rows of the product, so K and V still pass once.
+// relative to the row's largest such product so far: down to 2^-26 of it.  (Two terms would
+// hold a weight near the largest to bf16's 2^-8, but one 2^-10 of it to 2^-4, and a long
+// request can consist of such.)  The terms stand side by side as further rows of the
+// product, so K and V still pass once.
 #pragma once
 
 #include "attn_common.cuh"
@@ -87,8 +96,8 @@ struct PagedWork {
     int slots, units;
 };
 
-// The ranges: CTA g has [start(g), start(g + 1)) of the units' slots, two pages at least, one for each chain, but no fewer
-// ranges than units.
+// The ranges: CTA g has [start(g), start(g + 1)) of the units' slots, two pages at least, but no fewer ranges than units (at
+// least 1, 2, 4 pages: one request of 300 tokens, 4 heads, 8.9, 9.4, 8.1 us; 2000: 9.6, 9.8, 11.1; 8700: 10.7, 10.5, 11.8).
 struct PagedSplit {
     int ctas, range, more;
     __device__ PagedSplit(const PagedWork &work, const PagedParams &p)
