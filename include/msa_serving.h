@@ -42,7 +42,8 @@ extern "C" {
  * cu_seqlens_q[batch] are no tokens: their outputs are left as they were.
  *
  *   q, out_q     optional (both or neither): bf16 [total_rows, q_heads, 128], rows
- *                q_stride / out_q_stride elements apart; out_q may be q itself.
+ *                q_stride / out_q_stride elements apart; out_q may be q itself, in q's
+ *                strides, and else overlaps none of the inputs.
  *   k, v         bf16 [total_rows, kv_heads, 128], rows k_stride / v_stride apart.
  *                v and v_cache may be NULL together: a cache of keys alone, such as
  *                the index-K cache (kv_heads 1).
@@ -91,7 +92,9 @@ msa_status msa_cache_append_fp8(const void *q, int64_t q_stride, int q_heads, vo
 
 /*
  * Attention over all of a request's tokens: msa_attention_sparse's formula, out
- * and out_lse with every block of the request selected.
+ * and out_lse with every block of the request selected.  out does not overlap q.
+ * q_len <= 64; batch x KV heads x tiles of 64 rows of a head x (pages of
+ * max_model_len + 8) is at most 2^30.
  *
  *   workspace    at least msa_attention_paged_workspace_bytes(batch * q_len,
  *                kv_heads * group, kv_heads) bytes.
@@ -104,7 +107,13 @@ msa_status msa_attention_paged(const void *q, int64_t q_stride, const void *k, c
                                int q_len, int kv_heads, int group, int max_model_len, float scale, void *out,
                                float *out_lse, void *workspace, size_t workspace_bytes, void *stream);
 
-/* The same on an E4M3 cache with fp32 scales [num_pages, kv_heads, 128] (see msa_attention_sparse_fp8). */
+/*
+ * The same on an E4M3 cache with fp32 scales [num_pages, kv_heads, 128] (see
+ * msa_attention_sparse_fp8).  Both products run on the codes as they are, with
+ * fp32 accumulation: a query value is held exactly from 2^-9 of its row's largest
+ * on, and to 2^-23 of that below; a product of weight and V scale to 2^-8 of
+ * itself, or to 2^-21 of the largest such product of its row.
+ */
 msa_status msa_attention_paged_fp8(const void *q, int64_t q_stride, const void *k, const int64_t *k_strides,
                                    const float *k_scale, const void *v, const int64_t *v_strides,
                                    const float *v_scale, int64_t num_pages, const int32_t *block_table,

@@ -503,7 +503,8 @@ static msa_status append_entry(AppendParams &p, const int64_t *k_strides, const 
         (values && !cache_ok(p.v_cache, v_strides, p.num_pages, p.kv_heads, fp8)) || unaligned(p.q, 16) ||
         unaligned(p.out_q, 16) || unaligned(p.k, 16) || unaligned(p.v, 16) || unaligned(workspace, 256) ||
         p.k_stride % 8 || p.k_stride < kv || (values && (p.v_stride % 8 || p.v_stride < kv)) ||
-        (p.q && (p.q_stride % 8 || p.q_stride < qd || p.out_q_stride % 8 || p.out_q_stride < qd)))
+        (p.q && (p.q_stride % 8 || p.q_stride < qd || p.out_q_stride % 8 || p.out_q_stride < qd)) ||
+        (p.q && p.out_q == p.q && p.out_q_stride != p.q_stride))
         return MSA_ERR_INVALID_ARG;
     if (fp8 && (!p.k_scale || (values && !p.v_scale) || unaligned(p.k_scale, 16) || unaligned(p.v_scale, 16)))
         return MSA_ERR_INVALID_ARG;

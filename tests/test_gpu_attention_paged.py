@@ -233,6 +233,7 @@ def test_refusals():
         assert status(scale=bad) == msa.MSA_ERR_INVALID_ARG
     assert status(ws=ws[:128]) == msa.MSA_ERR_WORKSPACE_TOO_SMALL
     assert status(k=kp[:1].expand(kp.shape[0], -1, -1, -1)) == msa.MSA_ERR_INVALID_ARG
+    assert status(out=q) == msa.MSA_ERR_INVALID_ARG  # read after it is written
     for kw in (dict(q=q.half()), dict(k=kp[..., :64]), dict(k=kp.float()), dict(out=out[:, :4]), dict(seq=seq.long()),
                dict(k=kp[:2]), dict(ws=ws.cpu()), dict(q=q[:, :3])):
         assert status(**kw) == "refused", kw

@@ -376,6 +376,9 @@ def test_refusals():
     assert status(k=wide, v=wide) == 0
     off = z(4 * 128 * 2 + 4)[4:].view(2, 4, 128)[:, :2]
     assert status(k=off) == msa.MSA_ERR_INVALID_ARG  # not on 16 bytes
+    twice = z(4, 4, 128)  # the same first row, other strides
+    assert status(q=twice[:2], out_q=twice[::2]) == msa.MSA_ERR_INVALID_ARG
+    assert status(q=twice[::2], out_q=twice[::2]) == 0
     for kw in (dict(k=z(2, 2, 128, dtype=f32)), dict(k=z(2, 3, 128)), dict(v=None), dict(vc=None), dict(q=z(2, 4, 128)),
                dict(q=z(2, 4, 128), out_q=z(2, 5, 128)), dict(q_len=2), dict(positions=z(3, dtype=i32)),
                dict(inv_freq=z(32, dtype=torch.float64)), dict(k_weight=z(64, dtype=f32)), dict(seq=z(3, dtype=i32)),

@@ -277,3 +277,42 @@ def test_calls_on_an_empty_batch():
     msa.msa_cache_append(k, k, kv, kv, table, seq, ws, cu_seqlens_q=cu)
     torch.cuda.synchronize()
     assert msa.msa_indexer_get_error(ws) == 0 and not bool(kv.any())
+
+
+@pytest.mark.gpu
+def test_the_example_s_new_stages():
+    """Appended tokens, attention over all pages and the answer's log probabilities of the example's step."""
+    import os
+    import sys
+    sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))
+    import serve_step as ex
+    lens, q_len, H, Hq = [700, 130, 2900], ex.DRAFTS + 1, ex.KV_HEADS, ex.KV_HEADS * ex.GROUP
+    s = ex.make_step(lens, prompt=300, vocab=500, seed=4)
+    before = {n: s[n].cpu() for n in ("k", "v", "index_k", "table", "qkv", "index_qk", "inv_freq", "positions", "logits")}
+    r = ex.step(s, budget=100)
+    assert r["faults"] == 0
+    w = dict(lens=lens, owner=[b for b in range(3) for _ in range(q_len)], token=[n - q_len + i for n in lens for i in range(q_len)],
+             positions=before["positions"], inv=before["inv_freq"], inter=False, qw=torch.ones(D), kw=torch.ones(D),
+             table=before["table"], ks=None, vs=None, q_len=q_len, scale=D ** -0.5)
+    assert before["positions"].tolist() == w["token"]
+
+    def rows(x, Hq, H, kp, vp, got):  # (the norm's eps is the default here, of the formula's 10^-5 elsewhere)
+        for part, at, want in ((x[:, :Hq], None, got["q"]), (x[:, Hq:Hq + H], kp, got["kp"]), (x[:, Hq + H:], vp, got["vp"])):
+            if want is None:
+                continue
+            values = at is vp and at is not None
+            y, tol = append.plain(part, None if values else torch.ones(D), 1e-6, before["positions"], None if values else w["inv"],
+                                  False)
+            z = want if at is None else torch.stack([want[int(before["table"][b, t // PAGE]), t % PAGE]
+                                                     for b, t in zip(w["owner"], w["token"])])
+            assert bool(((z.double() - y).abs() <= tol + 2.0 ** -8 * y.abs()).all())
+    got = dict(q=s["q"].cpu(), kp=s["k"].cpu(), vp=s["v"].cpu())
+    rows(before["qkv"], Hq, H, before["k"], before["v"], got)
+    rows(before["index_qk"], 4, 1, before["index_k"].unsqueeze(2), None,
+         dict(q=s["index_q"].cpu(), kp=s["index_k"].cpu().unsqueeze(2), vp=None))
+    ref.check(r["every"], paged.plain(dict(w, q=got["q"], kp=got["kp"], vp=got["vp"]))[0], "every")
+    tokens = r["tokens"].view(-1, 1).cpu()
+    want = logprobs.plain(before["logits"].view(len(tokens), -1), tokens, None, 5)
+    assert logprobs.near(r["again"], want[0], want[4]) and logprobs.near(r["entropy"], want[1], want[5])
+    assert torch.equal(r["top_ids"].cpu(), want[2]) and logprobs.near(r["top"], want[3], want[4])
+    assert bool(((r["again"].view_as(r["logp"]) - r["logp"]).abs() <= 2 ** -15 * (1 + r["logp"].abs())).all())

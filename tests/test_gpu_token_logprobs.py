@@ -198,6 +198,17 @@ def test_rows_of_many_stages(shape, dtype):
     assert verify(msa, x, tokens, temp, 20) == 0
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["fp32", "bf16"])
+def test_rows_past_4_gib(dtype):
+    """Rows whose distance, in elements, 32 bits do not hold."""
+    import sparse_attention_decode_gb300 as msa
+    V, apart = 5001, 2 ** 32 // 2 + 3
+    far = torch.empty(2 * apart + V, dtype=dtype, device="cuda").as_strided((3, V), (apart, 1))
+    far.copy_(torch.randn(3, V, generator=torch.Generator().manual_seed(39)) * 3)
+    tokens = torch.tensor([[0, 5000], [17, 4], [2500, 1]], dtype=torch.int32)
+    assert verify(msa, far, tokens, None, 9) == 0
+
+
 def test_tokens_outside_the_vocabulary_are_reported():
     import sparse_attention_decode_gb300 as msa
     x = torch.zeros(2, 100, device="cuda")
