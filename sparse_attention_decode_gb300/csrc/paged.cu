@@ -84,15 +84,15 @@ static msa_status paged_entry(const void *q, int64_t q_stride, const void *k, co
         !cache_ok(v, v_strides, num_pages, kv_heads, fp8) || unaligned(q, 16) || q_stride % 8 ||
         q_stride < static_cast<int64_t>(kv_heads) * group * kDim || unaligned(out, 16) || unaligned(workspace, 256))
         return MSA_ERR_INVALID_ARG;
+    if (fp8 && (!k_scale || !v_scale || unaligned(k_scale, 16) || unaligned(v_scale, 16)))
+        return MSA_ERR_INVALID_ARG;
+    if (workspace_bytes < paged_workspace(static_cast<int64_t>(batch) * q_len, group))
+        return MSA_ERR_WORKSPACE_TOO_SMALL;
     // a unit's rows are read by every CTA that has pages of it, at any time
     const int64_t width = static_cast<int64_t>(kv_heads) * group * kDim, q_rows = static_cast<int64_t>(batch) * q_len;
     const uint16_t *q_at = static_cast<const uint16_t *>(q), *out_at = static_cast<const uint16_t *>(out);
     if (q_at < out_at + q_rows * width && out_at < q_at + (q_rows - 1) * q_stride + width)
         return MSA_ERR_INVALID_ARG;
-    if (fp8 && (!k_scale || !v_scale || unaligned(k_scale, 16) || unaligned(v_scale, 16)))
-        return MSA_ERR_INVALID_ARG;
-    if (workspace_bytes < paged_workspace(static_cast<int64_t>(batch) * q_len, group))
-        return MSA_ERR_WORKSPACE_TOO_SMALL;
     PagedParams p;
     std::memset(&p, 0, sizeof p);
     p.tile_rows = paged_tile_rows(static_cast<int64_t>(q_len) * group);
