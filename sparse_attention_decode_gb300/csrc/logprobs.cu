@@ -17,8 +17,8 @@
 // shared memory by bulk copies, so that a thread's registers hold one group of 16 logits and
 // the loop is short: 4.5 instructions a bf16 logit.  Where a CTA has one slice of a row, what
 // follows one after the other: 128 x 100003 bf16, 20 alternatives, take 15 us, of which the
-// stream is 4; first stage 2, the others 4, noted places 0.7, order in the CTA 1.2, clusters'
-// barrier and lists 1.2, what is left 1 and the launch.
+// stream is 4; first stage and bound 2, the others 6, noted places 0.7, order and sums in the
+// CTA 1.9, clusters' barrier and lists 1.2, what is left 1.
 //
 // Alternatives.  16 logits a lane cost one comparison of their maximum with a bound that n
 // logits of the CTA are known to reach; where it passes, the lane's place is noted (a

@@ -296,7 +296,7 @@ def test_the_example_s_new_stages():
              table=before["table"], ks=None, vs=None, q_len=q_len, scale=D ** -0.5)
     assert before["positions"].tolist() == w["token"]
 
-    def rows(x, Hq, H, kp, vp, got):  # (the norm's eps is the default here, of the formula's 10^-5 elsewhere)
+    def rows(x, Hq, H, kp, vp, got):
         for part, at, want in ((x[:, :Hq], None, got["q"]), (x[:, Hq:Hq + H], kp, got["kp"]), (x[:, Hq + H:], vp, got["vp"])):
             if want is None:
                 continue
