@@ -539,8 +539,11 @@ __global__ void __launch_bounds__(kLpThreads + 32, kLpBlocks) logprobs_kernel(co
             const int v = lane < x.head ? lane : tail + lane - x.head;
             const float l = lane < x.head || v < V ? Logits<T>::one(x.row + v) : -INFINITY;
             part.join(LogSum{l, l > -INFINITY ? 1.0f : 0.0f, 0.0f}, c);
-            if (keep > 0)
+            if (keep > 0) {
                 cand.push(buffer, l > -INFINITY ? logit_key(l, v) : 0, lane);
+                if (cand.fill >= 32)  // (the next push has room for 32)
+                    cand = merge_candidates(cand, buffer, sm.list[warp], keep, lane);
+            }
         }
         part = lanes_join(part, c);
         if (noted > 0)

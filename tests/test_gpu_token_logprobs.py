@@ -198,6 +198,19 @@ def test_rows_of_many_stages(shape, dtype):
     assert verify(msa, x, tokens, temp, 20) == 0
 
 
+@pytest.mark.parametrize("R", [1, 45, 90, 400])
+def test_rising_rows_with_elements_behind_the_last_vector(R):
+    """Candidates that wait when a row's last elements join them: more than one warp's buffer would hold at once."""
+    import sparse_attention_decode_gb300 as msa
+    V = 120011
+    x = torch.linspace(-20, 20, V, device="cuda").to(torch.bfloat16).expand(R, V).contiguous()  # long runs of equal logits
+    first = int((x[0] == x[0, -1]).nonzero()[0])
+    want = torch.arange(first, first + 20, dtype=torch.int32).expand(R, 20)
+    tokens = torch.zeros(R, 1, dtype=torch.int32)
+    for _ in range(30):
+        assert torch.equal(call(msa, x, tokens, None, 20)[2].cpu(), want)
+
+
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["fp32", "bf16"])
 def test_rows_past_4_gib(dtype):
     """Rows whose distance, in elements, 32 bits do not hold."""
