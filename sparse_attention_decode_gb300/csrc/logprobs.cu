@@ -13,7 +13,7 @@
 // largest logit of its first ones, and moves when one passes it by 2^8.
 //
 // What bounds it: the stream of logits (1024 x 163840 fp32, 671 MB, one alternative: 117 us,
-// 5.7 TB/s; bf16 the instructions: 71 us, 4.7 TB/s).  Slices of a row come into a ring in
+// 5.7 TB/s; bf16 the instructions: 81 us, 69 without one).  Slices of a row come into a ring in
 // shared memory by bulk copies, so that a thread's registers hold one group of 16 logits and
 // the loop is short: 4.5 instructions a bf16 logit.  Where a CTA has one slice of a row, what
 // follows one after the other: 128 x 100003 bf16, 20 alternatives, take 15 us, of which the
