@@ -233,7 +233,7 @@ struct PagedSmem {
     alignas(16) float fac[kChains][N];     // what a moved reference multiplies a row's O by,
     alignas(16) float lfac[kChains][N];    // and its sum
     float vtop[kChains][N];                // E4M3: the row's largest weight x V scale at its reference
-    int wmax[kChains][4][N];               // the warps' maxima, in an order of integers
+    int wmax[kChains][4][N], omax[kChains][4][N];  // the warps' largest scores and products, in an order of integers
     float wsum[kChains][4][N];
     float share[WAYS][kRows];        // what a way's part of a row is multiplied by at the end
 };
@@ -814,48 +814,43 @@ __global__ void __launch_bounds__(PagedLayout<F, N, WAYS, GROUPS>::kThreads, 1) 
                     moves = barrier_any(3 + t, 128, top > kPagedLag || most > kPagedMost || bad);
                 }
                 if (moves) {
+                    // new references: the largest scores; E4M3: and the largest weight x V scale, in log2
+                    const float vs_log2 = F::kFp8 ? log2f(vs) : 0.0f;
+#pragma unroll
+                    for (int r = 0; r < N; ++r) {
+                        const float x = s[r] * to_log2;
+                        const int m = __reduce_max_sync(0xffffffffu, float_int(x));
+                        const int o = F::kFp8 ? __reduce_max_sync(0xffffffffu, float_int(x + vs_log2)) : 0;
+                        if (lane == r) {
+                            ctl->wmax[t][warp & 3][r] = m;
+                            if (F::kFp8)
+                                ctl->omax[t][warp & 3][r] = o;
+                        }
+                    }
                     stop = barrier_any(3 + t, 128, bad);  // (what one warp saw alone is no reason to leave the others)
                     if (stop)
                         break;
-                    // new references: the largest scores
-#pragma unroll
-                    for (int r = 0; r < N; ++r) {
-                        const int m = __reduce_max_sync(0xffffffffu, float_int(s[r] * to_log2));
-                        if (lane == r)
-                            ctl->wmax[t][warp & 3][r] = m;
-                    }
-                    barrier_sync(3 + t, 128);
                     if (tau < N) {
                         const float old = -ctl->nref[t][tau];
                         const float m = fmaxf(old, int_float(max(max(ctl->wmax[t][0][tau], ctl->wmax[t][1][tau]),
                                                                  max(ctl->wmax[t][2][tau], ctl->wmax[t][3][tau]))));
+                        const float lfac = rescale(old, m);
                         ctl->nref[t][tau] = -m;
-                        ctl->lfac[t][tau] = ctl->fac[t][tau] = rescale(old, m);
-                    }
-                    barrier_sync(3 + t, 128);
-                    if (F::kFp8) {
-                        // and the weights' units, by the largest weight x V scale
-#pragma unroll
-                        for (int r = 0; r < N; ++r) {
-                            const float x = s[r] == -INFINITY ? 0.0f : exp2_approx(s[r] + ctl->nref[t][r]) * vs;
-                            const int q = __reduce_max_sync(0xffffffffu, __float_as_int(x));
-                            if (lane == r)
-                                ctl->wmax[t][warp & 3][r] = q;
-                        }
-                        barrier_sync(3 + t, 128);
-                        if (tau < N) {
-                            const float before = ctl->vtop[t][tau] * ctl->lfac[t][tau], unit = ctl->unit[t][tau];
-                            const float most_now = fmaxf(before, __int_as_float(max(max(ctl->wmax[t][0][tau], ctl->wmax[t][1][tau]),
-                                                                                    max(ctl->wmax[t][2][tau], ctl->wmax[t][3][tau]))));
+                        ctl->lfac[t][tau] = ctl->fac[t][tau] = lfac;
+                        if (F::kFp8) {
+                            const float o = int_float(max(max(ctl->omax[t][0][tau], ctl->omax[t][1][tau]),
+                                                          max(ctl->omax[t][2][tau], ctl->omax[t][3][tau])));
+                            const float before = ctl->vtop[t][tau] * lfac, unit = ctl->unit[t][tau];
+                            const float most_now = fmaxf(before, o == -INFINITY ? 0.0f : exp2_approx(o - m));
                             // the power of two that brings it to [2^9, 2^10): room for 2^5 of growth until the next time
                             const int e = static_cast<int>(__float_as_uint(most_now) >> 23);
                             const float to_unit = most_now > 0.0f ? __int_as_float(max(10, min(244, 263 - e)) << 23) : 1.0f;
                             ctl->vtop[t][tau] = most_now;
                             ctl->unit[t][tau] = to_unit;
-                            ctl->fac[t][tau] = before > 0.0f ? ctl->lfac[t][tau] * to_unit * (1.0f / unit) : 0.0f;
+                            ctl->fac[t][tau] = before > 0.0f ? lfac * to_unit * (1.0f / unit) : 0.0f;
                         }
-                        barrier_sync(3 + t, 128);
                     }
+                    barrier_sync(3 + t, 128);
 #pragma unroll
                     for (int r = 0; r < N; r += 2) {
                         const float2 f = *reinterpret_cast<const float2 *>(&ctl->lfac[t][r]);
