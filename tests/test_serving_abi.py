@@ -85,6 +85,28 @@ def test_null_pointers_and_bad_sizes_are_refused_before_any_gpu_work(lib):
     assert logprobs(bytes=9) == 3 and logprobs(rows=0) == 0 and logprobs(rows=0, logits=None, ws=None) == 0
 
 
+def test_overlaps_and_sizes_past_32_bits_are_refused(lib):
+    from sparse_attention_decode_gb300 import _attention as A, _serving  # noqa: F401
+    if torch.cuda.is_available():
+        pytest.skip("host-only check: never hand placeholder pointers to a process with a GPU")
+    at = lambda n: ctypes.c_void_p((1 << 20) + n)  # noqa: E731
+    st = A._Strides(4 * 128 * 128, 128, 128 * 128)
+
+    def paged(**kw):
+        a = dict(q=at(0), qs=512, k=at(0), ks=st, v=at(0), vs=st, pages=10, table=at(0), stride=8, seq=at(0), batch=4, q_len=1,
+                 heads=4, group=1, limit=1024, scale=1.0, out=at(1 << 16), lse=None, ws=at(0), bytes=1 << 40, stream=None)
+        a.update(kw)
+        return A._fn("msa_attention_paged")(*a.values())
+
+    assert paged() == 4  # past every check: there is no GPU here
+    for n in (0, 16, 4096 - 16):  # four rows of 1024 bytes
+        assert paged(out=at(n)) == 1 and paged(q=at(n), out=at(0)) == 1, n
+    assert paged(out=at(4096)) == 4 and paged(q=at(4096), out=at(0)) == 4
+    assert paged(qs=1024, out=at(4096)) == 1 and paged(qs=1024, out=at(7168)) == 4  # the last row ends at 7 KiB
+    big = dict(stride=1 << 24, limit=(1 << 31) - 1, out=at(1 << 40))
+    assert paged(**big, batch=8) == 4 and paged(**big, batch=17) == 2
+
+
 def test_paged_workspace_bytes(lib):
     import sparse_attention_decode_gb300 as msa
     n = msa.msa_attention_paged_workspace_bytes
