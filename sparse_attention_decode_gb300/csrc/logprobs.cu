@@ -12,11 +12,11 @@
 // instruction), where 2^y is 0: -inf times 0 would be NaN.  A warp's reference is the
 // largest logit of its first ones, and moves when one passes it by 2^8.
 //
-// What bounds it: the stream of logits (1024 x 163840 fp32, 671 MB, one alternative: 117 us,
-// 5.7 TB/s; bf16 the instructions: 81 us, 69 without one).  Slices of a row come into a ring in
+// What bounds it: the stream of logits (1024 x 163840 fp32, 671 MB, one alternative: 115 us,
+// 5.8 TB/s; bf16 the instructions, 0.6 of the issue slots: 82 us).  Slices of a row come into a ring in
 // shared memory by bulk copies, so that a thread's registers hold one group of 16 logits and
 // the loop is short: 4.5 instructions a bf16 logit.  Where a CTA has one slice of a row, what
-// follows one after the other: 128 x 100003 bf16, 20 alternatives, take 15 us, of which the
+// follows one after the other: 128 x 100003 bf16, 20 alternatives, take 14.7 us, of which the
 // stream is 4; first stage and bound 2, the others 6, noted places 0.7, order and sums in the
 // CTA 1.9, clusters' barrier and lists 1.2, what is left 1.
 //
@@ -27,7 +27,8 @@
 // that reach it become 64-bit keys that order equal logits by the lower token; a key's
 // place is the number of larger ones.  The bound comes from the lanes' running maxima,
 // which are logits of their own: the n-th of the warps' four largest each.  It is brought
-// up to date after stages 1, 3, 11, .., without a barrier: old numbers make a bound as well.
+// up to date after stages 1, 5, 13, 29, .., without a barrier: old numbers make a bound as
+// well.
 // (Where logits rise along a row, every place is noted for a while: 64 of them are then
 // read at once, and 32 keys at a time sorted and merged into a list of the warp's 32
 // largest, which raises the bound.)
@@ -63,7 +64,7 @@ constexpr int kLpThreads = 256;  // eight warps that sum; a ninth issues the cop
 constexpr int kLpWarps = kLpThreads / 32;
 constexpr int kLpGroup = 16;     // logits of a lane that share a comparison
 constexpr int kLpBlocks = 2;     // CTAs an SM: with 3, and 72 registers, the sums' loop spills (1024 x 163840 bf16 90 us, 71)
-constexpr int kLpStages = 6;
+constexpr int kLpStages = 5;     // 160 KB an SM under way; 6 leave less of L1 to the noted places (20 alternatives: 142 us, 135)
 constexpr int kLpVectors = 1024;  // of a stage: 16 KiB
 constexpr int kLpBuffer = 64;    // keys of a warp: 32 that wait, and one a lane
 constexpr int kLpNoted = 128;    // places of a warp: 64 that wait, and a stage's
@@ -438,7 +439,7 @@ __global__ void __launch_bounds__(kLpThreads + 32, kLpBlocks) logprobs_kernel(co
             if (left > 0)
                 attn_wait(&sm.abort_flag, p.fault, smem_addr(&sm.full[s]), (it / kLpStages) & 1, 0);
             if (keep > 0 && stage == update) {
-                update = 4 * stage + 2;
+                update = 2 * stage + 4;
                 float top = run;
 #pragma unroll
                 for (int u = 0; u < kLpVectors / kLpThreads; ++u)
@@ -450,9 +451,15 @@ __global__ void __launch_bounds__(kLpThreads + 32, kLpBlocks) logprobs_kernel(co
                 if (u0 * kLpThreads + warp * 32 >= left)
                     break;
                 uint4 q[H];
+                if (left >= kLpVectors) {
 #pragma unroll
-                for (int w = 0; w < H; ++w)
-                    q[w] = vector((u0 + w) * kLpThreads + tid);
+                    for (int w = 0; w < H; ++w)
+                        q[w] = ring[(u0 + w) * kLpThreads + tid];
+                } else {
+#pragma unroll
+                    for (int w = 0; w < H; ++w)
+                        q[w] = vector((u0 + w) * kLpThreads + tid);
+                }
                 float top = top_of<N>(q[0]);
 #pragma unroll
                 for (int w = 1; w < H; ++w)
@@ -464,8 +471,8 @@ __global__ void __launch_bounds__(kLpThreads + 32, kLpBlocks) logprobs_kernel(co
                     if (passes)
                         sm.noted[warp][noted + __popc(who & ((1u << lane) - 1u))] = v0 + u0 * kLpThreads + tid;
                     noted += __popc(who);
-                    const float m = float_from_order_bits(__reduce_max_sync(0xffffffffu, float_order_bits(fmaxf(top, -INFINITY))));
-                    if (m > moves) {
+                    if (__any_sync(0xffffffffu, top > moves)) {
+                        const float m = float_from_order_bits(__reduce_max_sync(0xffffffffu, float_order_bits(fmaxf(top, -INFINITY))));
                         part.move(m, c);
                         const float at = m * c;
                         far = !(fabsf(at) < 4096.0f && floor_at < 1e37f);
