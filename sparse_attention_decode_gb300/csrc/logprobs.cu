@@ -12,7 +12,7 @@
 // instruction), where 2^y is 0: -inf times 0 would be NaN.  A warp's reference is the
 // largest logit of its first ones, and moves when one passes it by 2^8.
 //
-// What bounds it: the stream of logits (1024 x 163840 fp32, 671 MB, one alternative: 115 us,
+// What bounds it: the stream of logits (1024 x 163840 fp32, 671 MB, one alternative: 116 us,
 // 5.8 TB/s; bf16 the instructions, 0.6 of the issue slots: 82 us).  Slices of a row come into a ring in
 // shared memory by bulk copies, so that a thread's registers hold one group of 16 logits and
 // the loop is short: 4.5 instructions a bf16 logit.  Where a CTA has one slice of a row, what
