@@ -194,6 +194,41 @@ def test_a_captured_call_follows_its_inputs(e4m3):
 
 
 @pytest.mark.parametrize("e4m3", [False, True], ids=["bf16", "e4m3"])
+def test_graphs_that_share_a_workspace(e4m3):
+    """Two calls one after the other in a graph, and two graphs in turn, all on one workspace."""
+    import sparse_attention_decode_gb300 as msa
+    sets = [make(51, [6000, 500], 1, 4, 16, "hnd", e4m3), make(52, [300] * 30, 4, 2, 16, "nhd", e4m3),
+            make(53, [20000], 2, 1, 16, "hnd", e4m3)]
+    ws = torch.zeros(msa.msa_attention_paged_workspace_bytes(120, 64, 1), dtype=torch.uint8, device="cuda")
+    runs = []
+    for w in sets:
+        kp, vp, ks, vs, table = (ref.to_cuda(w[n]) for n in ("kp", "vp", "ks", "vs", "table"))
+        q, seq = w["q"].cuda(), torch.tensor(w["lens"], dtype=torch.int32, device="cuda")
+        out = torch.zeros_like(q)
+        if e4m3:
+            args, call_of = (q, kp, ks, vp, vs, table, seq, out, ws), msa.msa_attention_paged_fp8
+        else:
+            args, call_of = (q, kp, vp, table, seq, out, ws), msa.msa_attention_paged
+        runs.append((lambda f=call_of, a=args, w=w: f(*a, scale=w["scale"], q_len=w["q_len"]), out, call(msa, w)[0]))
+    graphs = []
+    for which in ((0, 1), (2, 0)):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            for i in which:
+                runs[i][0]()
+        graphs.append((graph, which))
+    for _ in range(20):
+        for graph, which in graphs:
+            for _, out, _ in runs:
+                out.fill_(7.0)
+            graph.replay()
+            torch.cuda.synchronize()
+            for i in range(3):
+                assert torch.equal(runs[i][1], runs[i][2]) if i in which else bool((runs[i][1] == 7.0).all())
+    assert msa.msa_indexer_get_error(ws) == 0
+
+
+@pytest.mark.parametrize("e4m3", [False, True], ids=["bf16", "e4m3"])
 def test_bad_device_data_is_absent_and_reported(e4m3):
     import sparse_attention_decode_gb300 as msa
     w = make(48, [1000, 600, 400, 300], 2, 4, 16, "hnd", e4m3)
