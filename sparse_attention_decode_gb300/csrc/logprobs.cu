@@ -13,7 +13,7 @@
 // largest logit of its first ones, and moves when one passes it by 2^8.
 //
 // What bounds it: the stream of logits (1024 x 163840 fp32, 671 MB, one alternative: 116 us,
-// 5.8 TB/s; bf16 the instructions, 0.6 of the issue slots: 82 us).  Slices of a row come into a ring in
+// 5.8 TB/s; bf16 the instructions, 0.6 of the issue slots: 79 us).  Slices of a row come into a ring in
 // shared memory by bulk copies, so that a thread's registers hold one group of 16 logits and
 // the loop is short: 4.5 instructions a bf16 logit.  Where a CTA has one slice of a row, what
 // follows one after the other: 128 x 100003 bf16, 20 alternatives, take 14.7 us, of which the
@@ -297,15 +297,22 @@ __device__ __forceinline__ uint32_t bf16x2_max(uint32_t a, uint32_t b)
     return r;
 }
 
-// The largest of a vector's logits; NaN where all are.
-template <int N>
-__device__ __forceinline__ float top_of(const uint4 &x)
+// The largest of some vectors' logits; NaN where all are.
+template <int N, int H>
+__device__ __forceinline__ float top_of(const uint4 (&q)[H])
 {
     if (N == 8) {
-        const uint32_t m = bf16x2_max(bf16x2_max(x.x, x.y), bf16x2_max(x.z, x.w));
+        uint32_t m = bf16x2_max(bf16x2_max(q[0].x, q[0].y), bf16x2_max(q[0].z, q[0].w));
+#pragma unroll
+        for (int i = 1; i < H; ++i)
+            m = bf16x2_max(m, bf16x2_max(bf16x2_max(q[i].x, q[i].y), bf16x2_max(q[i].z, q[i].w)));
         return fmaxf(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u));
     }
-    return fmaxf(max3(__uint_as_float(x.x), __uint_as_float(x.y), __uint_as_float(x.z)), __uint_as_float(x.w));
+    float top = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < H; ++i)
+        top = max3(top, max3(__uint_as_float(q[i].x), __uint_as_float(q[i].y), __uint_as_float(q[i].z)), __uint_as_float(q[i].w));
+    return top;
 }
 
 __device__ __forceinline__ void sums_barrier() { asm volatile("bar.sync 1, %0;" ::"n"(kLpThreads) : "memory"); }
@@ -442,8 +449,10 @@ __global__ void __launch_bounds__(kLpThreads + 32, kLpBlocks) logprobs_kernel(co
                 update = 2 * stage + 4;
                 float top = run;
 #pragma unroll
-                for (int u = 0; u < kLpVectors / kLpThreads; ++u)
-                    top = fmaxf(top, top_of<N>(vector(u * kLpThreads + tid)));
+                for (int u = 0; u < kLpVectors / kLpThreads; ++u) {
+                    const uint4 q[1] = {vector(u * kLpThreads + tid)};
+                    top = fmaxf(top, top_of<N>(q));
+                }
                 raise(top, stage == 0);
             }
 #pragma unroll 1
@@ -460,10 +469,7 @@ __global__ void __launch_bounds__(kLpThreads + 32, kLpBlocks) logprobs_kernel(co
                     for (int w = 0; w < H; ++w)
                         q[w] = vector((u0 + w) * kLpThreads + tid);
                 }
-                float top = top_of<N>(q[0]);
-#pragma unroll
-                for (int w = 1; w < H; ++w)
-                    top = fmaxf(top, top_of<N>(q[w]));
+                const float top = top_of<N>(q);
                 run = fmaxf(run, top);
                 if (__any_sync(0xffffffffu, top >= fminf(cand.at_least, moves))) {
                     const bool passes = top >= cand.at_least && top > -INFINITY;
