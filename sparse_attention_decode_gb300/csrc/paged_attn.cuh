@@ -39,6 +39,8 @@
 // product, so K and V still pass once.
 #pragma once
 
+#include <type_traits>
+
 #include "attn_common.cuh"
 #include "host_util.cuh"
 #include "tcgen05.cuh"
@@ -64,6 +66,7 @@ constexpr int kPagedMaxGrid = 256;
 constexpr int kPagedMaxRows = 64;   // of a unit
 constexpr float kPagedLag = 8.0f;
 constexpr float kPagedMost = 32768.0f;  // of an E4M3 weight, in units of 2^-11 (what its terms are taken from)
+constexpr float kPagedWideScale = 1024.0f;  // of V: times a unit, 2^117 at most, one above this may pass fp32
 constexpr float kPagedTermDown = 1.0f / 512.0f;  // an E4M3 term's unit over the one before
 
 struct PagedParams {
@@ -778,8 +781,11 @@ __global__ void __launch_bounds__(PagedLayout<F, N, WAYS, GROUPS>::kThreads, 1) 
                 const uint64_t c2 = pack2(to_log2, to_log2), vs2 = pack2(vs, vs);
                 float w[N];
                 uint64_t ls2[N / 2];
-                float top = 0.0f, most = 0.0f;
-                auto weigh = [&] {
+                float top = 0.0f, most = F::kFp8 ? vs * (kPagedMost / kPagedWideScale) : 0.0f;
+                // At new references (`wide`) the weight comes before the scale, since scale x unit may pass fp32, and 0 times that
+                // is NaN: pages with a scale where it may, by what `most` starts from, always go there.  (In this order everywhere
+                // 64 rows spill: 32 requests of 31000 tokens 323 us for 317.)
+                auto weigh = [&](auto wide) {
 #pragma unroll
                     for (int r = 0; r < N; r += 4) {
                         float nr[4], un[4];
@@ -802,7 +808,8 @@ __global__ void __launch_bounds__(PagedLayout<F, N, WAYS, GROUPS>::kThreads, 1) 
                             w[k + 1] = exp2_approx(y);
                             ls2[k / 2] = pack2(w[k], w[k + 1]);
                             if (F::kFp8) {
-                                unpack2(mul2(ls2[k / 2], mul2(vs2, pack2(un[e], un[e + 1]))), w[k], w[k + 1]);
+                                const uint64_t un2 = pack2(un[e], un[e + 1]);
+                                unpack2(decltype(wide)::value ? mul2(mul2(ls2[k / 2], un2), vs2) : mul2(ls2[k / 2], mul2(vs2, un2)), w[k], w[k + 1]);
                                 most = max3(most, w[k], w[k + 1]);
                             }
                         }
@@ -810,7 +817,7 @@ __global__ void __launch_bounds__(PagedLayout<F, N, WAYS, GROUPS>::kThreads, 1) 
                 };
                 bool moves = j < WAYS;  // a unit's first page: no references yet
                 if (!moves) {
-                    weigh();
+                    weigh(std::false_type());
                     moves = barrier_any(3 + t, 128, top > kPagedLag || most > kPagedMost || bad);
                 }
                 if (moves) {
@@ -842,12 +849,14 @@ __global__ void __launch_bounds__(PagedLayout<F, N, WAYS, GROUPS>::kThreads, 1) 
                                                           max(ctl->omax[t][2][tau], ctl->omax[t][3][tau])));
                             const float before = ctl->vtop[t][tau] * lfac, unit = ctl->unit[t][tau];
                             const float most_now = fmaxf(before, o == -INFINITY ? 0.0f : exp2_approx(o - m));
-                            // the power of two that brings it to [2^9, 2^10): room for 2^5 of growth until the next time
+                            // the power of two that brings it to [2^9, 2^10): room for 2^5 of growth until the next time.  Where every
+                            // product so far is 0 the largest there is: the first one that is not passes kPagedMost, or is held in it.
                             const int e = static_cast<int>(__float_as_uint(most_now) >> 23);
-                            const float to_unit = most_now > 0.0f ? __int_as_float(max(10, min(244, 263 - e)) << 23) : 1.0f;
+                            const float to_unit = __int_as_float(max(10, min(244, 263 - e)) << 23);
                             ctl->vtop[t][tau] = most_now;
                             ctl->unit[t][tau] = to_unit;
-                            ctl->fac[t][tau] = before > 0.0f ? lfac * to_unit * (1.0f / unit) : 0.0f;
+                            // (4 at most: to_unit x before is below 2^10, unit x vtop from 2^9 on or unit the largest there is)
+                            ctl->fac[t][tau] = lfac * to_unit * (1.0f / unit);
                         }
                     }
                     barrier_sync(3 + t, 128);
@@ -871,7 +880,7 @@ __global__ void __launch_bounds__(PagedLayout<F, N, WAYS, GROUPS>::kThreads, 1) 
                         }
                         tmem_wait_st();
                     }
-                    weigh();
+                    weigh(std::true_type());
                 }
                 if (stop)
                     break;
