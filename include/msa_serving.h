@@ -110,8 +110,8 @@ msa_status msa_attention_paged(const void *q, int64_t q_stride, const void *k, c
 /*
  * The same on an E4M3 cache with fp32 scales [num_pages, kv_heads, 128] (see
  * msa_attention_sparse_fp8).  Both products run on the codes as they are, with
- * fp32 accumulation: a query value is held exactly from 2^-9 of its row's largest
- * on, and to 2^-23 of that below; a product of weight and V scale to 2^-8 of
+ * fp32 accumulation: a query value is held exactly from 2^-14 of its row's largest
+ * on, and to 2^-22 of that below; a product of weight and V scale to 2^-8 of
  * itself, or to 2^-21 of the largest such product of its row.
  */
 msa_status msa_attention_paged_fp8(const void *q, int64_t q_stride, const void *k, const int64_t *k_strides,

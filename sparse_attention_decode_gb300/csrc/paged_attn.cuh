@@ -29,9 +29,9 @@
 // O in tensor memory, follow only where somebody has passed it: once a unit as a rule.
 //
 // E4M3: the codes go into the products as they are (kind::f8f6f4), so the other operand
-// has to be E4M3 as well.  A query row, brought to [2^3, 2^4) by a power of two, is the
-// sum of two E4M3 numbers, the second 2^-9 on: exactly where it is within 2^-9 of the
-// row's largest (4 bits each), and to 2^-23 of that largest below.  A weight times its
+// has to be E4M3 as well.  A query row, its largest brought to [2^7, 2^8) by a power of two, is
+// the sum of two E4M3 numbers, the second 2^-5 on: exactly where it is within 2^-14 of the
+// row's largest (4 bits each), and to 2^-22 of that largest below.  A weight times its
 // token's V scale is the sum of three, after one rounding to f16 (11 bits), and held
 // relative to the row's largest such product so far: down to 2^-26 of it.  (Two terms would
 // hold a weight near the largest to bf16's 2^-8, but one 2^-10 of it to 2^-4, and a long
@@ -67,7 +67,6 @@ constexpr int kPagedMaxRows = 64;   // of a unit
 constexpr float kPagedLag = 8.0f;
 constexpr float kPagedMost = 32768.0f;  // of an E4M3 weight, in units of 2^-11 (what its terms are taken from)
 constexpr float kPagedWideScale = 1024.0f;  // of V: times a unit, 2^117 at most, one above this may pass fp32
-constexpr float kPagedTermDown = 1.0f / 512.0f;  // an E4M3 term's unit over the one before
 
 struct PagedParams {
     CUtensorMap kmap, vmap;
@@ -355,22 +354,51 @@ __device__ __forceinline__ int float_int(float x)
 }
 __device__ __forceinline__ float int_float(int i) { return __int_as_float(i ^ ((i >> 31) & 0x7fffffff)); }
 
-// x, y (at most 16, times 2^11) as sums of E4M3 numbers t[0] + t[1] / 2^9 + t[2] / 2^18, two codes each, after one rounding
-// to f16.  What a term leaves is exact in f16: half a unit in the last of 4 bits, 256 at most for the second term.  The third
-// can be asked for up to 2^12 where x passes 1, and ends at 448: 8 bits are left then, 11 below.
-template <int TERMS>
+// E4M3 terms: an f16 value times down(0) is the first; what that leaves, exact in f16, times down(1) the second, and so on.
+// back(i) takes term i out.
+// A query row, its largest in [2^14, 2^15): t[0] 2^7 + t[1] 2^2.  The first term's last bit of 4 leaves half of it, which is
+// 2^8 at most in the second.  Exact from 1 on, where the first term is normal; 2^-8 off below.
+struct QueryTerms {
+    static __device__ constexpr uint32_t down(int i)
+    {
+        constexpr uint32_t kDown[2] = {0x20002000u, 0x34003400u};  // 2^-7, 2^-2, two each
+        return kDown[i];
+    }
+    static __device__ constexpr uint32_t back(int i)
+    {
+        constexpr uint32_t kBack[2] = {0xd800d800u, 0xc400c400u};  // -2^7, -2^2
+        return kBack[i];
+    }
+    static constexpr float kStep = 1.0f / 32.0f;  // a term's unit over the one before
+};
+// A weight x V scale, its row's largest 2^9 to 2^10 when its unit was chosen: t[0] 2^11 + t[1] 2^2 + t[2] 2^-7.  The second is
+// 256 at most; the third can be asked for up to 2^12 where the value passes 2^11, and ends at 448: 8 bits are left then, 11 below.
+struct WeightTerms {
+    static __device__ constexpr uint32_t down(int i)
+    {
+        constexpr uint32_t kDown[3] = {0x10001000u, 0x34003400u, 0x58005800u};  // 2^-11, 2^-2, 2^7
+        return kDown[i];
+    }
+    static __device__ constexpr uint32_t back(int i)
+    {
+        constexpr uint32_t kBack[3] = {0xe800e800u, 0xc400c400u, 0xa000a000u};  // -2^11, -2^2, -2^-7
+        return kBack[i];
+    }
+    static constexpr float kStep = 1.0f / 512.0f;
+};
+
+// x, y as sums of E4M3 terms, two codes each, after one rounding to f16.
+template <class V, int TERMS>
 __device__ __forceinline__ void e4m3_terms(float x, float y, uint32_t (&t)[TERMS])
 {
     uint32_t left = f32x2_to_f16x2(x, y);
 #pragma unroll
     for (int i = 0; i < TERMS; ++i) {
-        constexpr uint32_t kDown[3] = {0x10001000u, 0x34003400u, 0x58005800u};  // 2^-11, 2^-2, 2^7, two each
-        constexpr uint32_t kBack[3] = {0xe800e800u, 0xc400c400u, 0xa000a000u};  // -2^11, -2^2, -2^-7
         uint16_t code;
-        asm("{\n  .reg .b32 a;\n  mul.f16x2 a, %1, %2;\n  cvt.rn.satfinite.e4m3x2.f16x2 %0, a;\n}\n" : "=h"(code) : "r"(left), "r"(kDown[i]));
+        asm("{\n  .reg .b32 a;\n  mul.f16x2 a, %1, %2;\n  cvt.rn.satfinite.e4m3x2.f16x2 %0, a;\n}\n" : "=h"(code) : "r"(left), "r"(V::down(i)));
         t[i] = code;
         if (i + 1 < TERMS)
-            asm("fma.rn.f16x2 %0, %1, %2, %0;" : "+r"(left) : "r"(e4m3x2_to_f16x2(code)), "r"(kBack[i]));
+            asm("fma.rn.f16x2 %0, %1, %2, %0;" : "+r"(left) : "r"(e4m3x2_to_f16x2(code)), "r"(V::back(i)));
     }
 }
 
@@ -658,7 +686,7 @@ __global__ void __launch_bounds__(PagedLayout<F, N, WAYS, GROUPS>::kThreads, 1) 
                 uint32_t term[4][F::kQTerms];
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
-                    e4m3_terms(bf16_lo(x[k]) * f, bf16_hi(x[k]) * f, term[k]);
+                    e4m3_terms<QueryTerms>(bf16_lo(x[k]) * f, bf16_hi(x[k]) * f, term[k]);
 #pragma unroll
                 for (int k = 0; k < F::kQTerms; ++k) {
                     const int at = (r / N) * L::kSCols + k * N + r % N;
@@ -666,7 +694,7 @@ __global__ void __launch_bounds__(PagedLayout<F, N, WAYS, GROUPS>::kThreads, 1) 
                         make_uint2(term[0][k] | term[1][k] << 16, term[2][k] | term[3][k] << 16);
                 }
                 if (c == 0)
-                    ctl->coef[r] = __int_as_float((e - 3) << 23) * p.scale_log2;  // (2^-11 is in the terms)
+                    ctl->coef[r] = __int_as_float((e - 7) << 23) * p.scale_log2;  // (2^-7 is in the terms)
             }
             if (tid < R)
                 ctl->sees[tid] = max(0, w.len - ctl->hidden[tid]);
@@ -740,7 +768,7 @@ __global__ void __launch_bounds__(PagedLayout<F, N, WAYS, GROUPS>::kThreads, 1) 
                     __syncwarp();
                     if (lane == 0)
                         mbar_arrive(smem_addr(&ctl->s_free[way]));
-                    const uint64_t down = pack2(kPagedTermDown, kPagedTermDown), ks2 = pack2(ks, ks);
+                    const uint64_t down = pack2(QueryTerms::kStep, QueryTerms::kStep), ks2 = pack2(ks, ks);
 #pragma unroll
                     for (int r = 0; r < N; r += 4) {
                         float cf[4];
@@ -900,8 +928,8 @@ __global__ void __launch_bounds__(PagedLayout<F, N, WAYS, GROUPS>::kThreads, 1) 
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             uint32_t a[F::kPTerms], b[F::kPTerms];
-                            e4m3_terms(w[r + 4 * i], w[r + 4 * i + 1], a);
-                            e4m3_terms(w[r + 4 * i + 2], w[r + 4 * i + 3], b);
+                            e4m3_terms<WeightTerms>(w[r + 4 * i], w[r + 4 * i + 1], a);
+                            e4m3_terms<WeightTerms>(w[r + 4 * i + 2], w[r + 4 * i + 3], b);
 #pragma unroll
                             for (int k = 0; k < F::kPTerms; ++k)
                                 c[k][i] = a[k] | b[k] << 16;
@@ -1017,8 +1045,8 @@ __global__ void __launch_bounds__(PagedLayout<F, N, WAYS, GROUPS>::kThreads, 1) 
                     for (int k = 0; k < 8; ++k) {
                         float x = __uint_as_float(o[0][k]);
                         if (F::kFp8)
-                            x += kPagedTermDown * (__uint_as_float(o[F::kPTerms / 2][k]) +
-                                                   kPagedTermDown * __uint_as_float(o[F::kPTerms - 1][k]));
+                            x += WeightTerms::kStep * (__uint_as_float(o[F::kPTerms / 2][k]) +
+                                                       WeightTerms::kStep * __uint_as_float(o[F::kPTerms - 1][k]));
                         const float share = ctl->share[c][r0 + k];
                         acc[k] += share != 0.0f ? share * x : 0.0f;
                     }
