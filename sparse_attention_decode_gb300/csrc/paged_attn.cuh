@@ -681,7 +681,7 @@ __global__ void __launch_bounds__(PagedLayout<F, N, WAYS, GROUPS>::kThreads, 1) 
                 for (int o = 8; o >= 1; o >>= 1)
                     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
                 // the power of two that brings it to [2^14, 2^15)
-                const int e = max(22, min(240, static_cast<int>(__float_as_uint(top) >> 23)));
+                const int e = max(14, min(254, static_cast<int>(__float_as_uint(top) >> 23)));
                 const float f = __int_as_float((268 - e) << 23);
                 uint32_t term[4][F::kQTerms];
 #pragma unroll

@@ -1,4 +1,4 @@
-"""E4M3 attention over all pages: query rows with values far apart, against 64 bits."""
+"""E4M3 attention over all pages: query rows with values far apart, and near the ends of bf16, against 64 bits."""
 
 import pytest
 import torch
@@ -72,3 +72,13 @@ def test_values_far_below_the_row_s_largest_are_exact(lens, q_len):
 def test_values_further_below_keep_2_to_minus_22_of_the_largest(k):
     import sparse_attention_decode_gb300 as msa
     verify(msa, make(72, [1, 1, 2, 1, 300], 1, outlier(k), quiet=True), 2.0 ** -22)
+
+
+@pytest.mark.parametrize("q_len", [1, 4])
+@pytest.mark.parametrize("power", [125, 120, 110, -90, -105, -109])
+def test_rows_near_the_ends_of_bf16(power, q_len):
+    """Queries of 2^power, keys the other way round: ordinary scores."""
+    import sparse_attention_decode_gb300 as msa
+    w = make(73, [300, 1000, 1], q_len, lambda q: q.clamp(-7.9, 7.9) * 2.0 ** (power - 1 if power == 125 else power))
+    w["ks"] = (w["ks"].double() * 2.0 ** -power).float()
+    verify(msa, w, 0.0)
