@@ -51,7 +51,7 @@ extern "C" {
  *                a row contiguous; values are finite, and below 2^60 where a norm
  *                squares them.
  *   q_weight, k_weight   optional fp32 [128]; NULL: no norm (of that tensor).
- *   eps          finite, >= 0.
+ *   eps          finite, >= 0.  (Where it is 0 a head of zeros stays one.)
  *   inv_freq     fp32 [rotary_dim / 2], finite (NULL where rotary_dim is 0).
  *   rotary_dim   0..128, a multiple of 16.
  *   positions    optional int32 [total_rows]: the rows' rotary positions, where they
