@@ -43,7 +43,8 @@ extern "C" {
  *
  *   q, out_q     optional (both or neither): bf16 [total_rows, q_heads, 128], rows
  *                q_stride / out_q_stride elements apart; out_q may be q itself, in q's
- *                strides, and else overlaps none of the inputs.
+ *                strides, and else overlaps none of the inputs (over rows of q, k or v:
+ *                MSA_ERR_INVALID_ARG; it may lie between them).
  *   k, v         bf16 [total_rows, kv_heads, 128], rows k_stride / v_stride apart.
  *                v and v_cache may be NULL together: a cache of keys alone, such as
  *                the index-K cache (kv_heads 1).
@@ -64,7 +65,8 @@ extern "C" {
  *                not within its request's is passed over.)  q_len is not used with it.
  *   workspace    at least 256 bytes (the fault word).
  *
- * A slot is written by one row: the pages that get new tokens are not shared.
+ * A slot is written by one row: the pages that get new tokens are not shared, and
+ * overlap neither the inputs nor out_q.
  */
 msa_status msa_cache_append(const void *q, int64_t q_stride, int q_heads, void *out_q, int64_t out_q_stride,
                             const void *k, int64_t k_stride, const void *v, int64_t v_stride, int kv_heads,

@@ -25,6 +25,7 @@
 #include "attn_ptx.cuh"
 #include "host_util.cuh"
 #include "layout.cuh"
+#include "overlap.h"
 
 #include "msa_serving.h"
 
@@ -537,6 +538,14 @@ static msa_status append_entry(AppendParams &p, const int64_t *k_strides, const 
         return MSA_ERR_INVALID_ARG;
     if (fp8 && (!p.k_scale || (values && !p.v_scale) || unaligned(p.k_scale, 16) || unaligned(p.v_scale, 16)))
         return MSA_ERR_INVALID_ARG;
+    // Heads are read by who writes them, so out_q may be q itself; any other overlap is a race between rows or heads.
+    const bool in_place = p.out_q == p.q;
+    auto rows_of = [&](const uint16_t *x, int64_t stride, int64_t width) { return RowSpan(x, stride * 2, width * 2, total_rows); };
+    auto over = [&](const uint16_t *x, int64_t stride, int64_t width) {
+        return p.q && x && rows_overlap(rows_of(p.out_q, p.out_q_stride, qd), rows_of(x, stride, width));
+    };
+    if (!in_place && (over(p.q, p.q_stride, qd) || over(p.k, p.k_stride, kv) || over(p.v, p.v_stride, kv)))
+        return MSA_ERR_INVALID_ARG;
     if (workspace_bytes < kHeaderBytes)
         return MSA_ERR_WORKSPACE_TOO_SMALL;
     int dev = 0;
@@ -545,6 +554,8 @@ static msa_status append_entry(AppendParams &p, const int64_t *k_strides, const 
     const int sms = device_sms(dev);
     if (sms <= 0)
         return MSA_ERR_CUDA;
+    if (in_place && (over(p.k, p.k_stride, kv) || over(p.v, p.v_stride, kv)))
+        return MSA_ERR_INVALID_ARG;
     for (int i = 0; i < 3; ++i) {
         p.kc_stride[i] = k_strides[i];
         p.vc_stride[i] = values ? v_strides[i] : 0;
