@@ -94,7 +94,8 @@ msa_status msa_cache_append_fp8(const void *q, int64_t q_stride, int q_heads, vo
 
 /*
  * Attention over all of a request's tokens: msa_attention_sparse's formula, out
- * and out_lse with every block of the request selected.  out does not overlap q.
+ * and out_lse with every block of the request selected.  out shares no memory with
+ * a row of q (MSA_ERR_INVALID_ARG).
  * q_len <= 64; batch x KV heads x tiles of 64 rows of a head x (pages of
  * max_model_len + 8) is at most 2^30.
  *

@@ -1,4 +1,5 @@
 // Attention over all of a request's tokens: argument checks and launches.
+#include "overlap.h"
 #include "paged_attn.cuh"
 
 namespace msa {
@@ -89,9 +90,8 @@ static msa_status paged_entry(const void *q, int64_t q_stride, const void *k, co
     if (workspace_bytes < paged_workspace(static_cast<int64_t>(batch) * q_len, group))
         return MSA_ERR_WORKSPACE_TOO_SMALL;
     // a unit's rows are read by every CTA that has pages of it, at any time
-    const int64_t width = static_cast<int64_t>(kv_heads) * group * kDim, q_rows = static_cast<int64_t>(batch) * q_len;
-    const uint16_t *q_at = static_cast<const uint16_t *>(q), *out_at = static_cast<const uint16_t *>(out);
-    if (q_at < out_at + q_rows * width && out_at < q_at + (q_rows - 1) * q_stride + width)
+    const int64_t width = static_cast<int64_t>(kv_heads) * group * kDim * 2, q_rows = static_cast<int64_t>(batch) * q_len;
+    if (rows_overlap(RowSpan(out, width, width, q_rows), RowSpan(q, q_stride * 2, width, q_rows)))
         return MSA_ERR_INVALID_ARG;
     PagedParams p;
     std::memset(&p, 0, sizeof p);

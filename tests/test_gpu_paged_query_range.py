@@ -82,3 +82,23 @@ def test_rows_near_the_ends_of_bf16(power, q_len):
     w = make(73, [300, 1000, 1], q_len, lambda q: q.clamp(-7.9, 7.9) * 2.0 ** (power - 1 if power == 125 else power))
     w["ks"] = (w["ks"].double() * 2.0 ** -power).float()
     verify(msa, w, 0.0)
+
+
+def test_output_between_two_query_rows():
+    import sparse_attention_decode_gb300 as msa
+    for e4m3 in (False, True):
+        w = paged.make(74, [700, 300], 1, 2, 16, "hnd", e4m3)
+        whole = paged.call(msa, w)
+        kp, vp, ks, vs = (ref.to_cuda(w[n]) for n in ("kp", "vp", "ks", "vs"))
+        room = torch.full((2, 4 * 32, D), 7.0, dtype=torch.bfloat16, device="cuda")
+        room[:, :32] = w["q"].cuda()
+        q, out = room[:, :32], room[0, 48:112].view(2, 32, D)
+        args = (w["table"].cuda(), torch.tensor(w["lens"], dtype=torch.int32, device="cuda"), out,
+                torch.zeros(msa.msa_attention_paged_workspace_bytes(2, 32, 2), dtype=torch.uint8, device="cuda"))
+        if e4m3:
+            msa.msa_attention_paged_fp8(q, kp, ks, vp, vs, *args, scale=w["scale"])
+        else:
+            msa.msa_attention_paged(q, kp, vp, *args, scale=w["scale"])
+        torch.cuda.synchronize()
+        assert torch.equal(out, whole[0]) and torch.equal(room[:, :32].cpu(), w["q"])
+        assert bool((room[0, 32:48] == 7.0).all()) and bool((room[0, 112:] == 7.0).all()) and bool((room[1, 32:] == 7.0).all())

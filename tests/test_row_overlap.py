@@ -84,3 +84,25 @@ def test_many_rows_of_any_distance_are_looked_at_at_once(lib):
     assert append(oq=BASE, os=4096, rows=n, q=BASE + 256 - 16, qs=8192) == REFUSED
     assert append(oq=BASE, os=6144, rows=n, k=BASE + 2 * n * 4096 + 1024, ks=4096) == PAST_EVERY_CHECK
     assert time.perf_counter() - start < 1.0
+
+
+def paged(q, qs, out, batch, heads):
+    from sparse_attention_decode_gb300 import _attention as A, _serving  # noqa: F401
+    st, far = A._Strides(4 * 128 * 128, 128, 128 * 128), at(FAR)
+    return A._fn("msa_attention_paged")(at(q), qs, far, st, far, st, 10, far, 8, far, batch, 1, heads, 1, 1024, 1.0, at(out), None,
+                                        far, 1 << 40, None)
+
+
+def test_output_of_the_attention_over_all_pages(lib):
+    """An output between two query rows is no overlap."""
+    assert paged(BASE, 1024, BASE + 512, 2, 1) == PAST_EVERY_CHECK  # rows of 256 bytes, 2 KiB apart; 512 bytes of output
+    assert paged(BASE, 1024, BASE + 2048 - 512, 2, 1) == PAST_EVERY_CHECK
+    assert paged(BASE, 1024, BASE + 240, 2, 1) == paged(BASE, 1024, BASE + 2048 - 496, 2, 1) == REFUSED
+    r, seen = random.Random(4), set()
+    for _ in range(3000):
+        rows, heads = r.randint(1, 6), r.randint(1, 2)
+        stride, shift = 16 * heads + r.choice([0, r.randint(0, 200)]), r.randint(-250, 700)
+        want = shared(0, stride, 16 * heads, shift, 16 * heads, 16 * heads, rows)
+        assert paged(BASE, stride * 8, BASE + 16 * shift, rows, heads) == (REFUSED if want else PAST_EVERY_CHECK)
+        seen.add((want, rows > 1, 0 < shift < (rows - 1) * stride))
+    assert len(seen) >= 5
