@@ -11,8 +11,6 @@
 
 namespace msa {
 
-__device__ __forceinline__ int pages_of(int tokens) { return tokens / kPage + (tokens % kPage != 0); }
-
 __device__ __forceinline__ bool mbar_test_wait(uint32_t bar, uint32_t parity)
 {
     uint32_t done;

@@ -29,6 +29,8 @@ constexpr size_t kHeaderBytes = 256;
 
 __host__ __device__ constexpr size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
+__host__ __device__ inline int pages_of(int tokens) { return tokens / kPage + (tokens % kPage != 0); }
+
 __host__ __device__ inline int kmax_for(int k) { return k <= 16 ? 16 : 32; }
 
 __host__ __device__ inline size_t prefix_offset() { return kHeaderBytes; }

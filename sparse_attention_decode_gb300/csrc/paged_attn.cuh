@@ -43,6 +43,7 @@
 
 #include "attn_common.cuh"
 #include "host_util.cuh"
+#include "paged_split.cuh"
 #include "tcgen05.cuh"
 
 #include "msa_serving.h"
@@ -86,42 +87,6 @@ struct PagedParams {
     int withhold;  // test of the bounded waits: the producer loads and signals no page
 };
 
-__device__ __forceinline__ int paged_len(const PagedParams &p, int b)
-{
-    const int n = p.seq_lens[b];
-    return n < 0 || n > p.seq_limit ? 0 : n;
-}
-
-// The batch's work: slots of all units, and units that have some.  A unit of P pages has `lead` slots, in which there is
-// nothing to do and which stand for its start and its end, and then a slot a page.
-struct PagedWork {
-    int slots, units;
-};
-
-// The ranges: CTA g has [start(g), start(g + 1)) of the units' slots, two pages at least, but no fewer ranges than units (at
-// least 1, 2, 4 pages: one request of 300 tokens, 4 heads, 8.9, 9.4, 8.1 us; 2000: 9.6, 9.8, 11.1; 8700: 10.7, 10.5, 11.8).
-struct PagedSplit {
-    int ctas, range, more;
-    __device__ PagedSplit(const PagedWork &work, const PagedParams &p)
-    {
-        ctas = min(p.grid, max((work.slots - work.units * p.lead + 1) / 2, work.units));
-        range = ctas > 0 ? work.slots / ctas : 0;
-        more = work.slots - range * ctas;
-    }
-    __device__ int start(int g) const { return g * range + min(g, more); }
-    // the CTA whose range holds slot x
-    __device__ int owner(int x) const
-    {
-        const int longer = more * (range + 1);
-        return x < longer ? x / (range + 1) : more + (x - longer) / range;
-    }
-};
-
-// A place in the sequence of the units' slots.
-struct PagedAt {
-    int b, u, j;  // request, its unit, the unit's page (negative: its lead)
-};
-
 struct PagedScan {
     int slots[32], requests[32], early[32];  // the warps' sums
     PagedAt at;
@@ -138,7 +103,7 @@ __device__ __forceinline__ PagedWork paged_find(const PagedParams &p, PagedScan 
     const int b0 = min(p.batch, tid * each), b1 = min(p.batch, b0 + each);
     int mine = 0, some = 0, early = 0;
     for (int b = b0; b < b1; ++b) {
-        const int P = pages_of(paged_len(p, b)), n = P > 0 ? (P + p.lead) * units : 0;
+        const int n = paged_slots(p, b, units);
         mine += n;
         some += n > 0;
         early += b < request ? n : 0;
@@ -169,53 +134,12 @@ __device__ __forceinline__ PagedWork paged_find(const PagedParams &p, PagedScan 
         before += sc->early[w];
     }
     const int x = want(work);
-    int from = prior + upto - mine;
-    if (x >= from && x < from + mine) {
-        for (int b = b0; b < b1; ++b) {
-            const int P = pages_of(paged_len(p, b)), each_unit = P > 0 ? P + p.lead : 0, n = each_unit * units;
-            if (x < from + n) {
-                const int u = (x - from) / each_unit;
-                sc->at = PagedAt{b, u, x - from - u * each_unit - p.lead};
-                break;
-            }
-            from += n;
-        }
-    }
+    const int from = prior + upto - mine;
+    if (x >= from && x < from + mine)
+        sc->at = paged_at(p, b0, b1, from, x);
     __syncthreads();
     return work;
 }
-
-// Runs through a range unit by unit.
-struct PagedWalk {
-    int b, u, j, left;  // the next page, and slots left from there on
-    int len, P;         // of request b
-    __device__ PagedWalk(const PagedParams &p, const PagedAt &at, int n) : b(at.b), u(at.u), j(at.j), left(n), len(0), P(0)
-    {
-        left += min(j, 0);
-        j = max(j, 0);
-        if (left > 0) {
-            len = paged_len(p, b);
-            P = pages_of(len);
-        }
-    }
-    __device__ int run() const { return min(left, P - j); }
-    __device__ void next(const PagedParams &p)
-    {
-        left -= run() + p.lead;
-        j = 0;
-        if (++u == p.row_tiles * p.kv_heads && left > 0) {
-            u = 0;
-            do {
-                if (++b >= p.batch) {  // not while the lengths stay as they are
-                    left = 0;
-                    return;
-                }
-                len = paged_len(p, b);
-                P = pages_of(len);
-            } while (P == 0);
-        }
-    }
-};
 
 template <int N, int WAYS, int GROUPS, int STAGES>
 struct PagedSmem {
@@ -726,7 +650,7 @@ __global__ void __launch_bounds__(PagedLayout<F, N, WAYS, GROUPS>::kThreads, 1) 
             const int n = walk.run(), tile_at = walk.u / p.kv_heads, h = walk.u - tile_at * p.kv_heads;
             const int rows = min(p.tile_rows, unit_rows - tile_at * p.tile_rows), len = walk.len, j0 = walk.j;
             const bool whole = n == walk.P;
-            const int64_t slot = static_cast<int64_t>(2 * cta + (seg > 0)) * p.tile_rows;
+            const int64_t slot = static_cast<int64_t>(paged_part(cta, seg)) * p.tile_rows;
             const int64_t place0 = static_cast<int64_t>(walk.b) * p.q_len * heads + h * p.group;  // the first row's, ctl->at from there
             const int begins = WAYS == 2 ? done & 1 : 0;  // the way that has the run's first page
             walk_next = walk;
@@ -1104,19 +1028,15 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__
     const int P = at.b < p.batch ? pages_of(paged_len(p, at.b)) : 0;
     // the slots of the unit's pages [from, from + P), and the CTA that has the first
     const int from = UNITS ? before + at.u * (P + p.lead) + p.lead : (x + 1 < split.ctas ? split.start(x + 1) : 0) - at.j;
-    const int c = UNITS ? (P > 0 ? split.owner(from) : 0) : x;
+    const PagedParts where(split, from, P, p.lead);
+    const int parts = where.n;
     griddep_wait();  // also where there is nothing to do: who waits for this grid reads what both have written
-    if (P == 0 || (!UNITS && (at.j <= 0 || split.start(c) > from)))
+    if (parts < 2 || (!UNITS && (at.j <= 0 || where.first != x)))
         return;  // no unit goes on there, or another block has it
-    const int parts = split.owner(from + P - 1) - c + 1;
-    if (parts == 1)
-        return;
-    // slot of part i: the CTA's first run, but for the unit's first part where the CTA has others before it
-    const int slot0 = 2 * c + (split.start(c) < from - p.lead);
     const int h = at.u % p.kv_heads, row0 = at.u / p.kv_heads * p.tile_rows;
     const int rows = min(p.tile_rows, p.q_len * p.group - row0);
     const int r = blockIdx.y * kRows + warp / WPR;
-    auto slot = [&](int i) { return static_cast<int64_t>(i == 0 ? slot0 : 2 * (c + i)) * p.tile_rows + r; };
+    auto slot = [&](int i) { return static_cast<int64_t>(where.part(i)) * p.tile_rows + r; };
     float M = -INFINITY, sum = 0.0f;
     float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     bool bad = false;
