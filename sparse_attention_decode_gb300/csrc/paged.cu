@@ -18,9 +18,11 @@ static size_t paged_workspace(int64_t max_rows, int group)
     return kHeaderBytes + 2 * kPagedMaxGrid * static_cast<size_t>(paged_tile_rows(max_rows * group)) * (kDim + 1) * sizeof(float);
 }
 
-// What a unit costs beside its pages (its query rows, its first page's references, its epilogue), in pages of the same type:
-// bf16, E4M3.  64 requests of 1 to 3000 tokens, 4 heads: 16 rows 52.8 us without, 44.4 with 2 to 4, 45.2 with 8; 64 rows 90.2,
-// 56.0 with 4, 57.3 with 8; E4M3 64.4, 37.5 with 4, 34.3 with 8, 37.5 with 16.
+// What a unit costs beside its pages (its query rows, its first page's references, its epilogue), in pages of the same type
+// and rows: bf16, E4M3 up to 32 rows; E4M3 with 64, whose pages cost twice as much, counts as bf16.  64 requests of 1 to 3000
+// tokens, 4 heads, with 0 / 4 / 8 / 12 / 16 pages: bf16 16 rows 52.8 us, 44.4, 45.2 with 8, 64 rows 90.2, 56.0, 57.3; E4M3 16
+// rows 54.0, 29.3, 28.1, 29.2, 31.0, 32 rows 71.1, 37.8, 37.4, 39.5, 41.6, 64 rows 97.0, 54.9, 58.5, 62.0, 65.3.  24 requests of
+// 2000 to 12000, E4M3: 38.5, 35.8, 36.3, 37.8, 39.1; 50.1, 45.6, 45.5, 47.7, 49.4; 75.9, 70.9, 74.0, 78.4, 82.3.
 constexpr int kPagedLead[2] = {4, 8};
 
 template <class F, int N, int WAYS, int GROUPS>
@@ -98,7 +100,7 @@ static msa_status paged_entry(const void *q, int64_t q_stride, const void *k, co
     p.tile_rows = paged_tile_rows(static_cast<int64_t>(q_len) * group);
     p.row_tiles = (q_len * group + p.tile_rows - 1) / p.tile_rows;
     p.seq_limit = static_cast<int>(std::min<int64_t>(max_model_len, kPage * bt_stride));
-    p.lead = fp8 ? kPagedLead[1] : kPagedLead[0];
+    p.lead = kPagedLead[fp8 && p.tile_rows < kPagedMaxRows];
     // the slots of all units are counted in 32 bits
     if (((static_cast<int64_t>(p.seq_limit) + kPage - 1) / kPage + p.lead) * batch * p.row_tiles * kv_heads > (1 << 30))
         return MSA_ERR_UNSUPPORTED;
