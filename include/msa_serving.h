@@ -53,7 +53,8 @@ extern "C" {
  *                squares them.
  *   q_weight, k_weight   optional fp32 [128]; NULL: no norm (of that tensor).
  *   eps          finite, >= 0.  (Where it is 0 a head of zeros stays one.)
- *   inv_freq     fp32 [rotary_dim / 2], finite (NULL where rotary_dim is 0).
+ *   inv_freq     fp32 [rotary_dim / 2] (NULL where rotary_dim is 0), of at most 2^10 in
+ *                magnitude (the angles of larger ones lose digits).
  *   rotary_dim   0..128, a multiple of 16.
  *   positions    optional int32 [total_rows]: the rows' rotary positions, where they
  *                are not t (after msa_cache_evict, keys keep the positions they were
@@ -79,8 +80,9 @@ msa_status msa_cache_append(const void *q, int64_t q_stride, int q_heads, void *
 
 /*
  * The same on an E4M3 cache: for every token and head scale = max|z| / 448 and
- * code = e4m3(z / scale), to the nearest; a head whose largest value is below
- * 2^-117 has scale 0 and codes 0.  Scales fp32 [num_pages, kv_heads, 128],
+ * code = e4m3(z / scale), to the nearest (z times fp32's 1 / scale: within 2^-22
+ * of the middle between two codes it may be either); a head whose largest value is
+ * below 2^-117 has scale 0 and codes 0.  Scales fp32 [num_pages, kv_heads, 128],
  * contiguous, 16-byte aligned (an index-K cache's [num_pages, 128]).
  */
 msa_status msa_cache_append_fp8(const void *q, int64_t q_stride, int q_heads, void *out_q, int64_t out_q_stride,
@@ -95,7 +97,8 @@ msa_status msa_cache_append_fp8(const void *q, int64_t q_stride, int q_heads, vo
 /*
  * Attention over all of a request's tokens: msa_attention_sparse's formula, out
  * and out_lse with every block of the request selected.  out shares no memory with
- * a row of q (MSA_ERR_INVALID_ARG).
+ * a row of q (MSA_ERR_INVALID_ARG).  Both products accumulate in fp32; a token's
+ * weight is rounded to bf16 for the second one, their sum is not.
  * q_len <= 64; batch x KV heads x tiles of 64 rows of a head x (pages of
  * max_model_len + 8) is at most 2^30.
  *

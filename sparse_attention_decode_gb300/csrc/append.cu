@@ -10,7 +10,8 @@
 // Angles.  position * inv_freq is wanted modulo one turn.  Turns are counted in units of
 // 2^-64 in a 64-bit integer, which wraps where a turn ends: F = inv_freq 2^64 / (2 pi)
 // once, from the bits of the fp32 value and a 64-bit 1 / (2 pi), then position * F.
-// That is exact but for F's own rounding (position * 2^-64 turns); an fp32 product
+// That is exact but for F's own rounding (position * 2^-64 turns, or that times inv_freq / 4 where it is more: below 2^-22
+// rad up to an inv_freq of 2^10 and any position); an fp32 product
 // would be off by 0.06 rad at a position of 10^6, and 64-bit floating-point products run
 // at a 64th of the rate.  (Integer work of one thread a pair: nothing beside the heads.)
 //
@@ -63,7 +64,7 @@ __device__ __forceinline__ uint64_t turns_of(float f)
     const uint64_t lo = m * kInverseTurn, hi = __umul64hi(m, kInverseTurn);
     uint64_t r;
     if (e >= 64)
-        r = 0;  // whole turns
+        r = 0;  // (none of the digits that count are among the 64)
     else if (e >= 0)
         r = lo << e;
     else if (e > -64)
@@ -486,8 +487,10 @@ static msa_status launch_append(const AppendParams &p, int sms, int dev, cudaStr
     const int64_t bytes = static_cast<int64_t>(heads) * kDim * 2;
     const int blocks = bytes < kAppendSmBytes / 4 ? std::min(kAppendBlocks, kAppendSmBytes / append_block_bytes(static_cast<int>(bytes))) : 0;
     // The ring: more rows than SMs (160 rows of 72 heads 5.9 us with it, 6.2 without), lines of 24 heads and more, where a
-    // row is enough to hide its set-up (6440 rows of 40 heads 34.4 and 39.2, 24 27.7 and 27.6, 16 23.9 and 21.2, 5 17.0 and
-    // 13.5), that fit twice an SM.
+    // row is enough to hide its set-up, that fit twice an SM.  With it and without, 6440 rows of 40 / 32 / 24 / 20 / 16 heads:
+    // 31.1 and 39.2, 28.3 and 33.2, 25.1 and 27.2, 23.9 and 24.1, 20.9 and 21.1 us; a quarter of the rows: 11.9 and 13.1, 10.8
+    // and 11.1, 9.5 and 9.6, 9.2 and 8.3, 8.2 and 7.6; E4M3, 6440 rows: 36.5 and 51.1, 32.9 and 42.9, 29.3 and 36.7, 28.3 and
+    // 31.0, 24.5 and 27.7, 200 rows: 5.7 and 5.9, 5.5 and 5.7, 5.2 and 4.6, 5.1 and 4.6, 4.8 and 4.3.
     if (p.rows > sms && heads >= 24 && blocks >= 2) {
         static std::atomic<bool> allowed[kMaxDevices];
         auto *kernel = append_rows_kernel<FP8, INTER, LIFT>;

@@ -9,7 +9,7 @@ bool make_cache_map(CUtensorMap *map, const void *base, const int64_t *strides, 
 bool cache_ok(const void *base, const int64_t *strides, int64_t pages, int heads, bool fp8);
 bool unaligned(const void *p, uintptr_t a);
 
-// Rows of a unit: a chain's 16 or 32, or both chains' 32.
+// Rows of a unit: the GROUPS * N of the forms in launch_paged_rows.
 static int paged_tile_rows(int64_t rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : kPagedMaxRows; }
 
 // Two parts a CTA: a row of each is 516 bytes.
