@@ -59,8 +59,9 @@ template <class F>
 static msa_status launch_paged_rows(const PagedParams &p, int dev, cudaStream_t st)
 {
     // Up to 32 rows: two ways; 64: one.  E4M3 rows are worked on 16 a warpgroup, bf16 ones, which need no second and third
-    // term, 32 (32 requests of 31000 E4M3 tokens: 32 rows 193 us with 16, 198 with 32, 64 rows 314 and 360; 8 of 32768 bf16
-    // ones: 88.8 and 88.2, 93.2 and 92.5).
+    // term, 32.  With 16 and 32: E4M3, 32 rows, 256 requests of 100 to 300 tokens 59.4 and 67.4 us, 64 of 1 to 3000 37.5 and
+    // 40.9, 24 of 2000 to 12000 45.7 and 45.8, 32 of 31000 186.3 and 182.5; 64 rows, 32 of 31000 317 and 354, 1 of 131072 53.0
+    // and 58.5; bf16, 8 of 32768, 32 rows 88.8 and 88.2, 64 rows 93.2 and 92.5.
     if (p.tile_rows == 16)
         return launch_paged<F, 16, 2, 1>(p, dev, st);
     if constexpr (F::kFp8)

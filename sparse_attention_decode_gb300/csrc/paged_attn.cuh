@@ -16,9 +16,9 @@
 // E4M3 token is one number for all its weights.
 //
 // What bounds it: the stream of pages, where a unit has many and its rows are 16 to 32
-// (256 requests of 8000 to 8704 tokens, 4.4 GB: 627 us, 7.0 TB/s; E4M3, 32 of 30000 to
-// 32768: 162 us, 6.5 TB/s; 64 bf16 rows, 8 of 32768: 92.5 us, 5.8 TB/s).  On one E4M3
-// request of 131072 (30.6 us for a floor of 20.5) and below, what a unit costs once: its
+// (256 requests of 8000 to 8704 tokens, 4.4 GB: 625 us, 7.0 TB/s; E4M3, 32 of 30000 to
+// 32768: 162 us, 6.5 TB/s; 64 bf16 rows, 8 of 32768: 89.6 us, 6.0 TB/s).  On one E4M3
+// request of 131072 (30.0 us for a floor of 20.5) and below, what a unit costs once: its
 // rows, the first page's references, the epilogue, the join, one after the other.  With
 // 64 E4M3 rows the weights' arithmetic: 1.5 us a page for 0.8 of the stream.
 //
