@@ -118,7 +118,8 @@ msa_status msa_attention_paged(const void *q, int64_t q_stride, const void *k, c
  * msa_attention_sparse_fp8).  Both products run on the codes as they are, with
  * fp32 accumulation: a query value is held exactly from 2^-14 of its row's largest
  * on, and to 2^-22 of that below; a product of weight and V scale to 2^-8 of
- * itself, or to 2^-21 of the largest such product of its row.
+ * itself, or to 2^-21 of the largest such product of its row (a weight below
+ * 2^-126 of the row's largest is 0, whatever its scale).
  */
 msa_status msa_attention_paged_fp8(const void *q, int64_t q_stride, const void *k, const int64_t *k_strides,
                                    const float *k_scale, const void *v, const int64_t *v_strides,
